@@ -360,6 +360,153 @@ I8MM_API int i8mm_workspace_layout(int64_t M, int64_t K, int64_t* offsets);
  */
 I8MM_API int i8mm_gelu_f16(const uint16_t* X, int64_t count, uint16_t* Y, i8mm_stream_t stream);
 
+/*
+ * Paged 8-bit key/value cache: the keys and values between the projections of
+ * an attention block, held as the weights of the layer are, in absmax int8.
+ *
+ * The unit is a block of I8MM_KV_BLOCK = 16 consecutive tokens of one
+ * sequence and one key/value head, with one absmax a: a code q stands for
+ * q * fl32(a / 127). Codes are rne(fl32(x * fl32(127 / a))), in [-127, 127]; a
+ * block whose absmax is at most 2^-119 has a = 0 and zero codes. A NaN or
+ * infinite element makes its whole block NaN.
+ *
+ * A block's codes are 16 x 16 byte tiles, so that an MFMA operand is one
+ * 16-byte load:
+ *   k_codes[page][head][block][D/16][16 tokens][16 features]
+ *   v_codes[page][head][block][D/16][16 features][16 tokens]
+ *   k_absmax, v_absmax fp32 [page][head][block]
+ * with page_tokens / 16 blocks a page. All four are device memory, codes and
+ * absmaxes 16-byte aligned. What an empty cache holds does not matter.
+ */
+#define I8MM_KV_BLOCK 16
+typedef struct i8mm_kv_cache {
+  int8_t* k_codes;
+  float* k_absmax;
+  int8_t* v_codes;
+  float* v_absmax;
+  int64_t num_pages;
+  int64_t page_tokens; /* a multiple of 16, at most 65536                     */
+  int64_t kv_heads;
+  int64_t head_dim;    /* D: 64, 80, 96, 128 or 256                           */
+} i8mm_kv_cache;
+
+/*
+ * The sequences of one call. Sequence b has the length L = seq_lens[b], its
+ * new tokens included; the n = cu_tokens[b+1] - cu_tokens[b] new ones are its
+ * last, at positions L - n .. L - 1, and are rows cu_tokens[b] .. of the
+ * packed tensors. Position t stands in page page_table[b][t / page_tokens].
+ *
+ * The arrays are read on the device, so no call waits for the host, and what
+ * they hold is bounded there: L is cut to min(max_len, max_pages *
+ * page_tokens), n to max_tokens and to the rows below total_tokens; a page
+ * outside [0, num_pages) is absent (nothing is written to it, no query sees
+ * its tokens, it reads as 0); a token at a negative position (n > L) is not
+ * stored, sees nothing and reads as 0.
+ *
+ * page_table int32 [num_seqs, max_pages], seq_lens int32 [num_seqs],
+ * cu_tokens int32 [num_seqs + 1] ascending from 0, or NULL for one new token
+ * a sequence (total_tokens == num_seqs); each 4-byte aligned. max_tokens and
+ * max_len are the host's bounds on n and L: they size the launch.
+ */
+typedef struct i8mm_kv_batch {
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  const int32_t* cu_tokens;
+  int64_t num_seqs;
+  int64_t max_pages;
+  int64_t total_tokens;
+  int64_t max_tokens;
+  int64_t max_len;
+} i8mm_kv_batch;
+
+/*
+ * Position rotation of the first `dim` features of a head: the pair (x1, x2)
+ * at position p becomes (x1 c - x2 s, x2 c + x1 s) with c = cos[p][i], s =
+ * sin[p][i], each product and sum rounded to fp32. Pair i is features
+ * (i, i + dim / 2), or (2 i, 2 i + 1) when interleaved != 0.
+ * cos, sin: fp32 [positions, dim / 2], 16-byte aligned; dim a multiple of 16,
+ * at most the head's; positions at least the batch's max_len.
+ */
+typedef struct i8mm_rotary {
+  const float* cos;
+  const float* sin;
+  int64_t dim;
+  int64_t positions;
+  int interleaved;
+} i8mm_rotary;
+
+/*
+ * int8_kv_cache_append: rotate and quantize new keys, quantize new values, and
+ * store both.
+ *
+ *   k, v     fp16 [total_tokens, kv_heads, D], features contiguous, the other
+ *            strides given in elements and multiples of 8 (slices of a fused
+ *            projection's output need no copy).
+ *   rotary   host struct or NULL: applied to k in fp32, with no rounding
+ *            before the codes'.
+ *
+ * New tokens that share a block with older ones take the larger absmax a' of
+ * the block's and theirs; where it grows, the older codes become
+ * rne(q * fl32(a / a')). Rows of a block past the sequence's end get code 0.
+ * A page may belong to several sequences (a shared prefix) as long as no call
+ * appends to it. Repeating a call on the same data changes nothing.
+ * Errors: EINVAL, EALIGN, ENODEVICE, ELAUNCH.
+ */
+I8MM_API int int8_kv_cache_append(const uint16_t* k, int64_t k_token_stride, int64_t k_head_stride,
+                                  const uint16_t* v, int64_t v_token_stride, int64_t v_head_stride,
+                                  const i8mm_kv_cache* cache, const i8mm_kv_batch* batch,
+                                  const i8mm_rotary* rotary, i8mm_stream_t stream);
+
+/*
+ * int8_kv_cache_attention: softmax attention of the new tokens' queries over
+ * the cached tokens, the new ones included (append them first).
+ *
+ * Query head h reads key/value head h / (q_heads / kv_heads). For the query
+ * at position p:
+ *   S_t = scale * <q, k_t> - slope_h * (p - t),  O = sum_t softmax(S)_t v_t
+ * over the visible tokens t < L: t <= p when causal, and t > p - window when
+ * window > 0. A query that sees no token gets O = 0.
+ *
+ *   q        fp16 [total_tokens, q_heads, D], strides as for append; rotated
+ *            here when `rotary` is given.
+ *   scale    finite and > 0.
+ *   causal   0 or 1; window >= 0, 0 = no limit, needs causal.
+ *   alibi_slopes  fp32 [q_heads] (4-byte aligned), or NULL.
+ *   out      fp16 [total_tokens, q_heads, D], contiguous, 16-byte aligned.
+ *   workspace  int8_kv_cache_attention_workspace_bytes(...) bytes, 256-byte
+ *            aligned (NULL when that is 0). What it holds on entry does not
+ *            matter.
+ *
+ * The query is taken as 15-bit integers over its row's absmax, so its product
+ * with the key codes is an exact integer; the softmax runs in fp32, its
+ * weights are rounded to fp16 against their row's maximum, and the sums over
+ * tokens are fp32. Results do not depend on what ran before.
+ * Errors: EINVAL, EALIGN, EWORKSPACE, ENODEVICE, ELAUNCH.
+ */
+I8MM_API int int8_kv_cache_attention(const uint16_t* q, int64_t q_token_stride,
+                                     int64_t q_head_stride, int64_t q_heads,
+                                     const i8mm_kv_cache* cache, const i8mm_kv_batch* batch,
+                                     const i8mm_rotary* rotary, float scale, int causal,
+                                     int64_t window, const float* alibi_slopes, uint16_t* out,
+                                     void* workspace, size_t workspace_bytes,
+                                     i8mm_stream_t stream);
+
+/* Bytes of workspace int8_kv_cache_attention needs (0 also if the sizes are
+ * invalid). Host-only, pure: it reads the structs' sizes, not their
+ * pointers. */
+I8MM_API size_t int8_kv_cache_attention_workspace_bytes(const i8mm_kv_cache* cache,
+                                                        const i8mm_kv_batch* batch,
+                                                        int64_t q_heads);
+
+/*
+ * int8_kv_cache_read: the cached keys (rotated, as stored) and values of the
+ * batch's tokens in fp16, fp16(fl32(q * fl32(a / 127))).
+ *   k, v   fp16 [total_tokens, kv_heads, D], contiguous; either may be NULL.
+ * Errors: EINVAL, EALIGN, ENODEVICE, ELAUNCH.
+ */
+I8MM_API int int8_kv_cache_read(const i8mm_kv_cache* cache, const i8mm_kv_batch* batch,
+                                uint16_t* k, uint16_t* v, i8mm_stream_t stream);
+
 /* Text of the last error raised on the calling host thread ("" if none). */
 I8MM_API const char* i8mm_last_error(void);
 

@@ -20,9 +20,12 @@ def ensure_built():
 
 def __getattr__(name):
     # ops and the module are imported on first use (they import torch)
-    if name in ("ops", "linear", "synth"):
+    if name in ("ops", "linear", "synth", "kv_cache"):
         import importlib
         return importlib.import_module("." + name, __name__)
+    if name in ("Int8KVCache", "KVBatch", "Rotary"):
+        from . import kv_cache
+        return getattr(kv_cache, name)
     if name == "Int8Linear":
         from .linear import Int8Linear
         return Int8Linear

@@ -30,12 +30,38 @@ EXPORTS = (
     "linear_int8_mixed_workspace_bytes_many_outliers",
     "i8mm_workspace_layout",
     "i8mm_gelu_f16",
+    "int8_kv_cache_append",
+    "int8_kv_cache_attention",
+    "int8_kv_cache_attention_workspace_bytes",
+    "int8_kv_cache_read",
     "i8mm_last_error",
     "i8mm_status_string",
 )
 
 _lock = threading.Lock()
 _lib = None
+
+
+class KVCacheStruct(ctypes.Structure):
+    """i8mm_kv_cache"""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_absmax", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_absmax", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("page_tokens", ctypes.c_int64),
+                ("kv_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64)]
+
+
+class KVBatchStruct(ctypes.Structure):
+    """i8mm_kv_batch"""
+    _fields_ = [("page_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("cu_tokens", ctypes.c_void_p), ("num_seqs", ctypes.c_int64),
+                ("max_pages", ctypes.c_int64), ("total_tokens", ctypes.c_int64),
+                ("max_tokens", ctypes.c_int64), ("max_len", ctypes.c_int64)]
+
+
+class RotaryStruct(ctypes.Structure):
+    """i8mm_rotary"""
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("dim", ctypes.c_int64),
+                ("positions", ctypes.c_int64), ("interleaved", ctypes.c_int)]
 
 
 class I8mmError(RuntimeError):
@@ -52,6 +78,7 @@ def _status_name(status):
 
 def _declare(lib):
     vp, i64, f32, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_float, ctypes.c_int
+    cache, batch, rotary = (ctypes.POINTER(t) for t in (KVCacheStruct, KVBatchStruct, RotaryStruct))
     sig = {
         "int8_quantize_colwise_weight": ([vp, i64, i64, vp, vp, vp], i32),
         "int8_quantize_rowwise": ([vp, i64, i64, vp, vp, vp, vp], i32),
@@ -67,6 +94,11 @@ def _declare(lib):
         "linear_int8_mixed_workspace_bytes_many_outliers": ([i64, i64, i64], ctypes.c_size_t),
         "i8mm_workspace_layout": ([i64, i64, ctypes.POINTER(ctypes.c_int64)], i32),
         "i8mm_gelu_f16": ([vp, i64, vp, vp], i32),
+        "int8_kv_cache_append": ([vp, i64, i64, vp, i64, i64, cache, batch, rotary, vp], i32),
+        "int8_kv_cache_attention": ([vp, i64, i64, i64, cache, batch, rotary, f32, i32, i64, vp, vp,
+                                     vp, ctypes.c_size_t, vp], i32),
+        "int8_kv_cache_attention_workspace_bytes": ([cache, batch, i64], ctypes.c_size_t),
+        "int8_kv_cache_read": ([cache, batch, vp, vp, vp], i32),
         "i8mm_last_error": ([], ctypes.c_char_p),
         "i8mm_status_string": ([i32], ctypes.c_char_p),
     }

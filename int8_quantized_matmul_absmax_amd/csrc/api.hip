@@ -452,3 +452,190 @@ int i8mm_gelu_f16(const uint16_t* X, int64_t count, uint16_t* Y, i8mm_stream_t s
 }
 
 }  // extern "C"
+
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Sizes of a cache and a batch, checked and narrowed into *a (pointers not
+// looked at).
+int kv_sizes(const char* fn, const i8mm_kv_cache* c, const i8mm_kv_batch* b, i8mm::KvArgs* a) {
+  if (!c || !b) return fail(I8MM_EINVAL, "%s: cache or batch is NULL", fn);
+  if (c->num_pages < 0 || c->page_tokens <= 0 || c->page_tokens > 65536 || c->kv_heads <= 0)
+    return fail(I8MM_EINVAL, "%s: cache of %lld pages of %lld tokens, %lld heads", fn,
+                (long long)c->num_pages, (long long)c->page_tokens, (long long)c->kv_heads);
+  if (c->page_tokens % I8MM_KV_BLOCK != 0)
+    return fail(I8MM_EALIGN, "%s: page_tokens=%lld is not a multiple of %d", fn,
+                (long long)c->page_tokens, I8MM_KV_BLOCK);
+  if (!i8mm::kv_head_dim_ok(c->head_dim))
+    return fail(I8MM_EINVAL, "%s: head_dim=%lld is none of 64, 80, 96, 128, 256", fn,
+                (long long)c->head_dim);
+  const int64_t slots = c->page_tokens / I8MM_KV_BLOCK;
+  // blocks are numbered in int32; heads and sequences are grid dimensions
+  if (c->kv_heads > 65535 || slots > INT32_MAX / c->kv_heads ||
+      c->num_pages > INT32_MAX / (slots * c->kv_heads))
+    return fail(I8MM_EINVAL, "%s: more than 2^31 - 1 blocks or 65535 heads", fn);
+  if (b->num_seqs < 0 || b->max_pages < 0 || b->total_tokens < 0 || b->max_tokens < 0 ||
+      b->max_len < 0)
+    return fail(I8MM_EINVAL, "%s: negative size in the batch", fn);
+  if (b->num_seqs > 65535 || b->total_tokens > INT32_MAX || b->max_tokens > INT32_MAX / 4 ||
+      b->max_pages > INT32_MAX)
+    return fail(I8MM_EINVAL, "%s: more than 65535 sequences or a size beyond int32", fn);
+  if (!b->cu_tokens && b->total_tokens != b->num_seqs)
+    return fail(I8MM_EINVAL, "%s: no cu_tokens, but %lld tokens for %lld sequences", fn,
+                (long long)b->total_tokens, (long long)b->num_seqs);
+  const int64_t room = b->max_pages * c->page_tokens;
+  const int64_t cap = std::min(b->max_len, room);
+  if (cap > INT32_MAX / 2) return fail(I8MM_EINVAL, "%s: max_len beyond 2^30 tokens", fn);
+  a->num_pages = (int)c->num_pages;
+  a->slots = (int)slots;
+  a->kv_heads = (int)c->kv_heads;
+  a->head_dim = (int)c->head_dim;
+  a->num_seqs = (int)b->num_seqs;
+  a->max_pages = (int)b->max_pages;
+  a->total_tokens = (int)b->total_tokens;
+  a->max_tokens = (int)std::min(b->max_tokens, b->cu_tokens ? b->total_tokens : (int64_t)1);
+  a->len_cap = (int)cap;
+  return I8MM_OK;
+}
+
+int kv_check(const char* fn, const i8mm_kv_cache* c, const i8mm_kv_batch* b, i8mm::KvArgs* a) {
+  I8MM_TRY(kv_sizes(fn, c, b, a));
+  const bool some = c->num_pages > 0;
+  I8MM_TRY(check_ptr(fn, "k_codes", c->k_codes, some));
+  I8MM_TRY(check_ptr(fn, "k_absmax", c->k_absmax, some));
+  I8MM_TRY(check_ptr(fn, "v_codes", c->v_codes, some));
+  I8MM_TRY(check_ptr(fn, "v_absmax", c->v_absmax, some));
+  if (!b->page_table && b->num_seqs * b->max_pages > 0)
+    return fail(I8MM_EINVAL, "%s: page_table is NULL", fn);
+  if (!b->seq_lens && b->num_seqs > 0) return fail(I8MM_EINVAL, "%s: seq_lens is NULL", fn);
+  if (!aligned4(b->page_table) || !aligned4(b->seq_lens) || !aligned4(b->cu_tokens))
+    return fail(I8MM_EALIGN, "%s: page_table, seq_lens or cu_tokens is not 4-byte aligned", fn);
+  a->k_codes = c->k_codes;
+  a->k_absmax = c->k_absmax;
+  a->v_codes = c->v_codes;
+  a->v_absmax = c->v_absmax;
+  a->page_table = b->page_table;
+  a->seq_lens = b->seq_lens;
+  a->cu_tokens = b->cu_tokens;
+  return I8MM_OK;
+}
+
+int rotary_check(const char* fn, const i8mm_rotary* r, const i8mm::KvArgs& a,
+                 i8mm::RotaryArgs* out) {
+  *out = i8mm::RotaryArgs{nullptr, nullptr, 0, 0};
+  if (!r) return I8MM_OK;
+  if (r->dim <= 0 || r->dim % 16 != 0 || r->dim > a.head_dim)
+    return fail(I8MM_EINVAL, "%s: rotary dim=%lld is not a multiple of 16 up to %d", fn,
+                (long long)r->dim, a.head_dim);
+  if (r->positions < a.len_cap)
+    return fail(I8MM_EINVAL, "%s: rotary tables of %lld positions, sequences up to %d", fn,
+                (long long)r->positions, a.len_cap);
+  I8MM_TRY(check_ptr(fn, "cos", r->cos, a.len_cap > 0));
+  I8MM_TRY(check_ptr(fn, "sin", r->sin, a.len_cap > 0));
+  *out = i8mm::RotaryArgs{r->cos, r->sin, (int)r->dim, r->interleaved != 0};
+  return I8MM_OK;
+}
+
+// 16-byte loads of 8 halfs at any token and head.
+int strides_check(const char* fn, const char* name, const void* p, bool required, int64_t ts,
+                  int64_t hs) {
+  I8MM_TRY(check_ptr(fn, name, p, required));
+  if (ts < 0 || hs < 0) return fail(I8MM_EINVAL, "%s: negative stride of %s", fn, name);
+  if (ts % 8 != 0 || hs % 8 != 0)
+    return fail(I8MM_EALIGN, "%s: strides of %s are not multiples of 8 elements", fn, name);
+  return I8MM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int int8_kv_cache_append(const uint16_t* k, int64_t k_token_stride, int64_t k_head_stride,
+                         const uint16_t* v, int64_t v_token_stride, int64_t v_head_stride,
+                         const i8mm_kv_cache* cache, const i8mm_kv_batch* batch,
+                         const i8mm_rotary* rotary, i8mm_stream_t stream) {
+  const char* fn = "int8_kv_cache_append";
+  i8mm::KvArgs a;
+  i8mm::RotaryArgs r;
+  I8MM_TRY(kv_check(fn, cache, batch, &a));
+  I8MM_TRY(rotary_check(fn, rotary, a, &r));
+  I8MM_TRY(strides_check(fn, "k", k, a.total_tokens > 0, k_token_stride, k_head_stride));
+  I8MM_TRY(strides_check(fn, "v", v, a.total_tokens > 0, v_token_stride, v_head_stride));
+  if (a.total_tokens == 0 || a.max_tokens == 0 || a.len_cap == 0 || a.num_pages == 0) return ok();
+  I8MM_TRY(check_device());
+  I8MM_TRY(launched(i8mm::launch_kv_append(k, k_token_stride, k_head_stride, v, v_token_stride,
+                                           v_head_stride, a, r, (hipStream_t)stream),
+                    fn));
+  return ok();
+}
+
+int int8_kv_cache_read(const i8mm_kv_cache* cache, const i8mm_kv_batch* batch, uint16_t* k,
+                       uint16_t* v, i8mm_stream_t stream) {
+  const char* fn = "int8_kv_cache_read";
+  i8mm::KvArgs a;
+  I8MM_TRY(kv_check(fn, cache, batch, &a));
+  I8MM_TRY(check_ptr(fn, "k", k, false));
+  I8MM_TRY(check_ptr(fn, "v", v, false));
+  if ((!k && !v) || a.total_tokens == 0 || a.max_tokens == 0) return ok();
+  I8MM_TRY(check_device());
+  I8MM_TRY(launched(i8mm::launch_kv_read(a, k, v, (hipStream_t)stream), fn));
+  return ok();
+}
+
+size_t int8_kv_cache_attention_workspace_bytes(const i8mm_kv_cache* cache,
+                                               const i8mm_kv_batch* batch, int64_t q_heads) {
+  i8mm::KvArgs a;
+  if (kv_sizes("int8_kv_cache_attention_workspace_bytes", cache, batch, &a) != I8MM_OK) return 0;
+  if (q_heads <= 0 || q_heads > 65535 || q_heads % a.kv_heads != 0) return 0;
+  return i8mm::attn_workspace_bytes(a, (int)q_heads);
+}
+
+int int8_kv_cache_attention(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride,
+                            int64_t q_heads, const i8mm_kv_cache* cache,
+                            const i8mm_kv_batch* batch, const i8mm_rotary* rotary, float scale,
+                            int causal, int64_t window, const float* alibi_slopes, uint16_t* out,
+                            void* workspace, size_t workspace_bytes, i8mm_stream_t stream) {
+  const char* fn = "int8_kv_cache_attention";
+  i8mm::KvArgs a;
+  i8mm::RotaryArgs r;
+  I8MM_TRY(kv_check(fn, cache, batch, &a));
+  I8MM_TRY(rotary_check(fn, rotary, a, &r));
+  if (q_heads <= 0 || q_heads > 65535 || q_heads % a.kv_heads != 0)
+    return fail(I8MM_EINVAL, "%s: q_heads=%lld is not a multiple of %d key/value heads", fn,
+                (long long)q_heads, a.kv_heads);
+  I8MM_TRY(strides_check(fn, "q", q, a.total_tokens > 0, q_token_stride, q_head_stride));
+  if (!std::isfinite(scale) || !(scale > 0.f))
+    return fail(I8MM_EINVAL, "%s: scale is not finite and positive", fn);
+  if (causal != 0 && causal != 1) return fail(I8MM_EINVAL, "%s: causal is not 0 or 1", fn);
+  if (window < 0 || (window > 0 && !causal))
+    return fail(I8MM_EINVAL, "%s: window is negative, or given without causal", fn);
+  if (!aligned4(alibi_slopes))
+    return fail(I8MM_EALIGN, "%s: alibi_slopes is not 4-byte aligned", fn);
+  I8MM_TRY(check_ptr(fn, "out", out, a.total_tokens > 0));
+  const size_t need = i8mm::attn_workspace_bytes(a, (int)q_heads);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need)
+      return fail(I8MM_EWORKSPACE, "%s: workspace has %zu bytes, needs %zu", fn,
+                  workspace ? workspace_bytes : (size_t)0, need);
+    if ((reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0)
+      return fail(I8MM_EALIGN, "%s: workspace is not 256-byte aligned", fn);
+  }
+  if (a.total_tokens == 0 || a.max_tokens == 0) return ok();
+  I8MM_TRY(check_device());
+  i8mm::AttnArgs t;
+  t.q = q;
+  t.q_ts = q_token_stride;
+  t.q_hs = q_head_stride;
+  t.slopes = alibi_slopes;
+  t.out = out;
+  t.part = static_cast<float*>(workspace);
+  t.scale_log2 = scale * 1.44269504088896340736f;
+  t.q_heads = (int)q_heads;
+  t.causal = causal;
+  t.window = (int)std::min<int64_t>(window, INT32_MAX / 2);
+  I8MM_TRY(launched(i8mm::launch_kv_attention(a, r, t, (hipStream_t)stream), fn));
+  return ok();
+}
+
+}  // extern "C"

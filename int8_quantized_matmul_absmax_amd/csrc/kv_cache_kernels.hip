@@ -1,0 +1,279 @@
+// Append to and read from the paged 8-bit key/value cache.
+//
+// Both move one block of 16 tokens and one head a wave, keys and values apart.
+// Keys: codes of a token lie along the features, so lanes hold 8 features of a
+// token. Values: codes of a feature lie along the tokens, so a lane holds a
+// pair of features for all 16 tokens, and the transposition costs no exchange.
+
+#include "kv_common.h"
+
+namespace i8mm {
+
+namespace {
+
+// Absmaxes up to 2^-119 count as 0 (127 / a stays finite above it).
+constexpr uint32_t kTinyAbsmax = 0x04000000u;
+
+__device__ __forceinline__ uint32_t abs_bits(float x) {
+  return __builtin_bit_cast(uint32_t, x) & 0x7fffffffu;
+}
+
+// Low byte: the code rne(y), abs(y) <= 127 up to one rounding.
+__device__ __forceinline__ uint32_t code_bits(float y) {
+  return __builtin_bit_cast(uint32_t, y + 12582912.0f);
+}
+__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  const uint32_t lo = __builtin_amdgcn_perm(b, a, 0x0c0c0400u);
+  const uint32_t hi = __builtin_amdgcn_perm(d, c, 0x0c0c0400u);
+  return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+}
+__device__ __forceinline__ float byte_code(uint32_t w, int i) {
+  return (float)(int8_t)(w >> (8 * i));
+}
+// Four old codes over a larger absmax.
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
+  return pack4(code_bits(byte_code(w, 0) * ratio), code_bits(byte_code(w, 1) * ratio),
+               code_bits(byte_code(w, 2) * ratio), code_bits(byte_code(w, 3) * ratio));
+}
+
+struct BlockScale {
+  float s, ratio, a;
+  bool grown;   // the old codes change
+};
+// The block's absmax after the append from the bit patterns of the old one
+// and of the new elements' (unsigned order: NaN above infinity above finite).
+__device__ __forceinline__ BlockScale block_scale(uint32_t a_old, uint32_t a_new) {
+  uint32_t a = a_old > a_new ? a_old : a_new;
+  if (a <= kTinyAbsmax) a = 0;
+  BlockScale r;
+  r.a = __builtin_bit_cast(float, a);
+  r.s = a ? 127.0f / r.a : 0.f;
+  r.ratio = a ? __builtin_bit_cast(float, a_old) / r.a : 0.f;
+  r.grown = a != a_old;
+  return r;
+}
+
+template <int D>
+__global__ __launch_bounds__(kBlockThreads) void k_kv_append(
+    const uint16_t* __restrict__ k, int64_t k_ts, int64_t k_hs, const uint16_t* __restrict__ v,
+    int64_t v_ts, int64_t v_hs, KvArgs a, RotaryArgs rot, int tasks) {
+  const int lane = threadIdx.x & 63;
+  const int task = blockIdx.x * (kBlockThreads / kWave) + (threadIdx.x >> 6);
+  const int b = blockIdx.y;
+  if (task >= tasks) return;
+  const bool values = task & 1;
+  const int h = (task >> 1) % a.kv_heads;
+  const KvSeq sq = kv_seq(a, b);
+  const int blk = max(sq.first, 0) / kKvBlock + (task >> 1) / a.kv_heads;
+  const int t0 = blk * kKvBlock;
+  if (sq.n <= 0 || t0 >= sq.len) return;
+  const int r0 = max(sq.first - t0, 0);             // rows [0, r0) are older tokens
+  const int r1 = min(kKvBlock, sq.len - t0);        // rows [r0, r1) are new
+  const int lin = kv_block(a, b, h, blk);
+  if (lin < 0) return;
+  const int64_t src0 = (int64_t)sq.row0 + t0 - sq.first;   // packed row of block row 0
+
+  if (!values) {
+    constexpr int kChunks = D / 8, kItems = kKvBlock * kChunks;
+    constexpr int kIter = (kItems + kWave - 1) / kWave;
+    int8_t* tile = a.k_codes + (int64_t)lin * (kKvBlock * D);
+    const uint32_t a_old = r0 > 0 ? abs_bits(a.k_absmax[lin]) : 0u;
+    float x[kIter][8];
+    uint32_t top = 0;
+#pragma unroll
+    for (int it = 0; it < kIter; ++it) {
+      const int idx = it * kWave + lane, tok = idx / kChunks, e0 = idx % kChunks * 8;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[it][e] = 0.f;
+      if (tok >= r0 && tok < r1)
+        load8_rotated(k + (src0 + tok) * k_ts + h * k_hs, e0, t0 + tok, rot, x[it]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t m = abs_bits(x[it][e]);
+        top = top > m ? top : m;
+      }
+    }
+    const BlockScale sc = block_scale(a_old, wave_max_u32_dpp(top));
+#pragma unroll
+    for (int it = 0; it < kIter; ++it) {
+      const int idx = it * kWave + lane, tok = idx / kChunks, e0 = idx % kChunks * 8;
+      if (idx >= kItems) continue;
+      uint2* dst = reinterpret_cast<uint2*>(tile + (e0 >> 4) * kTile + tok * 16 + (e0 & 15));
+      if (tok < r0) {
+        if (!sc.grown) continue;
+        const uint2 w = *dst;
+        *dst = make_uint2(rescale4(w.x, sc.ratio), rescale4(w.y, sc.ratio));
+      } else {
+        uint32_t c[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) c[e] = code_bits(x[it][e] * sc.s);
+        *dst = make_uint2(pack4(c[0], c[1], c[2], c[3]), pack4(c[4], c[5], c[6], c[7]));
+      }
+    }
+    if (lane == 0) a.k_absmax[lin] = sc.a;
+    return;
+  }
+
+  constexpr int kPairs = D / 2, kIter = (kPairs + kWave - 1) / kWave;
+  int8_t* tile = a.v_codes + (int64_t)lin * (kKvBlock * D);
+  const uint32_t a_old = r0 > 0 ? abs_bits(a.v_absmax[lin]) : 0u;
+  uint32_t x[kIter][kKvBlock];   // pairs of fp16
+  uint32_t top = 0;
+#pragma unroll
+  for (int it = 0; it < kIter; ++it) {
+    const int p = it * kWave + lane;
+#pragma unroll
+    for (int r = 0; r < kKvBlock; ++r) {
+      x[it][r] = 0;
+      if (r >= r0 && r < r1 && p < kPairs)
+        x[it][r] = *reinterpret_cast<const uint32_t*>(v + (src0 + r) * v_ts + h * v_hs + 2 * p);
+    }
+  }
+#pragma unroll
+  for (int it = 0; it < kIter; ++it)
+#pragma unroll
+    for (int r = 0; r < kKvBlock; ++r) {
+      const uint32_t lo = x[it][r] & 0x7fffu, hi = (x[it][r] >> 16) & 0x7fffu;
+      const uint32_t m = lo > hi ? lo : hi;   // fp16 patterns order as their magnitudes
+      top = top > m ? top : m;
+    }
+  const BlockScale sc = block_scale(a_old, abs_bits(h2f(wave_max_u32_dpp(top))));
+#pragma unroll
+  for (int it = 0; it < kIter; ++it) {
+    const int p = it * kWave + lane;
+    if (p >= kPairs) continue;
+    // the pair's two features are 32 consecutive bytes
+    uint4* dst = reinterpret_cast<uint4*>(tile + p * 32);
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      uint32_t w[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t c[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          c[i] = code_bits(h2f((x[it][4 * q + i] >> (16 * f)) & 0xffffu) * sc.s);
+        w[q] = pack4(c[0], c[1], c[2], c[3]);
+      }
+      if (r0 > 0) {
+        const uint4 o = dst[f];
+        const uint32_t old[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int rows = min(max(r0 - 4 * q, 0), 4);   // old rows among these four
+          const uint32_t keep = rows >= 4 ? 0xffffffffu : (1u << (8 * rows)) - 1u;
+          const uint32_t ow = sc.grown ? rescale4(old[q], sc.ratio) : old[q];
+          w[q] = (ow & keep) | (w[q] & ~keep);
+        }
+      }
+      dst[f] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  if (lane == 0) a.v_absmax[lin] = sc.a;
+}
+
+template <int D>
+__global__ __launch_bounds__(kBlockThreads) void k_kv_read(KvArgs a, uint16_t* __restrict__ k,
+                                                           uint16_t* __restrict__ v, int tasks) {
+  const int lane = threadIdx.x & 63;
+  const int task = blockIdx.x * (kBlockThreads / kWave) + (threadIdx.x >> 6);
+  const int b = blockIdx.y;
+  if (task >= tasks) return;
+  const bool values = task & 1;
+  uint16_t* out = values ? v : k;
+  if (!out) return;
+  const int h = (task >> 1) % a.kv_heads;
+  const KvSeq sq = kv_seq(a, b);
+  // floor division: a sequence with n > len starts at a negative position
+  const int blk = (sq.first >> 4) + (task >> 1) / a.kv_heads;
+  const int t0 = blk * kKvBlock;
+  if (sq.n <= 0 || t0 >= sq.len) return;
+  const int r0 = max(sq.first - t0, 0), r1 = min(kKvBlock, sq.len - t0);
+  const int lin = blk >= 0 ? kv_block(a, b, h, blk) : -1;
+  const int64_t ts = (int64_t)a.kv_heads * D;
+  uint16_t* dst0 = out + ((int64_t)sq.row0 + t0 - sq.first) * ts + (int64_t)h * D;
+
+  if (!values) {
+    constexpr int kTiles = D / 16, kItems = kKvBlock * kTiles;
+    constexpr int kIter = (kItems + kWave - 1) / kWave;
+    const float step = lin >= 0 ? a.k_absmax[lin] / 127.0f : 0.f;
+    const int8_t* tile = a.k_codes + (int64_t)lin * (kKvBlock * D);
+#pragma unroll
+    for (int it = 0; it < kIter; ++it) {
+      const int idx = it * kWave + lane, tok = idx / kTiles, c = idx % kTiles;
+      if (tok < r0 || tok >= r1) continue;
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (lin >= 0) w = ld16(tile + c * kTile + tok * 16);
+      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+      uint32_t o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        o[i] = f2h2(byte_code(ww[i >> 1], (2 * i) & 3) * step,
+                    byte_code(ww[i >> 1], (2 * i + 1) & 3) * step);
+      uint16_t* dst = dst0 + tok * ts + c * 16;
+      st16(dst, make_uint4(o[0], o[1], o[2], o[3]));
+      st16(dst + 8, make_uint4(o[4], o[5], o[6], o[7]));
+    }
+    return;
+  }
+  constexpr int kPairs = D / 2, kIter = (kPairs + kWave - 1) / kWave;
+  const float step = lin >= 0 ? a.v_absmax[lin] / 127.0f : 0.f;
+  const int8_t* tile = a.v_codes + (int64_t)lin * (kKvBlock * D);
+#pragma unroll
+  for (int it = 0; it < kIter; ++it) {
+    const int p = it * kWave + lane;
+    if (p >= kPairs) continue;
+    uint4 f0 = make_uint4(0, 0, 0, 0), f1 = f0;
+    if (lin >= 0) {
+      f0 = ld16(tile + p * 32);
+      f1 = ld16(tile + p * 32 + 16);
+    }
+    const uint32_t w0[4] = {f0.x, f0.y, f0.z, f0.w}, w1[4] = {f1.x, f1.y, f1.z, f1.w};
+#pragma unroll
+    for (int r = 0; r < kKvBlock; ++r)
+      if (r >= r0 && r < r1)
+        *reinterpret_cast<uint32_t*>(dst0 + r * ts + 2 * p) =
+            f2h2(byte_code(w0[r >> 2], r & 3) * step, byte_code(w1[r >> 2], r & 3) * step);
+  }
+}
+
+// Blocks that the new tokens of one sequence can touch.
+int64_t max_blocks(const KvArgs& a) { return ((int64_t)a.max_tokens + 2 * kKvBlock - 2) / kKvBlock; }
+
+}  // namespace
+
+bool kv_head_dim_ok(int64_t D) { return D == 64 || D == 80 || D == 96 || D == 128 || D == 256; }
+
+#define I8MM_KV_DIMS(D, CALL) \
+  switch (D) {                \
+    case 64: { CALL(64); } break;   \
+    case 80: { CALL(80); } break;   \
+    case 96: { CALL(96); } break;   \
+    case 128: { CALL(128); } break; \
+    default: { CALL(256); } break;  \
+  }
+
+hipError_t launch_kv_append(const uint16_t* k, int64_t k_ts, int64_t k_hs, const uint16_t* v,
+                            int64_t v_ts, int64_t v_hs, const KvArgs& a, const RotaryArgs& r,
+                            hipStream_t s) {
+  const int64_t tasks = max_blocks(a) * a.kv_heads * 2;
+  if (tasks > INT32_MAX - 4) return hipErrorInvalidValue;
+  const dim3 grid((uint32_t)((tasks + 3) / 4), (uint32_t)a.num_seqs);
+#define CALL(D) \
+  k_kv_append<D><<<grid, kBlockThreads, 0, s>>>(k, k_ts, k_hs, v, v_ts, v_hs, a, r, (int)tasks)
+  I8MM_KV_DIMS(a.head_dim, CALL)
+#undef CALL
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_read(const KvArgs& a, uint16_t* k, uint16_t* v, hipStream_t s) {
+  const int64_t tasks = max_blocks(a) * a.kv_heads * 2;
+  if (tasks > INT32_MAX - 4) return hipErrorInvalidValue;
+  const dim3 grid((uint32_t)((tasks + 3) / 4), (uint32_t)a.num_seqs);
+#define CALL(D) k_kv_read<D><<<grid, kBlockThreads, 0, s>>>(a, k, v, (int)tasks)
+  I8MM_KV_DIMS(a.head_dim, CALL)
+#undef CALL
+  return hipGetLastError();
+}
+
+}  // namespace i8mm

@@ -96,6 +96,47 @@ hipError_t launch_gemv(const int8_t* Xq, const int8_t* Wq, const float* sx, cons
                        const int32_t* cols, const int32_t* n_out, const uint16_t* bias,
                        uint16_t* Y, int32_t* C, const uint16_t* Wf, hipStream_t s);
 
+// ---- paged 8-bit key/value cache
+// The cache and batch structs of the C ABI narrowed to what kernels index
+// with, arguments validated: slots = page_tokens / 16 blocks a page, len_cap =
+// min(max_len, max_pages * page_tokens).
+struct KvArgs {
+  int8_t* k_codes;
+  float* k_absmax;
+  int8_t* v_codes;
+  float* v_absmax;
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  const int32_t* cu_tokens;   // or nullptr: one token a sequence
+  int num_pages, slots, kv_heads, head_dim;
+  int num_seqs, max_pages, total_tokens, max_tokens, len_cap;
+};
+struct RotaryArgs {
+  const float* cos;           // nullptr: no rotation
+  const float* sin;
+  int dim, interleaved;
+};
+
+bool kv_head_dim_ok(int64_t D);
+
+hipError_t launch_kv_append(const uint16_t* k, int64_t k_ts, int64_t k_hs, const uint16_t* v,
+                            int64_t v_ts, int64_t v_hs, const KvArgs& a, const RotaryArgs& r,
+                            hipStream_t s);
+hipError_t launch_kv_read(const KvArgs& a, uint16_t* k, uint16_t* v, hipStream_t s);
+
+struct AttnArgs {
+  const uint16_t* q;
+  int64_t q_ts, q_hs;
+  const float* slopes;        // or nullptr
+  uint16_t* out;
+  float* part;                // workspace of attn_workspace_bytes
+  float scale_log2;           // scale * log2(e)
+  int q_heads, causal, window;
+};
+size_t attn_workspace_bytes(const KvArgs& a, int q_heads);
+hipError_t launch_kv_attention(const KvArgs& a, const RotaryArgs& r, const AttnArgs& t,
+                               hipStream_t s);
+
 hipError_t launch_gelu(const uint16_t* X, int64_t count, uint16_t* Y, hipStream_t s);
 
 }  // namespace i8mm

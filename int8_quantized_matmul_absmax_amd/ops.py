@@ -34,6 +34,10 @@ def _stream(device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+def _raw_stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
 def _need(t, name, dtype, ndim=None, shape=None, min_numel=None):
     """Type, dtype, contiguity and size of one tensor argument (no device check:
     _on_gpu does that for all arguments of a call together)."""
@@ -307,6 +311,110 @@ def gelu_f16(X, out=None):
     Y = out if out is not None else torch.empty_like(X)
     _lib.check(lib.i8mm_gelu_f16(_ptr(X), X.numel(), _ptr(Y), _stream(dev)))
     return Y
+
+
+# ---- paged 8-bit key/value cache (cache, batch, rotary: kv_cache.Int8KVCache,
+# KVBatch and Rotary, which check and hold their own tensors)
+
+KV_BLOCK = 16   # I8MM_KV_BLOCK
+
+
+def _need_heads(t, name, tokens, heads, dim, device):
+    """fp16 [tokens, heads, dim] on device, features contiguous, 16-byte rows."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype != torch.float16:
+        raise TypeError("%s must be torch.float16, got %s" % (name, t.dtype))
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != tokens or shape[2] != dim or heads not in (None, shape[1]):
+        raise ValueError("%s must have shape %s, got %s"
+                         % (name, (tokens, "heads" if heads is None else heads, dim),
+                            tuple(shape)))
+    if t.device != device:
+        raise ValueError("%s is on %s, the cache on %s" % (name, t.device, device))
+    ts, hs, fs = t.stride()
+    if fs != 1 and t.numel() > 0:
+        raise ValueError("the features of %s must be contiguous" % name)
+    return t.data_ptr(), ts, hs
+
+
+def _kv_args(cache, batch, rotary):
+    if batch.device != cache.device:
+        raise ValueError("the batch is on %s, the cache on %s" % (batch.device, cache.device))
+    if rotary is None:
+        return None
+    if rotary.device != cache.device:
+        raise ValueError("the rotary tables are on %s, the cache on %s"
+                         % (rotary.device, cache.device))
+    return rotary.ref
+
+
+def int8_kv_cache_append(k, v, cache, batch, rotary=None):
+    """Quantize new keys (rotated first when `rotary` is given) and values into
+    the cache. k, v fp16 [total_tokens, kv_heads, D]; the token and head strides
+    are free (multiples of 8)."""
+    lib = _lib.load_library()
+    rot = _kv_args(cache, batch, rotary)
+    kp, kts, khs = _need_heads(k, "k", batch.total_tokens, cache.kv_heads, cache.head_dim,
+                               cache.device)
+    vp, vts, vhs = _need_heads(v, "v", batch.total_tokens, cache.kv_heads, cache.head_dim,
+                               cache.device)
+    _lib.check(lib.int8_kv_cache_append(kp, kts, khs, vp, vts, vhs, cache.ref, batch.ref, rot,
+                                        _raw_stream(cache.device)))
+
+
+def int8_kv_cache_attention_workspace_bytes(cache, batch, q_heads):
+    """Bytes of workspace int8_kv_cache_attention needs."""
+    return _lib.load_library().int8_kv_cache_attention_workspace_bytes(cache.ref, batch.ref,
+                                                                       int(q_heads))
+
+
+def int8_kv_cache_attention(q, cache, batch, rotary=None, scale=None, causal=True, window=0,
+                            alibi_slopes=None, workspace=None, out=None):
+    """Attention of the queries q fp16 [total_tokens, q_heads, D] (rotated here
+    when `rotary` is given) over the cached tokens -> fp16 [total_tokens,
+    q_heads, D]. scale defaults to 1 / sqrt(D)."""
+    lib = _lib.load_library()
+    rot = _kv_args(cache, batch, rotary)
+    dev = cache.device
+    D = cache.head_dim
+    qp, qts, qhs = _need_heads(q, "q", batch.total_tokens, None, D, dev)
+    heads = q.shape[1]
+    if alibi_slopes is not None:
+        _need(alibi_slopes, "alibi_slopes", torch.float32, shape=(heads,))
+        _on_gpu(q=q, alibi_slopes=alibi_slopes)
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.float16, device=dev)
+    else:
+        _need(out, "out", torch.float16, shape=q.shape)
+        _on_gpu(q=q, out=out)
+    need = lib.int8_kv_cache_attention_workspace_bytes(cache.ref, batch.ref, heads)
+    if need and workspace is None:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    wp, wn = None, 0
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8, 1)
+        _on_gpu(q=q, workspace=workspace)
+        wp, wn = workspace.data_ptr(), workspace.numel()
+    _lib.check(lib.int8_kv_cache_attention(
+        qp, qts, qhs, heads, cache.ref, batch.ref, rot,
+        1.0 / math.sqrt(D) if scale is None else float(scale), 1 if causal else 0, int(window),
+        None if alibi_slopes is None else alibi_slopes.data_ptr(), out.data_ptr(), wp, wn,
+        _raw_stream(dev)))
+    return out
+
+
+def int8_kv_cache_read(cache, batch):
+    """The cached keys (rotated, as stored) and values of the batch's tokens:
+    two fp16 tensors [total_tokens, kv_heads, D]."""
+    lib = _lib.load_library()
+    _kv_args(cache, batch, None)
+    kv = torch.empty((2, batch.total_tokens, cache.kv_heads, cache.head_dim),
+                     dtype=torch.float16, device=cache.device)
+    k, v = kv[0], kv[1]
+    _lib.check(lib.int8_kv_cache_read(cache.ref, batch.ref, k.data_ptr(), v.data_ptr(),
+                                      _raw_stream(cache.device)))
+    return k, v
 
 
 OUTLIER_REGION_COLS = 512   # I8MM_OUTLIER_REGION_COLS
