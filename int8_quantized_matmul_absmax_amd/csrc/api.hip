@@ -485,7 +485,8 @@ int kv_sizes(const char* fn, const i8mm_kv_cache* c, const i8mm_kv_batch* b, i8m
     return fail(I8MM_EINVAL, "%s: no cu_tokens, but %lld tokens for %lld sequences", fn,
                 (long long)b->total_tokens, (long long)b->num_seqs);
   const int64_t room = b->max_pages * c->page_tokens;
-  const int64_t cap = std::min(b->max_len, room);
+  // (no pages: every token is absent, as in sequences of length 0)
+  const int64_t cap = c->num_pages > 0 ? std::min(b->max_len, room) : 0;
   if (cap > INT32_MAX / 2) return fail(I8MM_EINVAL, "%s: max_len beyond 2^30 tokens", fn);
   a->num_pages = (int)c->num_pages;
   a->slots = (int)slots;

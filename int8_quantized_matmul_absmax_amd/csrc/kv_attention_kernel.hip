@@ -58,12 +58,11 @@ __device__ __forceinline__ float max_over_groups(float v) {
 }
 
 // 16 codes as fp16: 0x6400 | (code + 128) is 1152 + code.
-__device__ __forceinline__ void codes_to_f16(const uint4& w, v8f16* lo, v8f16* hi) {
-  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+__device__ __forceinline__ void codes_to_f16(const v4i32& w, v8f16* lo, v8f16* hi) {
   uint32_t out[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t u = in[i] ^ 0x80808080u;
+    const uint32_t u = (uint32_t)w[i] ^ 0x80808080u;
     out[2 * i] = __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u);
     out[2 * i + 1] = __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u);
   }
@@ -130,17 +129,153 @@ struct BlockList {
   float log_r, inv_r; // of the value absmax over the wave's ref
 };
 
-// ---- Few rows: each wave streams its own groups from the cache into
-// registers; the four waves of a block join through LDS, the blocks of a row
-// tile through the workspace and k_kv_attn_join.
+// ---- Codes through LDS. A group is staged as its four blocks, each as it lies
+// in the cache, kPitch apart: 64 bytes more than a block, so that the four
+// blocks a key operand touches lie in different banks. Staging is LDS-DMA, 1 KB
+// an instruction, with no registers in between; the waits count its
+// instructions, so each stage issues the same number of them.
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+template <int D>
+struct Stage {
+  static constexpr int kBytes = kKvBlock * D;
+  static constexpr int kPitch = kBytes + 64;
+  static constexpr int kLoads = (kBytes + 1023) / 1024;   // a block
+  static constexpr int kGroupBytes = 4 * kPitch;
+};
+
+// Starts the copy of a block (lin in a scalar register) to dst.
+template <int D>
+__device__ __forceinline__ void stage_block(const int8_t* codes, int lin, int8_t* dst, int lane) {
+  typedef Stage<D> S;
+  const __amdgpu_buffer_rsrc_t rsrc = buffer_rsrc(codes + (int64_t)lin * S::kBytes, S::kBytes);
+#pragma unroll
+  for (int j = 0; j < S::kLoads; ++j) {
+    if (S::kBytes % 1024 == 0 || j < S::kBytes / 1024 || lane < S::kBytes % 1024 / 16)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr_t)(dst + j * 1024), 16, lane * 16,
+                                               j * 1024, 0, 0);
+  }
+}
+
+// s_waitcnt with only the vector-memory counter constrained.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N >= 0 && N < 64, "vmcnt");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+  asm volatile("" ::: "memory");
+}
+// This wave's LDS reads have returned.
+__device__ __forceinline__ void wait_lds_reads() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);
+  asm volatile("" ::: "memory");
+}
+
+// (Staged codes are read as v4i32, never as the struct uint4: a load without a
+// type for alias analysis makes the compiler wait for every copy in flight.)
+
+// A staged group's keys as the A operands of a lane (n, g): operand q of chunk
+// c is token 4 q + n % 4 of block n / 4, features 64 c + 16 g .. + 15 (past D,
+// where the query is zero, some other ones).
+template <int D>
+__device__ __forceinline__ void read_keys(const int8_t* st, int n, int g,
+                                          v4i32 (&k)[(D + 63) / 64][4]) {
+  const int8_t* p = st + (n >> 2) * Stage<D>::kPitch + (n & 3) * 16;
+#pragma unroll
+  for (int c = 0; c < (D + 63) / 64; ++c) {
+    const int8_t* pc = p + min(4 * c + g, D / 16 - 1) * kTile;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) k[c][q] = *reinterpret_cast<const v4i32*>(pc + q * 64);
+  }
+}
+// Its values: feature 16 d + n, the 16 tokens of block g.
+template <int D>
+__device__ __forceinline__ v4i32 read_values(const int8_t* st, int n, int g, int d) {
+  return *reinterpret_cast<const v4i32*>(st + g * Stage<D>::kPitch + d * kTile + n * 16);
+}
+
+// One column tile's scores of a group, S^T = K Q^T as integers: element e of a
+// lane is (e >> 2, e & 3) of s.
+template <int D>
+__device__ __forceinline__ void scores(const v4i32 (&k)[(D + 63) / 64][4], const v4i32* qh,
+                                       const v4i32* ql, v4i32 (&s)[4]) {
+  constexpr int kC = (D + 63) / 64;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    s[q] = v4i32{0, 0, 0, 0};
+#pragma unroll
+    for (int c = 0; c < kC; ++c)
+      s[q] = __builtin_amdgcn_mfma_i32_16x16x64_i8(k[c][q], qh[c], s[q],
+                                                   0, 0, 0);
+    s[q] = s[q] << 7;
+#pragma unroll
+    for (int c = 0; c < kC; ++c)
+      s[q] = __builtin_amdgcn_mfma_i32_16x16x64_i8(k[c][q], ql[c], s[q],
+                                                   0, 0, 0);
+  }
+}
+
+// A lane's row: its position, visible tokens and factors.
+struct Row {
+  int pos, lo, hi;
+  float qf;      // query absmax / 16256 * scale * log2(e)
+  float slope;   // * log2(e)
+};
+
+// Logits of a group in base 2, hidden ones -infinity.
+template <bool kAlibi>
+__device__ __forceinline__ void logits(const v4i32 (&s)[4], const Row& row, float ks, int t0, int g,
+                                       bool masked, bool here, float (&z)[16]) {
+  const float f = ks * row.qf;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    z[e] = (float)s[e >> 2][e & 3] * f;
+    if (kAlibi) z[e] += row.slope * (float)(t0 + 16 * g + e - row.pos);
+  }
+  if (masked) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int tok = t0 + 16 * g + e;
+      if (!here || tok < row.lo || tok >= row.hi) z[e] = -INFINITY;
+    }
+  }
+}
+
+// The running maximum over a group's logits: true (the whole wave) when rows
+// are to be rescaled, each by its alpha.
+__device__ __forceinline__ bool new_maximum(const float (&z)[16], float* m, float* alpha) {
+  float top = z[0];
+#pragma unroll
+  for (int e = 1; e < 16; ++e) top = fmaxf(top, z[e]);
+  top = max_over_groups(top);
+  if (!__any(top > *m + kLazy)) return false;
+  const float next = fmaxf(*m, top);
+  *alpha = next == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(*m - next);
+  *m = next;
+  return true;
+}
+
+// ---- Few rows: each wave streams its own groups through its own part of
+// LDS, keys and values apart: a buffer is refilled as soon as it has been read,
+// so something is always in flight. The four waves of a block join through LDS,
+// the blocks of a row tile through the workspace and k_kv_attn_join.
 template <int D, bool kAlibi>
 __global__ __launch_bounds__(kBlockThreads) void k_kv_attn_rows(KvArgs a, RotaryArgs rot,
                                                                 AttnArgs t, int group, int tiles,
                                                                 int splits, int chunk) {
   constexpr int kC = (D + 63) / 64, kT = D / 16, kLd = D + 4;
-  __shared__ __attribute__((aligned(16))) float s_o[4][kRows][kLd];
-  __shared__ float s_m[4][kRows], s_l[4][kRows];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  typedef Stage<D> S;
+  constexpr int kSlots = D <= 64 ? 2 : 1;
+  constexpr int kAhead = (2 * kSlots - 1) * 4 * S::kLoads;   // loads younger than the awaited
+  constexpr int kJoinBytes = (4 * kRows * kLd + 8 * kRows) * 4;
+  constexpr int kStageBytes = 4 * 2 * kSlots * S::kGroupBytes;
+  __shared__ __attribute__((aligned(1024)))
+  int8_t lds[kStageBytes > kJoinBytes ? kStageBytes : kJoinBytes];
+  float(*s_o)[kRows][kLd] = reinterpret_cast<float(*)[kRows][kLd]>(lds);
+  float(*s_m)[kRows] = reinterpret_cast<float(*)[kRows]>(lds + 4 * kRows * kLd * 4);
+  float(*s_l)[kRows] = s_m + 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   const int split = blockIdx.x, h = blockIdx.y / tiles, b = blockIdx.z;
   const int r_first = (blockIdx.y % tiles) * kRows;
@@ -158,15 +293,17 @@ __global__ __launch_bounds__(kBlockThreads) void k_kv_attn_rows(KvArgs a, Rotary
   const int r = min(r_first + n, r_last);
   const bool live = r_first + n <= r_last;
   const int i_row = r / group, head = h * group + r % group;
-  const int pos = sq.first + i_row;
+  Row row;
+  row.pos = sq.first + i_row;
   v4i32 qh[kC], ql[kC];
   const uint16_t* q_row = t.q + (int64_t)(sq.row0 + i_row) * t.q_ts + (int64_t)head * t.q_hs;
-  const float qf = load_query<D>(q_row, max(pos, 0), live && pos >= 0, rot, g, qh, ql) * t.scale_log2;
-  const int vis_lo = visible_lo(t, pos), vis_hi = live ? visible_hi(t, sq, pos) : 0;
+  row.qf = load_query<D>(q_row, max(row.pos, 0), live && row.pos >= 0, rot, g, qh, ql) * t.scale_log2;
+  row.lo = visible_lo(t, row.pos);
+  row.hi = live ? visible_hi(t, sq, row.pos) : 0;
+  row.slope = kAlibi ? t.slopes[head] * 1.44269504088896340736f : 0.f;
   // groups inside [all_lo, all_hi) are visible to every row
   const int all_lo = visible_lo(t, sq.first + r_last / group);
   const int all_hi = visible_hi(t, sq, sq.first + r_first / group);
-  const float slope = kAlibi ? t.slopes[head] * 1.44269504088896340736f : 0.f;
 
   v4f32 o[kT];
 #pragma unroll
@@ -178,18 +315,88 @@ __global__ __launch_bounds__(kBlockThreads) void k_kv_attn_rows(KvArgs a, Rotary
     BlockList bl;
     bl.lin = -1;
     bl.ks = 0.f;
-    float vs = 0.f;
+    float v_absmax = 0.f;
     {
       const int gi = gi0 + 4 * (lane >> 2), blk = 4 * gi + (lane & 3);
       if (gi < gi_end && blk * kKvBlock < end) bl.lin = kv_block(a, b, h, blk);
       if (bl.lin >= 0) {
         bl.ks = a.k_absmax[bl.lin] / 127.0f;
-        vs = a.v_absmax[bl.lin];
+        v_absmax = a.v_absmax[bl.lin];
       }
     }
     const uint64_t present = __ballot(bl.lin >= 0);
+    const int count = min(16, (gi_end - gi0 + 3) / 4);
+    // absent blocks are masked; block 0 is read in their place
+    auto load = [&](int i, const int8_t* codes, int8_t* dst) __attribute__((always_inline)) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        stage_block<D>(codes, max(__builtin_amdgcn_readlane(bl.lin, 4 * i + j), 0),
+                       dst + j * S::kPitch, lane);
+    };
+    auto step = [&](int i, int8_t* ks, int8_t* vs) __attribute__((always_inline)) {
+      const uint32_t have = (uint32_t)(present >> (4 * i)) & 15u;
+      const int t0 = (gi0 + 4 * i) * kGroup;
+      v4i32 s[4];
+      float z[16], alpha;
+      if (i + kSlots < count) wait_loads<kAhead>(); else wait_loads<0>();
+      {
+        v4i32 kf[kC][4];
+        read_keys<D>(ks, n, g, kf);
+        scores<D>(kf, qh, ql, s);
+      }
+      if (i + kSlots < count) {
+        wait_lds_reads();
+        load(i + kSlots, a.k_codes, ks);
+      }
+      logits<kAlibi>(s, row, __shfl(bl.ks, 4 * i + g, kWave), t0, g,
+                     t0 < all_lo || t0 + kGroup > all_hi || have != 15u, (have >> g) & 1u, z);
+      if (new_maximum(z, &m, &alpha)) {
+        l *= alpha;
+#pragma unroll
+        for (int d = 0; d < kT; ++d) o[d] *= alpha;
+      }
+      const float off = (m == -INFINITY ? 0.f : m) - __shfl(bl.log_r, 4 * i + g, kWave);
+      float sum = 0.f;
+      uint32_t ph[8], pl[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float p0 = __builtin_amdgcn_exp2f(z[2 * e] - off);
+        const float p1 = __builtin_amdgcn_exp2f(z[2 * e + 1] - off);
+        sum += p0 + p1;
+        ph[e] = f2h2(p0, p1);
+        pl[e] = f2h2(p0 - h2f(ph[e] & 0xffffu), p1 - h2f(ph[e] >> 16));
+      }
+      l += sum * __shfl(bl.inv_r, 4 * i + g, kWave);
+      const v8f16 p0h = __builtin_bit_cast(v8f16, make_uint4(ph[0], ph[1], ph[2], ph[3]));
+      const v8f16 p1h = __builtin_bit_cast(v8f16, make_uint4(ph[4], ph[5], ph[6], ph[7]));
+      const v8f16 p0l = __builtin_bit_cast(v8f16, make_uint4(pl[0], pl[1], pl[2], pl[3]));
+      const v8f16 p1l = __builtin_bit_cast(v8f16, make_uint4(pl[4], pl[5], pl[6], pl[7]));
+      if (i + kSlots < count) wait_loads<kAhead>(); else wait_loads<0>();
+#pragma unroll
+      for (int d = 0; d < kT; ++d) {
+        v8f16 v0, v1;
+        codes_to_f16(read_values<D>(vs, n, g, d), &v0, &v1);
+        o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, p0h, o[d], 0, 0, 0);
+        o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, p1h, o[d], 0, 0, 0);
+        o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, p0l, o[d], 0, 0, 0);
+        o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, p1l, o[d], 0, 0, 0);
+      }
+      if (i + kSlots < count) {
+        wait_lds_reads();
+        load(i + kSlots, a.v_codes, vs);
+      }
+    };
+    int8_t* const st_k = lds + wave * (2 * kSlots * S::kGroupBytes);
+    int8_t* const st_v = st_k + kSlots * S::kGroupBytes;
+    wait_lds_reads();   // of an earlier list's last groups
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i)
+      if (i < count) {
+        load(i, a.k_codes, st_k + i * S::kGroupBytes);
+        load(i, a.v_codes, st_v + i * S::kGroupBytes);
+      }
     {
-      float top = vs;
+      float top = v_absmax;
 #pragma unroll
       for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x, kWave));
       if (top > ref) {
@@ -198,98 +405,21 @@ __global__ __launch_bounds__(kBlockThreads) void k_kv_attn_rows(KvArgs a, Rotary
         for (int d = 0; d < kT; ++d) o[d] *= f;
         ref = top;
       }
-      float ratio = vs / (ref > 0.f ? ref : 1.f);
+      float ratio = v_absmax / (ref > 0.f ? ref : 1.f);
       ratio = ratio < kMinRatio ? kMinRatio : ratio;   // (keeps a NaN)
       bl.log_r = __builtin_amdgcn_logf(ratio);
       bl.inv_r = 1.0f / ratio;
     }
-    for (int i = 0; i < 16 && gi0 + 4 * i < gi_end; ++i) {
-      const uint32_t have = (uint32_t)(present >> (4 * i)) & 15u;
-      if (have == 0) continue;
-      const int t0 = (gi0 + 4 * i) * kGroup;
-      const int lin_k = max(__shfl(bl.lin, 4 * i + (n >> 2), kWave), 0);
-      const int lin_v = max(__shfl(bl.lin, 4 * i + g, kWave), 0);
-      const int8_t* kp = a.k_codes + (int64_t)lin_k * (kKvBlock * D) + (n & 3) * 16;
-      const int8_t* vp = a.v_codes + (int64_t)lin_v * (kKvBlock * D) + n * 16;
-      uint4 kf[kC][4], vf[kT];
-#pragma unroll
-      for (int c = 0; c < kC; ++c) {
-        const int tile = min(4 * c + g, kT - 1);   // (past D the query is zero)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) kf[c][q] = ld16(kp + tile * kTile + q * 64);
-      }
-#pragma unroll
-      for (int d = 0; d < kT; ++d) vf[d] = ld16(vp + d * kTile);
-
-      const float f = __shfl(bl.ks, 4 * i + g, kWave) * qf;
-      const float log_r = __shfl(bl.log_r, 4 * i + g, kWave);
-      const float inv_r = __shfl(bl.inv_r, 4 * i + g, kWave);
-      v4i32 s[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        s[q] = v4i32{0, 0, 0, 0};
-#pragma unroll
-        for (int c = 0; c < kC; ++c)
-          s[q] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i32, kf[c][q]), qh[c],
-                                                       s[q], 0, 0, 0);
-        s[q] = s[q] << 7;
-#pragma unroll
-        for (int c = 0; c < kC; ++c)
-          s[q] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i32, kf[c][q]), ql[c],
-                                                       s[q], 0, 0, 0);
-      }
-      float z[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        z[e] = (float)s[e >> 2][e & 3] * f;
-        if (kAlibi) z[e] += slope * (float)(t0 + 16 * g + e - pos);
-      }
-      if (t0 < all_lo || t0 + kGroup > all_hi || have != 15u) {
-        const bool here = (have >> g) & 1u;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int tok = t0 + 16 * g + e;
-          if (!here || tok < vis_lo || tok >= vis_hi) z[e] = -INFINITY;
-        }
-      }
-      float top = z[0];
-#pragma unroll
-      for (int e = 1; e < 16; ++e) top = fmaxf(top, z[e]);
-      top = max_over_groups(top);
-      if (__any(top > m + kLazy)) {
-        const float m_new = fmaxf(m, top);
-        const float alpha = m_new == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - m_new);
-        m = m_new;
-        l *= alpha;
-#pragma unroll
-        for (int d = 0; d < kT; ++d) o[d] *= alpha;
-      }
-      const float off = (m == -INFINITY ? 0.f : m) - log_r;
-      float sum = 0.f;
-      uint32_t pw[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float p0 = __builtin_amdgcn_exp2f(z[2 * e] - off);
-        const float p1 = __builtin_amdgcn_exp2f(z[2 * e + 1] - off);
-        sum += p0 + p1;
-        pw[e] = f2h2(p0, p1);
-      }
-      l += sum * inv_r;
-      const v8f16 p_lo = __builtin_bit_cast(v8f16, make_uint4(pw[0], pw[1], pw[2], pw[3]));
-      const v8f16 p_hi = __builtin_bit_cast(v8f16, make_uint4(pw[4], pw[5], pw[6], pw[7]));
-#pragma unroll
-      for (int d = 0; d < kT; ++d) {
-        v8f16 v_lo, v_hi;
-        codes_to_f16(vf[d], &v_lo, &v_hi);
-        o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v_lo, p_lo, o[d], 0, 0, 0);
-        o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v_hi, p_hi, o[d], 0, 0, 0);
-      }
+    for (int i = 0; i < count; ++i) {
+      const int slot = kSlots == 1 ? 0 : i % kSlots;
+      step(i, st_k + slot * S::kGroupBytes, st_v + slot * S::kGroupBytes);
     }
   }
 
   // join the four waves
   l += __shfl_xor(l, 16, kWave);
   l += __shfl_xor(l, 32, kWave);
+  __syncthreads();   // every wave is done with the staged groups
   const float unit = ref / 127.0f;
 #pragma unroll
   for (int d = 0; d < kT; ++d) *reinterpret_cast<v4f32*>(&s_o[wave][n][16 * d + 4 * g]) = o[d] * unit;
