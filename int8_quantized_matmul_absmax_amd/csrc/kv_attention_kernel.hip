@@ -22,6 +22,7 @@
 // maximum, 2^-25 absolute); all sums are fp32.
 
 #include <algorithm>
+#include <cstdlib>
 
 #include "kv_common.h"
 
@@ -223,37 +224,101 @@ struct Row {
   float slope;   // * log2(e)
 };
 
-// Logits of a group in base 2, hidden ones -infinity.
+// The running softmax of a lane's row over one group: the weights p of its 16
+// tokens, and m, l brought up to date. True (the whole wave) when sums over
+// earlier tokens are to be multiplied by alpha. When no token is hidden the
+// factor is common to the 16 scores, so their maximum is the integers'.
 template <bool kAlibi>
-__device__ __forceinline__ void logits(const v4i32 (&s)[4], const Row& row, float ks, int t0, int g,
-                                       bool masked, bool here, float (&z)[16]) {
+__device__ __forceinline__ bool softmax_step(const v4i32 (&s)[4], const Row& row, float ks,
+                                             float log_r, float inv_r, int t0, int g, bool masked,
+                                             bool here, float* m, float* l, float* alpha,
+                                             float (&p)[16]) {
   const float f = ks * row.qf;
+  float top, z[16];
+  const bool plain = !kAlibi && !masked;
+  if (plain) {
+    int i_top = s[0][0];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    z[e] = (float)s[e >> 2][e & 3] * f;
-    if (kAlibi) z[e] += row.slope * (float)(t0 + 16 * g + e - row.pos);
-  }
-  if (masked) {
+    for (int e = 1; e < 16; ++e) i_top = max(i_top, s[e >> 2][e & 3]);
+    top = (float)i_top * f;
+  } else {
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       const int tok = t0 + 16 * g + e;
-      if (!here || tok < row.lo || tok >= row.hi) z[e] = -INFINITY;
+      z[e] = (float)s[e >> 2][e & 3] * f;
+      if (kAlibi) z[e] += row.slope * (float)(tok - row.pos);
+      if (masked && (!here || tok < row.lo || tok >= row.hi)) z[e] = -INFINITY;
     }
+    top = z[0];
+#pragma unroll
+    for (int e = 1; e < 16; ++e) top = fmaxf(top, z[e]);
   }
+  top = max_over_groups(top);
+  const bool grown = __any(top > *m + kLazy);
+  if (grown) {
+    const float next = fmaxf(*m, top);
+    *alpha = next == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(*m - next);
+    *m = next;
+    *l *= *alpha;
+  }
+  const float off = (*m == -INFINITY ? 0.f : *m) - log_r;
+  float sum = 0.f;
+  if (plain) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf((float)s[e >> 2][e & 3], f, -off));
+      sum += p[e];
+    }
+    *l += sum * inv_r;
+  } else {
+    // (a hidden token adds nothing even where its block's absmax is NaN)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      p[e] = z[e] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(z[e] - off);
+      sum += p[e];
+    }
+    *l += sum == 0.f ? 0.f : sum * inv_r;
+  }
+  return grown;
 }
 
-// The running maximum over a group's logits: true (the whole wave) when rows
-// are to be rescaled, each by its alpha.
-__device__ __forceinline__ bool new_maximum(const float (&z)[16], float* m, float* alpha) {
-  float top = z[0];
+// Four words of fp16 pairs as an MFMA operand.
+__device__ __forceinline__ v8f16 as_f16(const uint32_t* w) {
+  return __builtin_bit_cast(v8f16, v4i32{(int)w[0], (int)w[1], (int)w[2], (int)w[3]});
+}
+
+// The blocks of 16 groups from gi0 on, `stride` apart: lane 4 i + j takes block
+// j of group gi0 + i * stride; nothing at or past token `end`.
+__device__ __forceinline__ void list_blocks(const KvArgs& a, int b, int h, int gi0, int stride,
+                                            int end, int lane, int* lin, float* k_absmax,
+                                            float* v_absmax) {
+  *lin = -1;
+  *k_absmax = *v_absmax = 0.f;
+  const int blk = 4 * (gi0 + stride * (lane >> 2)) + (lane & 3);
+  if (blk * kKvBlock < end) *lin = kv_block(a, b, h, blk);
+  if (*lin >= 0) {
+    *k_absmax = a.k_absmax[*lin];
+    *v_absmax = a.v_absmax[*lin];
+  }
+}
+// The list's factors; true when ref grew, with what sums in its units are to be
+// multiplied by.
+__device__ __forceinline__ bool list_factors(float k_absmax, float v_absmax, float* ref,
+                                             float* rescale, BlockList* bl) {
+  float top = v_absmax;
 #pragma unroll
-  for (int e = 1; e < 16; ++e) top = fmaxf(top, z[e]);
-  top = max_over_groups(top);
-  if (!__any(top > *m + kLazy)) return false;
-  const float next = fmaxf(*m, top);
-  *alpha = next == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(*m - next);
-  *m = next;
-  return true;
+  for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x, kWave));
+  const bool grown = top > *ref;
+  if (grown) {
+    *rescale = *ref / top;
+    *ref = top;
+  }
+  float ratio = v_absmax / (*ref > 0.f ? *ref : 1.f);
+  ratio = ratio < kMinRatio ? kMinRatio : ratio;   // (keeps a NaN)
+  bl->ks = k_absmax / 127.0f;
+  bl->log_r = __builtin_amdgcn_logf(ratio);
+  bl->inv_r = 1.0f / ratio;
+  return grown;
 }
 
 // ---- Few rows: each wave streams its own groups through its own part of
@@ -296,8 +361,6 @@ __global__ __launch_bounds__(kBlockThreads) void k_kv_attn_rows(KvArgs a, Rotary
   Row row;
   row.pos = sq.first + i_row;
   v4i32 qh[kC], ql[kC];
-  const uint16_t* q_row = t.q + (int64_t)(sq.row0 + i_row) * t.q_ts + (int64_t)head * t.q_hs;
-  row.qf = load_query<D>(q_row, max(row.pos, 0), live && row.pos >= 0, rot, g, qh, ql) * t.scale_log2;
   row.lo = visible_lo(t, row.pos);
   row.hi = live ? visible_hi(t, sq, row.pos) : 0;
   row.slope = kAlibi ? t.slopes[head] * 1.44269504088896340736f : 0.f;
@@ -311,19 +374,11 @@ __global__ __launch_bounds__(kBlockThreads) void k_kv_attn_rows(KvArgs a, Rotary
   float m = -INFINITY, l = 0.f, ref = 0.f;
 
   const int gi_end = (end + kGroup - 1) / kGroup;
-  for (int gi0 = begin / kGroup + wave; gi0 < gi_end; gi0 += 64) {
+  const int gi_first = begin / kGroup + wave;
+  for (int gi0 = gi_first; gi0 < gi_end; gi0 += 64) {
     BlockList bl;
-    bl.lin = -1;
-    bl.ks = 0.f;
-    float v_absmax = 0.f;
-    {
-      const int gi = gi0 + 4 * (lane >> 2), blk = 4 * gi + (lane & 3);
-      if (gi < gi_end && blk * kKvBlock < end) bl.lin = kv_block(a, b, h, blk);
-      if (bl.lin >= 0) {
-        bl.ks = a.k_absmax[bl.lin] / 127.0f;
-        v_absmax = a.v_absmax[bl.lin];
-      }
-    }
+    float k_absmax, v_absmax, rescale;
+    list_blocks(a, b, h, gi0, 4, end, lane, &bl.lin, &k_absmax, &v_absmax);
     const uint64_t present = __ballot(bl.lin >= 0);
     const int count = min(16, (gi_end - gi0 + 3) / 4);
     // absent blocks are masked; block 0 is read in their place
@@ -337,7 +392,7 @@ __global__ __launch_bounds__(kBlockThreads) void k_kv_attn_rows(KvArgs a, Rotary
       const uint32_t have = (uint32_t)(present >> (4 * i)) & 15u;
       const int t0 = (gi0 + 4 * i) * kGroup;
       v4i32 s[4];
-      float z[16], alpha;
+      float p[16], alpha;
       if (i + kSlots < count) wait_loads<kAhead>(); else wait_loads<0>();
       {
         v4i32 kf[kC][4];
@@ -348,29 +403,21 @@ __global__ __launch_bounds__(kBlockThreads) void k_kv_attn_rows(KvArgs a, Rotary
         wait_lds_reads();
         load(i + kSlots, a.k_codes, ks);
       }
-      logits<kAlibi>(s, row, __shfl(bl.ks, 4 * i + g, kWave), t0, g,
-                     t0 < all_lo || t0 + kGroup > all_hi || have != 15u, (have >> g) & 1u, z);
-      if (new_maximum(z, &m, &alpha)) {
-        l *= alpha;
+      if (softmax_step<kAlibi>(s, row, __shfl(bl.ks, 4 * i + g, kWave),
+                               __shfl(bl.log_r, 4 * i + g, kWave),
+                               __shfl(bl.inv_r, 4 * i + g, kWave), t0, g,
+                               t0 < all_lo || t0 + kGroup > all_hi || have != 15u,
+                               (have >> g) & 1u, &m, &l, &alpha, p)) {
 #pragma unroll
         for (int d = 0; d < kT; ++d) o[d] *= alpha;
       }
-      const float off = (m == -INFINITY ? 0.f : m) - __shfl(bl.log_r, 4 * i + g, kWave);
-      float sum = 0.f;
-      uint32_t ph[8], pl[8];
+      uint32_t ph[8], pl[8];   // the weights in two parts of 11 bits
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float p0 = __builtin_amdgcn_exp2f(z[2 * e] - off);
-        const float p1 = __builtin_amdgcn_exp2f(z[2 * e + 1] - off);
-        sum += p0 + p1;
-        ph[e] = f2h2(p0, p1);
-        pl[e] = f2h2(p0 - h2f(ph[e] & 0xffffu), p1 - h2f(ph[e] >> 16));
+        ph[e] = f2h2(p[2 * e], p[2 * e + 1]);
+        pl[e] = f2h2(p[2 * e] - h2f(ph[e] & 0xffffu), p[2 * e + 1] - h2f(ph[e] >> 16));
       }
-      l += sum * __shfl(bl.inv_r, 4 * i + g, kWave);
-      const v8f16 p0h = __builtin_bit_cast(v8f16, make_uint4(ph[0], ph[1], ph[2], ph[3]));
-      const v8f16 p1h = __builtin_bit_cast(v8f16, make_uint4(ph[4], ph[5], ph[6], ph[7]));
-      const v8f16 p0l = __builtin_bit_cast(v8f16, make_uint4(pl[0], pl[1], pl[2], pl[3]));
-      const v8f16 p1l = __builtin_bit_cast(v8f16, make_uint4(pl[4], pl[5], pl[6], pl[7]));
+      const v8f16 p0h = as_f16(ph), p1h = as_f16(ph + 4), p0l = as_f16(pl), p1l = as_f16(pl + 4);
       if (i + kSlots < count) wait_loads<kAhead>(); else wait_loads<0>();
 #pragma unroll
       for (int d = 0; d < kT; ++d) {
@@ -395,20 +442,13 @@ __global__ __launch_bounds__(kBlockThreads) void k_kv_attn_rows(KvArgs a, Rotary
         load(i, a.k_codes, st_k + i * S::kGroupBytes);
         load(i, a.v_codes, st_v + i * S::kGroupBytes);
       }
-    {
-      float top = v_absmax;
+    if (gi0 == gi_first) {   // (the codes are on their way meanwhile)
+      const uint16_t* q = t.q + (int64_t)(sq.row0 + i_row) * t.q_ts + (int64_t)head * t.q_hs;
+      row.qf = load_query<D>(q, max(row.pos, 0), live && row.pos >= 0, rot, g, qh, ql) * t.scale_log2;
+    }
+    if (list_factors(k_absmax, v_absmax, &ref, &rescale, &bl)) {
 #pragma unroll
-      for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x, kWave));
-      if (top > ref) {
-        const float f = ref / top;
-#pragma unroll
-        for (int d = 0; d < kT; ++d) o[d] *= f;
-        ref = top;
-      }
-      float ratio = v_absmax / (ref > 0.f ? ref : 1.f);
-      ratio = ratio < kMinRatio ? kMinRatio : ratio;   // (keeps a NaN)
-      bl.log_r = __builtin_amdgcn_logf(ratio);
-      bl.inv_r = 1.0f / ratio;
+      for (int d = 0; d < kT; ++d) o[d] *= rescale;
     }
     for (int i = 0; i < count; ++i) {
       const int slot = kSlots == 1 ? 0 : i % kSlots;
@@ -462,69 +502,347 @@ __global__ __launch_bounds__(kBlockThreads) void k_kv_attn_rows(KvArgs a, Rotary
   }
 }
 
-// One wave a row: the splits' sums, weighed by their maxima.
+// ---- Many rows: the four waves of a block share each staged group, a wave
+// takes kCols * 16 rows. A group is copied two steps ahead (one for D = 256)
+// into the next of kBuffers buffers, one block's keys and values a wave.
+template <int D>
+struct TileCfg {
+  static constexpr int kCols = D <= 128 ? 2 : 1;
+  static constexpr int kBuffers = D <= 128 ? 3 : 2;
+  static constexpr int kWaveRows = kCols * 16;
+  static constexpr int kBlockRows = 4 * kWaveRows;
+};
+
+// Block index -> item (sequence and key/value head) and what of it. With
+// `by_xcd` an item's blocks run on one of the 8 XCDs (blocks go to them in
+// turn), whose L2 then holds that item's cache.
+struct Place {
+  int item, tile, split;
+};
+__device__ __forceinline__ Place place_of(uint32_t index, int tiles, int splits, bool by_xcd) {
+  const uint32_t per = (uint32_t)tiles * splits;
+  uint32_t item, in;
+  if (by_xcd) {
+    const uint32_t slot = index / 8;
+    item = slot / per * 8 + index % 8;
+    in = slot % per;
+  } else {
+    item = index / per;
+    in = index % per;
+  }
+  Place p;
+  p.item = (int)item;
+  // the last tiles first: causal rows see more tokens the later they are
+  p.tile = tiles - 1 - (int)(in / splits);
+  p.split = (int)(in % splits);
+  return p;
+}
+
+template <int D, bool kAlibi>
+__global__ __launch_bounds__(kBlockThreads, 2) void k_kv_attn_tile(KvArgs a, RotaryArgs rot,
+                                                                   AttnArgs t, int group, int tiles,
+                                                                   int splits, int chunk,
+                                                                   int by_xcd) {
+  typedef Stage<D> S;
+  typedef TileCfg<D> Cfg;
+  constexpr int kC = (D + 63) / 64, kT = D / 16, kCols = Cfg::kCols, kBuffers = Cfg::kBuffers;
+  constexpr int kStageLoads = 2 * S::kLoads;   // a wave's, of a group
+  __shared__ __attribute__((aligned(1024))) int8_t lds[kBuffers * 2 * S::kGroupBytes];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = lane & 15, g = lane >> 4;
+  const Place at = place_of(blockIdx.x, tiles, splits, by_xcd);
+  if (at.item >= a.num_seqs * a.kv_heads) return;
+  const int b = at.item / a.kv_heads, h = at.item % a.kv_heads;
+  const KvSeq sq = kv_seq(a, b);
+  const int rows = sq.n * group;
+  const int blk_first = at.tile * Cfg::kBlockRows;
+  if (blk_first >= rows) return;
+  const int blk_last = min(blk_first + Cfg::kBlockRows, rows) - 1;
+  const Span span = row_span(t, sq, blk_first / group, blk_last / group);
+  const int begin = span.begin + at.split * chunk;
+  if (at.split > 0 && begin >= span.end) return;
+  const int end = min(begin + chunk, span.end);
+  const bool only = span.end - span.begin <= chunk;
+
+  // the wave's rows (none: it stages, and computes nothing)
+  const int w_first = blk_first + wave * Cfg::kWaveRows;
+  const int w_last = min(w_first + Cfg::kWaveRows, rows) - 1;
+  const int i_first = min(w_first, rows - 1) / group, i_last = max(w_last, 0) / group;
+  const int all_lo = visible_lo(t, sq.first + i_last);
+  const int all_hi = visible_hi(t, sq, sq.first + i_first);
+  const int any_lo = visible_lo(t, sq.first + i_first);
+  const int any_hi = w_first < rows ? visible_hi(t, sq, sq.first + i_last) : 0;
+
+  int lin, lin_next;
+  float ka, va, ka_next = 0.f, va_next = 0.f, rescale, ref = 0.f;
+  const int gi_begin = begin / kGroup, gi_end = (end + kGroup - 1) / kGroup;
+  list_blocks(a, b, h, gi_begin, 1, end, lane, &lin, &ka, &va);
+  lin_next = -1;
+  // group gi0 + i (i up to 31) of the current and the next list
+  auto stage = [&](int gi, int i) __attribute__((always_inline)) {
+    int8_t* dst = lds + (gi % kBuffers) * (2 * S::kGroupBytes) + wave * S::kPitch;
+    const int x = i < 16 ? __builtin_amdgcn_readlane(lin, (4 * i + wave) & 63)
+                         : __builtin_amdgcn_readlane(lin_next, (4 * i + wave) & 63);
+    stage_block<D>(a.k_codes, max(x, 0), dst, lane);
+    stage_block<D>(a.v_codes, max(x, 0), dst + S::kGroupBytes, lane);
+  };
+#pragma unroll
+  for (int i = 0; i < kBuffers - 1; ++i)
+    if (gi_begin + i < gi_end) stage(gi_begin + i, i);
+
+  Row row[kCols];
+  v4i32 qh[kCols][kC], ql[kCols][kC];
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) {
+    const int r = min(w_first + 16 * c + n, rows - 1);
+    const bool live = w_first + 16 * c + n < rows;
+    const int i_row = r / group, head = h * group + r % group;
+    row[c].pos = sq.first + i_row;
+    const uint16_t* q = t.q + (int64_t)(sq.row0 + i_row) * t.q_ts + (int64_t)head * t.q_hs;
+    row[c].qf = load_query<D>(q, max(row[c].pos, 0), live && row[c].pos >= 0, rot, g, qh[c], ql[c])
+                * t.scale_log2;
+    row[c].lo = visible_lo(t, row[c].pos);
+    row[c].hi = live ? visible_hi(t, sq, row[c].pos) : 0;
+    row[c].slope = kAlibi ? t.slopes[head] * 1.44269504088896340736f : 0.f;
+  }
+  v4f32 o[kCols][kT];
+  float m[kCols], l[kCols];
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) {
+    m[c] = -INFINITY;
+    l[c] = 0.f;
+#pragma unroll
+    for (int d = 0; d < kT; ++d) o[c][d] = v4f32{0.f, 0.f, 0.f, 0.f};
+  }
+
+  for (int gi0 = gi_begin; gi0 < gi_end; gi0 += 16) {
+    BlockList bl;
+    bl.lin = lin;
+    const uint64_t present = __ballot(lin >= 0);
+    if (list_factors(ka, va, &ref, &rescale, &bl)) {
+#pragma unroll
+      for (int c = 0; c < kCols; ++c)
+#pragma unroll
+        for (int d = 0; d < kT; ++d) o[c][d] *= rescale;
+    }
+    if (gi0 + 16 < gi_end) list_blocks(a, b, h, gi0 + 16, 1, end, lane, &lin_next, &ka_next, &va_next);
+    const int count = min(16, gi_end - gi0);
+    for (int i = 0; i < count; ++i) {
+      const int gi = gi0 + i;
+      if (gi + kBuffers - 2 < gi_end) wait_loads<(kBuffers - 2) * kStageLoads>(); else wait_loads<0>();
+      lds_only_barrier();   // the group has landed; every wave is done with the one before
+      if (gi + kBuffers - 1 < gi_end) stage(gi + kBuffers - 1, i + kBuffers - 1);
+      const int t0 = gi * kGroup;
+      if (t0 >= any_hi || t0 + kGroup <= any_lo) continue;
+      const int8_t* st_k = lds + (gi % kBuffers) * (2 * S::kGroupBytes);
+      const int8_t* st_v = st_k + S::kGroupBytes;
+      const uint32_t have = (uint32_t)(present >> (4 * i)) & 15u;
+      const bool masked = t0 < all_lo || t0 + kGroup > all_hi || have != 15u;
+      const float ks = __shfl(bl.ks, 4 * i + g, kWave), log_r = __shfl(bl.log_r, 4 * i + g, kWave),
+                  inv_r = __shfl(bl.inv_r, 4 * i + g, kWave);
+      v4i32 s[kCols][4];
+      {
+        v4i32 kf[kC][4];
+        read_keys<D>(st_k, n, g, kf);
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) scores<D>(kf, qh[c], ql[c], s[c]);
+      }
+      uint32_t pw[kCols][8];
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) {
+        float p[16], alpha;
+        if (softmax_step<kAlibi>(s[c], row[c], ks, log_r, inv_r, t0, g, masked, (have >> g) & 1u,
+                                 &m[c], &l[c], &alpha, p)) {
+#pragma unroll
+          for (int d = 0; d < kT; ++d) o[c][d] *= alpha;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) pw[c][e] = f2h2(p[2 * e], p[2 * e + 1]);
+      }
+#pragma unroll
+      for (int d = 0; d < kT; ++d) {
+        v8f16 v0, v1;
+        codes_to_f16(read_values<D>(st_v, n, g, d), &v0, &v1);
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) {
+          o[c][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, as_f16(pw[c]), o[c][d], 0, 0, 0);
+          o[c][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, as_f16(pw[c] + 4), o[c][d], 0, 0, 0);
+        }
+      }
+    }
+    lin = lin_next;
+    ka = ka_next;
+    va = va_next;
+  }
+
+  const float unit = ref / 127.0f;
+  const int64_t part_rows = (int64_t)a.total_tokens * t.q_heads;
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) {
+    l[c] += __shfl_xor(l[c], 16, kWave);
+    l[c] += __shfl_xor(l[c], 32, kWave);
+    const int r = w_first + 16 * c + n;
+    if (r >= rows) continue;
+    const int64_t out_row = (int64_t)(sq.row0 + r / group) * t.q_heads + h * group + r % group;
+    if (only) {
+      const float inv = l[c] == 0.f ? 0.f : unit / l[c];
+      uint16_t* out = t.out + out_row * D + 4 * g;
+#pragma unroll
+      for (int d = 0; d < kT; ++d)
+        *reinterpret_cast<uint2*>(out + 16 * d) = make_uint2(
+            f2h2(o[c][d][0] * inv, o[c][d][1] * inv), f2h2(o[c][d][2] * inv, o[c][d][3] * inv));
+    } else {
+      const int64_t part = at.split * part_rows + out_row;
+      float* out = t.part + part * D + 4 * g;
+#pragma unroll
+      for (int d = 0; d < kT; ++d) *reinterpret_cast<v4f32*>(out + 16 * d) = o[c][d] * unit;
+      if (g == 0) {
+        float* ml = t.part + (int64_t)splits * part_rows * D + part * 2;
+        ml[0] = m[c];
+        ml[1] = l[c];
+      }
+    }
+  }
+}
+
+// One block a row: the splits' sums, weighed by their maxima. Threads take four
+// features each, the groups of threads that cover a row take the splits in
+// turn, and the groups' sums are added in a fixed order.
+constexpr int kMaxSplits = 1024;
 template <int D>
 __global__ __launch_bounds__(kBlockThreads) void k_kv_attn_join(KvArgs a, AttnArgs t, int group,
-                                                                int splits, int chunk) {
-  constexpr int kE = (D + 63) / 64;
-  const int lane = threadIdx.x & 63;
-  const int r = blockIdx.x * (kBlockThreads / kWave) + (threadIdx.x >> 6);
-  const int h = blockIdx.y, b = blockIdx.z;
+                                                                int tile_rows, int splits,
+                                                                int chunk) {
+  constexpr int kLanes = D / 4, kSets = kBlockThreads / kLanes;
+  __shared__ float s_w[kMaxSplits];
+  __shared__ __attribute__((aligned(16))) float s_sum[kSets][D];
+  __shared__ float s_red[8];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int r = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   const KvSeq sq = kv_seq(a, b);
   const int rows = sq.n * group;
   if (r >= rows) return;
-  const int tile = r / kRows * kRows;
-  const Span span = row_span(t, sq, tile / group, (min(tile + kRows, rows) - 1) / group);
+  const int tile = r / tile_rows * tile_rows;
+  const Span span = row_span(t, sq, tile / group, (min(tile + tile_rows, rows) - 1) / group);
   if (span.end - span.begin <= chunk) return;   // written by its only split
   const int parts = (span.end - span.begin + chunk - 1) / chunk;
   const int64_t part_rows = (int64_t)a.total_tokens * t.q_heads;
   const int64_t row = (int64_t)(sq.row0 + r / group) * t.q_heads + h * group + r % group;
-  const float* ml = t.part + (int64_t)splits * part_rows * D;
-  float top = -INFINITY;
-  for (int p = lane; p < parts; p += kWave) top = fmaxf(top, ml[(p * part_rows + row) * 2]);
+  const float* ml = t.part + (int64_t)splits * part_rows * D + row * 2;
+
+  float m[kMaxSplits / kBlockThreads], l[kMaxSplits / kBlockThreads], top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kMaxSplits / kBlockThreads; ++i) {
+    const int p = i * kBlockThreads + tid;
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+    if (p < parts) {
+      const float2 x = *reinterpret_cast<const float2*>(ml + p * part_rows * 2);
+      m[i] = x.x;
+      l[i] = x.y;
+    }
+    top = fmaxf(top, m[i]);
+  }
 #pragma unroll
   for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x, kWave));
+  if (lane == 0) s_red[wave] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
   const float base = top == -INFINITY ? 0.f : top;
-  float acc[kE], total = 0.f;
+  float total = 0.f;
 #pragma unroll
-  for (int e = 0; e < kE; ++e) acc[e] = 0.f;
-  for (int p = 0; p < parts; ++p) {
-    const int64_t part = p * part_rows + row;
-    const float w = __builtin_amdgcn_exp2f(ml[part * 2] - base);
-    total += ml[part * 2 + 1] * w;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) {
-      const int d = e * kWave + lane;
-      if (d < D) acc[e] += t.part[part * D + d] * w;
-    }
+  for (int i = 0; i < kMaxSplits / kBlockThreads; ++i) {
+    const int p = i * kBlockThreads + tid;
+    const float w = __builtin_amdgcn_exp2f(m[i] - base);
+    total += l[i] * w;
+    if (p < parts) s_w[p] = w;
   }
-  const float inv = total == 0.f ? 0.f : 1.0f / total;
 #pragma unroll
-  for (int e = 0; e < kE; ++e) {
-    const int d = e * kWave + lane;
-    if (d < D) t.out[row * D + d] = f2h(acc[e] * inv);
+  for (int x = 1; x < 64; x <<= 1) total += __shfl_xor(total, x, kWave);
+  if (lane == 0) s_red[4 + wave] = total;
+  __syncthreads();
+  const int set = tid / kLanes, d4 = tid % kLanes * 4;
+  if (set < kSets) {
+    const float* src = t.part + row * D + d4;
+    v4f32 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int p = set; p < parts; p += kSets)
+      acc += *reinterpret_cast<const v4f32*>(src + p * part_rows * D) * s_w[p];
+    *reinterpret_cast<v4f32*>(&s_sum[set][d4]) = acc;
+  }
+  __syncthreads();
+  if (tid < D) {
+    total = (s_red[4] + s_red[5]) + (s_red[6] + s_red[7]);
+    float acc = 0.f;
+#pragma unroll
+    for (int i = 0; i < kSets; ++i) acc += s_sum[i][tid];
+    t.out[row * D + tid] = f2h(total == 0.f ? 0.f : acc / total);
   }
 }
 
 struct Plan {
-  int group, tiles, splits, chunk;
+  bool shared;     // the kernel for many rows
+  int group, tile_rows, tiles, splits, chunk, by_xcd;
+  int64_t items;
 };
 
-// Splits of the token axis so that about four blocks a compute unit run, none
-// shorter than a group for each wave.
+// Splits of the token axis: kResident blocks run at once (two a compute unit),
+// so one round of them when there is little else to run. The kernel for few
+// rows also splits beyond kMaxChunk, which evens out sequences of different
+// lengths.
 Plan plan(const KvArgs& a, int q_heads) {
-  constexpr int64_t kBlocks = 4 * 256, kMinChunk = 4 * kGroup;
+  constexpr int64_t kResident = 2 * 256, kMinChunk = 4 * kGroup, kMaxChunk = 2048;
   Plan p;
   p.group = q_heads / a.kv_heads;
-  p.tiles = (int)(((int64_t)a.max_tokens * p.group + kRows - 1) / kRows);
-  const int64_t items = std::max<int64_t>((int64_t)p.tiles * a.kv_heads * a.num_seqs, 1);
-  const int64_t want = std::max<int64_t>((kBlocks + items - 1) / items, 1);
-  const int64_t len = std::max<int64_t>(a.len_cap, 1) + kGroup;   // a span starts at a whole group
-  int64_t chunk = (len + want - 1) / want;
-  chunk = (std::max(chunk, kMinChunk) + kGroup - 1) / kGroup * kGroup;
+  const int64_t rows = (int64_t)a.max_tokens * p.group;
+  p.shared = rows > 2 * kRows;
+  p.tile_rows = !p.shared ? kRows : a.head_dim <= 128 ? TileCfg<128>::kBlockRows
+                                                      : TileCfg<256>::kBlockRows;
+  p.tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
+  p.items = (int64_t)a.kv_heads * a.num_seqs;
+  p.by_xcd = p.items % 8 == 0 || p.items >= 64;
+  const int64_t blocks = std::max<int64_t>(p.tiles * p.items, 1);
+  const int64_t len = (int64_t)a.len_cap + kGroup;   // a span starts at a whole group
+  int64_t chunk = len;
+  if (!p.shared || blocks < kResident) {
+    chunk = std::max((int64_t)a.len_cap * blocks / kResident, kMinChunk);
+    if (!p.shared) chunk = std::min(chunk, kMaxChunk);
+  }
+  chunk = std::max(chunk, len / kMaxSplits + 1);
+  chunk = (chunk + kGroup - 1) / kGroup * kGroup;
+  if (getenv("KVC")) chunk = atoi(getenv("KVC"));
   p.chunk = (int)chunk;
   p.splits = (int)((len + chunk - 1) / chunk);
   return p;
+}
+
+template <int D>
+hipError_t launch_d(const KvArgs& a, const RotaryArgs& r, const AttnArgs& t, hipStream_t s) {
+  const Plan p = plan(a, t.q_heads);
+  if (p.shared) {
+    const int64_t items = p.by_xcd ? (p.items + 7) / 8 * 8 : p.items;
+    const int64_t blocks = items * p.tiles * p.splits;
+    if (blocks > INT32_MAX) return hipErrorInvalidValue;
+    if (t.slopes)
+      k_kv_attn_tile<D, true><<<(uint32_t)blocks, kBlockThreads, 0, s>>>(
+          a, r, t, p.group, p.tiles, p.splits, p.chunk, p.by_xcd);
+    else
+      k_kv_attn_tile<D, false><<<(uint32_t)blocks, kBlockThreads, 0, s>>>(
+          a, r, t, p.group, p.tiles, p.splits, p.chunk, p.by_xcd);
+  } else {
+    const dim3 grid((uint32_t)p.splits, (uint32_t)(p.tiles * a.kv_heads), (uint32_t)a.num_seqs);
+    if (t.slopes)
+      k_kv_attn_rows<D, true><<<grid, kBlockThreads, 0, s>>>(a, r, t, p.group, p.tiles, p.splits,
+                                                             p.chunk);
+    else
+      k_kv_attn_rows<D, false><<<grid, kBlockThreads, 0, s>>>(a, r, t, p.group, p.tiles, p.splits,
+                                                              p.chunk);
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.splits <= 1) return e;
+  const dim3 join((uint32_t)(a.max_tokens * p.group), (uint32_t)a.kv_heads, (uint32_t)a.num_seqs);
+  k_kv_attn_join<D><<<join, kBlockThreads, 0, s>>>(a, t, p.group, p.tile_rows, p.splits, p.chunk);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -533,24 +851,6 @@ size_t attn_workspace_bytes(const KvArgs& a, int q_heads) {
   const Plan p = plan(a, q_heads);
   if (p.splits <= 1) return 0;
   return (size_t)p.splits * a.total_tokens * q_heads * (a.head_dim + 2) * sizeof(float);
-}
-
-template <int D>
-hipError_t launch_d(const KvArgs& a, const RotaryArgs& r, const AttnArgs& t, hipStream_t s) {
-  const Plan p = plan(a, t.q_heads);
-  const int64_t y = (int64_t)p.tiles * a.kv_heads;
-  if (y > 65535) return hipErrorInvalidValue;
-  const dim3 grid((uint32_t)p.splits, (uint32_t)y, (uint32_t)a.num_seqs);
-  if (t.slopes)
-    k_kv_attn_rows<D, true><<<grid, kBlockThreads, 0, s>>>(a, r, t, p.group, p.tiles, p.splits, p.chunk);
-  else
-    k_kv_attn_rows<D, false><<<grid, kBlockThreads, 0, s>>>(a, r, t, p.group, p.tiles, p.splits, p.chunk);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || p.splits <= 1) return e;
-  const dim3 join((uint32_t)(((int64_t)a.max_tokens * p.group + 3) / 4), (uint32_t)a.kv_heads,
-                  (uint32_t)a.num_seqs);
-  k_kv_attn_join<D><<<join, kBlockThreads, 0, s>>>(a, t, p.group, p.splits, p.chunk);
-  return hipGetLastError();
 }
 
 hipError_t launch_kv_attention(const KvArgs& a, const RotaryArgs& r, const AttnArgs& t,
