@@ -23,6 +23,7 @@
 
 #include <algorithm>
 #include <cstdlib>
+#include <type_traits>
 
 #include "kv_common.h"
 
@@ -197,24 +198,24 @@ __device__ __forceinline__ v4i32 read_values(const int8_t* st, int n, int g, int
 }
 
 // One column tile's scores of a group, S^T = K Q^T as integers: element e of a
-// lane is (e >> 2, e & 3) of s.
+// lane is (e >> 2, e & 3) of s. (The two parts have sums of their own: one
+// chain of MFMAs through the shift stalls on each of its links.)
 template <int D>
 __device__ __forceinline__ void scores(const v4i32 (&k)[(D + 63) / 64][4], const v4i32* qh,
                                        const v4i32* ql, v4i32 (&s)[4]) {
   constexpr int kC = (D + 63) / 64;
+  v4i32 hi[4], lo[4];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    s[q] = v4i32{0, 0, 0, 0};
+  for (int q = 0; q < 4; ++q) hi[q] = lo[q] = v4i32{0, 0, 0, 0};
 #pragma unroll
-    for (int c = 0; c < kC; ++c)
-      s[q] = __builtin_amdgcn_mfma_i32_16x16x64_i8(k[c][q], qh[c], s[q],
-                                                   0, 0, 0);
-    s[q] = s[q] << 7;
+  for (int c = 0; c < kC; ++c)
 #pragma unroll
-    for (int c = 0; c < kC; ++c)
-      s[q] = __builtin_amdgcn_mfma_i32_16x16x64_i8(k[c][q], ql[c], s[q],
-                                                   0, 0, 0);
-  }
+    for (int q = 0; q < 4; ++q) {
+      hi[q] = __builtin_amdgcn_mfma_i32_16x16x64_i8(k[c][q], qh[c], hi[q], 0, 0, 0);
+      lo[q] = __builtin_amdgcn_mfma_i32_16x16x64_i8(k[c][q], ql[c], lo[q], 0, 0, 0);
+    }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) s[q] = (hi[q] << 7) + lo[q];
 }
 
 // A lane's row: its position, visible tokens and factors.
@@ -228,15 +229,14 @@ struct Row {
 // tokens, and m, l brought up to date. True (the whole wave) when sums over
 // earlier tokens are to be multiplied by alpha. When no token is hidden the
 // factor is common to the 16 scores, so their maximum is the integers'.
-template <bool kAlibi>
+template <bool kAlibi, bool kMasked>
 __device__ __forceinline__ bool softmax_step(const v4i32 (&s)[4], const Row& row, float ks,
-                                             float log_r, float inv_r, int t0, int g, bool masked,
-                                             bool here, float* m, float* l, float* alpha,
-                                             float (&p)[16]) {
+                                             float log_r, float inv_r, int t0, int g, bool here,
+                                             float* m, float* l, float* alpha, float (&p)[16]) {
   const float f = ks * row.qf;
   float top, z[16];
-  const bool plain = !kAlibi && !masked;
-  if (plain) {
+  constexpr bool plain = !kAlibi && !kMasked;
+  if constexpr (plain) {
     int i_top = s[0][0];
 #pragma unroll
     for (int e = 1; e < 16; ++e) i_top = max(i_top, s[e >> 2][e & 3]);
@@ -247,7 +247,7 @@ __device__ __forceinline__ bool softmax_step(const v4i32 (&s)[4], const Row& row
       const int tok = t0 + 16 * g + e;
       z[e] = (float)s[e >> 2][e & 3] * f;
       if (kAlibi) z[e] += row.slope * (float)(tok - row.pos);
-      if (masked && (!here || tok < row.lo || tok >= row.hi)) z[e] = -INFINITY;
+      if (kMasked && (!here || tok < row.lo || tok >= row.hi)) z[e] = -INFINITY;
     }
     top = z[0];
 #pragma unroll
@@ -263,7 +263,7 @@ __device__ __forceinline__ bool softmax_step(const v4i32 (&s)[4], const Row& row
   }
   const float off = (*m == -INFINITY ? 0.f : *m) - log_r;
   float sum = 0.f;
-  if (plain) {
+  if constexpr (plain) {
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf((float)s[e >> 2][e & 3], f, -off));
@@ -274,10 +274,10 @@ __device__ __forceinline__ bool softmax_step(const v4i32 (&s)[4], const Row& row
     // (a hidden token adds nothing even where its block's absmax is NaN)
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      p[e] = z[e] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(z[e] - off);
+      p[e] = kMasked && z[e] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(z[e] - off);
       sum += p[e];
     }
-    *l += sum == 0.f ? 0.f : sum * inv_r;
+    *l += kMasked && sum == 0.f ? 0.f : sum * inv_r;
   }
   return grown;
 }
@@ -326,7 +326,7 @@ __device__ __forceinline__ bool list_factors(float k_absmax, float v_absmax, flo
 // so something is always in flight. The four waves of a block join through LDS,
 // the blocks of a row tile through the workspace and k_kv_attn_join.
 template <int D, bool kAlibi>
-__global__ __launch_bounds__(kBlockThreads) void k_kv_attn_rows(KvArgs a, RotaryArgs rot,
+__global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_rows(KvArgs a, RotaryArgs rot,
                                                                 AttnArgs t, int group, int tiles,
                                                                 int splits, int chunk) {
   constexpr int kC = (D + 63) / 64, kT = D / 16, kLd = D + 4;
@@ -403,11 +403,13 @@ __global__ __launch_bounds__(kBlockThreads) void k_kv_attn_rows(KvArgs a, Rotary
         wait_lds_reads();
         load(i + kSlots, a.k_codes, ks);
       }
-      if (softmax_step<kAlibi>(s, row, __shfl(bl.ks, 4 * i + g, kWave),
-                               __shfl(bl.log_r, 4 * i + g, kWave),
-                               __shfl(bl.inv_r, 4 * i + g, kWave), t0, g,
-                               t0 < all_lo || t0 + kGroup > all_hi || have != 15u,
-                               (have >> g) & 1u, &m, &l, &alpha, p)) {
+      const bool masked = t0 < all_lo || t0 + kGroup > all_hi || have != 15u;
+      const float ks1 = __shfl(bl.ks, 4 * i + g, kWave), log_r = __shfl(bl.log_r, 4 * i + g, kWave),
+                  inv_r = __shfl(bl.inv_r, 4 * i + g, kWave);
+      if (masked ? softmax_step<kAlibi, true>(s, row, ks1, log_r, inv_r, t0, g, (have >> g) & 1u,
+                                              &m, &l, &alpha, p)
+                 : softmax_step<kAlibi, false>(s, row, ks1, log_r, inv_r, t0, g, true, &m, &l,
+                                               &alpha, p)) {
 #pragma unroll
         for (int d = 0; d < kT; ++d) o[d] *= alpha;
       }
@@ -502,16 +504,34 @@ __global__ __launch_bounds__(kBlockThreads) void k_kv_attn_rows(KvArgs a, Rotary
   }
 }
 
-// ---- Many rows: the four waves of a block share each staged group, a wave
-// takes kCols * 16 rows. A group is copied two steps ahead (one for D = 256)
-// into the next of kBuffers buffers, one block's keys and values a wave.
+// ---- Many rows: the waves of a block share each group, a wave takes kCols * 16
+// rows. Keys are copied to LDS as they are, two groups ahead, into the next of
+// three buffers. Values are turned into fp16 once for the block (converted by
+// every wave for itself they were a third of its vector instructions): each wave
+// loads its share of a group one step ahead and stores it as operands, of which
+// LDS holds this group's and the next's.
 template <int D>
 struct TileCfg {
+  static constexpr int kWaves = D <= 128 ? 4 : 8;
+  static constexpr int kThreads = kWaves * kWave;
   static constexpr int kCols = D <= 128 ? 2 : 1;
-  static constexpr int kBuffers = D <= 128 ? 3 : 2;
   static constexpr int kWaveRows = kCols * 16;
-  static constexpr int kBlockRows = 4 * kWaveRows;
+  static constexpr int kBlockRows = kWaves * kWaveRows;
+  static constexpr int kKeyBuffers = 3;
+  static constexpr int kKeyLoads = 4 * Stage<D>::kLoads / kWaves;   // a wave's, of a group
+  static constexpr int kValueTiles = (D / 16 + kWaves - 1) / kWaves;
+  static constexpr int kValueBytes = kGroup * D * 2;
+  static constexpr int kLds = kKeyBuffers * Stage<D>::kGroupBytes + 2 * kValueBytes;
 };
+
+// A 16-byte LDS store. Written as the instruction itself: before a plain store
+// the compiler waits for every copy into LDS in flight, which it never meets.
+// The barrier before the bytes are read waits for it.
+__device__ __forceinline__ void lds_store16(int8_t* p, v8f16 x) {
+  const uint32_t addr = (uint32_t)(uintptr_t)(lds_ptr_t)p;
+  const v4i32 d = __builtin_bit_cast(v4i32, x);
+  asm volatile("ds_write_b128 %0, %1" : : "v"(addr), "v"(d) : "memory");
+}
 
 // Block index -> item (sequence and key/value head) and what of it. With
 // `by_xcd` an item's blocks run on one of the 8 XCDs (blocks go to them in
@@ -539,15 +559,16 @@ __device__ __forceinline__ Place place_of(uint32_t index, int tiles, int splits,
 }
 
 template <int D, bool kAlibi>
-__global__ __launch_bounds__(kBlockThreads, 2) void k_kv_attn_tile(KvArgs a, RotaryArgs rot,
-                                                                   AttnArgs t, int group, int tiles,
-                                                                   int splits, int chunk,
-                                                                   int by_xcd) {
+__global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
+    KvArgs a, RotaryArgs rot, AttnArgs t, int group, int tiles, int splits, int chunk, int by_xcd) {
   typedef Stage<D> S;
   typedef TileCfg<D> Cfg;
-  constexpr int kC = (D + 63) / 64, kT = D / 16, kCols = Cfg::kCols, kBuffers = Cfg::kBuffers;
-  constexpr int kStageLoads = 2 * S::kLoads;   // a wave's, of a group
-  __shared__ __attribute__((aligned(1024))) int8_t lds[kBuffers * 2 * S::kGroupBytes];
+  constexpr int kC = (D + 63) / 64, kT = D / 16, kCols = Cfg::kCols;
+  // loads of a wave younger than the keys it waits for: the next group's keys,
+  // and its own values of that group (at least)
+  constexpr int kAhead = Cfg::kKeyLoads + kT / Cfg::kWaves;
+  __shared__ __attribute__((aligned(1024))) int8_t lds[Cfg::kLds];
+  int8_t* const lds_v = lds + Cfg::kKeyBuffers * S::kGroupBytes;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   const Place at = place_of(blockIdx.x, tiles, splits, by_xcd);
@@ -573,22 +594,60 @@ __global__ __launch_bounds__(kBlockThreads, 2) void k_kv_attn_tile(KvArgs a, Rot
   const int any_lo = visible_lo(t, sq.first + i_first);
   const int any_hi = w_first < rows ? visible_hi(t, sq, sq.first + i_last) : 0;
 
-  int lin, lin_next;
+  int lin, lin_next = -1;
   float ka, va, ka_next = 0.f, va_next = 0.f, rescale, ref = 0.f;
   const int gi_begin = begin / kGroup, gi_end = (end + kGroup - 1) / kGroup;
   list_blocks(a, b, h, gi_begin, 1, end, lane, &lin, &ka, &va);
-  lin_next = -1;
-  // group gi0 + i (i up to 31) of the current and the next list
-  auto stage = [&](int gi, int i) __attribute__((always_inline)) {
-    int8_t* dst = lds + (gi % kBuffers) * (2 * S::kGroupBytes) + wave * S::kPitch;
-    const int x = i < 16 ? __builtin_amdgcn_readlane(lin, (4 * i + wave) & 63)
-                         : __builtin_amdgcn_readlane(lin_next, (4 * i + wave) & 63);
-    stage_block<D>(a.k_codes, max(x, 0), dst, lane);
-    stage_block<D>(a.v_codes, max(x, 0), dst + S::kGroupBytes, lane);
-  };
+  // What follows takes group gi as the i-th (up to 31st) of the current and
+  // the next list. Absent blocks are masked; block 0 is read in their place.
+  auto stage_keys = [&](int gi, int i) __attribute__((always_inline)) {
+    constexpr int kPer = Cfg::kWaves / 4;   // waves a block
+    const int blk = wave / kPer;
+    const int x = i < 16 ? __builtin_amdgcn_readlane(lin, (4 * i + blk) & 63)
+                         : __builtin_amdgcn_readlane(lin_next, (4 * i + blk) & 63);
+    const __amdgpu_buffer_rsrc_t rsrc =
+        buffer_rsrc(a.k_codes + (int64_t)max(x, 0) * S::kBytes, S::kBytes);
+    int8_t* dst = lds + gi % Cfg::kKeyBuffers * S::kGroupBytes + blk * S::kPitch;
 #pragma unroll
-  for (int i = 0; i < kBuffers - 1; ++i)
-    if (gi_begin + i < gi_end) stage(gi_begin + i, i);
+    for (int jj = 0; jj < Cfg::kKeyLoads; ++jj) {
+      const int j = wave % kPer * Cfg::kKeyLoads + jj;
+      if (S::kBytes % 1024 == 0 || j < S::kBytes / 1024 || lane < S::kBytes % 1024 / 16)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr_t)(dst + j * 1024), 16, lane * 16,
+                                                 j * 1024, 0, 0);
+    }
+  };
+  v4i32 vr[Cfg::kValueTiles];   // the wave's tiles of a group: wave, wave + kWaves, ..
+  auto load_values = [&](int i) __attribute__((always_inline)) {
+    const int x = __shfl(i < 16 ? lin : lin_next, (4 * i + g) & 63, kWave);
+    const int8_t* p = a.v_codes + (int64_t)max(x, 0) * S::kBytes + n * 16;
+#pragma unroll
+    for (int j = 0; j < Cfg::kValueTiles; ++j) {
+      const int d = wave + j * Cfg::kWaves;
+      if (kT % Cfg::kWaves == 0 || d < kT) vr[j] = *reinterpret_cast<const v4i32*>(p + d * kTile);
+    }
+  };
+  auto store_values = [&](int gi) __attribute__((always_inline)) {
+    int8_t* dst = lds_v + (gi & 1) * Cfg::kValueBytes + lane * 16;
+#pragma unroll
+    for (int j = 0; j < Cfg::kValueTiles; ++j) {
+      const int d = wave + j * Cfg::kWaves;
+      if (kT % Cfg::kWaves == 0 || d < kT) {
+        v8f16 v0, v1;
+        codes_to_f16(vr[j], &v0, &v1);
+        lds_store16(dst + d * 2048, v0);
+        lds_store16(dst + d * 2048 + 1024, v1);
+      }
+    }
+  };
+  if (gi_begin < gi_end) {
+    load_values(0);
+    stage_keys(gi_begin, 0);
+    store_values(gi_begin);
+    if (gi_begin + 1 < gi_end) {
+      stage_keys(gi_begin + 1, 1);
+      load_values(1);
+    }
+  }
 
   Row row[kCols];
   v4i32 qh[kCols][kC], ql[kCols][kC];
@@ -617,7 +676,6 @@ __global__ __launch_bounds__(kBlockThreads, 2) void k_kv_attn_tile(KvArgs a, Rot
 
   for (int gi0 = gi_begin; gi0 < gi_end; gi0 += 16) {
     BlockList bl;
-    bl.lin = lin;
     const uint64_t present = __ballot(lin >= 0);
     if (list_factors(ka, va, &ref, &rescale, &bl)) {
 #pragma unroll
@@ -627,19 +685,14 @@ __global__ __launch_bounds__(kBlockThreads, 2) void k_kv_attn_tile(KvArgs a, Rot
     }
     if (gi0 + 16 < gi_end) list_blocks(a, b, h, gi0 + 16, 1, end, lane, &lin_next, &ka_next, &va_next);
     const int count = min(16, gi_end - gi0);
-    for (int i = 0; i < count; ++i) {
-      const int gi = gi0 + i;
-      if (gi + kBuffers - 2 < gi_end) wait_loads<(kBuffers - 2) * kStageLoads>(); else wait_loads<0>();
-      lds_only_barrier();   // the group has landed; every wave is done with the one before
-      if (gi + kBuffers - 1 < gi_end) stage(gi + kBuffers - 1, i + kBuffers - 1);
-      const int t0 = gi * kGroup;
-      if (t0 >= any_hi || t0 + kGroup <= any_lo) continue;
-      const int8_t* st_k = lds + (gi % kBuffers) * (2 * S::kGroupBytes);
-      const int8_t* st_v = st_k + S::kGroupBytes;
-      const uint32_t have = (uint32_t)(present >> (4 * i)) & 15u;
-      const bool masked = t0 < all_lo || t0 + kGroup > all_hi || have != 15u;
+
+    auto step = [&](int gi, int i, auto masked) __attribute__((always_inline)) {
+      constexpr bool kMasked = decltype(masked)::value;
+      const int8_t* st_k = lds + gi % Cfg::kKeyBuffers * S::kGroupBytes;
+      const int8_t* st_v = lds_v + (gi & 1) * Cfg::kValueBytes + lane * 16;
       const float ks = __shfl(bl.ks, 4 * i + g, kWave), log_r = __shfl(bl.log_r, 4 * i + g, kWave),
                   inv_r = __shfl(bl.inv_r, 4 * i + g, kWave);
+      const bool here = !kMasked || ((present >> (4 * i + g)) & 1u);
       v4i32 s[kCols][4];
       {
         v4i32 kf[kC][4];
@@ -651,8 +704,8 @@ __global__ __launch_bounds__(kBlockThreads, 2) void k_kv_attn_tile(KvArgs a, Rot
 #pragma unroll
       for (int c = 0; c < kCols; ++c) {
         float p[16], alpha;
-        if (softmax_step<kAlibi>(s[c], row[c], ks, log_r, inv_r, t0, g, masked, (have >> g) & 1u,
-                                 &m[c], &l[c], &alpha, p)) {
+        if (softmax_step<kAlibi, kMasked>(s[c], row[c], ks, log_r, inv_r, gi * kGroup, g, here,
+                                          &m[c], &l[c], &alpha, p)) {
 #pragma unroll
           for (int d = 0; d < kT; ++d) o[c][d] *= alpha;
         }
@@ -661,14 +714,31 @@ __global__ __launch_bounds__(kBlockThreads, 2) void k_kv_attn_tile(KvArgs a, Rot
       }
 #pragma unroll
       for (int d = 0; d < kT; ++d) {
-        v8f16 v0, v1;
-        codes_to_f16(read_values<D>(st_v, n, g, d), &v0, &v1);
+        const v8f16 v0 = __builtin_bit_cast(v8f16, *reinterpret_cast<const v4i32*>(st_v + d * 2048));
+        const v8f16 v1 =
+            __builtin_bit_cast(v8f16, *reinterpret_cast<const v4i32*>(st_v + d * 2048 + 1024));
 #pragma unroll
         for (int c = 0; c < kCols; ++c) {
           o[c][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, as_f16(pw[c]), o[c][d], 0, 0, 0);
           o[c][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, as_f16(pw[c] + 4), o[c][d], 0, 0, 0);
         }
       }
+    };
+    for (int i = 0; i < count; ++i) {
+      const int gi = gi0 + i;
+      if (gi + 1 < gi_end) wait_loads<kAhead>(); else wait_loads<0>();
+      lds_only_barrier();   // the group is in LDS; every wave is done with the one before
+      if (gi + 1 < gi_end) store_values(gi + 1);
+      if (gi + 2 < gi_end) {
+        stage_keys(gi + 2, i + 2);
+        load_values(i + 2);
+      }
+      const int t0 = gi * kGroup;
+      if (t0 >= any_hi || t0 + kGroup <= any_lo) continue;
+      if (t0 < all_lo || t0 + kGroup > all_hi || ((present >> (4 * i)) & 15u) != 15u)
+        step(gi, i, std::true_type{});
+      else
+        step(gi, i, std::false_type{});
     }
     lin = lin_next;
     ka = ka_next;
@@ -824,10 +894,10 @@ hipError_t launch_d(const KvArgs& a, const RotaryArgs& r, const AttnArgs& t, hip
     const int64_t blocks = items * p.tiles * p.splits;
     if (blocks > INT32_MAX) return hipErrorInvalidValue;
     if (t.slopes)
-      k_kv_attn_tile<D, true><<<(uint32_t)blocks, kBlockThreads, 0, s>>>(
+      k_kv_attn_tile<D, true><<<(uint32_t)blocks, TileCfg<D>::kThreads, 0, s>>>(
           a, r, t, p.group, p.tiles, p.splits, p.chunk, p.by_xcd);
     else
-      k_kv_attn_tile<D, false><<<(uint32_t)blocks, kBlockThreads, 0, s>>>(
+      k_kv_attn_tile<D, false><<<(uint32_t)blocks, TileCfg<D>::kThreads, 0, s>>>(
           a, r, t, p.group, p.tiles, p.splits, p.chunk, p.by_xcd);
   } else {
     const dim3 grid((uint32_t)p.splits, (uint32_t)(p.tiles * a.kv_heads), (uint32_t)a.num_seqs);
