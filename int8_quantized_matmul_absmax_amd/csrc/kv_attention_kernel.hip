@@ -54,9 +54,14 @@ __device__ __forceinline__ Span row_span(const AttnArgs& t, const KvSeq& sq, int
   return s;
 }
 
+// Maximum over the four lanes that share a row (lanes l ^ 32, l ^ 16).
 __device__ __forceinline__ float max_over_groups(float v) {
-  v = fmaxf(v, __shfl_xor(v, 16, kWave));
-  return fmaxf(v, __shfl_xor(v, 32, kWave));
+  uint32_t u = __builtin_bit_cast(uint32_t, v);
+  const auto p = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  v = fmaxf(__builtin_bit_cast(float, (uint32_t)p[0]), __builtin_bit_cast(float, (uint32_t)p[1]));
+  u = __builtin_bit_cast(uint32_t, v);
+  const auto q = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return fmaxf(__builtin_bit_cast(float, (uint32_t)q[0]), __builtin_bit_cast(float, (uint32_t)q[1]));
 }
 
 // 16 codes as fp16: 0x6400 | (code + 128) is 1152 + code.
@@ -181,15 +186,9 @@ __device__ __forceinline__ void wait_lds_reads() {
 // c is token 4 q + n % 4 of block n / 4, features 64 c + 16 g .. + 15 (past D,
 // where the query is zero, some other ones).
 template <int D>
-__device__ __forceinline__ void read_keys(const int8_t* st, int n, int g,
-                                          v4i32 (&k)[(D + 63) / 64][4]) {
-  const int8_t* p = st + (n >> 2) * Stage<D>::kPitch + (n & 3) * 16;
-#pragma unroll
-  for (int c = 0; c < (D + 63) / 64; ++c) {
-    const int8_t* pc = p + min(4 * c + g, D / 16 - 1) * kTile;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) k[c][q] = *reinterpret_cast<const v4i32*>(pc + q * 64);
-  }
+__device__ __forceinline__ v4i32 read_keys(const int8_t* st, int n, int g, int c, int q) {
+  return *reinterpret_cast<const v4i32*>(st + (n >> 2) * Stage<D>::kPitch + (n & 3) * 16 +
+                                         min(4 * c + g, D / 16 - 1) * kTile + q * 64);
 }
 // Its values: feature 16 d + n, the 16 tokens of block g.
 template <int D>
@@ -198,24 +197,30 @@ __device__ __forceinline__ v4i32 read_values(const int8_t* st, int n, int g, int
 }
 
 // One column tile's scores of a group, S^T = K Q^T as integers: element e of a
-// lane is (e >> 2, e & 3) of s. (The two parts have sums of their own: one
-// chain of MFMAs through the shift stalls on each of its links.)
+// lane is (e >> 2, e & 3) of s.
 template <int D>
-__device__ __forceinline__ void scores(const v4i32 (&k)[(D + 63) / 64][4], const v4i32* qh,
+__device__ __forceinline__ void scores(const int8_t* st, int n, int g, const v4i32* qh,
                                        const v4i32* ql, v4i32 (&s)[4]) {
   constexpr int kC = (D + 63) / 64;
-  v4i32 hi[4], lo[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) hi[q] = lo[q] = v4i32{0, 0, 0, 0};
+  v4i32 k[kC][4];
 #pragma unroll
   for (int c = 0; c < kC; ++c)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      hi[q] = __builtin_amdgcn_mfma_i32_16x16x64_i8(k[c][q], qh[c], hi[q], 0, 0, 0);
-      lo[q] = __builtin_amdgcn_mfma_i32_16x16x64_i8(k[c][q], ql[c], lo[q], 0, 0, 0);
-    }
+    for (int q = 0; q < 4; ++q) k[c][q] = read_keys<D>(st, n, g, c, q);
 #pragma unroll
-  for (int q = 0; q < 4; ++q) s[q] = (hi[q] << 7) + lo[q];
+  for (int q = 0; q < 4; ++q) s[q] = v4i32{0, 0, 0, 0};
+#pragma unroll
+  for (int c = 0; c < kC; ++c)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      s[q] = __builtin_amdgcn_mfma_i32_16x16x64_i8(k[c][q], qh[c], s[q], 0, 0, 0);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) s[q] = s[q] << 7;
+#pragma unroll
+  for (int c = 0; c < kC; ++c)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      s[q] = __builtin_amdgcn_mfma_i32_16x16x64_i8(k[c][q], ql[c], s[q], 0, 0, 0);
 }
 
 // A lane's row: its position, visible tokens and factors.
@@ -225,61 +230,63 @@ struct Row {
   float slope;   // * log2(e)
 };
 
-// The running softmax of a lane's row over one group: the weights p of its 16
-// tokens, and m, l brought up to date. True (the whole wave) when sums over
-// earlier tokens are to be multiplied by alpha. When no token is hidden the
-// factor is common to the 16 scores, so their maximum is the integers'.
-template <bool kAlibi, bool kMasked>
-__device__ __forceinline__ bool softmax_step(const v4i32 (&s)[4], const Row& row, float ks,
-                                             float log_r, float inv_r, int t0, int g, bool here,
-                                             float* m, float* l, float* alpha, float (&p)[16]) {
-  const float f = ks * row.qf;
-  float top, z[16];
-  constexpr bool plain = !kAlibi && !kMasked;
-  if constexpr (plain) {
-    int i_top = s[0][0];
+// A lane's factors of a group: logits are x f, weights 2^(x f - m + log_r), and
+// the row sum takes them times inv_r.
+struct Scale {
+  float f, log_r, inv_r;
+};
+
+// The logits' maximum over a lane's 16 tokens. With a bias x becomes the logit
+// itself; with `masked`, hidden tokens' x is -infinity, and a lane whose block
+// its row does not see at all drops the block's factors (they may be NaN).
+template <bool kAlibi>
+__device__ __forceinline__ float logits(float (&x)[16], Scale* sc, const Row& row, int t0, int g,
+                                        bool masked, bool here) {
+  constexpr float kMinFactor = 0x1p-100f;   // (0 times -infinity would be NaN)
+  sc->f *= row.qf;
+  sc->f = sc->f < kMinFactor ? kMinFactor : sc->f;   // (keeps a NaN)
+  const int tok0 = t0 + 16 * g;
+  if (kAlibi) {
+    const float base = row.slope * (float)(tok0 - row.pos);
 #pragma unroll
-    for (int e = 1; e < 16; ++e) i_top = max(i_top, s[e >> 2][e & 3]);
-    top = (float)i_top * f;
-  } else {
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const int tok = t0 + 16 * g + e;
-      z[e] = (float)s[e >> 2][e & 3] * f;
-      if (kAlibi) z[e] += row.slope * (float)(tok - row.pos);
-      if (kMasked && (!here || tok < row.lo || tok >= row.hi)) z[e] = -INFINITY;
-    }
-    top = z[0];
-#pragma unroll
-    for (int e = 1; e < 16; ++e) top = fmaxf(top, z[e]);
+    for (int e = 0; e < 16; ++e)
+      x[e] = __builtin_fmaf(x[e], sc->f, __builtin_fmaf(row.slope, (float)e, base));
+    sc->f = 1.f;
   }
-  top = max_over_groups(top);
-  const bool grown = __any(top > *m + kLazy);
-  if (grown) {
-    const float next = fmaxf(*m, top);
-    *alpha = next == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(*m - next);
-    *m = next;
-    *l *= *alpha;
-  }
-  const float off = (*m == -INFINITY ? 0.f : *m) - log_r;
-  float sum = 0.f;
-  if constexpr (plain) {
+  if (masked) {
+    const int lo = row.lo - tok0, hi = row.hi - tok0;
+    const bool some = here && hi > 0 && lo < 16;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf((float)s[e >> 2][e & 3], f, -off));
-      sum += p[e];
+    for (int e = 0; e < 16; ++e) x[e] = some && e >= lo && e < hi ? x[e] : -INFINITY;
+    if (!some) {
+      sc->f = 1.f;
+      sc->log_r = sc->inv_r = 0.f;
     }
-    *l += sum * inv_r;
-  } else {
-    // (a hidden token adds nothing even where its block's absmax is NaN)
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      p[e] = kMasked && z[e] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(z[e] - off);
-      sum += p[e];
-    }
-    *l += kMasked && sum == 0.f ? 0.f : sum * inv_r;
   }
-  return grown;
+  float top = fmaxf(x[0], x[1]);
+#pragma unroll
+  for (int e = 2; e < 16; e += 2) top = fmaxf(fmaxf(top, x[e]), x[e + 1]);
+  return top * sc->f;
+}
+
+// Takes a row's new maximum (over the lanes that share it) into m and l; what
+// its sums over earlier tokens are to be multiplied by.
+__device__ __forceinline__ float raise(float top, float* m, float* l) {
+  const float next = fmaxf(*m, top);
+  const float alpha = next == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(*m - next);
+  *m = next;
+  *l *= alpha;
+  return alpha;
+}
+
+// The weights of four of a lane's tokens, added to sum.
+__device__ __forceinline__ void weights4(const float* x, float f, float off, float* sum, float* p) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], f, -off));
+  *sum += (p[0] + p[1]) + (p[2] + p[3]);
+}
+__device__ __forceinline__ float weight_offset(float m, const Scale& sc) {
+  return (m == -INFINITY ? 0.f : m) - sc.log_r;
 }
 
 // Four words of fp16 pairs as an MFMA operand.
@@ -392,27 +399,30 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
       const uint32_t have = (uint32_t)(present >> (4 * i)) & 15u;
       const int t0 = (gi0 + 4 * i) * kGroup;
       v4i32 s[4];
-      float p[16], alpha;
+      float x[16], p[16];
       if (i + kSlots < count) wait_loads<kAhead>(); else wait_loads<0>();
-      {
-        v4i32 kf[kC][4];
-        read_keys<D>(ks, n, g, kf);
-        scores<D>(kf, qh, ql, s);
-      }
+      scores<D>(ks, n, g, qh, ql, s);
       if (i + kSlots < count) {
         wait_lds_reads();
         load(i + kSlots, a.k_codes, ks);
       }
-      const bool masked = t0 < all_lo || t0 + kGroup > all_hi || have != 15u;
-      const float ks1 = __shfl(bl.ks, 4 * i + g, kWave), log_r = __shfl(bl.log_r, 4 * i + g, kWave),
-                  inv_r = __shfl(bl.inv_r, 4 * i + g, kWave);
-      if (masked ? softmax_step<kAlibi, true>(s, row, ks1, log_r, inv_r, t0, g, (have >> g) & 1u,
-                                              &m, &l, &alpha, p)
-                 : softmax_step<kAlibi, false>(s, row, ks1, log_r, inv_r, t0, g, true, &m, &l,
-                                               &alpha, p)) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] = (float)s[e >> 2][e & 3];
+      Scale sc = {__shfl(bl.ks, 4 * i + g, kWave), __shfl(bl.log_r, 4 * i + g, kWave),
+                  __shfl(bl.inv_r, 4 * i + g, kWave)};
+      const float top = max_over_groups(
+          logits<kAlibi>(x, &sc, row, t0, g, t0 < all_lo || t0 + kGroup > all_hi || have != 15u,
+                         (have >> g) & 1u));
+      if (__any(top > m + kLazy)) {
+        const float alpha = raise(top, &m, &l);
 #pragma unroll
         for (int d = 0; d < kT; ++d) o[d] *= alpha;
       }
+      const float off = weight_offset(m, sc);
+      float sum = 0.f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) weights4(x + 4 * q, sc.f, off, &sum, p + 4 * q);
+      l += sum * sc.inv_r;
       uint32_t ph[8], pl[8];   // the weights in two parts of 11 bits
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -505,8 +515,8 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
 }
 
 // ---- Many rows: the waves of a block share each group, a wave takes kCols * 16
-// rows. Keys are copied to LDS as they are, two groups ahead, into the next of
-// three buffers. Values are turned into fp16 once for the block (converted by
+// rows. Keys are copied to LDS as they are, into the next of three buffers.
+// Values are turned into fp16 once for the block (converted by
 // every wave for itself they were a third of its vector instructions): each wave
 // loads its share of a group one step ahead and stores it as operands, of which
 // LDS holds this group's and the next's.
@@ -591,8 +601,7 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
   const int i_first = min(w_first, rows - 1) / group, i_last = max(w_last, 0) / group;
   const int all_lo = visible_lo(t, sq.first + i_last);
   const int all_hi = visible_hi(t, sq, sq.first + i_first);
-  const int any_lo = visible_lo(t, sq.first + i_first);
-  const int any_hi = w_first < rows ? visible_hi(t, sq, sq.first + i_last) : 0;
+  const bool works = w_first < rows;
 
   int lin, lin_next = -1;
   float ka, va, ka_next = 0.f, va_next = 0.f, rescale, ref = 0.f;
@@ -647,6 +656,7 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
       stage_keys(gi_begin + 1, 1);
       load_values(1);
     }
+    if (gi_begin + 2 < gi_end) stage_keys(gi_begin + 2, 2);
   }
 
   Row row[kCols];
@@ -674,75 +684,148 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
     for (int d = 0; d < kT; ++d) o[c][d] = v4f32{0.f, 0.f, 0.f, 0.f};
   }
 
-  for (int gi0 = gi_begin; gi0 < gi_end; gi0 += 16) {
-    BlockList bl;
-    const uint64_t present = __ballot(lin >= 0);
-    if (list_factors(ka, va, &ref, &rescale, &bl)) {
+  BlockList bl;
+  uint64_t present = __ballot(lin >= 0);
+  list_factors(ka, va, &ref, &rescale, &bl);
+  v4i32 s[kCols][4];
+  float x[kCols][16], top[kCols];
+  Scale sc[kCols];
+  // group gi, the i-th of the list
+  auto maxima = [&](int gi, int i) __attribute__((always_inline)) {
+    const int t0 = gi * kGroup;
+    const Scale of = {__shfl(bl.ks, 4 * i + g, kWave), __shfl(bl.log_r, 4 * i + g, kWave),
+                      __shfl(bl.inv_r, 4 * i + g, kWave)};
+    const uint32_t have = (uint32_t)(present >> (4 * i)) & 15u;
+    const bool masked = t0 < all_lo || t0 + kGroup > all_hi || have != 15u;
 #pragma unroll
-      for (int c = 0; c < kCols; ++c)
-#pragma unroll
-        for (int d = 0; d < kT; ++d) o[c][d] *= rescale;
+    for (int c = 0; c < kCols; ++c) {
+      sc[c] = of;
+      top[c] = max_over_groups(
+          logits<kAlibi>(x[c], &sc[c], row[c], t0, g, masked, (have >> g) & 1u));
     }
-    if (gi0 + 16 < gi_end) list_blocks(a, b, h, gi0 + 16, 1, end, lane, &lin_next, &ka_next, &va_next);
-    const int count = min(16, gi_end - gi0);
-
-    auto step = [&](int gi, int i, auto masked) __attribute__((always_inline)) {
-      constexpr bool kMasked = decltype(masked)::value;
-      const int8_t* st_k = lds + gi % Cfg::kKeyBuffers * S::kGroupBytes;
-      const int8_t* st_v = lds_v + (gi & 1) * Cfg::kValueBytes + lane * 16;
-      const float ks = __shfl(bl.ks, 4 * i + g, kWave), log_r = __shfl(bl.log_r, 4 * i + g, kWave),
-                  inv_r = __shfl(bl.inv_r, 4 * i + g, kWave);
-      const bool here = !kMasked || ((present >> (4 * i + g)) & 1u);
-      v4i32 s[kCols][4];
-      {
-        v4i32 kf[kC][4];
-        read_keys<D>(st_k, n, g, kf);
-#pragma unroll
-        for (int c = 0; c < kCols; ++c) scores<D>(kf, qh[c], ql[c], s[c]);
-      }
-      uint32_t pw[kCols][8];
+  };
+  if (gi_begin < gi_end) {
+    if (gi_begin + 2 < gi_end) wait_loads<kAhead>(); else wait_loads<0>();
+    lds_only_barrier();
+    if (works) {
 #pragma unroll
       for (int c = 0; c < kCols; ++c) {
-        float p[16], alpha;
-        if (softmax_step<kAlibi, kMasked>(s[c], row[c], ks, log_r, inv_r, gi * kGroup, g, here,
-                                          &m[c], &l[c], &alpha, p)) {
+        scores<D>(lds + gi_begin % Cfg::kKeyBuffers * S::kGroupBytes, n, g, qh[c], ql[c], s[c]);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[c][e] = (float)s[c][e >> 2][e & 3];
+      }
+      maxima(gi_begin, 0);
+    }
+  }
+
+  // Step gi: the products of group gi + 1 beside the weights of group gi, then
+  // the values of group gi beside the conversion of those products: the matrix
+  // pipe works on one group while the vector pipe works on the other.
+  for (int gi = gi_begin; gi < gi_end; ++gi) {
+    const int i = (gi - gi_begin) & 15;
+    if (i == 0 && gi + 16 < gi_end)
+      list_blocks(a, b, h, gi + 16, 1, end, lane, &lin_next, &ka_next, &va_next);
+    if (gi + 2 < gi_end) wait_loads<kAhead>(); else wait_loads<0>();
+    // the keys of gi + 1 and the values of gi are in LDS; every wave is done
+    // with the keys of gi and the values of gi - 1
+    lds_only_barrier();
+    if (gi + 1 < gi_end) store_values(gi + 1);
+    if (gi + 3 < gi_end) stage_keys(gi + 3, i + 3);
+    if (gi + 2 < gi_end) load_values(i + 2);
+    if (works) {
+      bool grown = false;
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) grown = grown || top[c] > m[c] + kLazy;
+      if (__any(grown)) {
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) {
+          const float alpha = raise(top[c], &m[c], &l[c]);
 #pragma unroll
           for (int d = 0; d < kT; ++d) o[c][d] *= alpha;
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) pw[c][e] = f2h2(p[2 * e], p[2 * e + 1]);
       }
+      // (the keys past the last group are what the buffer holds)
+      const int8_t* st_k = lds + (gi + 1) % Cfg::kKeyBuffers * S::kGroupBytes;
+      const int8_t* st_v = lds_v + (gi & 1) * Cfg::kValueBytes + lane * 16;
+      uint32_t pw[kCols][8];
+      float off[kCols], sum[kCols];
 #pragma unroll
-      for (int d = 0; d < kT; ++d) {
-        const v8f16 v0 = __builtin_bit_cast(v8f16, *reinterpret_cast<const v4i32*>(st_v + d * 2048));
-        const v8f16 v1 =
-            __builtin_bit_cast(v8f16, *reinterpret_cast<const v4i32*>(st_v + d * 2048 + 1024));
+      for (int c = 0; c < kCols; ++c) {
+        off[c] = weight_offset(m[c], sc[c]);
+        sum[c] = 0.f;
+      }
+      v4i32 kf[2][kC];
+#pragma unroll
+      for (int cc = 0; cc < kC; ++cc) kf[0][cc] = read_keys<D>(st_k, n, g, cc, 0);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (q < 3)
+#pragma unroll
+          for (int cc = 0; cc < kC; ++cc) kf[(q + 1) & 1][cc] = read_keys<D>(st_k, n, g, cc, q + 1);
+        v4i32 part[kCols];
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) part[c] = v4i32{0, 0, 0, 0};
+#pragma unroll
+        for (int cc = 0; cc < kC; ++cc)
+#pragma unroll
+          for (int c = 0; c < kCols; ++c)
+            part[c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf[q & 1][cc], qh[c][cc], part[c], 0, 0, 0);
 #pragma unroll
         for (int c = 0; c < kCols; ++c) {
-          o[c][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, as_f16(pw[c]), o[c][d], 0, 0, 0);
-          o[c][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, as_f16(pw[c] + 4), o[c][d], 0, 0, 0);
+          float p[4];
+          weights4(x[c] + 4 * q, sc[c].f, off[c], &sum[c], p);
+          pw[c][2 * q] = f2h2(p[0], p[1]);
+          pw[c][2 * q + 1] = f2h2(p[2], p[3]);
         }
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) part[c] = part[c] << 7;
+#pragma unroll
+        for (int cc = 0; cc < kC; ++cc)
+#pragma unroll
+          for (int c = 0; c < kCols; ++c)
+            part[c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf[q & 1][cc], ql[c][cc], part[c], 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) s[c][q] = part[c];
+        __builtin_amdgcn_sched_barrier(0);
       }
-    };
-    for (int i = 0; i < count; ++i) {
-      const int gi = gi0 + i;
-      if (gi + 1 < gi_end) wait_loads<kAhead>(); else wait_loads<0>();
-      lds_only_barrier();   // the group is in LDS; every wave is done with the one before
-      if (gi + 1 < gi_end) store_values(gi + 1);
-      if (gi + 2 < gi_end) {
-        stage_keys(gi + 2, i + 2);
-        load_values(i + 2);
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) l[c] += sum[c] * sc[c].inv_r;
+      v4i32 vf[2][2];
+      auto read_v = [&](int d, v4i32* v) __attribute__((always_inline)) {
+        v[0] = *reinterpret_cast<const v4i32*>(st_v + d * 2048);
+        v[1] = *reinterpret_cast<const v4i32*>(st_v + d * 2048 + 1024);
+      };
+      read_v(0, vf[0]);
+#pragma unroll
+      for (int d = 0; d < kT; ++d) {
+        if (d + 1 < kT) read_v(d + 1, vf[(d + 1) & 1]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int c = 0; c < kCols; ++c)
+            o[c][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                __builtin_bit_cast(v8f16, vf[d & 1][j]), as_f16(pw[c] + 4 * j), o[c][d], 0, 0, 0);
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (e * kT / 16 == d)
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) x[c][e] = (float)s[c][e >> 2][e & 3];
+        __builtin_amdgcn_sched_barrier(0);
       }
-      const int t0 = gi * kGroup;
-      if (t0 >= any_hi || t0 + kGroup <= any_lo) continue;
-      if (t0 < all_lo || t0 + kGroup > all_hi || ((present >> (4 * i)) & 15u) != 15u)
-        step(gi, i, std::true_type{});
-      else
-        step(gi, i, std::false_type{});
     }
-    lin = lin_next;
-    ka = ka_next;
-    va = va_next;
+    if (i == 15) {   // the next list, if any
+      lin = lin_next;
+      ka = ka_next;
+      va = va_next;
+      present = __ballot(lin >= 0);
+      if (list_factors(ka, va, &ref, &rescale, &bl)) {
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+#pragma unroll
+          for (int d = 0; d < kT; ++d) o[c][d] *= rescale;
+      }
+    }
+    if (works && gi + 1 < gi_end) maxima(gi + 1, (i + 1) & 15);
   }
 
   const float unit = ref / 127.0f;
