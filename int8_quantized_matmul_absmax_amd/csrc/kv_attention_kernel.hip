@@ -530,7 +530,8 @@ struct TileCfg {
   static constexpr int kKeyBuffers = 3;
   static constexpr int kKeyLoads = 4 * Stage<D>::kLoads / kWaves;   // a wave's, of a group
   static constexpr int kValueTiles = (D / 16 + kWaves - 1) / kWaves;
-  static constexpr int kValueBytes = kGroup * D * 2;
+  // (room for every wave's tiles: those past D / 16 are copies nobody reads)
+  static constexpr int kValueBytes = kWaves * kValueTiles * 2048;
   static constexpr int kLds = kKeyBuffers * Stage<D>::kGroupBytes + 2 * kValueBytes;
 };
 
@@ -574,9 +575,9 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
   typedef Stage<D> S;
   typedef TileCfg<D> Cfg;
   constexpr int kC = (D + 63) / 64, kT = D / 16, kCols = Cfg::kCols;
-  // loads of a wave younger than the keys it waits for: the next group's keys,
-  // and its own values of that group (at least)
-  constexpr int kAhead = Cfg::kKeyLoads + kT / Cfg::kWaves;
+  // loads of a wave younger than the keys it waits for: the next group's keys
+  // and its own values of that group
+  constexpr int kAhead = Cfg::kKeyLoads + Cfg::kValueTiles;
   __shared__ __attribute__((aligned(1024))) int8_t lds[Cfg::kLds];
   int8_t* const lds_v = lds + Cfg::kKeyBuffers * S::kGroupBytes;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -608,7 +609,8 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
   const int gi_begin = begin / kGroup, gi_end = (end + kGroup - 1) / kGroup;
   list_blocks(a, b, h, gi_begin, 1, end, lane, &lin, &ka, &va);
   // What follows takes group gi as the i-th (up to 31st) of the current and
-  // the next list. Absent blocks are masked; block 0 is read in their place.
+  // the next list. Absent blocks are masked; block 0 is read in their place, and
+  // past the last group too (so that each step issues the same loads).
   auto stage_keys = [&](int gi, int i) __attribute__((always_inline)) {
     constexpr int kPer = Cfg::kWaves / 4;   // waves a block
     const int blk = wave / kPer;
@@ -631,32 +633,27 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
     const int8_t* p = a.v_codes + (int64_t)max(x, 0) * S::kBytes + n * 16;
 #pragma unroll
     for (int j = 0; j < Cfg::kValueTiles; ++j) {
-      const int d = wave + j * Cfg::kWaves;
-      if (kT % Cfg::kWaves == 0 || d < kT) vr[j] = *reinterpret_cast<const v4i32*>(p + d * kTile);
+      vr[j] = *reinterpret_cast<const v4i32*>(p + min(wave + j * Cfg::kWaves, kT - 1) * kTile);
     }
   };
+  auto store_value_tile = [&](int gi, int j) __attribute__((always_inline)) {
+    int8_t* dst = lds_v + (gi & 1) * Cfg::kValueBytes + (wave + j * Cfg::kWaves) * 2048 + lane * 16;
+    v8f16 v0, v1;
+    codes_to_f16(vr[j], &v0, &v1);
+    lds_store16(dst, v0);
+    lds_store16(dst + 1024, v1);
+  };
   auto store_values = [&](int gi) __attribute__((always_inline)) {
-    int8_t* dst = lds_v + (gi & 1) * Cfg::kValueBytes + lane * 16;
 #pragma unroll
-    for (int j = 0; j < Cfg::kValueTiles; ++j) {
-      const int d = wave + j * Cfg::kWaves;
-      if (kT % Cfg::kWaves == 0 || d < kT) {
-        v8f16 v0, v1;
-        codes_to_f16(vr[j], &v0, &v1);
-        lds_store16(dst + d * 2048, v0);
-        lds_store16(dst + d * 2048 + 1024, v1);
-      }
-    }
+    for (int j = 0; j < Cfg::kValueTiles; ++j) store_value_tile(gi, j);
   };
   if (gi_begin < gi_end) {
     load_values(0);
     stage_keys(gi_begin, 0);
     store_values(gi_begin);
-    if (gi_begin + 1 < gi_end) {
-      stage_keys(gi_begin + 1, 1);
-      load_values(1);
-    }
-    if (gi_begin + 2 < gi_end) stage_keys(gi_begin + 2, 2);
+    stage_keys(gi_begin + 1, 1);
+    load_values(1);
+    stage_keys(gi_begin + 2, 2);
   }
 
   Row row[kCols];
@@ -690,11 +687,14 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
   v4i32 s[kCols][4];
   float x[kCols][16], top[kCols];
   Scale sc[kCols];
-  // group gi, the i-th of the list
-  auto maxima = [&](int gi, int i) __attribute__((always_inline)) {
+  // factors of the list's i-th group
+  auto factors = [&](int i) __attribute__((always_inline)) {
+    return Scale{__shfl(bl.ks, 4 * i + g, kWave), __shfl(bl.log_r, 4 * i + g, kWave),
+                 __shfl(bl.inv_r, 4 * i + g, kWave)};
+  };
+  // maxima of group gi, the i-th of the list
+  auto maxima = [&](int gi, int i, const Scale& of) __attribute__((always_inline)) {
     const int t0 = gi * kGroup;
-    const Scale of = {__shfl(bl.ks, 4 * i + g, kWave), __shfl(bl.log_r, 4 * i + g, kWave),
-                      __shfl(bl.inv_r, 4 * i + g, kWave)};
     const uint32_t have = (uint32_t)(present >> (4 * i)) & 15u;
     const bool masked = t0 < all_lo || t0 + kGroup > all_hi || have != 15u;
 #pragma unroll
@@ -705,7 +705,7 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
     }
   };
   if (gi_begin < gi_end) {
-    if (gi_begin + 2 < gi_end) wait_loads<kAhead>(); else wait_loads<0>();
+    wait_loads<kAhead>();
     lds_only_barrier();
     if (works) {
 #pragma unroll
@@ -714,7 +714,7 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
 #pragma unroll
         for (int e = 0; e < 16; ++e) x[c][e] = (float)s[c][e >> 2][e & 3];
       }
-      maxima(gi_begin, 0);
+      maxima(gi_begin, 0, factors(0));
     }
   }
 
@@ -725,13 +725,12 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
     const int i = (gi - gi_begin) & 15;
     if (i == 0 && gi + 16 < gi_end)
       list_blocks(a, b, h, gi + 16, 1, end, lane, &lin_next, &ka_next, &va_next);
-    if (gi + 2 < gi_end) wait_loads<kAhead>(); else wait_loads<0>();
+    wait_loads<kAhead>();
     // the keys of gi + 1 and the values of gi are in LDS; every wave is done
     // with the keys of gi and the values of gi - 1
     lds_only_barrier();
-    if (gi + 1 < gi_end) store_values(gi + 1);
-    if (gi + 3 < gi_end) stage_keys(gi + 3, i + 3);
-    if (gi + 2 < gi_end) load_values(i + 2);
+    stage_keys(gi + 3, i + 3);
+    Scale next = {0.f, 0.f, 0.f};
     if (works) {
       bool grown = false;
 #pragma unroll
@@ -754,14 +753,23 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
         off[c] = weight_offset(m[c], sc[c]);
         sum[c] = 0.f;
       }
-      v4i32 kf[2][kC];
+      // LDS reads run kKeyAhead operands, then kValueAhead tiles, ahead
+      constexpr int kKeyAhead = 2, kValueAhead = 2;
+      v4i32 kf[4][kC], vf[kT][2];
+      auto read_k = [&](int q) __attribute__((always_inline)) {
 #pragma unroll
-      for (int cc = 0; cc < kC; ++cc) kf[0][cc] = read_keys<D>(st_k, n, g, cc, 0);
+        for (int cc = 0; cc < kC; ++cc) kf[q][cc] = read_keys<D>(st_k, n, g, cc, q);
+      };
+      auto read_v = [&](int d) __attribute__((always_inline)) {
+        vf[d][0] = *reinterpret_cast<const v4i32*>(st_v + d * 2048);
+        vf[d][1] = *reinterpret_cast<const v4i32*>(st_v + d * 2048 + 1024);
+      };
+#pragma unroll
+      for (int q = 0; q < kKeyAhead; ++q) read_k(q);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        if (q < 3)
-#pragma unroll
-          for (int cc = 0; cc < kC; ++cc) kf[(q + 1) & 1][cc] = read_keys<D>(st_k, n, g, cc, q + 1);
+        if (q + kKeyAhead < 4) read_k(q + kKeyAhead);
+        if (q + kValueAhead >= 4) read_v(q + kValueAhead - 4);
         v4i32 part[kCols];
 #pragma unroll
         for (int c = 0; c < kCols; ++c) part[c] = v4i32{0, 0, 0, 0};
@@ -769,7 +777,7 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
         for (int cc = 0; cc < kC; ++cc)
 #pragma unroll
           for (int c = 0; c < kCols; ++c)
-            part[c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf[q & 1][cc], qh[c][cc], part[c], 0, 0, 0);
+            part[c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf[q][cc], qh[c][cc], part[c], 0, 0, 0);
 #pragma unroll
         for (int c = 0; c < kCols; ++c) {
           float p[4];
@@ -783,36 +791,37 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
         for (int cc = 0; cc < kC; ++cc)
 #pragma unroll
           for (int c = 0; c < kCols; ++c)
-            part[c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf[q & 1][cc], ql[c][cc], part[c], 0, 0, 0);
+            part[c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf[q][cc], ql[c][cc], part[c], 0, 0, 0);
 #pragma unroll
         for (int c = 0; c < kCols; ++c) s[c][q] = part[c];
         __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
       for (int c = 0; c < kCols; ++c) l[c] += sum[c] * sc[c].inv_r;
-      v4i32 vf[2][2];
-      auto read_v = [&](int d, v4i32* v) __attribute__((always_inline)) {
-        v[0] = *reinterpret_cast<const v4i32*>(st_v + d * 2048);
-        v[1] = *reinterpret_cast<const v4i32*>(st_v + d * 2048 + 1024);
-      };
-      read_v(0, vf[0]);
+      next = factors((i + 1) & 15);
 #pragma unroll
       for (int d = 0; d < kT; ++d) {
-        if (d + 1 < kT) read_v(d + 1, vf[(d + 1) & 1]);
+        if (d + kValueAhead < kT) read_v(d + kValueAhead);
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int c = 0; c < kCols; ++c)
             o[c][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                __builtin_bit_cast(v8f16, vf[d & 1][j]), as_f16(pw[c] + 4 * j), o[c][d], 0, 0, 0);
+                __builtin_bit_cast(v8f16, vf[d][j]), as_f16(pw[c] + 4 * j), o[c][d], 0, 0, 0);
 #pragma unroll
         for (int e = 0; e < 16; ++e)
           if (e * kT / 16 == d)
 #pragma unroll
             for (int c = 0; c < kCols; ++c) x[c][e] = (float)s[c][e >> 2][e & 3];
+#pragma unroll
+        for (int j = 0; j < Cfg::kValueTiles; ++j)
+          if (d == j * (kT / Cfg::kValueTiles)) store_value_tile(gi + 1, j);
         __builtin_amdgcn_sched_barrier(0);
       }
+    } else {
+      store_values(gi + 1);
     }
+    load_values(i + 2);
     if (i == 15) {   // the next list, if any
       lin = lin_next;
       ka = ka_next;
@@ -824,9 +833,11 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
 #pragma unroll
           for (int d = 0; d < kT; ++d) o[c][d] *= rescale;
       }
+      next = factors(0);
     }
-    if (works && gi + 1 < gi_end) maxima(gi + 1, (i + 1) & 15);
+    if (works && gi + 1 < gi_end) maxima(gi + 1, (i + 1) & 15, next);
   }
+  wait_loads<0>();   // nothing may land in LDS after the block has ended
 
   const float unit = ref / 127.0f;
   const int64_t part_rows = (int64_t)a.total_tokens * t.q_heads;
