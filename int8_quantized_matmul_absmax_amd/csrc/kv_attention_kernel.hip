@@ -546,26 +546,26 @@ __device__ __forceinline__ void lds_store16(int8_t* p, v8f16 x) {
 
 // Block index -> item (sequence and key/value head) and what of it. With
 // `by_xcd` an item's blocks run on one of the 8 XCDs (blocks go to them in
-// turn), whose L2 then holds that item's cache.
+// turn), whose L2 then holds that item's cache. Items are taken four at a time
+// and in each four the last tiles first: causal rows see more tokens the later
+// they are, and what starts last should be short. (All items' last tiles
+// first would spread over more caches than the L2 holds; items one by one end
+// with long tiles on a few compute units.)
 struct Place {
   int item, tile, split;
 };
-__device__ __forceinline__ Place place_of(uint32_t index, int tiles, int splits, bool by_xcd) {
-  const uint32_t per = (uint32_t)tiles * splits;
-  uint32_t item, in;
-  if (by_xcd) {
-    const uint32_t slot = index / 8;
-    item = slot / per * 8 + index % 8;
-    in = slot % per;
-  } else {
-    item = index / per;
-    in = index % per;
-  }
+__device__ __forceinline__ Place place_of(uint32_t index, uint32_t items, uint32_t tiles,
+                                          uint32_t splits, bool by_xcd) {
+  constexpr uint32_t kTogether = 4;
+  const uint32_t lanes = by_xcd ? 8 : 1, own = by_xcd ? index % 8 : 0;
+  const uint32_t slot = index / lanes, per = tiles * splits;
+  const uint32_t count = (items + lanes - 1) / lanes;   // of an XCD, the last perhaps absent
+  const uint32_t first = slot / (kTogether * per) * kTogether, in = slot - first * per;
+  const uint32_t together = min(kTogether, count - first);
   Place p;
-  p.item = (int)item;
-  // the last tiles first: causal rows see more tokens the later they are
-  p.tile = tiles - 1 - (int)(in / splits);
-  p.split = (int)(in % splits);
+  p.item = (int)((first + in % together) * lanes + own);
+  p.tile = (int)(tiles - 1 - in / together / splits);
+  p.split = (int)(in / together % splits);
   return p;
 }
 
@@ -582,7 +582,7 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
   int8_t* const lds_v = lds + Cfg::kKeyBuffers * S::kGroupBytes;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
-  const Place at = place_of(blockIdx.x, tiles, splits, by_xcd);
+  const Place at = place_of(blockIdx.x, a.num_seqs * a.kv_heads, tiles, splits, by_xcd);
   if (at.item >= a.num_seqs * a.kv_heads) return;
   const int b = at.item / a.kv_heads, h = at.item % a.kv_heads;
   const KvSeq sq = kv_seq(a, b);
