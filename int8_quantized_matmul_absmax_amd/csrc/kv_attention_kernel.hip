@@ -82,28 +82,70 @@ __device__ __forceinline__ void codes_to_f16(const v4i32& w, v8f16* lo, v8f16* h
 }
 
 // The row's query as the B operand: lane (row, g) holds features 64 c + 16 g ..
-// + 15 of it, zero past D. Returns a / 16256.
+// + 15 of it, zero past D. In two parts, so that every load is on its way before
+// the first is waited for (with a wait for each, a row took ten microseconds).
 template <int D>
-__device__ __forceinline__ float load_query(const uint16_t* row, int pos, bool live,
+struct QueryLoads {
+  static constexpr int kC = (D + 63) / 64;
+  v4i32 own[kC][2], other[kC][2];           // features and, rotated, their partners
+  v4f32 cos[kC][2][2], sin[kC][2][2];
+};
+// Without branches: features that are not rotated load partners and factors that
+// are not used (the first ones', or with no rotation at all the row's bytes).
+template <int D>
+__device__ __forceinline__ void load_query(const uint16_t* row, int pos, const RotaryArgs& rot,
+                                           int g, QueryLoads<D>& in) {
+  const int half = rot.dim >> 1;
+  const float* cos = rot.cos ? rot.cos + (int64_t)pos * half : reinterpret_cast<const float*>(row);
+  const float* sin = rot.cos ? rot.sin + (int64_t)pos * half : reinterpret_cast<const float*>(row);
+#pragma unroll
+  for (int c = 0; c < QueryLoads<D>::kC; ++c)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int e0 = 64 * c + 16 * g + 8 * u, e = e0 < rot.dim ? e0 : 0;
+      const int partner = e < half ? e + half : e - half;
+      const int i0 = rot.interleaved ? e >> 1 : min(e, partner), i1 = i0 + (rot.interleaved ? 0 : 4);
+      in.own[c][u] = ld16v(row + min(e0, D - 8));
+      in.other[c][u] = ld16v(row + partner);
+      in.cos[c][u][0] = ld16f(cos + i0);
+      in.cos[c][u][1] = ld16f(cos + i1);
+      in.sin[c][u][0] = ld16f(sin + i0);
+      in.sin[c][u][1] = ld16f(sin + i1);
+    }
+}
+// Rotates and quantizes; returns a / 16256.
+template <int D>
+__device__ __forceinline__ float take_query(const QueryLoads<D>& in, bool live,
                                             const RotaryArgs& rot, int g, v4i32* hi, v4i32* lo) {
-  constexpr int kC = (D + 63) / 64;
+  constexpr int kC = QueryLoads<D>::kC;
+  const int half = rot.dim >> 1;
   float x[kC][16];
   uint32_t top = 0;
 #pragma unroll
-  for (int c = 0; c < kC; ++c) {
-    const int e0 = 64 * c + 16 * g;
+  for (int c = 0; c < kC; ++c)
 #pragma unroll
-    for (int e = 0; e < 16; ++e) x[c][e] = 0.f;
-    if (live && e0 < D) {
-      load8_rotated(row, e0, pos, rot, x[c]);
-      load8_rotated(row, e0 + 8, pos, rot, x[c] + 8);
-    }
+    for (int u = 0; u < 2; ++u) {
+      const int e0 = 64 * c + 16 * g + 8 * u;
+      float* y = x[c] + 8 * u;
+      unpack8(in.own[c][u], y);
+      float z[8];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const uint32_t m = __builtin_bit_cast(uint32_t, x[c][e]) & 0x7fffffffu;
-      top = top > m ? top : m;
+      for (int e = 0; e < 8; ++e) z[e] = y[e];
+      if (rot.interleaved) {
+        rotate_pairs(in.cos[c][u][0], in.sin[c][u][0], z);
+      } else {
+        float other[8];
+        unpack8(in.other[c][u], other);
+        rotate_half(in.cos[c][u][0], in.cos[c][u][1], in.sin[c][u][0], in.sin[c][u][1], other,
+                    e0 < half, z);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        y[e] = !live || e0 >= D ? 0.f : e0 < rot.dim ? z[e] : y[e];
+        const uint32_t m = __builtin_bit_cast(uint32_t, y[e]) & 0x7fffffffu;
+        top = top > m ? top : m;
+      }
     }
-  }
   uint32_t o = (uint32_t)__shfl_xor((int)top, 16, kWave);
   top = top > o ? top : o;
   o = (uint32_t)__shfl_xor((int)top, 32, kWave);
@@ -367,6 +409,9 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
   const int i_row = r / group, head = h * group + r % group;
   Row row;
   row.pos = sq.first + i_row;
+  QueryLoads<D> q_in;
+  load_query<D>(t.q + (int64_t)(sq.row0 + i_row) * t.q_ts + (int64_t)head * t.q_hs,
+                max(row.pos, 0), rot, g, q_in);
   v4i32 qh[kC], ql[kC];
   row.lo = visible_lo(t, row.pos);
   row.hi = live ? visible_hi(t, sq, row.pos) : 0;
@@ -454,10 +499,8 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
         load(i, a.k_codes, st_k + i * S::kGroupBytes);
         load(i, a.v_codes, st_v + i * S::kGroupBytes);
       }
-    if (gi0 == gi_first) {   // (the codes are on their way meanwhile)
-      const uint16_t* q = t.q + (int64_t)(sq.row0 + i_row) * t.q_ts + (int64_t)head * t.q_hs;
-      row.qf = load_query<D>(q, max(row.pos, 0), live && row.pos >= 0, rot, g, qh, ql) * t.scale_log2;
-    }
+    if (gi0 == gi_first)   // (the codes are on their way meanwhile)
+      row.qf = take_query<D>(q_in, live && row.pos >= 0, rot, g, qh, ql) * t.scale_log2;
     if (list_factors(k_absmax, v_absmax, &ref, &rescale, &bl)) {
 #pragma unroll
       for (int d = 0; d < kT; ++d) o[d] *= rescale;
@@ -544,34 +587,47 @@ __device__ __forceinline__ void lds_store16(int8_t* p, v8f16 x) {
   asm volatile("ds_write_b128 %0, %1" : : "v"(addr), "v"(d) : "memory");
 }
 
-// Block index -> item (sequence and key/value head) and what of it. With
-// `by_xcd` an item's blocks run on one of the 8 XCDs (blocks go to them in
-// turn), whose L2 then holds that item's cache. Items are taken four at a time
-// and in each four the last tiles first: causal rows see more tokens the later
-// they are, and what starts last should be short. (All items' last tiles
-// first would spread over more caches than the L2 holds; items one by one end
-// with long tiles on a few compute units.)
+// What a block does. Heads come first in the block index: blocks go to the 8
+// XCDs in turn, so with a multiple of 8 heads a head's blocks share one L2. A
+// head's blocks take the longest sequence first, of each the last tiles first
+// (causal rows see more tokens the later they are): what starts last should be
+// short. Blocks without work come last: among the others, they upset the turns
+// in which blocks go to compute units (a step of mixed prompt chunks took
+// twice as long). A wave's lanes hold a sequence each; beyond 64 sequences
+// they are taken in order, each with the most tiles and splits there can be.
 struct Place {
-  int item, tile, split;
+  int b, tile, split;   // b < 0: nothing to do
 };
-__device__ __forceinline__ Place place_of(uint32_t index, uint32_t items, uint32_t tiles,
-                                          uint32_t splits, bool by_xcd) {
-  constexpr uint32_t kTogether = 4;
-  const uint32_t lanes = by_xcd ? 8 : 1, own = by_xcd ? index % 8 : 0;
-  const uint32_t slot = index / lanes, per = tiles * splits;
-  const uint32_t count = (items + lanes - 1) / lanes;   // of an XCD, the last perhaps absent
-  const uint32_t first = slot / (kTogether * per) * kTogether, in = slot - first * per;
-  const uint32_t together = min(kTogether, count - first);
-  Place p;
-  p.item = (int)((first + in % together) * lanes + own);
-  p.tile = (int)(tiles - 1 - in / together / splits);
-  p.split = (int)(in / together % splits);
-  return p;
+__device__ __forceinline__ Place place_of(const KvArgs& a, const AttnArgs& t, int job, int group,
+                                          int tile_rows, int tiles, int splits, int chunk,
+                                          int lane) {
+  if (a.num_seqs > kWave)
+    return Place{job / (tiles * splits), tiles - 1 - job % (tiles * splits) / splits, job % splits};
+  int my_tiles = 0, my_splits = 0, len = -1;
+  if (lane < a.num_seqs) {
+    const KvSeq sq = kv_seq(a, lane);
+    len = sq.len;
+    my_tiles = (sq.n * group + tile_rows - 1) / tile_rows;
+    int seen = t.window > 0 ? min(len, t.window + sq.n) + kGroup : len;
+    my_splits = max((seen + chunk - 1) / chunk, 1);
+  }
+  const int jobs = my_tiles * my_splits;
+  int start = 0;
+  for (int k = 0; k < a.num_seqs; ++k) {
+    const int other = __builtin_amdgcn_readlane(len, k), n = __builtin_amdgcn_readlane(jobs, k);
+    start += other > len || (other == len && k < lane) ? n : 0;
+  }
+  const uint64_t mine = __ballot(job >= start && job < start + jobs);
+  if (!mine) return Place{-1, 0, 0};
+  const int b = __builtin_ctzll(mine);
+  const int in = job - __builtin_amdgcn_readlane(start, b);
+  const int s = __builtin_amdgcn_readlane(my_splits, b);
+  return Place{b, __builtin_amdgcn_readlane(my_tiles, b) - 1 - in / s, in % s};
 }
 
 template <int D, bool kAlibi>
 __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
-    KvArgs a, RotaryArgs rot, AttnArgs t, int group, int tiles, int splits, int chunk, int by_xcd) {
+    KvArgs a, RotaryArgs rot, AttnArgs t, int group, int tiles, int splits, int chunk) {
   typedef Stage<D> S;
   typedef TileCfg<D> Cfg;
   constexpr int kC = (D + 63) / 64, kT = D / 16, kCols = Cfg::kCols;
@@ -582,9 +638,11 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
   int8_t* const lds_v = lds + Cfg::kKeyBuffers * S::kGroupBytes;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
-  const Place at = place_of(blockIdx.x, a.num_seqs * a.kv_heads, tiles, splits, by_xcd);
-  if (at.item >= a.num_seqs * a.kv_heads) return;
-  const int b = at.item / a.kv_heads, h = at.item % a.kv_heads;
+  const int h = blockIdx.x % a.kv_heads;
+  const Place at = place_of(a, t, blockIdx.x / a.kv_heads, group, Cfg::kBlockRows, tiles, splits,
+                            chunk, lane);
+  const int b = at.b;
+  if (b < 0) return;
   const KvSeq sq = kv_seq(a, b);
   const int rows = sq.n * group;
   const int blk_first = at.tile * Cfg::kBlockRows;
@@ -603,6 +661,20 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
   const int all_lo = visible_lo(t, sq.first + i_last);
   const int all_hi = visible_hi(t, sq, sq.first + i_first);
   const bool works = w_first < rows;
+
+  Row row[kCols];
+  QueryLoads<D> q_in[kCols];
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) {
+    const int r = min(w_first + 16 * c + n, rows - 1);
+    const int i_row = r / group, head = h * group + r % group;
+    row[c].pos = sq.first + i_row;
+    load_query<D>(t.q + (int64_t)(sq.row0 + i_row) * t.q_ts + (int64_t)head * t.q_hs,
+                  max(row[c].pos, 0), rot, g, q_in[c]);
+    row[c].lo = visible_lo(t, row[c].pos);
+    row[c].hi = w_first + 16 * c + n < rows ? visible_hi(t, sq, row[c].pos) : 0;
+    row[c].slope = kAlibi ? t.slopes[head] * 1.44269504088896340736f : 0.f;
+  }
 
   int lin, lin_next = -1;
   float ka, va, ka_next = 0.f, va_next = 0.f, rescale, ref = 0.f;
@@ -656,21 +728,11 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
     stage_keys(gi_begin + 2, 2);
   }
 
-  Row row[kCols];
   v4i32 qh[kCols][kC], ql[kCols][kC];
 #pragma unroll
-  for (int c = 0; c < kCols; ++c) {
-    const int r = min(w_first + 16 * c + n, rows - 1);
-    const bool live = w_first + 16 * c + n < rows;
-    const int i_row = r / group, head = h * group + r % group;
-    row[c].pos = sq.first + i_row;
-    const uint16_t* q = t.q + (int64_t)(sq.row0 + i_row) * t.q_ts + (int64_t)head * t.q_hs;
-    row[c].qf = load_query<D>(q, max(row[c].pos, 0), live && row[c].pos >= 0, rot, g, qh[c], ql[c])
-                * t.scale_log2;
-    row[c].lo = visible_lo(t, row[c].pos);
-    row[c].hi = live ? visible_hi(t, sq, row[c].pos) : 0;
-    row[c].slope = kAlibi ? t.slopes[head] * 1.44269504088896340736f : 0.f;
-  }
+  for (int c = 0; c < kCols; ++c)
+    row[c].qf = take_query<D>(q_in[c], w_first + 16 * c + n < rows && row[c].pos >= 0, rot, g,
+                              qh[c], ql[c]) * t.scale_log2;
   v4f32 o[kCols][kT];
   float m[kCols], l[kCols];
 #pragma unroll
@@ -869,8 +931,53 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
   }
 }
 
-// One block a row: the splits' sums, weighed by their maxima. Threads take four
-// features each, the groups of threads that cover a row take the splits in
+// The splits' sums of a row, weighed by their maxima. Up to kFewSplits: one wave
+// a row.
+constexpr int kFewSplits = 16;
+template <int D>
+__global__ __launch_bounds__(kBlockThreads) void k_kv_attn_join_few(KvArgs a, AttnArgs t, int group,
+                                                                    int tile_rows, int splits,
+                                                                    int chunk) {
+  constexpr int kE = (D + 63) / 64;
+  const int lane = threadIdx.x & 63;
+  const int r = blockIdx.x * (kBlockThreads / kWave) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int h = blockIdx.y, b = blockIdx.z;
+  const KvSeq sq = kv_seq(a, b);
+  const int rows = sq.n * group;
+  if (r >= rows) return;
+  const int tile = r / tile_rows * tile_rows;
+  const Span span = row_span(t, sq, tile / group, (min(tile + tile_rows, rows) - 1) / group);
+  if (span.end - span.begin <= chunk) return;   // written by its only split
+  const int parts = (span.end - span.begin + chunk - 1) / chunk;
+  const int64_t part_rows = (int64_t)a.total_tokens * t.q_heads;
+  const int64_t row = (int64_t)(sq.row0 + r / group) * t.q_heads + h * group + r % group;
+  const float* ml = t.part + (int64_t)splits * part_rows * D + row * 2;
+  float m[kFewSplits], acc[kE], top = -INFINITY, total = 0.f;
+#pragma unroll
+  for (int p = 0; p < kFewSplits; ++p) {
+    m[p] = p < parts ? ml[p * part_rows * 2] : -INFINITY;
+    top = fmaxf(top, m[p]);
+  }
+  const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+  for (int e = 0; e < kE; ++e) acc[e] = 0.f;
+#pragma unroll
+  for (int p = 0; p < kFewSplits; ++p) {
+    if (p >= parts) continue;
+    const float w = __builtin_amdgcn_exp2f(m[p] - base);
+    total += ml[p * part_rows * 2 + 1] * w;
+    const float* src = t.part + (p * part_rows + row) * D + lane;
+#pragma unroll
+    for (int e = 0; e < kE; ++e)
+      if (e * kWave + lane < D) acc[e] += src[e * kWave] * w;
+  }
+#pragma unroll
+  for (int e = 0; e < kE; ++e)
+    if (e * kWave + lane < D)
+      t.out[row * D + e * kWave + lane] = f2h(total == 0.f ? 0.f : acc[e] / total);
+}
+
+// More splits: one block a row. Threads take four features each, the groups of threads that cover a row take the splits in
 // turn, and the groups' sums are added in a fixed order.
 constexpr int kMaxSplits = 1024;
 template <int D>
@@ -946,14 +1053,19 @@ __global__ __launch_bounds__(kBlockThreads) void k_kv_attn_join(KvArgs a, AttnAr
 
 struct Plan {
   bool shared;     // the kernel for many rows
-  int group, tile_rows, tiles, splits, chunk, by_xcd;
-  int64_t items;
+  int group, tile_rows, tiles, splits, chunk;
 };
 
-// Splits of the token axis: kResident blocks run at once (two a compute unit),
-// so one round of them when there is little else to run. The kernel for few
-// rows also splits beyond kMaxChunk, which evens out sequences of different
-// lengths.
+// Tiles of all sequences together, at most.
+int64_t most_tiles(const KvArgs& a, const Plan& p) {
+  return (int64_t)a.total_tokens * p.group / p.tile_rows + a.num_seqs;
+}
+
+// Splits of the token axis: kResident blocks run at once (two a compute unit).
+// For few rows, one round of them when there is little else to run, and chunks
+// of at most kMaxChunk, which evens out sequences of different lengths. For many
+// rows, no block longer than a fraction of a compute unit's whole share, the
+// smaller one when lengths may differ.
 Plan plan(const KvArgs& a, int q_heads) {
   constexpr int64_t kResident = 2 * 256, kMinChunk = 4 * kGroup, kMaxChunk = 2048;
   Plan p;
@@ -963,14 +1075,15 @@ Plan plan(const KvArgs& a, int q_heads) {
   p.tile_rows = !p.shared ? kRows : a.head_dim <= 128 ? TileCfg<128>::kBlockRows
                                                       : TileCfg<256>::kBlockRows;
   p.tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
-  p.items = (int64_t)a.kv_heads * a.num_seqs;
-  p.by_xcd = p.items % 8 == 0 || p.items >= 64;
-  const int64_t blocks = std::max<int64_t>(p.tiles * p.items, 1);
+  const int64_t blocks =
+      std::max<int64_t>(std::min<int64_t>((int64_t)p.tiles * a.num_seqs, most_tiles(a, p)) * a.kv_heads, 1);
   const int64_t len = (int64_t)a.len_cap + kGroup;   // a span starts at a whole group
   int64_t chunk = len;
-  if (!p.shared || blocks < kResident) {
-    chunk = std::max((int64_t)a.len_cap * blocks / kResident, kMinChunk);
-    if (!p.shared) chunk = std::min(chunk, kMaxChunk);
+  if (p.shared) {
+    const int64_t jobs = kResident * (a.num_seqs > 1 ? 8 : 4);
+    chunk = std::min(len, std::max((int64_t)a.len_cap * blocks / jobs, 2 * kMinChunk));
+  } else {
+    chunk = std::min(std::max((int64_t)a.len_cap * blocks / kResident, kMinChunk), kMaxChunk);
   }
   chunk = std::max(chunk, len / kMaxSplits + 1);
   chunk = (chunk + kGroup - 1) / kGroup * kGroup;
@@ -984,15 +1097,16 @@ template <int D>
 hipError_t launch_d(const KvArgs& a, const RotaryArgs& r, const AttnArgs& t, hipStream_t s) {
   const Plan p = plan(a, t.q_heads);
   if (p.shared) {
-    const int64_t items = p.by_xcd ? (p.items + 7) / 8 * 8 : p.items;
-    const int64_t blocks = items * p.tiles * p.splits;
+    int64_t jobs = (int64_t)p.tiles * a.num_seqs;
+    if (a.num_seqs <= kWave) jobs = std::min(jobs, most_tiles(a, p));
+    const int64_t blocks = jobs * p.splits * a.kv_heads;
     if (blocks > INT32_MAX) return hipErrorInvalidValue;
     if (t.slopes)
       k_kv_attn_tile<D, true><<<(uint32_t)blocks, TileCfg<D>::kThreads, 0, s>>>(
-          a, r, t, p.group, p.tiles, p.splits, p.chunk, p.by_xcd);
+          a, r, t, p.group, p.tiles, p.splits, p.chunk);
     else
       k_kv_attn_tile<D, false><<<(uint32_t)blocks, TileCfg<D>::kThreads, 0, s>>>(
-          a, r, t, p.group, p.tiles, p.splits, p.chunk, p.by_xcd);
+          a, r, t, p.group, p.tiles, p.splits, p.chunk);
   } else {
     const dim3 grid((uint32_t)p.splits, (uint32_t)(p.tiles * a.kv_heads), (uint32_t)a.num_seqs);
     if (t.slopes)
@@ -1004,8 +1118,13 @@ hipError_t launch_d(const KvArgs& a, const RotaryArgs& r, const AttnArgs& t, hip
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits <= 1) return e;
-  const dim3 join((uint32_t)(a.max_tokens * p.group), (uint32_t)a.kv_heads, (uint32_t)a.num_seqs);
-  k_kv_attn_join<D><<<join, kBlockThreads, 0, s>>>(a, t, p.group, p.tile_rows, p.splits, p.chunk);
+  const uint32_t rows = (uint32_t)(a.max_tokens * p.group);
+  if (p.splits <= kFewSplits)
+    k_kv_attn_join_few<D><<<dim3((rows + 3) / 4, (uint32_t)a.kv_heads, (uint32_t)a.num_seqs),
+                            kBlockThreads, 0, s>>>(a, t, p.group, p.tile_rows, p.splits, p.chunk);
+  else
+    k_kv_attn_join<D><<<dim3(rows, (uint32_t)a.kv_heads, (uint32_t)a.num_seqs), kBlockThreads, 0,
+                        s>>>(a, t, p.group, p.tile_rows, p.splits, p.chunk);
   return hipGetLastError();
 }
 

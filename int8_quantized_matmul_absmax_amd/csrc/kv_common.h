@@ -40,48 +40,58 @@ __device__ __forceinline__ int kv_block(const KvArgs& a, int b, int h, int blk) 
   return (page * a.kv_heads + h) * a.slots + (blk - (int)pg * a.slots);
 }
 
-__device__ __forceinline__ void unpack8(const uint4& t, float* x) {
+// 16 bytes as a vector type (the struct uint4 keeps values of branches in
+// memory, and loads of it without a type for alias analysis).
+__device__ __forceinline__ v4i32 ld16v(const void* p) { return *reinterpret_cast<const v4i32*>(p); }
+__device__ __forceinline__ v4f32 ld16f(const float* p) { return *reinterpret_cast<const v4f32*>(p); }
+
+__device__ __forceinline__ void unpack8(const v4i32& t, float* x) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = h2f(half_of(t, e));
+  for (int e = 0; e < 8; ++e) x[e] = h2f(((uint32_t)t[e >> 1] >> (16 * (e & 1))) & 0xffffu);
+}
+
+// The rotation of 8 features, one rounding an operation, in the order the
+// header states. rotate_pairs: four pairs of neighbours. rotate_half: x are
+// eight first (low) or second members of pairs, other their partners.
+__device__ __forceinline__ void rotate_pairs(const v4f32& c, const v4f32& s, float* x) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = x[2 * i], b = x[2 * i + 1];
+    x[2 * i] = a * c[i] - b * s[i];
+    x[2 * i + 1] = b * c[i] + a * s[i];
+  }
+}
+__device__ __forceinline__ void rotate_half(const v4f32& c0, const v4f32& c1, const v4f32& s0,
+                                            const v4f32& s1, const float* other, bool low,
+                                            float* x) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float own = x[i] * (i < 4 ? c0[i & 3] : c1[i & 3]);
+    const float far = other[i] * (i < 4 ? s0[i & 3] : s1[i & 3]);
+    x[i] = low ? own - far : own + far;
+  }
 }
 
 // Features e0 .. e0 + 7 of a head's row `p` in fp32, rotated for position pos
 // when they lie in the rotated part (r.cos set, e0 < r.dim). r.dim is a
 // multiple of 16, so a group of 8 lies on one side of r.dim / 2 and of r.dim.
-// One rounding an operation, in the order the header states.
 __device__ __forceinline__ void load8_rotated(const uint16_t* p, int e0, int pos,
                                               const RotaryArgs& r, float* x) {
-  unpack8(ld16(p + e0), x);
+  unpack8(ld16v(p + e0), x);
   if (!r.cos || e0 >= r.dim) return;
   const int half = r.dim >> 1;
-  const int64_t row = (int64_t)pos * half;
+  const float* cos = r.cos + (int64_t)pos * half;
+  const float* sin = r.sin + (int64_t)pos * half;
   if (r.interleaved) {
-    const float4 c = *reinterpret_cast<const float4*>(r.cos + row + (e0 >> 1));
-    const float4 s = *reinterpret_cast<const float4*>(r.sin + row + (e0 >> 1));
-    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a = x[2 * i], b = x[2 * i + 1];
-      x[2 * i] = a * cc[i] - b * ss[i];
-      x[2 * i + 1] = b * cc[i] + a * ss[i];
-    }
+    rotate_pairs(ld16f(cos + (e0 >> 1)), ld16f(sin + (e0 >> 1)), x);
     return;
   }
   const bool low = e0 < half;
   const int i0 = low ? e0 : e0 - half;
-  float y[8];
-  unpack8(ld16(p + (low ? e0 + half : e0 - half)), y);
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const float4 c = *reinterpret_cast<const float4*>(r.cos + row + i0 + 4 * u);
-    const float4 s = *reinterpret_cast<const float4*>(r.sin + row + i0 + 4 * u);
-    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float own = x[4 * u + i] * cc[i], other = y[4 * u + i] * ss[i];
-      x[4 * u + i] = low ? own - other : own + other;
-    }
-  }
+  float other[8];
+  unpack8(ld16v(p + (low ? e0 + half : i0)), other);
+  rotate_half(ld16f(cos + i0), ld16f(cos + i0 + 4), ld16f(sin + i0), ld16f(sin + i0 + 4), other,
+              low, x);
 }
 
 }  // namespace i8mm
