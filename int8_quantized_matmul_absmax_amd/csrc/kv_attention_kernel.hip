@@ -126,22 +126,28 @@ __device__ __forceinline__ float take_query(const QueryLoads<D>& in, bool live,
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int e0 = 64 * c + 16 * g + 8 * u;
-      float* y = x[c] + 8 * u;
-      unpack8(in.own[c][u], y);
-      float z[8];
+      // no branches here either: what is not rotated takes cos 1 and sin 0
+      const int keep = live && e0 < D ? -1 : 0;
+      const bool rotated = e0 < rot.dim;
+      v4f32 cs[2], sn[2];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] = y[e];
+      for (int w = 0; w < 2; ++w)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          cs[w][i] = rotated ? in.cos[c][u][w][i] : 1.f;
+          sn[w][i] = rotated ? in.sin[c][u][w][i] : 0.f;
+        }
+      float* y = x[c] + 8 * u;
+      unpack8(in.own[c][u] & keep, y);
       if (rot.interleaved) {
-        rotate_pairs(in.cos[c][u][0], in.sin[c][u][0], z);
+        rotate_pairs(cs[0], sn[0], y);
       } else {
         float other[8];
-        unpack8(in.other[c][u], other);
-        rotate_half(in.cos[c][u][0], in.cos[c][u][1], in.sin[c][u][0], in.sin[c][u][1], other,
-                    e0 < half, z);
+        unpack8(in.other[c][u] & keep, other);
+        rotate_half(cs[0], cs[1], sn[0], sn[1], other, e0 < half, y);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        y[e] = !live || e0 >= D ? 0.f : e0 < rot.dim ? z[e] : y[e];
         const uint32_t m = __builtin_bit_cast(uint32_t, y[e]) & 0x7fffffffu;
         top = top > m ? top : m;
       }
@@ -662,20 +668,6 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
   const int all_hi = visible_hi(t, sq, sq.first + i_first);
   const bool works = w_first < rows;
 
-  Row row[kCols];
-  QueryLoads<D> q_in[kCols];
-#pragma unroll
-  for (int c = 0; c < kCols; ++c) {
-    const int r = min(w_first + 16 * c + n, rows - 1);
-    const int i_row = r / group, head = h * group + r % group;
-    row[c].pos = sq.first + i_row;
-    load_query<D>(t.q + (int64_t)(sq.row0 + i_row) * t.q_ts + (int64_t)head * t.q_hs,
-                  max(row[c].pos, 0), rot, g, q_in[c]);
-    row[c].lo = visible_lo(t, row[c].pos);
-    row[c].hi = w_first + 16 * c + n < rows ? visible_hi(t, sq, row[c].pos) : 0;
-    row[c].slope = kAlibi ? t.slopes[head] * 1.44269504088896340736f : 0.f;
-  }
-
   int lin, lin_next = -1;
   float ka, va, ka_next = 0.f, va_next = 0.f, rescale, ref = 0.f;
   const int gi_begin = begin / kGroup, gi_end = (end + kGroup - 1) / kGroup;
@@ -722,10 +714,25 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
   if (gi_begin < gi_end) {
     load_values(0);
     stage_keys(gi_begin, 0);
-    store_values(gi_begin);
     stage_keys(gi_begin + 1, 1);
-    load_values(1);
     stage_keys(gi_begin + 2, 2);
+  }
+  Row row[kCols];
+  QueryLoads<D> q_in[kCols];
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) {
+    const int r = min(w_first + 16 * c + n, rows - 1);
+    const int i_row = r / group, head = h * group + r % group;
+    row[c].pos = sq.first + i_row;
+    load_query<D>(t.q + (int64_t)(sq.row0 + i_row) * t.q_ts + (int64_t)head * t.q_hs,
+                  max(row[c].pos, 0), rot, g, q_in[c]);
+    row[c].lo = visible_lo(t, row[c].pos);
+    row[c].hi = w_first + 16 * c + n < rows ? visible_hi(t, sq, row[c].pos) : 0;
+    row[c].slope = kAlibi ? t.slopes[head] * 1.44269504088896340736f : 0.f;
+  }
+  if (gi_begin < gi_end) {
+    store_values(gi_begin);
+    load_values(1);
   }
 
   v4i32 qh[kCols][kC], ql[kCols][kC];
