@@ -81,100 +81,124 @@ __device__ __forceinline__ void codes_to_f16(const v4i32& w, v8f16* lo, v8f16* h
   *hi = __builtin_bit_cast(v8f16, make_uint4(out[4], out[5], out[6], out[7]));
 }
 
-// The row's query as the B operand: lane (row, g) holds features 64 c + 16 g ..
-// + 15 of it, zero past D. In two parts, so that every load is on its way before
-// the first is waited for (with a wait for each, a row took ten microseconds).
+// LDS stores written as the instruction itself: before a plain store the
+// compiler waits for every copy into LDS in flight, which these never meet. A
+// wave's own reads come after them in order; for other waves, the barrier in
+// between waits for them.
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+typedef int32_t v2i32 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ void lds_store(int8_t* p, v4i32 x) {
+  asm volatile("ds_write_b128 %0, %1" : : "v"((uint32_t)(uintptr_t)(lds_ptr_t)p), "v"(x) : "memory");
+}
+__device__ __forceinline__ void lds_store(int8_t* p, v2i32 x) {
+  asm volatile("ds_write_b64 %0, %1" : : "v"((uint32_t)(uintptr_t)(lds_ptr_t)p), "v"(x) : "memory");
+}
+__device__ __forceinline__ void lds_store(float* p, float x) {
+  asm volatile("ds_write_b32 %0, %1" : : "v"((uint32_t)(uintptr_t)(lds_ptr_t)p), "v"(x) : "memory");
+}
+
+// Queries into LDS as the products take them: per row kC * 64 bytes of hi, then
+// as many of lo, zero past D, and q's factor a / 16256. Lanes lie along the rows,
+// eight features a lane, so that features and rotation factors are read in whole
+// lines (read as operands, 16 rows an instruction, they cost each block 15 us).
+// Loads and what is made of them are apart, so that every load is on its way
+// before the first is waited for; and without branches: features that are not
+// rotated load partners and factors that are not used (the first ones', or with
+// no rotation at all `some` memory's) and take cos 1, sin 0.
 template <int D>
-struct QueryLoads {
+struct QueryCfg {
   static constexpr int kC = (D + 63) / 64;
-  v4i32 own[kC][2], other[kC][2];           // features and, rotated, their partners
-  v4f32 cos[kC][2][2], sin[kC][2][2];
+  static constexpr int kLanes = 8 * kC;                 // of a row
+  static constexpr int kPassRows = kWave / kLanes;
+  static constexpr int kRowBytes = 2 * 64 * kC;
 };
-// Without branches: features that are not rotated load partners and factors that
-// are not used (the first ones', or with no rotation at all the row's bytes).
+struct QueryLoads {
+  v4i32 own, other;
+  v4f32 cos[2], sin[2];
+};
 template <int D>
 __device__ __forceinline__ void load_query(const uint16_t* row, int pos, const RotaryArgs& rot,
-                                           int g, QueryLoads<D>& in) {
+                                           const void* some, int lane, QueryLoads& in) {
   const int half = rot.dim >> 1;
-  const float* cos = rot.cos ? rot.cos + (int64_t)pos * half : reinterpret_cast<const float*>(row);
-  const float* sin = rot.cos ? rot.sin + (int64_t)pos * half : reinterpret_cast<const float*>(row);
-#pragma unroll
-  for (int c = 0; c < QueryLoads<D>::kC; ++c)
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int e0 = 64 * c + 16 * g + 8 * u, e = e0 < rot.dim ? e0 : 0;
-      const int partner = e < half ? e + half : e - half;
-      const int i0 = rot.interleaved ? e >> 1 : min(e, partner), i1 = i0 + (rot.interleaved ? 0 : 4);
-      in.own[c][u] = ld16v(row + min(e0, D - 8));
-      in.other[c][u] = ld16v(row + partner);
-      in.cos[c][u][0] = ld16f(cos + i0);
-      in.cos[c][u][1] = ld16f(cos + i1);
-      in.sin[c][u][0] = ld16f(sin + i0);
-      in.sin[c][u][1] = ld16f(sin + i1);
-    }
+  const float* none = static_cast<const float*>(some);
+  const float* cos = rot.cos ? rot.cos + (int64_t)pos * half : none;
+  const float* sin = rot.cos ? rot.sin + (int64_t)pos * half : none;
+  const int e0 = lane % QueryCfg<D>::kLanes * 8, e = e0 < rot.dim ? e0 : 0;
+  const int i0 = rot.interleaved ? e >> 1 : e < half ? e : e - half;
+  const int i1 = i0 + (rot.interleaved ? 0 : 4);
+  in.own = ld16v(row + min(e0, D - 8));
+  in.other = ld16v(row + (e < half ? e + half : e - half));
+  in.cos[0] = ld16f(cos + i0);
+  in.cos[1] = ld16f(cos + i1);
+  in.sin[0] = ld16f(sin + i0);
+  in.sin[1] = ld16f(sin + i1);
 }
-// Rotates and quantizes; returns a / 16256.
+// The row's part of a lane, to dst (the row's bytes) and factor.
 template <int D>
-__device__ __forceinline__ float take_query(const QueryLoads<D>& in, bool live,
-                                            const RotaryArgs& rot, int g, v4i32* hi, v4i32* lo) {
-  constexpr int kC = QueryLoads<D>::kC;
-  const int half = rot.dim >> 1;
-  float x[kC][16];
+__device__ __forceinline__ void take_query(const QueryLoads& in, bool live, const RotaryArgs& rot,
+                                           int lane, int8_t* dst, float* factor) {
+  typedef QueryCfg<D> Q;
+  const int half = rot.dim >> 1, e0 = lane % Q::kLanes * 8;
+  const int keep = live && e0 < D ? -1 : 0;
+  const bool rotated = e0 < rot.dim;
+  v4f32 cs[2], sn[2];
+#pragma unroll
+  for (int w = 0; w < 2; ++w)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      cs[w][i] = rotated ? in.cos[w][i] : 1.f;
+      sn[w][i] = rotated ? in.sin[w][i] : 0.f;
+    }
+  float x[8];
+  unpack8(in.own & keep, x);
+  if (rot.interleaved) {
+    rotate_pairs(cs[0], sn[0], x);
+  } else {
+    float other[8];
+    unpack8(in.other & keep, other);
+    rotate_half(cs[0], cs[1], sn[0], sn[1], other, e0 < half, x);
+  }
   uint32_t top = 0;
 #pragma unroll
-  for (int c = 0; c < kC; ++c)
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t m = __builtin_bit_cast(uint32_t, x[e]) & 0x7fffffffu;
+    top = top > m ? top : m;
+  }
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int e0 = 64 * c + 16 * g + 8 * u;
-      // no branches here either: what is not rotated takes cos 1 and sin 0
-      const int keep = live && e0 < D ? -1 : 0;
-      const bool rotated = e0 < rot.dim;
-      v4f32 cs[2], sn[2];
-#pragma unroll
-      for (int w = 0; w < 2; ++w)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          cs[w][i] = rotated ? in.cos[c][u][w][i] : 1.f;
-          sn[w][i] = rotated ? in.sin[c][u][w][i] : 0.f;
-        }
-      float* y = x[c] + 8 * u;
-      unpack8(in.own[c][u] & keep, y);
-      if (rot.interleaved) {
-        rotate_pairs(cs[0], sn[0], y);
-      } else {
-        float other[8];
-        unpack8(in.other[c][u] & keep, other);
-        rotate_half(cs[0], cs[1], sn[0], sn[1], other, e0 < half, y);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t m = __builtin_bit_cast(uint32_t, y[e]) & 0x7fffffffu;
-        top = top > m ? top : m;
-      }
-    }
-  uint32_t o = (uint32_t)__shfl_xor((int)top, 16, kWave);
-  top = top > o ? top : o;
-  o = (uint32_t)__shfl_xor((int)top, 32, kWave);
-  top = top > o ? top : o;
+  for (int d = 1; d < Q::kLanes; d <<= 1) {
+    const uint32_t o = (uint32_t)__shfl_xor((int)top, d, kWave);
+    top = top > o ? top : o;
+  }
   if (top <= 0x08000000u) top = 0;   // 2^-111: 16256 / a stays finite
   const float a = __builtin_bit_cast(float, top);
   const float s = top ? 16256.0f / a : 0.f;
+  v2i32 hi, lo;
 #pragma unroll
-  for (int c = 0; c < kC; ++c)
+  for (int w = 0; w < 2; ++w) {
+    uint32_t ph = 0, pl = 0;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      uint32_t ph = 0, pl = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int q = (int)rintf(x[c][4 * w + i] * s);
-        const int h = (q + 64) >> 7;
-        ph |= ((uint32_t)h & 0xffu) << (8 * i);
-        pl |= ((uint32_t)(q - (h << 7)) & 0xffu) << (8 * i);
-      }
-      hi[c][w] = (int)ph;
-      lo[c][w] = (int)pl;
+    for (int i = 0; i < 4; ++i) {
+      const int q = (int)rintf(x[4 * w + i] * s);
+      const int h = (q + 64) >> 7;
+      ph |= ((uint32_t)h & 0xffu) << (8 * i);
+      pl |= ((uint32_t)(q - (h << 7)) & 0xffu) << (8 * i);
     }
-  return a / 16256.0f;
+    hi[w] = (int)ph;
+    lo[w] = (int)pl;
+  }
+  lds_store(dst + e0, hi);
+  lds_store(dst + 64 * Q::kC + e0, lo);
+  if (e0 == 0) lds_store(factor, a / 16256.0f);
+}
+// A row's B operands: lane (row, g) holds features 64 c + 16 g .. + 15 of it.
+template <int D>
+__device__ __forceinline__ void read_query(const int8_t* row, int g, v4i32* hi, v4i32* lo) {
+  constexpr int kC = QueryCfg<D>::kC;
+#pragma unroll
+  for (int c = 0; c < kC; ++c) {
+    hi[c] = ld16v(row + 64 * c + 16 * g);
+    lo[c] = ld16v(row + 64 * kC + 64 * c + 16 * g);
+  }
 }
 
 // A wave's blocks: lane 4 i + j holds block j of its i-th group.
@@ -189,8 +213,6 @@ struct BlockList {
 // blocks a key operand touches lie in different banks. Staging is LDS-DMA, 1 KB
 // an instruction, with no registers in between; the waits count its
 // instructions, so each stage issues the same number of them.
-typedef __attribute__((address_space(3))) void* lds_ptr_t;
-
 template <int D>
 struct Stage {
   static constexpr int kBytes = kKvBlock * D;
@@ -390,8 +412,11 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
   constexpr int kAhead = (2 * kSlots - 1) * 4 * S::kLoads;   // loads younger than the awaited
   constexpr int kJoinBytes = (4 * kRows * kLd + 8 * kRows) * 4;
   constexpr int kStageBytes = 4 * 2 * kSlots * S::kGroupBytes;
+  typedef QueryCfg<D> Q;
   __shared__ __attribute__((aligned(1024)))
-  int8_t lds[kStageBytes > kJoinBytes ? kStageBytes : kJoinBytes];
+  int8_t lds[(kStageBytes > kJoinBytes ? kStageBytes : kJoinBytes) + kRows * (Q::kRowBytes + 4)];
+  int8_t* const lds_q = lds + (sizeof(lds) - kRows * (Q::kRowBytes + 4));
+  float* const s_qf = reinterpret_cast<float*>(lds_q + kRows * Q::kRowBytes);
   float(*s_o)[kRows][kLd] = reinterpret_cast<float(*)[kRows][kLd]>(lds);
   float(*s_m)[kRows] = reinterpret_cast<float(*)[kRows]>(lds + 4 * kRows * kLd * 4);
   float(*s_l)[kRows] = s_m + 4;
@@ -415,9 +440,16 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
   const int i_row = r / group, head = h * group + r % group;
   Row row;
   row.pos = sq.first + i_row;
-  QueryLoads<D> q_in;
-  load_query<D>(t.q + (int64_t)(sq.row0 + i_row) * t.q_ts + (int64_t)head * t.q_hs,
-                max(row.pos, 0), rot, g, q_in);
+  // the waves share the queries' preparation
+  constexpr int kPasses = (kRows + 4 * Q::kPassRows - 1) / (4 * Q::kPassRows);
+  QueryLoads q_in[kPasses];
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    const int rr = min(r_first + (4 * p + wave) * Q::kPassRows + lane / Q::kLanes, r_last);
+    load_query<D>(t.q + (int64_t)(sq.row0 + rr / group) * t.q_ts +
+                      (int64_t)(h * group + rr % group) * t.q_hs,
+                  max(sq.first + rr / group, 0), rot, t.q, lane, q_in[p]);
+  }
   v4i32 qh[kC], ql[kC];
   row.lo = visible_lo(t, row.pos);
   row.hi = live ? visible_hi(t, sq, row.pos) : 0;
@@ -433,19 +465,45 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
 
   const int gi_end = (end + kGroup - 1) / kGroup;
   const int gi_first = begin / kGroup + wave;
-  for (int gi0 = gi_first; gi0 < gi_end; gi0 += 64) {
-    BlockList bl;
-    float k_absmax, v_absmax, rescale;
+  int8_t* const st_k = lds + wave * (2 * kSlots * S::kGroupBytes);
+  int8_t* const st_v = st_k + kSlots * S::kGroupBytes;
+  BlockList bl;
+  float k_absmax, v_absmax, rescale;
+  // absent blocks are masked; block 0 is read in their place
+  auto load = [&](int i, const int8_t* codes, int8_t* dst) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      stage_block<D>(codes, max(__builtin_amdgcn_readlane(bl.lin, 4 * i + j), 0),
+                     dst + j * S::kPitch, lane);
+  };
+  // the list of 16 groups from gi0 on, and the first groups' copies
+  auto start = [&](int gi0) __attribute__((always_inline)) {
     list_blocks(a, b, h, gi0, 4, end, lane, &bl.lin, &k_absmax, &v_absmax);
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i)
+      if (gi0 + 4 * i < gi_end) {
+        load(i, a.k_codes, st_k + i * S::kGroupBytes);
+        load(i, a.v_codes, st_v + i * S::kGroupBytes);
+      }
+  };
+  if (gi_first < gi_end) start(gi_first);
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {   // (the codes are on their way meanwhile)
+    const int rr = (4 * p + wave) * Q::kPassRows + lane / Q::kLanes;
+    const bool sees = r_first + rr <= r_last && sq.first + (r_first + rr) / group >= 0;
+    if (rr < kRows) take_query<D>(q_in[p], sees, rot, lane, lds_q + rr * Q::kRowBytes, s_qf + rr);
+  }
+  lds_only_barrier();
+  read_query<D>(lds_q + n * Q::kRowBytes, g, qh, ql);
+  row.qf = s_qf[n] * t.scale_log2;
+
+  for (int gi0 = gi_first; gi0 < gi_end; gi0 += 64) {
+    if (gi0 != gi_first) {
+      wait_lds_reads();   // of the list before
+      start(gi0);
+    }
     const uint64_t present = __ballot(bl.lin >= 0);
     const int count = min(16, (gi_end - gi0 + 3) / 4);
-    // absent blocks are masked; block 0 is read in their place
-    auto load = [&](int i, const int8_t* codes, int8_t* dst) __attribute__((always_inline)) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        stage_block<D>(codes, max(__builtin_amdgcn_readlane(bl.lin, 4 * i + j), 0),
-                       dst + j * S::kPitch, lane);
-    };
     auto step = [&](int i, int8_t* ks, int8_t* vs) __attribute__((always_inline)) {
       const uint32_t have = (uint32_t)(present >> (4 * i)) & 15u;
       const int t0 = (gi0 + 4 * i) * kGroup;
@@ -496,17 +554,6 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
         load(i + kSlots, a.v_codes, vs);
       }
     };
-    int8_t* const st_k = lds + wave * (2 * kSlots * S::kGroupBytes);
-    int8_t* const st_v = st_k + kSlots * S::kGroupBytes;
-    wait_lds_reads();   // of an earlier list's last groups
-#pragma unroll
-    for (int i = 0; i < kSlots; ++i)
-      if (i < count) {
-        load(i, a.k_codes, st_k + i * S::kGroupBytes);
-        load(i, a.v_codes, st_v + i * S::kGroupBytes);
-      }
-    if (gi0 == gi_first)   // (the codes are on their way meanwhile)
-      row.qf = take_query<D>(q_in, live && row.pos >= 0, rot, g, qh, ql) * t.scale_log2;
     if (list_factors(k_absmax, v_absmax, &ref, &rescale, &bl)) {
 #pragma unroll
       for (int d = 0; d < kT; ++d) o[d] *= rescale;
@@ -581,17 +628,10 @@ struct TileCfg {
   static constexpr int kValueTiles = (D / 16 + kWaves - 1) / kWaves;
   // (room for every wave's tiles: those past D / 16 are copies nobody reads)
   static constexpr int kValueBytes = kWaves * kValueTiles * 2048;
-  static constexpr int kLds = kKeyBuffers * Stage<D>::kGroupBytes + 2 * kValueBytes;
+  // (the queries stand where values will)
+  static constexpr int kLds = kKeyBuffers * Stage<D>::kGroupBytes + 2 * kValueBytes + kBlockRows * 4;
+  static_assert(kBlockRows * QueryCfg<D>::kRowBytes <= 2 * kValueBytes, "room for the queries");
 };
-
-// A 16-byte LDS store. Written as the instruction itself: before a plain store
-// the compiler waits for every copy into LDS in flight, which it never meets.
-// The barrier before the bytes are read waits for it.
-__device__ __forceinline__ void lds_store16(int8_t* p, v8f16 x) {
-  const uint32_t addr = (uint32_t)(uintptr_t)(lds_ptr_t)p;
-  const v4i32 d = __builtin_bit_cast(v4i32, x);
-  asm volatile("ds_write_b128 %0, %1" : : "v"(addr), "v"(d) : "memory");
-}
 
 // What a block does. Heads come first in the block index: blocks go to the 8
 // XCDs in turn, so with a multiple of 8 heads a head's blocks share one L2. A
@@ -704,8 +744,8 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
     int8_t* dst = lds_v + (gi & 1) * Cfg::kValueBytes + (wave + j * Cfg::kWaves) * 2048 + lane * 16;
     v8f16 v0, v1;
     codes_to_f16(vr[j], &v0, &v1);
-    lds_store16(dst, v0);
-    lds_store16(dst + 1024, v1);
+    lds_store(dst, __builtin_bit_cast(v4i32, v0));
+    lds_store(dst + 1024, __builtin_bit_cast(v4i32, v1));
   };
   auto store_values = [&](int gi) __attribute__((always_inline)) {
 #pragma unroll
@@ -717,29 +757,41 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
     stage_keys(gi_begin + 1, 1);
     stage_keys(gi_begin + 2, 2);
   }
+  typedef QueryCfg<D> Q;
+  constexpr int kPasses = Cfg::kWaveRows / Q::kPassRows;
+  int8_t* const lds_q = lds_v + wave * (Cfg::kWaveRows * Q::kRowBytes);
+  float* const s_qf = reinterpret_cast<float*>(lds_v + 2 * Cfg::kValueBytes) + wave * Cfg::kWaveRows;
+  QueryLoads q_in[kPasses];
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    const int r = min(w_first + p * Q::kPassRows + lane / Q::kLanes, rows - 1), i_row = r / group;
+    load_query<D>(t.q + (int64_t)(sq.row0 + i_row) * t.q_ts +
+                      (int64_t)(h * group + r % group) * t.q_hs,
+                  max(sq.first + i_row, 0), rot, t.q, lane, q_in[p]);
+  }
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    const int rr = p * Q::kPassRows + lane / Q::kLanes, r = w_first + rr;
+    take_query<D>(q_in[p], r < rows && sq.first + r / group >= 0, rot, lane,
+                  lds_q + rr * Q::kRowBytes, s_qf + rr);
+  }
   Row row[kCols];
-  QueryLoads<D> q_in[kCols];
+  v4i32 qh[kCols][kC], ql[kCols][kC];
 #pragma unroll
   for (int c = 0; c < kCols; ++c) {
     const int r = min(w_first + 16 * c + n, rows - 1);
-    const int i_row = r / group, head = h * group + r % group;
-    row[c].pos = sq.first + i_row;
-    load_query<D>(t.q + (int64_t)(sq.row0 + i_row) * t.q_ts + (int64_t)head * t.q_hs,
-                  max(row[c].pos, 0), rot, g, q_in[c]);
+    read_query<D>(lds_q + (16 * c + n) * Q::kRowBytes, g, qh[c], ql[c]);
+    row[c].qf = s_qf[16 * c + n] * t.scale_log2;
+    row[c].pos = sq.first + r / group;
     row[c].lo = visible_lo(t, row[c].pos);
     row[c].hi = w_first + 16 * c + n < rows ? visible_hi(t, sq, row[c].pos) : 0;
-    row[c].slope = kAlibi ? t.slopes[head] * 1.44269504088896340736f : 0.f;
+    row[c].slope = kAlibi ? t.slopes[h * group + r % group] * 1.44269504088896340736f : 0.f;
   }
+  lds_only_barrier();   // every wave has its queries
   if (gi_begin < gi_end) {
     store_values(gi_begin);
     load_values(1);
   }
-
-  v4i32 qh[kCols][kC], ql[kCols][kC];
-#pragma unroll
-  for (int c = 0; c < kCols; ++c)
-    row[c].qf = take_query<D>(q_in[c], w_first + 16 * c + n < rows && row[c].pos >= 0, rot, g,
-                              qh[c], ql[c]) * t.scale_log2;
   v4f32 o[kCols][kT];
   float m[kCols], l[kCols];
 #pragma unroll
