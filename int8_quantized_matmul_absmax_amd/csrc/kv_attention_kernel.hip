@@ -133,12 +133,11 @@ __device__ __forceinline__ void load_query(const uint16_t* row, int pos, const R
   in.sin[0] = ld16f(sin + i0);
   in.sin[1] = ld16f(sin + i1);
 }
-// The row's part of a lane, to dst (the row's bytes) and factor.
+// A lane's rotated part of the row, and its absmax's bit pattern.
 template <int D>
-__device__ __forceinline__ void take_query(const QueryLoads& in, bool live, const RotaryArgs& rot,
-                                           int lane, int8_t* dst, float* factor) {
-  typedef QueryCfg<D> Q;
-  const int half = rot.dim >> 1, e0 = lane % Q::kLanes * 8;
+__device__ __forceinline__ uint32_t rotate_query(const QueryLoads& in, bool live,
+                                                 const RotaryArgs& rot, int lane, float (&x)[8]) {
+  const int half = rot.dim >> 1, e0 = lane % QueryCfg<D>::kLanes * 8;
   const int keep = live && e0 < D ? -1 : 0;
   const bool rotated = e0 < rot.dim;
   v4f32 cs[2], sn[2];
@@ -149,7 +148,6 @@ __device__ __forceinline__ void take_query(const QueryLoads& in, bool live, cons
       cs[w][i] = rotated ? in.cos[w][i] : 1.f;
       sn[w][i] = rotated ? in.sin[w][i] : 0.f;
     }
-  float x[8];
   unpack8(in.own & keep, x);
   if (rot.interleaved) {
     rotate_pairs(cs[0], sn[0], x);
@@ -164,31 +162,43 @@ __device__ __forceinline__ void take_query(const QueryLoads& in, bool live, cons
     const uint32_t m = __builtin_bit_cast(uint32_t, x[e]) & 0x7fffffffu;
     top = top > m ? top : m;
   }
-#pragma unroll
-  for (int d = 1; d < Q::kLanes; d <<= 1) {
-    const uint32_t o = (uint32_t)__shfl_xor((int)top, d, kWave);
-    top = top > o ? top : o;
-  }
+  return top;
+}
+// The lane's part given the row's absmax, to dst (the row's bytes) and factor.
+// fma(x, s, 1.5 * 2^23 + 64) leaves w = q + 64 in its low bits, q = rne(x s):
+// hi = w >> 7 and lo = (w & 127) - 64, seven bits made signed in their bytes.
+template <int D>
+__device__ __forceinline__ void store_query(const float (&x)[8], uint32_t top, int lane,
+                                            int8_t* dst, float* factor) {
+  const int e0 = lane % QueryCfg<D>::kLanes * 8;
   if (top <= 0x08000000u) top = 0;   // 2^-111: 16256 / a stays finite
   const float a = __builtin_bit_cast(float, top);
-  const float s = top ? 16256.0f / a : 0.f;
+  const float s = top ? 16256.0f * __builtin_amdgcn_rcpf(a) : 0.f;   // (within 2^-22 of 16256 / a)
   v2i32 hi, lo;
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
-    uint32_t ph = 0, pl = 0;
+    uint32_t b[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int q = (int)rintf(x[4 * w + i] * s);
-      const int h = (q + 64) >> 7;
-      ph |= ((uint32_t)h & 0xffu) << (8 * i);
-      pl |= ((uint32_t)(q - (h << 7)) & 0xffu) << (8 * i);
-    }
-    hi[w] = (int)ph;
-    lo[w] = (int)pl;
+    for (int i = 0; i < 4; ++i)
+      b[i] = __builtin_bit_cast(uint32_t, __builtin_fmaf(x[4 * w + i], s, 12582912.0f + 64.f));
+    const uint32_t t = (pack4(b[0], b[1], b[2], b[3]) & 0x7f7f7f7fu) ^ 0x40404040u;
+    lo[w] = (int)(t | ((t & 0x40404040u) << 1));
+    hi[w] = (int)pack4(b[0] >> 7, b[1] >> 7, b[2] >> 7, b[3] >> 7);
   }
   lds_store(dst + e0, hi);
-  lds_store(dst + 64 * Q::kC + e0, lo);
-  if (e0 == 0) lds_store(factor, a / 16256.0f);
+  lds_store(dst + 64 * QueryCfg<D>::kC + e0, lo);
+  if (e0 == 0) lds_store(factor, a * (1.0f / 16256.0f));
+}
+// kPasses rows of a lane together (their reductions overlap).
+template <int D, int kPasses>
+__device__ __forceinline__ void row_absmax(uint32_t (&top)[kPasses]) {
+#pragma unroll
+  for (int d = 1; d < QueryCfg<D>::kLanes; d <<= 1)
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      const uint32_t o = (uint32_t)__shfl_xor((int)top[p], d, kWave);
+      top[p] = top[p] > o ? top[p] : o;
+    }
 }
 // A row's B operands: lane (row, g) holds features 64 c + 16 g .. + 15 of it.
 template <int D>
@@ -487,11 +497,19 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
       }
   };
   if (gi_first < gi_end) start(gi_first);
+  // (the codes are on their way meanwhile)
+  float x_in[kPasses][8];
+  uint32_t x_top[kPasses];
 #pragma unroll
-  for (int p = 0; p < kPasses; ++p) {   // (the codes are on their way meanwhile)
+  for (int p = 0; p < kPasses; ++p) {
+    const int r = r_first + (4 * p + wave) * Q::kPassRows + lane / Q::kLanes;
+    x_top[p] = rotate_query<D>(q_in[p], r <= r_last && sq.first + r / group >= 0, rot, lane, x_in[p]);
+  }
+  row_absmax<D>(x_top);
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
     const int rr = (4 * p + wave) * Q::kPassRows + lane / Q::kLanes;
-    const bool sees = r_first + rr <= r_last && sq.first + (r_first + rr) / group >= 0;
-    if (rr < kRows) take_query<D>(q_in[p], sees, rot, lane, lds_q + rr * Q::kRowBytes, s_qf + rr);
+    if (rr < kRows) store_query<D>(x_in[p], x_top[p], lane, lds_q + rr * Q::kRowBytes, s_qf + rr);
   }
   lds_only_barrier();
   read_query<D>(lds_q + n * Q::kRowBytes, g, qh, ql);
@@ -762,18 +780,35 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
   int8_t* const lds_q = lds_v + wave * (Cfg::kWaveRows * Q::kRowBytes);
   float* const s_qf = reinterpret_cast<float*>(lds_v + 2 * Cfg::kValueBytes) + wave * Cfg::kWaveRows;
   QueryLoads q_in[kPasses];
+  // token and head of the lane's row, pass by pass without a division each
+  const int tok_last = (rows - 1) / group, j_last = rows - 1 - tok_last * group;
+  const int tok_step = Q::kPassRows / group, j_step = Q::kPassRows - tok_step * group;
+  int tok = (w_first + lane / Q::kLanes) / group, j = w_first + lane / Q::kLanes - tok * group;
+  uint32_t sees = 0;
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
-    const int r = min(w_first + p * Q::kPassRows + lane / Q::kLanes, rows - 1), i_row = r / group;
-    load_query<D>(t.q + (int64_t)(sq.row0 + i_row) * t.q_ts +
-                      (int64_t)(h * group + r % group) * t.q_hs,
-                  max(sq.first + i_row, 0), rot, t.q, lane, q_in[p]);
+    const bool live = w_first + p * Q::kPassRows + lane / Q::kLanes < rows;
+    const int tok_p = live ? tok : tok_last, j_p = live ? j : j_last, pos = sq.first + tok_p;
+    load_query<D>(t.q + (int64_t)(sq.row0 + tok_p) * t.q_ts + (int64_t)(h * group + j_p) * t.q_hs,
+                  max(pos, 0), rot, t.q, lane, q_in[p]);
+    sees |= (live && pos >= 0 ? 1u : 0u) << p;
+    tok += tok_step;
+    j += j_step;
+    if (j >= group) {
+      j -= group;
+      ++tok;
+    }
   }
+  float x_in[kPasses][8];
+  uint32_t x_top[kPasses];
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p)
+    x_top[p] = rotate_query<D>(q_in[p], (sees >> p) & 1u, rot, lane, x_in[p]);
+  row_absmax<D>(x_top);
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
-    const int rr = p * Q::kPassRows + lane / Q::kLanes, r = w_first + rr;
-    take_query<D>(q_in[p], r < rows && sq.first + r / group >= 0, rot, lane,
-                  lds_q + rr * Q::kRowBytes, s_qf + rr);
+    const int rr = p * Q::kPassRows + lane / Q::kLanes;
+    store_query<D>(x_in[p], x_top[p], lane, lds_q + rr * Q::kRowBytes, s_qf + rr);
   }
   Row row[kCols];
   v4i32 qh[kCols][kC], ql[kCols][kC];

@@ -22,11 +22,6 @@ __device__ __forceinline__ uint32_t abs_bits(float x) {
 __device__ __forceinline__ uint32_t code_bits(float y) {
   return __builtin_bit_cast(uint32_t, y + 12582912.0f);
 }
-__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  const uint32_t lo = __builtin_amdgcn_perm(b, a, 0x0c0c0400u);
-  const uint32_t hi = __builtin_amdgcn_perm(d, c, 0x0c0c0400u);
-  return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
-}
 __device__ __forceinline__ float byte_code(uint32_t w, int i) {
   return (float)(int8_t)(w >> (8 * i));
 }

@@ -45,6 +45,13 @@ __device__ __forceinline__ int kv_block(const KvArgs& a, int b, int h, int blk) 
 __device__ __forceinline__ v4i32 ld16v(const void* p) { return *reinterpret_cast<const v4i32*>(p); }
 __device__ __forceinline__ v4f32 ld16f(const float* p) { return *reinterpret_cast<const v4f32*>(p); }
 
+// The low bytes of four words.
+__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  const uint32_t lo = __builtin_amdgcn_perm(b, a, 0x0c0c0400u);
+  const uint32_t hi = __builtin_amdgcn_perm(d, c, 0x0c0c0400u);
+  return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+}
+
 __device__ __forceinline__ void unpack8(const v4i32& t, float* x) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] = h2f(((uint32_t)t[e >> 1] >> (16 * (e & 1))) & 0xffffu);
