@@ -5,6 +5,8 @@
 // token. Values: codes of a feature lie along the tokens, so a lane holds a
 // pair of features for all 16 tokens, and the transposition costs no exchange.
 
+#include <cstdlib>
+
 #include "kv_common.h"
 
 namespace i8mm {
@@ -48,42 +50,72 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t a_old, uint32_t a_new
   return r;
 }
 
-template <int D>
-__global__ __launch_bounds__(kBlockThreads) void k_kv_append(
-    const uint16_t* __restrict__ k, int64_t k_ts, int64_t k_hs, const uint16_t* __restrict__ v,
-    int64_t v_ts, int64_t v_hs, KvArgs a, RotaryArgs rot, int tasks) {
-  const int lane = threadIdx.x & 63;
-  const int task = blockIdx.x * (kBlockThreads / kWave) + (threadIdx.x >> 6);
-  const int b = blockIdx.y;
-  if (task >= tasks) return;
-  const bool values = task & 1;
-  const int h = (task >> 1) % a.kv_heads;
-  const KvSeq sq = kv_seq(a, b);
-  const int blk = max(sq.first, 0) / kKvBlock + (task >> 1) / a.kv_heads;
-  const int t0 = blk * kKvBlock;
-  if (sq.n <= 0 || t0 >= sq.len) return;
-  const int r0 = max(sq.first - t0, 0);             // rows [0, r0) are older tokens
-  const int r1 = min(kKvBlock, sq.len - t0);        // rows [r0, r1) are new
-  const int lin = kv_block(a, b, h, blk);
-  if (lin < 0) return;
-  const int64_t src0 = (int64_t)sq.row0 + t0 - sq.first;   // packed row of block row 0
+// One block of 16 tokens of `heads` heads from head h0 on. Rows [0, r0) of the
+// block are older tokens, [r0, r1) new ones, src0 the packed row of row 0 (which
+// need not exist), t0 its position.
+struct NewRows {
+  int b, blk, h0, heads, r0, r1, t0;
+  int64_t src0;
+};
 
-  if (!values) {
-    constexpr int kChunks = D / 8, kItems = kKvBlock * kChunks;
-    constexpr int kIter = (kItems + kWave - 1) / kWave;
+// Lanes hold 8 features of a token. The rotation's factors are the same for
+// every head and loaded once.
+template <int D>
+__device__ __forceinline__ void append_keys(const uint16_t* __restrict__ k, int64_t ts, int64_t hs,
+                                            const KvArgs& a, const RotaryArgs& rot,
+                                            const NewRows& w, int lane) {
+  constexpr int kChunks = D / 8, kItems = kKvBlock * kChunks;
+  constexpr int kIter = (kItems + kWave - 1) / kWave;
+  const int half = rot.dim >> 1;
+  v4f32 cos[kIter][2], sin[kIter][2];
+  if (rot.cos) {
+#pragma unroll
+    for (int it = 0; it < kIter; ++it) {
+      const int idx = it * kWave + lane, tok = min(max(idx / kChunks, w.r0), w.r1 - 1);
+      const int e0 = idx % kChunks * 8, e = e0 < rot.dim ? e0 : 0;
+      const int i0 = rot.interleaved ? e >> 1 : e < half ? e : e - half;
+      const int64_t at = (int64_t)(w.t0 + tok) * half + i0;
+      const int more = rot.interleaved ? 0 : 4;
+      cos[it][0] = ld16f(rot.cos + at);
+      cos[it][1] = ld16f(rot.cos + at + more);
+      sin[it][0] = ld16f(rot.sin + at);
+      sin[it][1] = ld16f(rot.sin + at + more);
+    }
+  }
+  for (int h = w.h0; h < w.h0 + w.heads; ++h) {
+    const uint16_t* src = k + (int64_t)h * hs;
+    v4i32 own[kIter], other[kIter];
+#pragma unroll
+    for (int it = 0; it < kIter; ++it) {
+      const int idx = it * kWave + lane, tok = min(max(idx / kChunks, w.r0), w.r1 - 1);
+      const int e0 = idx % kChunks * 8, e = e0 < rot.dim ? e0 : 0;
+      const uint16_t* row = src + (w.src0 + tok) * ts;
+      own[it] = ld16v(row + e0);
+      if (rot.cos && !rot.interleaved) other[it] = ld16v(row + (e < half ? e + half : e - half));
+    }
+    const int lin = kv_block(a, w.b, h, w.blk);
+    if (lin < 0) continue;
     int8_t* tile = a.k_codes + (int64_t)lin * (kKvBlock * D);
-    const uint32_t a_old = r0 > 0 ? abs_bits(a.k_absmax[lin]) : 0u;
+    const uint32_t a_old = w.r0 > 0 ? abs_bits(a.k_absmax[lin]) : 0u;
     float x[kIter][8];
     uint32_t top = 0;
 #pragma unroll
     for (int it = 0; it < kIter; ++it) {
       const int idx = it * kWave + lane, tok = idx / kChunks, e0 = idx % kChunks * 8;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[it][e] = 0.f;
-      if (tok >= r0 && tok < r1)
-        load8_rotated(k + (src0 + tok) * k_ts + h * k_hs, e0, t0 + tok, rot, x[it]);
+      unpack8(own[it], x[it]);
+      if (rot.cos && e0 < rot.dim) {
+        if (rot.interleaved) {
+          rotate_pairs(cos[it][0], sin[it][0], x[it]);
+        } else {
+          float far[8];
+          unpack8(other[it], far);
+          rotate_half(cos[it][0], cos[it][1], sin[it][0], sin[it][1], far, e0 < half, x[it]);
+        }
+      }
+      const bool live = tok >= w.r0 && tok < w.r1;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
+        x[it][e] = live ? x[it][e] : 0.f;
         const uint32_t m = abs_bits(x[it][e]);
         top = top > m ? top : m;
       }
@@ -94,10 +126,10 @@ __global__ __launch_bounds__(kBlockThreads) void k_kv_append(
       const int idx = it * kWave + lane, tok = idx / kChunks, e0 = idx % kChunks * 8;
       if (idx >= kItems) continue;
       uint2* dst = reinterpret_cast<uint2*>(tile + (e0 >> 4) * kTile + tok * 16 + (e0 & 15));
-      if (tok < r0) {
+      if (tok < w.r0) {
         if (!sc.grown) continue;
-        const uint2 w = *dst;
-        *dst = make_uint2(rescale4(w.x, sc.ratio), rescale4(w.y, sc.ratio));
+        const uint2 o = *dst;
+        *dst = make_uint2(rescale4(o.x, sc.ratio), rescale4(o.y, sc.ratio));
       } else {
         uint32_t c[8];
 #pragma unroll
@@ -106,65 +138,101 @@ __global__ __launch_bounds__(kBlockThreads) void k_kv_append(
       }
     }
     if (lane == 0) a.k_absmax[lin] = sc.a;
-    return;
   }
+}
 
+// A lane holds a pair of features for all 16 tokens.
+template <int D>
+__device__ __forceinline__ void append_values(const uint16_t* __restrict__ v, int64_t ts,
+                                              int64_t hs, const KvArgs& a, const NewRows& w,
+                                              int lane) {
   constexpr int kPairs = D / 2, kIter = (kPairs + kWave - 1) / kWave;
-  int8_t* tile = a.v_codes + (int64_t)lin * (kKvBlock * D);
-  const uint32_t a_old = r0 > 0 ? abs_bits(a.v_absmax[lin]) : 0u;
-  uint32_t x[kIter][kKvBlock];   // pairs of fp16
-  uint32_t top = 0;
+  for (int h = w.h0; h < w.h0 + w.heads; ++h) {
+    uint32_t x[kIter][kKvBlock];   // pairs of fp16
+    uint32_t top = 0;
 #pragma unroll
-  for (int it = 0; it < kIter; ++it) {
-    const int p = it * kWave + lane;
+    for (int it = 0; it < kIter; ++it) {
+      const int p = it * kWave + lane;
 #pragma unroll
-    for (int r = 0; r < kKvBlock; ++r) {
-      x[it][r] = 0;
-      if (r >= r0 && r < r1 && p < kPairs)
-        x[it][r] = *reinterpret_cast<const uint32_t*>(v + (src0 + r) * v_ts + h * v_hs + 2 * p);
-    }
-  }
-#pragma unroll
-  for (int it = 0; it < kIter; ++it)
-#pragma unroll
-    for (int r = 0; r < kKvBlock; ++r) {
-      const uint32_t lo = x[it][r] & 0x7fffu, hi = (x[it][r] >> 16) & 0x7fffu;
-      const uint32_t m = lo > hi ? lo : hi;   // fp16 patterns order as their magnitudes
-      top = top > m ? top : m;
-    }
-  const BlockScale sc = block_scale(a_old, abs_bits(h2f(wave_max_u32_dpp(top))));
-#pragma unroll
-  for (int it = 0; it < kIter; ++it) {
-    const int p = it * kWave + lane;
-    if (p >= kPairs) continue;
-    // the pair's two features are 32 consecutive bytes
-    uint4* dst = reinterpret_cast<uint4*>(tile + p * 32);
-#pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      uint32_t w[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t c[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          c[i] = code_bits(h2f((x[it][4 * q + i] >> (16 * f)) & 0xffffu) * sc.s);
-        w[q] = pack4(c[0], c[1], c[2], c[3]);
+      for (int r = 0; r < kKvBlock; ++r) {
+        x[it][r] = 0;
+        if (r >= w.r0 && r < w.r1 && p < kPairs)
+          x[it][r] = *reinterpret_cast<const uint32_t*>(v + (w.src0 + r) * ts + h * hs + 2 * p);
       }
-      if (r0 > 0) {
-        const uint4 o = dst[f];
-        const uint32_t old[4] = {o.x, o.y, o.z, o.w};
+    }
+    const int lin = kv_block(a, w.b, h, w.blk);
+    if (lin < 0) continue;
+    int8_t* tile = a.v_codes + (int64_t)lin * (kKvBlock * D);
+    const uint32_t a_old = w.r0 > 0 ? abs_bits(a.v_absmax[lin]) : 0u;
+#pragma unroll
+    for (int it = 0; it < kIter; ++it)
+#pragma unroll
+      for (int r = 0; r < kKvBlock; ++r) {
+        const uint32_t lo = x[it][r] & 0x7fffu, hi = (x[it][r] >> 16) & 0x7fffu;
+        const uint32_t m = lo > hi ? lo : hi;   // fp16 patterns order as their magnitudes
+        top = top > m ? top : m;
+      }
+    const BlockScale sc = block_scale(a_old, abs_bits(h2f(wave_max_u32_dpp(top))));
+#pragma unroll
+    for (int it = 0; it < kIter; ++it) {
+      const int p = it * kWave + lane;
+      if (p >= kPairs) continue;
+      // the pair's two features are 32 consecutive bytes
+      uint4* dst = reinterpret_cast<uint4*>(tile + p * 32);
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        uint32_t c4[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int rows = min(max(r0 - 4 * q, 0), 4);   // old rows among these four
-          const uint32_t keep = rows >= 4 ? 0xffffffffu : (1u << (8 * rows)) - 1u;
-          const uint32_t ow = sc.grown ? rescale4(old[q], sc.ratio) : old[q];
-          w[q] = (ow & keep) | (w[q] & ~keep);
+          uint32_t c[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            c[i] = code_bits(h2f((x[it][4 * q + i] >> (16 * f)) & 0xffffu) * sc.s);
+          c4[q] = pack4(c[0], c[1], c[2], c[3]);
         }
+        if (w.r0 > 0) {
+          const uint4 o = dst[f];
+          const uint32_t old[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int rows = min(max(w.r0 - 4 * q, 0), 4);   // old rows among these four
+            const uint32_t keep = rows >= 4 ? 0xffffffffu : (1u << (8 * rows)) - 1u;
+            const uint32_t ow = sc.grown ? rescale4(old[q], sc.ratio) : old[q];
+            c4[q] = (ow & keep) | (c4[q] & ~keep);
+          }
+        }
+        dst[f] = make_uint4(c4[0], c4[1], c4[2], c4[3]);
       }
-      dst[f] = make_uint4(w[0], w[1], w[2], w[3]);
     }
+    if (lane == 0) a.v_absmax[lin] = sc.a;
   }
-  if (lane == 0) a.v_absmax[lin] = sc.a;
+}
+
+// A wave takes a block's keys or values for `per_wave` heads.
+template <int D>
+__global__ __launch_bounds__(kBlockThreads) void k_kv_append(
+    const uint16_t* __restrict__ k, int64_t k_ts, int64_t k_hs, const uint16_t* __restrict__ v,
+    int64_t v_ts, int64_t v_hs, KvArgs a, RotaryArgs rot, int tasks, int per_wave) {
+  const int lane = threadIdx.x & 63;
+  const int task = blockIdx.x * (kBlockThreads / kWave) +
+                   __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (task >= tasks) return;
+  const int parts = (a.kv_heads + per_wave - 1) / per_wave, part = (task >> 1) % parts;
+  NewRows w;
+  w.b = blockIdx.y;
+  const KvSeq sq = kv_seq(a, w.b);
+  w.blk = max(sq.first, 0) / kKvBlock + (task >> 1) / parts;
+  w.t0 = w.blk * kKvBlock;
+  if (sq.n <= 0 || w.t0 >= sq.len) return;
+  w.h0 = part * per_wave;
+  w.heads = min(per_wave, a.kv_heads - w.h0);
+  w.r0 = max(sq.first - w.t0, 0);
+  w.r1 = min(kKvBlock, sq.len - w.t0);
+  w.src0 = (int64_t)sq.row0 + w.t0 - sq.first;
+  if (task & 1)
+    append_values<D>(v, v_ts, v_hs, a, w, lane);
+  else
+    append_keys<D>(k, k_ts, k_hs, a, rot, w, lane);
 }
 
 template <int D>
@@ -251,11 +319,14 @@ bool kv_head_dim_ok(int64_t D) { return D == 64 || D == 80 || D == 96 || D == 12
 hipError_t launch_kv_append(const uint16_t* k, int64_t k_ts, int64_t k_hs, const uint16_t* v,
                             int64_t v_ts, int64_t v_hs, const KvArgs& a, const RotaryArgs& r,
                             hipStream_t s) {
-  const int64_t tasks = max_blocks(a) * a.kv_heads * 2;
+  const int per_wave = getenv("KVP") ? atoi(getenv("KVP")) : 1;
+  const int64_t parts = (a.kv_heads + per_wave - 1) / per_wave;
+  const int64_t tasks = max_blocks(a) * parts * 2;
   if (tasks > INT32_MAX - 4) return hipErrorInvalidValue;
   const dim3 grid((uint32_t)((tasks + 3) / 4), (uint32_t)a.num_seqs);
-#define CALL(D) \
-  k_kv_append<D><<<grid, kBlockThreads, 0, s>>>(k, k_ts, k_hs, v, v_ts, v_hs, a, r, (int)tasks)
+#define CALL(D)                                                                                  \
+  k_kv_append<D><<<grid, kBlockThreads, 0, s>>>(k, k_ts, k_hs, v, v_ts, v_hs, a, r, (int)tasks, \
+                                                per_wave)
   I8MM_KV_DIMS(a.head_dim, CALL)
 #undef CALL
   return hipGetLastError();

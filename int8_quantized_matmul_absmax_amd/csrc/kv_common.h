@@ -79,26 +79,4 @@ __device__ __forceinline__ void rotate_half(const v4f32& c0, const v4f32& c1, co
   }
 }
 
-// Features e0 .. e0 + 7 of a head's row `p` in fp32, rotated for position pos
-// when they lie in the rotated part (r.cos set, e0 < r.dim). r.dim is a
-// multiple of 16, so a group of 8 lies on one side of r.dim / 2 and of r.dim.
-__device__ __forceinline__ void load8_rotated(const uint16_t* p, int e0, int pos,
-                                              const RotaryArgs& r, float* x) {
-  unpack8(ld16v(p + e0), x);
-  if (!r.cos || e0 >= r.dim) return;
-  const int half = r.dim >> 1;
-  const float* cos = r.cos + (int64_t)pos * half;
-  const float* sin = r.sin + (int64_t)pos * half;
-  if (r.interleaved) {
-    rotate_pairs(ld16f(cos + (e0 >> 1)), ld16f(sin + (e0 >> 1)), x);
-    return;
-  }
-  const bool low = e0 < half;
-  const int i0 = low ? e0 : e0 - half;
-  float other[8];
-  unpack8(ld16v(p + (low ? e0 + half : i0)), other);
-  rotate_half(ld16f(cos + i0), ld16f(cos + i0 + 4), ld16f(sin + i0), ld16f(sin + i0 + 4), other,
-              low, x);
-}
-
 }  // namespace i8mm

@@ -15,6 +15,7 @@ import ctypes
 import torch
 
 from . import _lib, ops
+from .linear import shared_workspace
 
 BLOCK = ops.KV_BLOCK
 HEAD_DIMS = (64, 80, 96, 128, 256)
@@ -83,13 +84,8 @@ class Int8KVCache:
                   alibi_slopes=None, out=None):
         """Attention of the batch's queries over the cached tokens. Its workspace
         is the current stream's shared one, as for the linear layers."""
-        need = ops.int8_kv_cache_attention_workspace_bytes(self, batch, q.shape[1])
-        ws = None
-        if need:
-            from .linear import shared_workspace
-            ws = shared_workspace(self.device, need)[:need]
         return ops.int8_kv_cache_attention(q, self, batch, rotary, scale, causal, window,
-                                           alibi_slopes, ws, out)
+                                           alibi_slopes, shared_workspace, out)
 
     def read(self, batch):
         """Keys and values of the batch's tokens in fp16."""
@@ -104,9 +100,9 @@ class KVBatch:
     cu_tokens  [num_seqs + 1] first row of each sequence's new tokens, the rows'
                total last; None: one new token a sequence
     total_tokens, max_tokens, max_len  the host's figures: rows of the packed
-               tensors, bounds on a sequence's new tokens and on its length
-               (default: what the page table has room for is not known here, so
-               max_len is required for a rotation or a tight launch)."""
+               tensors (default: num_seqs, without cu_tokens), and bounds on a
+               sequence's new tokens (default: total_tokens) and on its length
+               (default: what its row of the page table has room for)."""
 
     def __init__(self, page_table, seq_lens, cu_tokens=None, total_tokens=None, max_tokens=None,
                  max_len=None):

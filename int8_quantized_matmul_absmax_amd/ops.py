@@ -35,7 +35,8 @@ def _stream(device):
 
 
 def _raw_stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+    # (the handle alone: a Stream object costs 2 us a call)
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _need(t, name, dtype, ndim=None, shape=None, min_numel=None):
@@ -373,34 +374,39 @@ def int8_kv_cache_attention(q, cache, batch, rotary=None, scale=None, causal=Tru
                             alibi_slopes=None, workspace=None, out=None):
     """Attention of the queries q fp16 [total_tokens, q_heads, D] (rotated here
     when `rotary` is given) over the cached tokens -> fp16 [total_tokens,
-    q_heads, D]. scale defaults to 1 / sqrt(D)."""
+    q_heads, D]. scale defaults to 1 / sqrt(D). workspace: a uint8 tensor, or a
+    function of the device and a number of bytes that gives one; allocated here
+    when None."""
     lib = _lib.load_library()
     rot = _kv_args(cache, batch, rotary)
-    dev = cache.device
-    D = cache.head_dim
+    dev, D = cache.device, cache.head_dim
     qp, qts, qhs = _need_heads(q, "q", batch.total_tokens, None, D, dev)
     heads = q.shape[1]
+    slopes = None
     if alibi_slopes is not None:
         _need(alibi_slopes, "alibi_slopes", torch.float32, shape=(heads,))
         _on_gpu(q=q, alibi_slopes=alibi_slopes)
+        slopes = alibi_slopes.data_ptr()
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.float16, device=dev)
+        out = q.new_empty(q.shape)
     else:
         _need(out, "out", torch.float16, shape=q.shape)
         _on_gpu(q=q, out=out)
-    need = lib.int8_kv_cache_attention_workspace_bytes(cache.ref, batch.ref, heads)
-    if need and workspace is None:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
     wp, wn = None, 0
-    if workspace is not None:
+    if workspace is None or callable(workspace):
+        wn = lib.int8_kv_cache_attention_workspace_bytes(cache.ref, batch.ref, heads)
+        if wn:
+            workspace = workspace(dev, wn) if workspace else \
+                torch.empty((wn,), dtype=torch.uint8, device=dev)
+            wp = workspace.data_ptr()
+    else:
         _need(workspace, "workspace", torch.uint8, 1)
         _on_gpu(q=q, workspace=workspace)
         wp, wn = workspace.data_ptr(), workspace.numel()
     _lib.check(lib.int8_kv_cache_attention(
         qp, qts, qhs, heads, cache.ref, batch.ref, rot,
-        1.0 / math.sqrt(D) if scale is None else float(scale), 1 if causal else 0, int(window),
-        None if alibi_slopes is None else alibi_slopes.data_ptr(), out.data_ptr(), wp, wn,
-        _raw_stream(dev)))
+        1.0 / math.sqrt(D) if scale is None else scale, 1 if causal else 0, window, slopes,
+        out.data_ptr(), wp, wn, _raw_stream(dev)))
     return out
 
 
@@ -409,9 +415,8 @@ def int8_kv_cache_read(cache, batch):
     two fp16 tensors [total_tokens, kv_heads, D]."""
     lib = _lib.load_library()
     _kv_args(cache, batch, None)
-    kv = torch.empty((2, batch.total_tokens, cache.kv_heads, cache.head_dim),
-                     dtype=torch.float16, device=cache.device)
-    k, v = kv[0], kv[1]
+    k, v = torch.empty((2, batch.total_tokens, cache.kv_heads, cache.head_dim),
+                       dtype=torch.float16, device=cache.device).unbind(0)
     _lib.check(lib.int8_kv_cache_read(cache.ref, batch.ref, k.data_ptr(), v.data_ptr(),
                                       _raw_stream(cache.device)))
     return k, v
