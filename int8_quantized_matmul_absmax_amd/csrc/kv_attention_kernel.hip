@@ -310,15 +310,16 @@ struct Row {
   float slope;   // * log2(e)
 };
 
-// A lane's factors of a group: logits are x f, weights 2^(x f - m + log_r), and
-// the row sum takes them times inv_r.
+// A lane's factors of a group: weights are 2^(x f - m + log_r), and the row sum
+// takes them times inv_r.
 struct Scale {
   float f, log_r, inv_r;
 };
 
-// The logits' maximum over a lane's 16 tokens. With a bias x becomes the logit
-// itself; with `masked`, hidden tokens' x is -infinity, and a lane whose block
-// its row does not see at all drops the block's factors (they may be NaN).
+// The logits' maximum over a lane's 16 tokens. A position bias goes into x in
+// units of f, its part common to the 16 into log_r. With `masked`, hidden
+// tokens' x is -infinity, and a lane whose block its row does not see at all
+// drops the block's factors (they may be NaN).
 template <bool kAlibi>
 __device__ __forceinline__ float logits(float (&x)[16], Scale* sc, const Row& row, int t0, int g,
                                         bool masked, bool here) {
@@ -326,12 +327,13 @@ __device__ __forceinline__ float logits(float (&x)[16], Scale* sc, const Row& ro
   sc->f *= row.qf;
   sc->f = sc->f < kMinFactor ? kMinFactor : sc->f;   // (keeps a NaN)
   const int tok0 = t0 + 16 * g;
+  float base = 0.f;
   if (kAlibi) {
-    const float base = row.slope * (float)(tok0 - row.pos);
+    base = row.slope * (float)(tok0 - row.pos);
+    const float step = row.slope * __builtin_amdgcn_rcpf(sc->f);
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
-      x[e] = __builtin_fmaf(x[e], sc->f, __builtin_fmaf(row.slope, (float)e, base));
-    sc->f = 1.f;
+    for (int e = 1; e < 16; ++e) x[e] = __builtin_fmaf(step, (float)e, x[e]);
+    sc->log_r += base;
   }
   if (masked) {
     const int lo = row.lo - tok0, hi = row.hi - tok0;
@@ -340,13 +342,13 @@ __device__ __forceinline__ float logits(float (&x)[16], Scale* sc, const Row& ro
     for (int e = 0; e < 16; ++e) x[e] = some && e >= lo && e < hi ? x[e] : -INFINITY;
     if (!some) {
       sc->f = 1.f;
-      sc->log_r = sc->inv_r = 0.f;
+      sc->log_r = sc->inv_r = base = 0.f;
     }
   }
   float top = fmaxf(x[0], x[1]);
 #pragma unroll
   for (int e = 2; e < 16; e += 2) top = fmaxf(fmaxf(top, x[e]), x[e + 1]);
-  return top * sc->f;
+  return top * sc->f + base;
 }
 
 // Takes a row's new maximum (over the lanes that share it) into m and l; what
@@ -734,19 +736,16 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
   // the next list. Absent blocks are masked; block 0 is read in their place, and
   // past the last group too (so that each step issues the same loads).
   auto stage_keys = [&](int gi, int i) __attribute__((always_inline)) {
-    constexpr int kPer = Cfg::kWaves / 4;   // waves a block
-    const int blk = wave / kPer;
-    const int x = i < 16 ? __builtin_amdgcn_readlane(lin, (4 * i + blk) & 63)
-                         : __builtin_amdgcn_readlane(lin_next, (4 * i + blk) & 63);
-    const __amdgpu_buffer_rsrc_t rsrc =
-        buffer_rsrc(a.k_codes + (int64_t)max(x, 0) * S::kBytes, S::kBytes);
-    int8_t* dst = lds + gi % Cfg::kKeyBuffers * S::kGroupBytes + blk * S::kPitch;
 #pragma unroll
     for (int jj = 0; jj < Cfg::kKeyLoads; ++jj) {
-      const int j = wave % kPer * Cfg::kKeyLoads + jj;
+      const int blk = (wave * Cfg::kKeyLoads + jj) / S::kLoads, j = (wave * Cfg::kKeyLoads + jj) % S::kLoads;
+      const int x = i < 16 ? __builtin_amdgcn_readlane(lin, (4 * i + blk) & 63)
+                           : __builtin_amdgcn_readlane(lin_next, (4 * i + blk) & 63);
+      const __amdgpu_buffer_rsrc_t rsrc =
+          buffer_rsrc(a.k_codes + (int64_t)max(x, 0) * S::kBytes, S::kBytes);
+      int8_t* dst = lds + gi % Cfg::kKeyBuffers * S::kGroupBytes + blk * S::kPitch + j * 1024;
       if (S::kBytes % 1024 == 0 || j < S::kBytes / 1024 || lane < S::kBytes % 1024 / 16)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr_t)(dst + j * 1024), 16, lane * 16,
-                                                 j * 1024, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr_t)dst, 16, lane * 16, j * 1024, 0, 0);
     }
   };
   v4i32 vr[Cfg::kValueTiles];   // the wave's tiles of a group: wave, wave + kWaves, ..
