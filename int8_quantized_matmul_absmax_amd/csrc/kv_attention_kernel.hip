@@ -36,6 +36,24 @@ constexpr int kRows = 16;           // rows of a tile
 constexpr float kLazy = 8.f;        // a row is rescaled when its maximum grew by more
 constexpr float kMinRatio = 0x1p-40f;   // weights of such values vanish in fp16 anyway
 
+// The workspace of a launch with several splits: for each split and row the sum
+// O (not divided) and its maximum and row sum, and for each row the number of
+// splits that see some of it, written by the first.
+struct Parts {
+  float* o;        // [splits][rows][D]
+  float* ml;       // [splits][rows][2]
+  int32_t* count;  // [rows]
+  int64_t rows;
+};
+__host__ __device__ __forceinline__ Parts parts_of(float* ws, int64_t rows, int splits, int D) {
+  Parts p;
+  p.o = ws;
+  p.ml = ws + splits * rows * D;
+  p.count = reinterpret_cast<int32_t*>(p.ml + splits * rows * 2);
+  p.rows = rows;
+  return p;
+}
+
 // Visible tokens [lo, hi) of the query at position pos.
 __device__ __forceinline__ int visible_hi(const AttnArgs& t, const KvSeq& sq, int pos) {
   return pos < 0 ? 0 : t.causal ? min(pos + 1, sq.len) : sq.len;
@@ -596,7 +614,7 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
     s_l[wave][n] = l;
   }
   __syncthreads();
-  const int64_t part_rows = (int64_t)a.total_tokens * t.q_heads;
+  const Parts parts = parts_of(t.part, (int64_t)a.total_tokens * t.q_heads, splits, D);
   for (int x = threadIdx.x; x < kRows * (D / 4); x += kBlockThreads) {
     const int row = x / (D / 4), d4 = x % (D / 4) * 4;
     if (r_first + row > r_last) continue;
@@ -619,14 +637,15 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
       *reinterpret_cast<uint2*>(t.out + out_row * D + d4) =
           make_uint2(f2h2(acc[0] * inv, acc[1] * inv), f2h2(acc[2] * inv, acc[3] * inv));
     } else {
-      const int64_t part = split * part_rows + out_row;
-      *reinterpret_cast<v4f32*>(t.part + part * D + d4) = acc;
+      const int64_t part = split * parts.rows + out_row;
+      *reinterpret_cast<v4f32*>(parts.o + part * D + d4) = acc;
       if (d4 == 0) {
-        float* ml = t.part + (int64_t)splits * part_rows * D + part * 2;
-        ml[0] = top;
-        ml[1] = total;
+        parts.ml[part * 2] = top;
+        parts.ml[part * 2 + 1] = total;
       }
     }
+    if (splits > 1 && split == 0 && d4 == 0)
+      parts.count[out_row] = (span.end - span.begin + chunk - 1) / chunk;
   }
 }
 
@@ -995,7 +1014,7 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
   wait_loads<0>();   // nothing may land in LDS after the block has ended
 
   const float unit = ref / 127.0f;
-  const int64_t part_rows = (int64_t)a.total_tokens * t.q_heads;
+  const Parts parts = parts_of(t.part, (int64_t)a.total_tokens * t.q_heads, splits, D);
 #pragma unroll
   for (int c = 0; c < kCols; ++c) {
     l[c] += __shfl_xor(l[c], 16, kWave);
@@ -1011,97 +1030,79 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
         *reinterpret_cast<uint2*>(out + 16 * d) = make_uint2(
             f2h2(o[c][d][0] * inv, o[c][d][1] * inv), f2h2(o[c][d][2] * inv, o[c][d][3] * inv));
     } else {
-      const int64_t part = at.split * part_rows + out_row;
-      float* out = t.part + part * D + 4 * g;
+      const int64_t part = at.split * parts.rows + out_row;
+      float* out = parts.o + part * D + 4 * g;
 #pragma unroll
       for (int d = 0; d < kT; ++d) *reinterpret_cast<v4f32*>(out + 16 * d) = o[c][d] * unit;
       if (g == 0) {
-        float* ml = t.part + (int64_t)splits * part_rows * D + part * 2;
-        ml[0] = m[c];
-        ml[1] = l[c];
+        parts.ml[part * 2] = m[c];
+        parts.ml[part * 2 + 1] = l[c];
       }
     }
+    if (splits > 1 && at.split == 0 && g == 0)
+      parts.count[out_row] = (span.end - span.begin + chunk - 1) / chunk;
   }
 }
 
-// The splits' sums of a row, weighed by their maxima. Up to kFewSplits: one wave
-// a row.
+// The splits' sums of a row, weighed by their maxima, into the output of rows
+// with more than one. (Rows of the packed tensor that belong to no sequence have
+// no count: what they are given is unspecified, and bounded by `splits`.)
+// Up to kFewSplits: a lane takes four features, a wave several rows.
 constexpr int kFewSplits = 16;
 template <int D>
-__global__ __launch_bounds__(kBlockThreads) void k_kv_attn_join_few(KvArgs a, AttnArgs t, int group,
-                                                                    int tile_rows, int splits,
-                                                                    int chunk) {
-  constexpr int kE = (D + 63) / 64;
-  const int lane = threadIdx.x & 63;
-  const int r = blockIdx.x * (kBlockThreads / kWave) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int h = blockIdx.y, b = blockIdx.z;
-  const KvSeq sq = kv_seq(a, b);
-  const int rows = sq.n * group;
-  if (r >= rows) return;
-  const int tile = r / tile_rows * tile_rows;
-  const Span span = row_span(t, sq, tile / group, (min(tile + tile_rows, rows) - 1) / group);
-  if (span.end - span.begin <= chunk) return;   // written by its only split
-  const int parts = (span.end - span.begin + chunk - 1) / chunk;
-  const int64_t part_rows = (int64_t)a.total_tokens * t.q_heads;
-  const int64_t row = (int64_t)(sq.row0 + r / group) * t.q_heads + h * group + r % group;
-  const float* ml = t.part + (int64_t)splits * part_rows * D + row * 2;
-  float m[kFewSplits], acc[kE], top = -INFINITY, total = 0.f;
+__global__ __launch_bounds__(kBlockThreads) void k_kv_attn_join_few(float* ws, int64_t rows,
+                                                                    int splits, uint16_t* out) {
+  constexpr int kLanes = D / 4, kWaveRows = kWave / kLanes;
+  const int lane = threadIdx.x & 63, sub = lane / kLanes, d4 = lane % kLanes * 4;
+  const int64_t row =
+      ((int64_t)blockIdx.x * (kBlockThreads / kWave) + (threadIdx.x >> 6)) * kWaveRows + sub;
+  if (sub >= kWaveRows || row >= rows) return;
+  const Parts parts = parts_of(ws, rows, splits, D);
+  const int n = min(parts.count[row], splits);
+  if (n <= 1) return;
+  float m[kFewSplits], top = -INFINITY, total = 0.f;
 #pragma unroll
   for (int p = 0; p < kFewSplits; ++p) {
-    m[p] = p < parts ? ml[p * part_rows * 2] : -INFINITY;
+    m[p] = p < n ? parts.ml[(p * rows + row) * 2] : -INFINITY;
     top = fmaxf(top, m[p]);
   }
   const float base = top == -INFINITY ? 0.f : top;
-#pragma unroll
-  for (int e = 0; e < kE; ++e) acc[e] = 0.f;
+  v4f32 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int p = 0; p < kFewSplits; ++p) {
-    if (p >= parts) continue;
+    if (p >= n) continue;
     const float w = __builtin_amdgcn_exp2f(m[p] - base);
-    total += ml[p * part_rows * 2 + 1] * w;
-    const float* src = t.part + (p * part_rows + row) * D + lane;
-#pragma unroll
-    for (int e = 0; e < kE; ++e)
-      if (e * kWave + lane < D) acc[e] += src[e * kWave] * w;
+    total += parts.ml[(p * rows + row) * 2 + 1] * w;
+    acc += ld16f(parts.o + (p * rows + row) * D + d4) * w;
   }
-#pragma unroll
-  for (int e = 0; e < kE; ++e)
-    if (e * kWave + lane < D)
-      t.out[row * D + e * kWave + lane] = f2h(total == 0.f ? 0.f : acc[e] / total);
+  acc *= total == 0.f ? 0.f : 1.0f / total;
+  *reinterpret_cast<uint2*>(out + row * D + d4) = make_uint2(f2h2(acc[0], acc[1]), f2h2(acc[2], acc[3]));
 }
 
-// More splits: one block a row. Threads take four features each, the groups of threads that cover a row take the splits in
-// turn, and the groups' sums are added in a fixed order.
+// More splits: one block a row. Threads take four features each, the groups of
+// threads that cover a row take the splits in turn, and the groups' sums are
+// added in a fixed order.
 constexpr int kMaxSplits = 1024;
 template <int D>
-__global__ __launch_bounds__(kBlockThreads) void k_kv_attn_join(KvArgs a, AttnArgs t, int group,
-                                                                int tile_rows, int splits,
-                                                                int chunk) {
+__global__ __launch_bounds__(kBlockThreads) void k_kv_attn_join(float* ws, int64_t rows, int splits,
+                                                                uint16_t* out) {
   constexpr int kLanes = D / 4, kSets = kBlockThreads / kLanes;
   __shared__ float s_w[kMaxSplits];
   __shared__ __attribute__((aligned(16))) float s_sum[kSets][D];
   __shared__ float s_red[8];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int r = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
-  const KvSeq sq = kv_seq(a, b);
-  const int rows = sq.n * group;
-  if (r >= rows) return;
-  const int tile = r / tile_rows * tile_rows;
-  const Span span = row_span(t, sq, tile / group, (min(tile + tile_rows, rows) - 1) / group);
-  if (span.end - span.begin <= chunk) return;   // written by its only split
-  const int parts = (span.end - span.begin + chunk - 1) / chunk;
-  const int64_t part_rows = (int64_t)a.total_tokens * t.q_heads;
-  const int64_t row = (int64_t)(sq.row0 + r / group) * t.q_heads + h * group + r % group;
-  const float* ml = t.part + (int64_t)splits * part_rows * D + row * 2;
-
+  const int64_t row = blockIdx.x;
+  const Parts parts = parts_of(ws, rows, splits, D);
+  const int n = min(parts.count[row], splits);
+  if (n <= 1) return;
   float m[kMaxSplits / kBlockThreads], l[kMaxSplits / kBlockThreads], top = -INFINITY;
 #pragma unroll
   for (int i = 0; i < kMaxSplits / kBlockThreads; ++i) {
     const int p = i * kBlockThreads + tid;
     m[i] = -INFINITY;
     l[i] = 0.f;
-    if (p < parts) {
-      const float2 x = *reinterpret_cast<const float2*>(ml + p * part_rows * 2);
+    if (p < n) {
+      const float2 x = *reinterpret_cast<const float2*>(parts.ml + (p * rows + row) * 2);
       m[i] = x.x;
       l[i] = x.y;
     }
@@ -1119,7 +1120,7 @@ __global__ __launch_bounds__(kBlockThreads) void k_kv_attn_join(KvArgs a, AttnAr
     const int p = i * kBlockThreads + tid;
     const float w = __builtin_amdgcn_exp2f(m[i] - base);
     total += l[i] * w;
-    if (p < parts) s_w[p] = w;
+    if (p < n) s_w[p] = w;
   }
 #pragma unroll
   for (int x = 1; x < 64; x <<= 1) total += __shfl_xor(total, x, kWave);
@@ -1127,11 +1128,9 @@ __global__ __launch_bounds__(kBlockThreads) void k_kv_attn_join(KvArgs a, AttnAr
   __syncthreads();
   const int set = tid / kLanes, d4 = tid % kLanes * 4;
   if (set < kSets) {
-    const float* src = t.part + row * D + d4;
     v4f32 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-    for (int p = set; p < parts; p += kSets)
-      acc += *reinterpret_cast<const v4f32*>(src + p * part_rows * D) * s_w[p];
+    for (int p = set; p < n; p += kSets) acc += ld16f(parts.o + (p * rows + row) * D + d4) * s_w[p];
     *reinterpret_cast<v4f32*>(&s_sum[set][d4]) = acc;
   }
   __syncthreads();
@@ -1140,7 +1139,7 @@ __global__ __launch_bounds__(kBlockThreads) void k_kv_attn_join(KvArgs a, AttnAr
     float acc = 0.f;
 #pragma unroll
     for (int i = 0; i < kSets; ++i) acc += s_sum[i][tid];
-    t.out[row * D + tid] = f2h(total == 0.f ? 0.f : acc / total);
+    out[row * D + tid] = f2h(total == 0.f ? 0.f : acc / total);
   }
 }
 
@@ -1211,13 +1210,16 @@ hipError_t launch_d(const KvArgs& a, const RotaryArgs& r, const AttnArgs& t, hip
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits <= 1) return e;
-  const uint32_t rows = (uint32_t)(a.max_tokens * p.group);
-  if (p.splits <= kFewSplits)
-    k_kv_attn_join_few<D><<<dim3((rows + 3) / 4, (uint32_t)a.kv_heads, (uint32_t)a.num_seqs),
-                            kBlockThreads, 0, s>>>(a, t, p.group, p.tile_rows, p.splits, p.chunk);
-  else
-    k_kv_attn_join<D><<<dim3(rows, (uint32_t)a.kv_heads, (uint32_t)a.num_seqs), kBlockThreads, 0,
-                        s>>>(a, t, p.group, p.tile_rows, p.splits, p.chunk);
+  const int64_t rows = (int64_t)a.total_tokens * t.q_heads;
+  if (p.splits <= kFewSplits) {
+    constexpr int kBlockRows = kBlockThreads / kWave * (kWave / (D / 4));
+    if (rows > (int64_t)INT32_MAX * kBlockRows) return hipErrorInvalidValue;
+    k_kv_attn_join_few<D><<<(uint32_t)((rows + kBlockRows - 1) / kBlockRows), kBlockThreads, 0, s>>>(
+        t.part, rows, p.splits, t.out);
+  } else {
+    if (rows > INT32_MAX) return hipErrorInvalidValue;
+    k_kv_attn_join<D><<<(uint32_t)rows, kBlockThreads, 0, s>>>(t.part, rows, p.splits, t.out);
+  }
   return hipGetLastError();
 }
 
@@ -1226,7 +1228,7 @@ hipError_t launch_d(const KvArgs& a, const RotaryArgs& r, const AttnArgs& t, hip
 size_t attn_workspace_bytes(const KvArgs& a, int q_heads) {
   const Plan p = plan(a, q_heads);
   if (p.splits <= 1) return 0;
-  return (size_t)p.splits * a.total_tokens * q_heads * (a.head_dim + 2) * sizeof(float);
+  return (size_t)a.total_tokens * q_heads * (p.splits * ((int64_t)a.head_dim + 2) + 1) * sizeof(float);
 }
 
 hipError_t launch_kv_attention(const KvArgs& a, const RotaryArgs& r, const AttnArgs& t,
