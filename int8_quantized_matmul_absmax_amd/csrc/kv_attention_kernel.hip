@@ -22,7 +22,6 @@
 // maximum, 2^-25 absolute); all sums are fp32.
 
 #include <algorithm>
-#include <cstdlib>
 #include <type_traits>
 
 #include "kv_common.h"
@@ -72,14 +71,18 @@ __device__ __forceinline__ Span row_span(const AttnArgs& t, const KvSeq& sq, int
   return s;
 }
 
-// Maximum over the four lanes that share a row (lanes l ^ 32, l ^ 16).
+// Maximum over the lanes that share a row: l ^ 32, and with four also l ^ 16.
+template <int kLanes>
 __device__ __forceinline__ float max_over_groups(float v) {
   uint32_t u = __builtin_bit_cast(uint32_t, v);
   const auto p = __builtin_amdgcn_permlane32_swap(u, u, false, false);
   v = fmaxf(__builtin_bit_cast(float, (uint32_t)p[0]), __builtin_bit_cast(float, (uint32_t)p[1]));
-  u = __builtin_bit_cast(uint32_t, v);
-  const auto q = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-  return fmaxf(__builtin_bit_cast(float, (uint32_t)q[0]), __builtin_bit_cast(float, (uint32_t)q[1]));
+  if constexpr (kLanes == 4) {
+    u = __builtin_bit_cast(uint32_t, v);
+    const auto q = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    v = fmaxf(__builtin_bit_cast(float, (uint32_t)q[0]), __builtin_bit_cast(float, (uint32_t)q[1]));
+  }
+  return v;
 }
 
 // 16 codes as fp16: 0x6400 | (code + 128) is 1152 + code.
@@ -117,67 +120,82 @@ __device__ __forceinline__ void lds_store(float* p, float x) {
 
 // Queries into LDS as the products take them: per row kC * 64 bytes of hi, then
 // as many of lo, zero past D, and q's factor a / 16256. Lanes lie along the rows,
-// eight features a lane, so that features and rotation factors are read in whole
-// lines (read as operands, 16 rows an instruction, they cost each block 15 us).
+// so that features and rotation factors are read in whole lines (read as
+// operands, 16 rows an instruction, they cost each block 15 us), and a lane has
+// twice eight features: of the rotated ones eight and their partners (or, for
+// pairs of neighbours, eight of each half), of the rest sixteen in a row.
 // Loads and what is made of them are apart, so that every load is on its way
 // before the first is waited for; and without branches: features that are not
-// rotated load partners and factors that are not used (the first ones', or with
-// no rotation at all `some` memory's) and take cos 1, sin 0.
+// rotated load factors that are not used (the first ones', or with no rotation at
+// all `some` memory's) and take cos 1, sin 0.
 template <int D>
 struct QueryCfg {
   static constexpr int kC = (D + 63) / 64;
-  static constexpr int kLanes = 8 * kC;                 // of a row
+  static constexpr int kLanes = 4 * kC;                 // of a row
   static constexpr int kPassRows = kWave / kLanes;
   static constexpr int kRowBytes = 2 * 64 * kC;
 };
 struct QueryLoads {
-  v4i32 own, other;
+  v4i32 x[2];
   v4f32 cos[2], sin[2];
 };
+// Where a lane's two runs of eight features lie; whether they are rotated.
+template <int D>
+__device__ __forceinline__ bool query_features(const RotaryArgs& rot, int lane, int (&e)[2]) {
+  const int u = lane % QueryCfg<D>::kLanes;
+  const bool rotated = 16 * u < rot.dim;
+  e[0] = rotated ? 8 * u : 16 * u;
+  e[1] = e[0] + (rotated ? rot.dim >> 1 : 8);
+  return rotated;
+}
 template <int D>
 __device__ __forceinline__ void load_query(const uint16_t* row, int pos, const RotaryArgs& rot,
                                            const void* some, int lane, QueryLoads& in) {
-  const int half = rot.dim >> 1;
-  const float* none = static_cast<const float*>(some);
-  const float* cos = rot.cos ? rot.cos + (int64_t)pos * half : none;
-  const float* sin = rot.cos ? rot.sin + (int64_t)pos * half : none;
-  const int e0 = lane % QueryCfg<D>::kLanes * 8, e = e0 < rot.dim ? e0 : 0;
-  const int i0 = rot.interleaved ? e >> 1 : e < half ? e : e - half;
-  const int i1 = i0 + (rot.interleaved ? 0 : 4);
-  in.own = ld16v(row + min(e0, D - 8));
-  in.other = ld16v(row + (e < half ? e + half : e - half));
-  in.cos[0] = ld16f(cos + i0);
-  in.cos[1] = ld16f(cos + i1);
-  in.sin[0] = ld16f(sin + i0);
-  in.sin[1] = ld16f(sin + i1);
+  int e[2];
+  const bool rotated = query_features<D>(rot, lane, e);
+  const int64_t at = rot.cos ? (int64_t)pos * (rot.dim >> 1) : 0;
+  const float* cos = (rot.cos ? rot.cos : static_cast<const float*>(some)) + at;
+  const float* sin = (rot.cos ? rot.sin : static_cast<const float*>(some)) + at;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const int i = !rotated ? 0 : rot.interleaved ? e[w] >> 1 : e[0] + 4 * w;
+    in.x[w] = ld16v(row + min(e[w], D - 8));
+    in.cos[w] = ld16f(cos + i);
+    in.sin[w] = ld16f(sin + i);
+  }
 }
 // A lane's rotated part of the row, and its absmax's bit pattern.
 template <int D>
 __device__ __forceinline__ uint32_t rotate_query(const QueryLoads& in, bool live,
-                                                 const RotaryArgs& rot, int lane, float (&x)[8]) {
-  const int half = rot.dim >> 1, e0 = lane % QueryCfg<D>::kLanes * 8;
-  const int keep = live && e0 < D ? -1 : 0;
-  const bool rotated = e0 < rot.dim;
+                                                 const RotaryArgs& rot, int lane, float (&x)[16]) {
+  int e[2];
+  const bool rotated = query_features<D>(rot, lane, e);
+  const int keep = live && e[0] < D ? -1 : 0;
   v4f32 cs[2], sn[2];
 #pragma unroll
-  for (int w = 0; w < 2; ++w)
+  for (int w = 0; w < 2; ++w) {
+    unpack8(in.x[w] & keep, x + 8 * w);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       cs[w][i] = rotated ? in.cos[w][i] : 1.f;
       sn[w][i] = rotated ? in.sin[w][i] : 0.f;
     }
-  unpack8(in.own & keep, x);
+  }
   if (rot.interleaved) {
     rotate_pairs(cs[0], sn[0], x);
+    rotate_pairs(cs[1], sn[1], x + 8);
   } else {
-    float other[8];
-    unpack8(in.other & keep, other);
-    rotate_half(cs[0], cs[1], sn[0], sn[1], other, e0 < half, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float c = cs[i >> 2][i & 3], s = sn[i >> 2][i & 3], lo = x[i], hi = x[8 + i];
+      x[i] = lo * c - hi * s;
+      x[8 + i] = hi * c + lo * s;
+    }
   }
   uint32_t top = 0;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t m = __builtin_bit_cast(uint32_t, x[e]) & 0x7fffffffu;
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t m = __builtin_bit_cast(uint32_t, x[i]) & 0x7fffffffu;
     top = top > m ? top : m;
   }
   return top;
@@ -186,26 +204,32 @@ __device__ __forceinline__ uint32_t rotate_query(const QueryLoads& in, bool live
 // fma(x, s, 1.5 * 2^23 + 64) leaves w = q + 64 in its low bits, q = rne(x s):
 // hi = w >> 7 and lo = (w & 127) - 64, seven bits made signed in their bytes.
 template <int D>
-__device__ __forceinline__ void store_query(const float (&x)[8], uint32_t top, int lane,
-                                            int8_t* dst, float* factor) {
-  const int e0 = lane % QueryCfg<D>::kLanes * 8;
+__device__ __forceinline__ void store_query(const float (&x)[16], uint32_t top,
+                                            const RotaryArgs& rot, int lane, int8_t* dst,
+                                            float* factor) {
+  int e[2];
+  query_features<D>(rot, lane, e);
   if (top <= 0x08000000u) top = 0;   // 2^-111: 16256 / a stays finite
   const float a = __builtin_bit_cast(float, top);
   const float s = top ? 16256.0f * __builtin_amdgcn_rcpf(a) : 0.f;   // (within 2^-22 of 16256 / a)
-  v2i32 hi, lo;
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    uint32_t b[4];
+  for (int r = 0; r < 2; ++r) {
+    v2i32 hi, lo;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      b[i] = __builtin_bit_cast(uint32_t, __builtin_fmaf(x[4 * w + i], s, 12582912.0f + 64.f));
-    const uint32_t t = (pack4(b[0], b[1], b[2], b[3]) & 0x7f7f7f7fu) ^ 0x40404040u;
-    lo[w] = (int)(t | ((t & 0x40404040u) << 1));
-    hi[w] = (int)pack4(b[0] >> 7, b[1] >> 7, b[2] >> 7, b[3] >> 7);
+    for (int w = 0; w < 2; ++w) {
+      uint32_t b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        b[i] = __builtin_bit_cast(uint32_t,
+                                  __builtin_fmaf(x[8 * r + 4 * w + i], s, 12582912.0f + 64.f));
+      const uint32_t t = (pack4(b[0], b[1], b[2], b[3]) & 0x7f7f7f7fu) ^ 0x40404040u;
+      lo[w] = (int)(t | ((t & 0x40404040u) << 1));
+      hi[w] = (int)pack4(b[0] >> 7, b[1] >> 7, b[2] >> 7, b[3] >> 7);
+    }
+    lds_store(dst + e[r], hi);
+    lds_store(dst + 64 * QueryCfg<D>::kC + e[r], lo);
   }
-  lds_store(dst + e0, hi);
-  lds_store(dst + 64 * QueryCfg<D>::kC + e0, lo);
-  if (e0 == 0) lds_store(factor, a * (1.0f / 16256.0f));
+  if (e[0] == 0) lds_store(factor, a * (1.0f / 16256.0f));
 }
 // kPasses rows of a lane together (their reductions overlap).
 template <int D, int kPasses>
@@ -339,7 +363,7 @@ struct Scale {
 // tokens' x is -infinity, and a lane whose block its row does not see at all
 // drops the block's factors (they may be NaN).
 template <bool kAlibi>
-__device__ __forceinline__ float logits(float (&x)[16], Scale* sc, const Row& row, int t0, int g,
+__device__ __forceinline__ float logits(float* x, Scale* sc, const Row& row, int t0, int g,
                                         bool masked, bool here) {
   constexpr float kMinFactor = 0x1p-100f;   // (0 times -infinity would be NaN)
   sc->f *= row.qf;
@@ -518,7 +542,7 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
   };
   if (gi_first < gi_end) start(gi_first);
   // (the codes are on their way meanwhile)
-  float x_in[kPasses][8];
+  float x_in[kPasses][16];
   uint32_t x_top[kPasses];
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
@@ -529,7 +553,7 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
     const int rr = (4 * p + wave) * Q::kPassRows + lane / Q::kLanes;
-    if (rr < kRows) store_query<D>(x_in[p], x_top[p], lane, lds_q + rr * Q::kRowBytes, s_qf + rr);
+    if (rr < kRows) store_query<D>(x_in[p], x_top[p], rot, lane, lds_q + rr * Q::kRowBytes, s_qf + rr);
   }
   lds_only_barrier();
   read_query<D>(lds_q + n * Q::kRowBytes, g, qh, ql);
@@ -557,7 +581,7 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
       for (int e = 0; e < 16; ++e) x[e] = (float)s[e >> 2][e & 3];
       Scale sc = {__shfl(bl.ks, 4 * i + g, kWave), __shfl(bl.log_r, 4 * i + g, kWave),
                   __shfl(bl.inv_r, 4 * i + g, kWave)};
-      const float top = max_over_groups(
+      const float top = max_over_groups<4>(
           logits<kAlibi>(x, &sc, row, t0, g, t0 < all_lo || t0 + kGroup > all_hi || have != 15u,
                          (have >> g) & 1u));
       if (__any(top > m + kLazy)) {
@@ -649,28 +673,72 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
   }
 }
 
-// ---- Many rows: the waves of a block share each group, a wave takes kCols * 16
-// rows. Keys are copied to LDS as they are, into the next of three buffers.
-// Values are turned into fp16 once for the block (converted by
-// every wave for itself they were a third of its vector instructions): each wave
-// loads its share of a group one step ahead and stores it as operands, of which
-// LDS holds this group's and the next's.
+// ---- Many rows: the waves of a block share each group, a wave takes kR rows: 32
+// by MFMAs of 32 x 32 (half the instructions of 16 x 16, which keep the vector
+// pipe from issuing; the two lanes of a row hold two blocks of a group each), or
+// for D = 256, whose sums would not leave room for them, 16 as above. Keys are
+// copied to LDS as they are, into the next of three buffers. Values are turned
+// into fp16 once for the block (converted by every wave for itself they were a
+// third of its vector instructions): each wave loads its share of a group one
+// step ahead and stores it as operands, of which LDS holds this group's and the
+// next's.
 template <int D>
 struct TileCfg {
+  static constexpr int kR = D <= 128 ? 32 : 16;
+  static constexpr int kLaneGroups = kWave / kR;        // lanes of a row
+  static constexpr int kBlocks = 4 / kLaneGroups;       // blocks of a group a lane holds
+  static constexpr int kTiles = kGroup / kR;            // score tiles of a group
+  static constexpr int kValues = 16 * kBlocks / kTiles; // of a lane, of a score tile
+  static constexpr int kChunk = 16 * kLaneGroups;       // features of an int8 MFMA
+  static constexpr int kC = (D + kChunk - 1) / kChunk;
+  static constexpr int kO = (D + kR - 1) / kR;          // output tiles of kR features
   static constexpr int kWaves = D <= 128 ? 4 : 8;
   static constexpr int kThreads = kWaves * kWave;
-  static constexpr int kCols = D <= 128 ? 2 : 1;
-  static constexpr int kWaveRows = kCols * 16;
-  static constexpr int kBlockRows = kWaves * kWaveRows;
+  static constexpr int kBlockRows = kWaves * kR;
   static constexpr int kKeyBuffers = 3;
   static constexpr int kKeyLoads = 4 * Stage<D>::kLoads / kWaves;   // a wave's, of a group
   static constexpr int kValueTiles = (D / 16 + kWaves - 1) / kWaves;
   // (room for every wave's tiles: those past D / 16 are copies nobody reads)
   static constexpr int kValueBytes = kWaves * kValueTiles * 2048;
+  static constexpr int kValues0 = kKeyBuffers * Stage<D>::kGroupBytes;
+  static constexpr int kFactors0 = kValues0 + 2 * kValueBytes;
+  static constexpr int kQueryFactors0 = kFactors0 + kWaves * kWave * 16;
+  static constexpr int kLds = kQueryFactors0 + kBlockRows * 4;
   // (the queries stand where values will)
-  static constexpr int kLds = kKeyBuffers * Stage<D>::kGroupBytes + 2 * kValueBytes + kBlockRows * 4;
   static_assert(kBlockRows * QueryCfg<D>::kRowBytes <= 2 * kValueBytes, "room for the queries");
+  static_assert(kO * kR <= kWaves * kValueTiles * 16, "operands of every output tile");
 };
+
+__device__ __forceinline__ v16i32 mfma_i8(v4i32 a, v4i32 b, v16i32 c) {
+  return __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ v4i32 mfma_i8(v4i32 a, v4i32 b, v4i32 c) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ v16f32 mfma_f16(v8f16 a, v8f16 b, v16f32 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ v4f32 mfma_f16(v8f16 a, v8f16 b, v4f32 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// The keys of score tile q as an operand. Its rows are taken such that a lane's
+// values over the tiles are the tokens of its first block in order, then those
+// of its second.
+template <int D>
+__device__ __forceinline__ void read_key_tile(const int8_t* st, int n, int g, int q,
+                                              v4i32 (&k)[TileCfg<D>::kC]) {
+  typedef TileCfg<D> Cfg;
+  const int8_t* p = st + (Cfg::kR == 32
+                              ? (2 * q + ((n >> 2) & 1)) * Stage<D>::kPitch + 64 * (n >> 3)
+                              : (n >> 2) * Stage<D>::kPitch + 64 * q) + 16 * (n & 3);
+#pragma unroll
+  for (int c = 0; c < Cfg::kC; ++c) {
+    // (a lane past the last feature meets zeros of the query)
+    const int tile = Cfg::kLaneGroups * c + g;
+    k[c] = ld16v(p + (D % Cfg::kChunk == 0 ? tile : min(tile, D / 16 - 1)) * kTile);
+  }
+}
 
 // What a block does. Heads come first in the block index: blocks go to the 8
 // XCDs in turn, so with a multiple of 8 heads a head's blocks share one L2. A
@@ -715,14 +783,16 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
     KvArgs a, RotaryArgs rot, AttnArgs t, int group, int tiles, int splits, int chunk) {
   typedef Stage<D> S;
   typedef TileCfg<D> Cfg;
-  constexpr int kC = (D + 63) / 64, kT = D / 16, kCols = Cfg::kCols;
+  constexpr int kC = Cfg::kC, kR = Cfg::kR, kT = Cfg::kBlocks, kO = Cfg::kO;
+  constexpr int kTiles = Cfg::kTiles, kValues = Cfg::kValues;
   // loads of a wave younger than the keys it waits for: the next group's keys
   // and its own values of that group
   constexpr int kAhead = Cfg::kKeyLoads + Cfg::kValueTiles;
   __shared__ __attribute__((aligned(1024))) int8_t lds[Cfg::kLds];
-  int8_t* const lds_v = lds + Cfg::kKeyBuffers * S::kGroupBytes;
+  int8_t* const lds_v = lds + Cfg::kValues0;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n = lane & 15, g = lane >> 4;
+  const int n = lane % kR, g = lane / kR;            // row, lane group
+  const int n16 = lane & 15, g16 = lane >> 4;
   const int h = blockIdx.x % a.kv_heads;
   const Place at = place_of(a, t, blockIdx.x / a.kv_heads, group, Cfg::kBlockRows, tiles, splits,
                             chunk, lane);
@@ -740,8 +810,8 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
   const bool only = span.end - span.begin <= chunk;
 
   // the wave's rows (none: it stages, and computes nothing)
-  const int w_first = blk_first + wave * Cfg::kWaveRows;
-  const int w_last = min(w_first + Cfg::kWaveRows, rows) - 1;
+  const int w_first = blk_first + wave * kR;
+  const int w_last = min(w_first + kR, rows) - 1;
   const int i_first = min(w_first, rows - 1) / group, i_last = max(w_last, 0) / group;
   const int all_lo = visible_lo(t, sq.first + i_last);
   const int all_hi = visible_hi(t, sq, sq.first + i_first);
@@ -769,15 +839,22 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
   };
   v4i32 vr[Cfg::kValueTiles];   // the wave's tiles of a group: wave, wave + kWaves, ..
   auto load_values = [&](int i) __attribute__((always_inline)) {
-    const int x = __shfl(i < 16 ? lin : lin_next, (4 * i + g) & 63, kWave);
-    const int8_t* p = a.v_codes + (int64_t)max(x, 0) * S::kBytes + n * 16;
+    const int x = __shfl(i < 16 ? lin : lin_next, (4 * i + g16) & 63, kWave);
+    const int8_t* p = a.v_codes + (int64_t)max(x, 0) * S::kBytes + n16 * 16;
 #pragma unroll
-    for (int j = 0; j < Cfg::kValueTiles; ++j) {
-      vr[j] = *reinterpret_cast<const v4i32*>(p + min(wave + j * Cfg::kWaves, kT - 1) * kTile);
-    }
+    for (int j = 0; j < Cfg::kValueTiles; ++j)
+      vr[j] = ld16v(p + min(wave + j * Cfg::kWaves, D / 16 - 1) * kTile);
   };
+  // Features 16 d + n16, block g16, to the operands of the second product: 1 KB for
+  // each output tile, block of a lane and half of it, the lane's 8 tokens in 16
+  // bytes.
   auto store_value_tile = [&](int gi, int j) __attribute__((always_inline)) {
-    int8_t* dst = lds_v + (gi & 1) * Cfg::kValueBytes + (wave + j * Cfg::kWaves) * 2048 + lane * 16;
+    const int d = wave + j * Cfg::kWaves;
+    int8_t* dst = lds_v + (gi & 1) * Cfg::kValueBytes;
+    if constexpr (kR == 32)
+      dst += (d >> 1) * 4096 + (g16 >> 1) * 2048 + (16 * (d & 1) + n16 + 32 * (g16 & 1)) * 16;
+    else
+      dst += d * 2048 + lane * 16;
     v8f16 v0, v1;
     codes_to_f16(vr[j], &v0, &v1);
     lds_store(dst, __builtin_bit_cast(v4i32, v0));
@@ -794,9 +871,9 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
     stage_keys(gi_begin + 2, 2);
   }
   typedef QueryCfg<D> Q;
-  constexpr int kPasses = Cfg::kWaveRows / Q::kPassRows;
-  int8_t* const lds_q = lds_v + wave * (Cfg::kWaveRows * Q::kRowBytes);
-  float* const s_qf = reinterpret_cast<float*>(lds_v + 2 * Cfg::kValueBytes) + wave * Cfg::kWaveRows;
+  constexpr int kPasses = kR / Q::kPassRows;
+  int8_t* const lds_q = lds_v + wave * (kR * Q::kRowBytes);
+  float* const s_qf = reinterpret_cast<float*>(lds + Cfg::kQueryFactors0) + wave * kR;
   QueryLoads q_in[kPasses];
   // token and head of the lane's row, pass by pass without a division each
   const int tok_last = (rows - 1) / group, j_last = rows - 1 - tok_last * group;
@@ -817,7 +894,7 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
       ++tok;
     }
   }
-  float x_in[kPasses][8];
+  float x_in[kPasses][16];
   uint32_t x_top[kPasses];
 #pragma unroll
   for (int p = 0; p < kPasses; ++p)
@@ -826,69 +903,96 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
     const int rr = p * Q::kPassRows + lane / Q::kLanes;
-    store_query<D>(x_in[p], x_top[p], lane, lds_q + rr * Q::kRowBytes, s_qf + rr);
+    store_query<D>(x_in[p], x_top[p], rot, lane, lds_q + rr * Q::kRowBytes, s_qf + rr);
   }
-  Row row[kCols];
-  v4i32 qh[kCols][kC], ql[kCols][kC];
+  Row row;
+  v4i32 qh[kC], ql[kC];
+  const int r = min(w_first + n, rows - 1), i_row = r / group, head = h * group + r % group;
+  const bool live = w_first + n < rows;
 #pragma unroll
-  for (int c = 0; c < kCols; ++c) {
-    const int r = min(w_first + 16 * c + n, rows - 1);
-    read_query<D>(lds_q + (16 * c + n) * Q::kRowBytes, g, qh[c], ql[c]);
-    row[c].qf = s_qf[16 * c + n] * t.scale_log2;
-    row[c].pos = sq.first + r / group;
-    row[c].lo = visible_lo(t, row[c].pos);
-    row[c].hi = w_first + 16 * c + n < rows ? visible_hi(t, sq, row[c].pos) : 0;
-    row[c].slope = kAlibi ? t.slopes[h * group + r % group] * 1.44269504088896340736f : 0.f;
+  for (int c = 0; c < kC; ++c) {
+    qh[c] = ld16v(lds_q + n * Q::kRowBytes + Cfg::kChunk * c + 16 * g);
+    ql[c] = ld16v(lds_q + n * Q::kRowBytes + Q::kRowBytes / 2 + Cfg::kChunk * c + 16 * g);
   }
+  row.qf = s_qf[n] * t.scale_log2;
+  row.pos = sq.first + i_row;
+  row.lo = visible_lo(t, row.pos);
+  row.hi = live ? visible_hi(t, sq, row.pos) : 0;
+  row.slope = kAlibi ? t.slopes[head] * 1.44269504088896340736f : 0.f;
   lds_only_barrier();   // every wave has its queries
   if (gi_begin < gi_end) {
     store_values(gi_begin);
     load_values(1);
   }
-  v4f32 o[kCols][kT];
-  float m[kCols], l[kCols];
+  typedef typename std::conditional<kR == 32, v16f32, v4f32>::type OTile;
+  OTile o[kO];
 #pragma unroll
-  for (int c = 0; c < kCols; ++c) {
-    m[c] = -INFINITY;
-    l[c] = 0.f;
-#pragma unroll
-    for (int d = 0; d < kT; ++d) o[c][d] = v4f32{0.f, 0.f, 0.f, 0.f};
-  }
+  for (int d = 0; d < kO; ++d) o[d] = OTile{};
+  float m = -INFINITY, l = 0.f;
 
-  BlockList bl;
-  uint64_t present = __ballot(lin >= 0);
-  list_factors(ka, va, &ref, &rescale, &bl);
-  v4i32 s[kCols][4];
-  float x[kCols][16], top[kCols];
-  Scale sc[kCols];
-  // factors of the list's i-th group
-  auto factors = [&](int i) __attribute__((always_inline)) {
-    return Scale{__shfl(bl.ks, 4 * i + g, kWave), __shfl(bl.log_r, 4 * i + g, kWave),
-                 __shfl(bl.inv_r, 4 * i + g, kWave)};
+  // the list's factors, a copy for each wave: lane 4 i + j, block j of group i
+  v4f32* const s_factors = reinterpret_cast<v4f32*>(lds + Cfg::kFactors0) + wave * kWave;
+  uint64_t present;
+  auto take_list = [&]() __attribute__((always_inline)) {
+    BlockList bl;
+    present = __ballot(lin >= 0);
+    if (list_factors(ka, va, &ref, &rescale, &bl)) {
+#pragma unroll
+      for (int d = 0; d < kO; ++d) o[d] *= rescale;
+    }
+    lds_store(reinterpret_cast<int8_t*>(s_factors + lane),
+              __builtin_bit_cast(v4i32, v4f32{bl.ks, bl.log_r, bl.inv_r, 0.f}));
   };
-  // maxima of group gi, the i-th of the list
-  auto maxima = [&](int gi, int i, const Scale& of) __attribute__((always_inline)) {
+  take_list();
+  float x[16 * kT], top = -INFINITY;
+  Scale sc[kT];
+  // factors of the list's i-th group
+  auto factors = [&](int i, v4f32 (&f)[kT]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int T = 0; T < kT; ++T) f[T] = s_factors[4 * i + Cfg::kLaneGroups * T + g];
+  };
+  // the maximum of group gi, the i-th of the list
+  auto maximum = [&](int gi, int i, const v4f32 (&f)[kT]) __attribute__((always_inline)) {
     const int t0 = gi * kGroup;
     const uint32_t have = (uint32_t)(present >> (4 * i)) & 15u;
     const bool masked = t0 < all_lo || t0 + kGroup > all_hi || have != 15u;
+    top = -INFINITY;
 #pragma unroll
-    for (int c = 0; c < kCols; ++c) {
-      sc[c] = of;
-      top[c] = max_over_groups(
-          logits<kAlibi>(x[c], &sc[c], row[c], t0, g, masked, (have >> g) & 1u));
+    for (int T = 0; T < kT; ++T) {
+      const int blk = Cfg::kLaneGroups * T + g;
+      sc[T] = Scale{f[T][0], f[T][1], f[T][2]};
+      top = fmaxf(top, logits<kAlibi>(x + 16 * T, &sc[T], row, t0, blk, masked, (have >> blk) & 1u));
     }
+    top = max_over_groups<Cfg::kLaneGroups>(top);
   };
+  typedef typename std::conditional<kR == 32, v16i32, v4i32>::type STile;
+  // a score tile; between its two halves, `middle`
+  auto products = [&](const v4i32 (&k)[kC], auto middle) __attribute__((always_inline)) {
+    STile acc = {};
+#pragma unroll
+    for (int c = 0; c < kC; ++c) acc = mfma_i8(k[c], qh[c], acc);
+    middle();
+    acc = acc << 7;
+#pragma unroll
+    for (int c = 0; c < kC; ++c) acc = mfma_i8(k[c], ql[c], acc);
+    return acc;
+  };
+  STile s[kTiles];
   if (gi_begin < gi_end) {
     wait_loads<kAhead>();
     lds_only_barrier();
     if (works) {
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) {
-        scores<D>(lds + gi_begin % Cfg::kKeyBuffers * S::kGroupBytes, n, g, qh[c], ql[c], s[c]);
+      for (int q = 0; q < kTiles; ++q) {
+        v4i32 k[kC];
+        read_key_tile<D>(lds + gi_begin % Cfg::kKeyBuffers * S::kGroupBytes, n, g, q, k);
+        s[q] = products(k, [] {});
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[c][e] = (float)s[c][e >> 2][e & 3];
+        for (int e = 0; e < kValues; ++e) x[q * kValues + e] = (float)s[q][e];
       }
-      maxima(gi_begin, 0, factors(0));
+      v4f32 f[kT];
+      factors(0, f);
+      maximum(gi_begin, 0, f);
     }
   }
 
@@ -904,92 +1008,62 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
     // with the keys of gi and the values of gi - 1
     lds_only_barrier();
     stage_keys(gi + 3, i + 3);
-    Scale next = {0.f, 0.f, 0.f};
+    v4f32 next[kT];
     if (works) {
-      bool grown = false;
+      if (__any(top > m + kLazy)) {
+        const float alpha = raise(top, &m, &l);
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) grown = grown || top[c] > m[c] + kLazy;
-      if (__any(grown)) {
-#pragma unroll
-        for (int c = 0; c < kCols; ++c) {
-          const float alpha = raise(top[c], &m[c], &l[c]);
-#pragma unroll
-          for (int d = 0; d < kT; ++d) o[c][d] *= alpha;
-        }
+        for (int d = 0; d < kO; ++d) o[d] *= alpha;
       }
       // (the keys past the last group are what the buffer holds)
       const int8_t* st_k = lds + (gi + 1) % Cfg::kKeyBuffers * S::kGroupBytes;
       const int8_t* st_v = lds_v + (gi & 1) * Cfg::kValueBytes + lane * 16;
-      uint32_t pw[kCols][8];
-      float off[kCols], sum[kCols];
-#pragma unroll
-      for (int c = 0; c < kCols; ++c) {
-        off[c] = weight_offset(m[c], sc[c]);
-        sum[c] = 0.f;
-      }
-      // LDS reads run kKeyAhead operands, then kValueAhead tiles, ahead
-      constexpr int kKeyAhead = 2, kValueAhead = 2;
-      v4i32 kf[4][kC], vf[kT][2];
-      auto read_k = [&](int q) __attribute__((always_inline)) {
-#pragma unroll
-        for (int cc = 0; cc < kC; ++cc) kf[q][cc] = read_keys<D>(st_k, n, g, cc, q);
+      uint32_t pw[8 * kT];
+      v4i32 k[kTiles][kC], v[kO * kT][2];
+      // LDS reads run kValueAhead pairs of operands ahead
+      constexpr int kValueAhead = 1;
+      auto read_v = [&](int i) __attribute__((always_inline)) {
+        v[i][0] = ld16v(st_v + i * 2048);
+        v[i][1] = ld16v(st_v + i * 2048 + 1024);
       };
-      auto read_v = [&](int d) __attribute__((always_inline)) {
-        vf[d][0] = *reinterpret_cast<const v4i32*>(st_v + d * 2048);
-        vf[d][1] = *reinterpret_cast<const v4i32*>(st_v + d * 2048 + 1024);
-      };
+      read_key_tile<D>(st_k, n, g, 0, k[0]);
 #pragma unroll
-      for (int q = 0; q < kKeyAhead; ++q) read_k(q);
+      for (int q = 0; q < kTiles; ++q) {
+        if (q + 1 == kTiles)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (q + kKeyAhead < 4) read_k(q + kKeyAhead);
-        if (q + kValueAhead >= 4) read_v(q + kValueAhead - 4);
-        v4i32 part[kCols];
+          for (int i = 0; i < kValueAhead; ++i) read_v(i);
+        s[q] = products(k[q], [&]() __attribute__((always_inline)) {
+          // weights of group gi (the row sum takes them unrounded: those of a block
+          // of far smaller values vanish in fp16)
+          const Scale& of = sc[q * kValues / 16];
+          const float off = weight_offset(m, of);
+          float sum = 0.f;
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) part[c] = v4i32{0, 0, 0, 0};
-#pragma unroll
-        for (int cc = 0; cc < kC; ++cc)
-#pragma unroll
-          for (int c = 0; c < kCols; ++c)
-            part[c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf[q][cc], qh[c][cc], part[c], 0, 0, 0);
-#pragma unroll
-        for (int c = 0; c < kCols; ++c) {
-          float p[4];
-          weights4(x[c] + 4 * q, sc[c].f, off[c], &sum[c], p);
-          pw[c][2 * q] = f2h2(p[0], p[1]);
-          pw[c][2 * q + 1] = f2h2(p[2], p[3]);
-        }
-#pragma unroll
-        for (int c = 0; c < kCols; ++c) part[c] = part[c] << 7;
-#pragma unroll
-        for (int cc = 0; cc < kC; ++cc)
-#pragma unroll
-          for (int c = 0; c < kCols; ++c)
-            part[c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(kf[q][cc], ql[c][cc], part[c], 0, 0, 0);
-#pragma unroll
-        for (int c = 0; c < kCols; ++c) s[c][q] = part[c];
+          for (int w = q * kValues / 2; w < (q + 1) * kValues / 2; ++w) {
+            const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[2 * w], of.f, -off));
+            const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[2 * w + 1], of.f, -off));
+            sum += p0 + p1;
+            pw[w] = f2h2(p0, p1);
+          }
+          l += sum * of.inv_r;
+        });
+        if (q + 1 < kTiles) read_key_tile<D>(st_k, n, g, q + 1, k[q + 1]);
         __builtin_amdgcn_sched_barrier(0);
       }
+      factors((i + 1) & 15, next);
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) l[c] += sum[c] * sc[c].inv_r;
-      next = factors((i + 1) & 15);
+      for (int dT = 0; dT < kO * kT; ++dT) {
+        const int d = dT / kT, T = dT % kT;
+        if (dT + kValueAhead < kO * kT) read_v(dT + kValueAhead);
 #pragma unroll
-      for (int d = 0; d < kT; ++d) {
-        if (d + kValueAhead < kT) read_v(d + kValueAhead);
+        for (int u = 0; u < 2; ++u)
+          o[d] = mfma_f16(__builtin_bit_cast(v8f16, v[dT][u]), as_f16(pw + 8 * T + 4 * u), o[d]);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int c = 0; c < kCols; ++c)
-            o[c][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                __builtin_bit_cast(v8f16, vf[d][j]), as_f16(pw[c] + 4 * j), o[c][d], 0, 0, 0);
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (e * kT / 16 == d)
-#pragma unroll
-            for (int c = 0; c < kCols; ++c) x[c][e] = (float)s[c][e >> 2][e & 3];
+        for (int e = 0; e < 16 * kT; ++e)
+          if (e * kO / 16 == dT) x[e] = (float)s[e / kValues][e % kValues];
 #pragma unroll
         for (int j = 0; j < Cfg::kValueTiles; ++j)
-          if (d == j * (kT / Cfg::kValueTiles)) store_value_tile(gi + 1, j);
+          if (dT == j * (kO * kT / Cfg::kValueTiles)) store_value_tile(gi + 1, j);
         __builtin_amdgcn_sched_barrier(0);
       }
     } else {
@@ -1000,48 +1074,42 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
       lin = lin_next;
       ka = ka_next;
       va = va_next;
-      present = __ballot(lin >= 0);
-      if (list_factors(ka, va, &ref, &rescale, &bl)) {
-#pragma unroll
-        for (int c = 0; c < kCols; ++c)
-#pragma unroll
-          for (int d = 0; d < kT; ++d) o[c][d] *= rescale;
-      }
-      next = factors(0);
+      take_list();
+      factors(0, next);
     }
-    if (works && gi + 1 < gi_end) maxima(gi + 1, (i + 1) & 15, next);
+    if (works && gi + 1 < gi_end) maximum(gi + 1, (i + 1) & 15, next);
   }
   wait_loads<0>();   // nothing may land in LDS after the block has ended
 
   const float unit = ref / 127.0f;
   const Parts parts = parts_of(t.part, (int64_t)a.total_tokens * t.q_heads, splits, D);
+  if constexpr (Cfg::kLaneGroups == 4) l += __shfl_xor(l, 16, kWave);
+  l += __shfl_xor(l, 32, kWave);
+  if (!live) return;
+  const int64_t out_row = (int64_t)(sq.row0 + i_row) * t.q_heads + head;
+  // a lane's sums: of each output tile, runs of four features
+  constexpr int kRuns = kR == 32 ? 4 : 1;
+  const float inv = l == 0.f ? 0.f : unit / l;
+  const int64_t part = at.split * parts.rows + out_row;
 #pragma unroll
-  for (int c = 0; c < kCols; ++c) {
-    l[c] += __shfl_xor(l[c], 16, kWave);
-    l[c] += __shfl_xor(l[c], 32, kWave);
-    const int r = w_first + 16 * c + n;
-    if (r >= rows) continue;
-    const int64_t out_row = (int64_t)(sq.row0 + r / group) * t.q_heads + h * group + r % group;
-    if (only) {
-      const float inv = l[c] == 0.f ? 0.f : unit / l[c];
-      uint16_t* out = t.out + out_row * D + 4 * g;
+  for (int d = 0; d < kO; ++d)
 #pragma unroll
-      for (int d = 0; d < kT; ++d)
-        *reinterpret_cast<uint2*>(out + 16 * d) = make_uint2(
-            f2h2(o[c][d][0] * inv, o[c][d][1] * inv), f2h2(o[c][d][2] * inv, o[c][d][3] * inv));
-    } else {
-      const int64_t part = at.split * parts.rows + out_row;
-      float* out = parts.o + part * D + 4 * g;
-#pragma unroll
-      for (int d = 0; d < kT; ++d) *reinterpret_cast<v4f32*>(out + 16 * d) = o[c][d] * unit;
-      if (g == 0) {
-        parts.ml[part * 2] = m[c];
-        parts.ml[part * 2 + 1] = l[c];
-      }
+    for (int k = 0; k < kRuns; ++k) {
+      const int e0 = d * kR + 8 * k + 4 * g;
+      if (D % kR != 0 && e0 >= D) continue;
+      const v4f32 y = {o[d][4 * k], o[d][4 * k + 1], o[d][4 * k + 2], o[d][4 * k + 3]};
+      if (only)
+        *reinterpret_cast<uint2*>(t.out + out_row * D + e0) =
+            make_uint2(f2h2(y[0] * inv, y[1] * inv), f2h2(y[2] * inv, y[3] * inv));
+      else
+        *reinterpret_cast<v4f32*>(parts.o + part * D + e0) = y * unit;
     }
-    if (splits > 1 && at.split == 0 && g == 0)
-      parts.count[out_row] = (span.end - span.begin + chunk - 1) / chunk;
+  if (g == 0 && !only) {
+    parts.ml[part * 2] = m;
+    parts.ml[part * 2 + 1] = l;
   }
+  if (g == 0 && splits > 1 && at.split == 0)
+    parts.count[out_row] = (span.end - span.begin + chunk - 1) / chunk;
 }
 
 // The splits' sums of a row, weighed by their maxima, into the output of rows
@@ -1164,8 +1232,10 @@ Plan plan(const KvArgs& a, int q_heads) {
   p.group = q_heads / a.kv_heads;
   const int64_t rows = (int64_t)a.max_tokens * p.group;
   p.shared = rows > 2 * kRows;
-  p.tile_rows = !p.shared ? kRows : a.head_dim <= 128 ? TileCfg<128>::kBlockRows
-                                                      : TileCfg<256>::kBlockRows;
+  static_assert(TileCfg<64>::kBlockRows == 128 && TileCfg<80>::kBlockRows == 128 &&
+                    TileCfg<96>::kBlockRows == 128 && TileCfg<128>::kBlockRows == 128 &&
+                    TileCfg<256>::kBlockRows == 128, "one tile height");
+  p.tile_rows = p.shared ? 128 : kRows;
   p.tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
   const int64_t blocks =
       std::max<int64_t>(std::min<int64_t>((int64_t)p.tiles * a.num_seqs, most_tiles(a, p)) * a.kv_heads, 1);
@@ -1179,7 +1249,6 @@ Plan plan(const KvArgs& a, int q_heads) {
   }
   chunk = std::max(chunk, len / kMaxSplits + 1);
   chunk = (chunk + kGroup - 1) / kGroup * kGroup;
-  if (getenv("KVC")) chunk = atoi(getenv("KVC"));
   p.chunk = (int)chunk;
   p.splits = (int)((len + chunk - 1) / chunk);
   return p;
