@@ -538,6 +538,12 @@ int rotary_check(const char* fn, const i8mm_rotary* r, const i8mm::KvArgs& a,
   return I8MM_OK;
 }
 
+// The queries that share a key/value head are rows, numbered in int32.
+bool heads_ok(const i8mm::KvArgs& a, int64_t q_heads) {
+  return q_heads > 0 && q_heads <= 65535 && q_heads % a.kv_heads == 0 &&
+         a.max_tokens <= INT32_MAX / 2 / (q_heads / a.kv_heads);
+}
+
 // 16-byte loads of 8 halfs at any token and head.
 int strides_check(const char* fn, const char* name, const void* p, bool required, int64_t ts,
                   int64_t hs) {
@@ -588,7 +594,7 @@ size_t int8_kv_cache_attention_workspace_bytes(const i8mm_kv_cache* cache,
                                                const i8mm_kv_batch* batch, int64_t q_heads) {
   i8mm::KvArgs a;
   if (kv_sizes("int8_kv_cache_attention_workspace_bytes", cache, batch, &a) != I8MM_OK) return 0;
-  if (q_heads <= 0 || q_heads > 65535 || q_heads % a.kv_heads != 0) return 0;
+  if (!heads_ok(a, q_heads)) return 0;
   return i8mm::attn_workspace_bytes(a, (int)q_heads);
 }
 
@@ -602,9 +608,9 @@ int int8_kv_cache_attention(const uint16_t* q, int64_t q_token_stride, int64_t q
   i8mm::RotaryArgs r;
   I8MM_TRY(kv_check(fn, cache, batch, &a));
   I8MM_TRY(rotary_check(fn, rotary, a, &r));
-  if (q_heads <= 0 || q_heads > 65535 || q_heads % a.kv_heads != 0)
-    return fail(I8MM_EINVAL, "%s: q_heads=%lld is not a multiple of %d key/value heads", fn,
-                (long long)q_heads, a.kv_heads);
+  if (!heads_ok(a, q_heads))
+    return fail(I8MM_EINVAL, "%s: q_heads=%lld is not a multiple of %d key/value heads, or too many "
+                "for %d tokens a sequence", fn, (long long)q_heads, a.kv_heads, a.max_tokens);
   I8MM_TRY(strides_check(fn, "q", q, a.total_tokens > 0, q_token_stride, q_head_stride));
   if (!std::isfinite(scale) || !(scale > 0.f))
     return fail(I8MM_EINVAL, "%s: scale is not finite and positive", fn);

@@ -133,6 +133,13 @@ def test_refused_attention(lib, kw, status):
     assert call_attention(lib, cache(), batch(), **kw) == status
 
 
+def test_refused_rows_beyond_int32(lib):
+    """The queries of a sequence that share a head are numbered in int32."""
+    b = batch(total_tokens=1 << 28, max_tokens=1 << 28)
+    assert lib.int8_kv_cache_attention_workspace_bytes(cache(), b, 20) == 0
+    assert call_attention(lib, cache(), b, heads=20) == _lib.I8MM_EINVAL
+
+
 def test_attention_workspace(lib):
     """A long cache with few rows needs one; it is refused when missing, short
     or misaligned."""
