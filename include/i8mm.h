@@ -478,9 +478,12 @@ I8MM_API int int8_kv_cache_append(const uint16_t* k, int64_t k_token_stride, int
  *            matter.
  *
  * The query is taken as 15-bit integers over its row's absmax, so its product
- * with the key codes is an exact integer; the softmax runs in fp32, its
- * weights are rounded to fp16 against their row's maximum, and the sums over
- * tokens are fp32. Results do not depend on what ran before.
+ * with the key codes is an exact integer. The softmax and the sums over tokens
+ * are fp32. The weights that meet the values are rounded against their row's
+ * maximum, to fp16 where max_tokens * q_heads / kv_heads is more than 48 (32
+ * for D = 256), to two parts of fp16 (22 bits) where it is not. Results do not
+ * depend on what ran before. Rows of `out` that belong to no sequence (past
+ * cu_tokens[num_seqs]) are left as they are.
  * Errors: EINVAL, EALIGN, EWORKSPACE, ENODEVICE, ELAUNCH.
  */
 I8MM_API int int8_kv_cache_attention(const uint16_t* q, int64_t q_token_stride,

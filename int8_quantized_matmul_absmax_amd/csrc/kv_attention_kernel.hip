@@ -1221,6 +1221,11 @@ int64_t most_tiles(const KvArgs& a, const Plan& p) {
   return (int64_t)a.total_tokens * p.group / p.tile_rows + a.num_seqs;
 }
 
+// Which kernel: up to 48 rows the one for few rows, each 16 of them another block
+// (8 sequences of up to 8191 tokens, 8 heads: 48 rows of 64 features 26 us against
+// 41, of 128 features 40 against 53; 64 rows 34 against 30 and 46 against 40); of
+// 256 features up to 32 (48 rows 82 us against 86, but 50 against 30 where one
+// sequence is alone).
 // Splits of the token axis: kResident blocks run at once (two a compute unit).
 // For few rows, one round of them when there is little else to run, and chunks
 // of at most kMaxChunk, which evens out sequences of different lengths. For many
@@ -1231,7 +1236,7 @@ Plan plan(const KvArgs& a, int q_heads) {
   Plan p;
   p.group = q_heads / a.kv_heads;
   const int64_t rows = (int64_t)a.max_tokens * p.group;
-  p.shared = rows > 2 * kRows;
+  p.shared = rows > (a.head_dim <= 128 ? 3 : 2) * kRows;
   static_assert(TileCfg<64>::kBlockRows == 128 && TileCfg<80>::kBlockRows == 128 &&
                     TileCfg<96>::kBlockRows == 128 && TileCfg<128>::kBlockRows == 128 &&
                     TileCfg<256>::kBlockRows == 128, "one tile height");

@@ -240,6 +240,23 @@ def test_attention_grouped_heads(gpu, group):
                     rotary=64)
 
 
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
+@pytest.mark.parametrize("count", [16, 17, 32, 33, 48, 49, 128, 129])
+def test_attention_row_counts(gpu, dim, count):
+    """Rows that just fill a tile, or just do not, of each kernel."""
+    rng = np.random.default_rng(dim + count)
+    check_attention(gpu, rng, [count + 77, count, 1], [count, count, 1], dim=dim, heads=2)
+
+
+@pytest.mark.parametrize("dim", [64, 80, 96, 128, 256])
+@pytest.mark.parametrize("rotary", [16, 48, 64])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_attention_partial_rotation(gpu, dim, rotary, interleaved):
+    rng = np.random.default_rng(dim + rotary)
+    check_attention(gpu, rng, [130, 70], [1, 63], dim=dim, heads=2, rotary=rotary,
+                    interleaved=interleaved)
+
+
 @pytest.mark.parametrize("count", [1, 2, 40])
 def test_attention_long_axis_split(gpu, count):
     """Few rows over a long cache: several splits of the token axis are joined,
