@@ -259,3 +259,22 @@ def test_reference_attention_closed_forms():
     assert not R.attention(c, q, absent)[0].any()
     o2, _ = R.attention(c, q, b, causal=False)
     assert np.allclose(o2[-1], out[-1]) and not np.allclose(o2[0], out[0])
+
+
+def test_cached_attention_layer_refusals():
+    with pytest.raises(ValueError):
+        i8.Int8CachedAttention(256, 4, 3, device="cpu")
+    with pytest.raises(ValueError):
+        i8.Int8CachedAttention(256, 0, device="cpu")
+    with pytest.raises(ValueError):
+        i8.Int8CachedAttention(256, 6, device="cpu")
+    layer = i8.Int8CachedAttention(256, 4, 2, device="cpu")
+    assert (layer.qkv.out_features, layer.out.in_features, layer.head_dim) == (512, 256, 64)
+
+    class Sizes:
+        kv_heads, head_dim, total_tokens = 2, 80, 3
+    with pytest.raises(ValueError):     # another cache's head size
+        layer(torch.zeros((3, 256), dtype=torch.float16), Sizes, Sizes)
+    Sizes.head_dim = 64
+    with pytest.raises(ValueError):     # rows that the batch does not have
+        layer(torch.zeros((2, 256), dtype=torch.float16), Sizes, Sizes)
