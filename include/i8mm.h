@@ -482,8 +482,8 @@ I8MM_API int int8_kv_cache_append(const uint16_t* k, int64_t k_token_stride, int
  * are fp32. The weights that meet the values are rounded against their row's
  * maximum, to fp16 where max_tokens * q_heads / kv_heads is more than 48 (32
  * for D = 256), to two parts of fp16 (22 bits) where it is not. Results do not
- * depend on what ran before. Rows of `out` that belong to no sequence (past
- * cu_tokens[num_seqs]) are left as they are.
+ * depend on what ran before. What rows of `out` that belong to no sequence
+ * (past cu_tokens[num_seqs]) get is unspecified.
  * Errors: EINVAL, EALIGN, EWORKSPACE, ENODEVICE, ELAUNCH.
  */
 I8MM_API int int8_kv_cache_attention(const uint16_t* q, int64_t q_token_stride,

@@ -462,10 +462,9 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
                                                                 int splits, int chunk) {
   constexpr int kC = (D + 63) / 64, kT = D / 16, kLd = D + 4;
   typedef Stage<D> S;
-  constexpr int kSlots = D <= 64 ? 2 : 1;
-  constexpr int kAhead = (2 * kSlots - 1) * 4 * S::kLoads;   // loads younger than the awaited
+  constexpr int kAhead = 4 * S::kLoads;   // loads younger than the awaited: the other buffer's
   constexpr int kJoinBytes = (4 * kRows * kLd + 8 * kRows) * 4;
-  constexpr int kStageBytes = 4 * 2 * kSlots * S::kGroupBytes;
+  constexpr int kStageBytes = 4 * 2 * S::kGroupBytes;
   typedef QueryCfg<D> Q;
   __shared__ __attribute__((aligned(1024)))
   int8_t lds[(kStageBytes > kJoinBytes ? kStageBytes : kJoinBytes) + kRows * (Q::kRowBytes + 4)];
@@ -519,8 +518,8 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
 
   const int gi_end = (end + kGroup - 1) / kGroup;
   const int gi_first = begin / kGroup + wave;
-  int8_t* const st_k = lds + wave * (2 * kSlots * S::kGroupBytes);
-  int8_t* const st_v = st_k + kSlots * S::kGroupBytes;
+  int8_t* const st_k = lds + wave * (2 * S::kGroupBytes);
+  int8_t* const st_v = st_k + S::kGroupBytes;
   BlockList bl;
   float k_absmax, v_absmax, rescale;
   // absent blocks are masked; block 0 is read in their place
@@ -530,15 +529,11 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
       stage_block<D>(codes, max(__builtin_amdgcn_readlane(bl.lin, 4 * i + j), 0),
                      dst + j * S::kPitch, lane);
   };
-  // the list of 16 groups from gi0 on, and the first groups' copies
+  // the list of 16 groups from gi0 on, and the first group's copies
   auto start = [&](int gi0) __attribute__((always_inline)) {
     list_blocks(a, b, h, gi0, 4, end, lane, &bl.lin, &k_absmax, &v_absmax);
-#pragma unroll
-    for (int i = 0; i < kSlots; ++i)
-      if (gi0 + 4 * i < gi_end) {
-        load(i, a.k_codes, st_k + i * S::kGroupBytes);
-        load(i, a.v_codes, st_v + i * S::kGroupBytes);
-      }
+    load(0, a.k_codes, st_k);
+    load(0, a.v_codes, st_v);
   };
   if (gi_first < gi_end) start(gi_first);
   // (the codes are on their way meanwhile)
@@ -566,16 +561,20 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
     }
     const uint64_t present = __ballot(bl.lin >= 0);
     const int count = min(16, (gi_end - gi0 + 3) / 4);
-    auto step = [&](int i, int8_t* ks, int8_t* vs) __attribute__((always_inline)) {
+    if (list_factors(k_absmax, v_absmax, &ref, &rescale, &bl)) {
+#pragma unroll
+      for (int d = 0; d < kT; ++d) o[d] *= rescale;
+    }
+    for (int i = 0; i < count; ++i) {
       const uint32_t have = (uint32_t)(present >> (4 * i)) & 15u;
       const int t0 = (gi0 + 4 * i) * kGroup;
       v4i32 s[4];
       float x[16], p[16];
-      if (i + kSlots < count) wait_loads<kAhead>(); else wait_loads<0>();
-      scores<D>(ks, n, g, qh, ql, s);
-      if (i + kSlots < count) {
+      if (i + 1 < count) wait_loads<kAhead>(); else wait_loads<0>();
+      scores<D>(st_k, n, g, qh, ql, s);
+      if (i + 1 < count) {
         wait_lds_reads();
-        load(i + kSlots, a.k_codes, ks);
+        load(i + 1, a.k_codes, st_k);
       }
 #pragma unroll
       for (int e = 0; e < 16; ++e) x[e] = (float)s[e >> 2][e & 3];
@@ -601,28 +600,20 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
         pl[e] = f2h2(p[2 * e] - h2f(ph[e] & 0xffffu), p[2 * e + 1] - h2f(ph[e] >> 16));
       }
       const v8f16 p0h = as_f16(ph), p1h = as_f16(ph + 4), p0l = as_f16(pl), p1l = as_f16(pl + 4);
-      if (i + kSlots < count) wait_loads<kAhead>(); else wait_loads<0>();
+      if (i + 1 < count) wait_loads<kAhead>(); else wait_loads<0>();
 #pragma unroll
       for (int d = 0; d < kT; ++d) {
         v8f16 v0, v1;
-        codes_to_f16(read_values<D>(vs, n, g, d), &v0, &v1);
+        codes_to_f16(read_values<D>(st_v, n, g, d), &v0, &v1);
         o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, p0h, o[d], 0, 0, 0);
         o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, p1h, o[d], 0, 0, 0);
         o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, p0l, o[d], 0, 0, 0);
         o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, p1l, o[d], 0, 0, 0);
       }
-      if (i + kSlots < count) {
+      if (i + 1 < count) {
         wait_lds_reads();
-        load(i + kSlots, a.v_codes, vs);
+        load(i + 1, a.v_codes, st_v);
       }
-    };
-    if (list_factors(k_absmax, v_absmax, &ref, &rescale, &bl)) {
-#pragma unroll
-      for (int d = 0; d < kT; ++d) o[d] *= rescale;
-    }
-    for (int i = 0; i < count; ++i) {
-      const int slot = kSlots == 1 ? 0 : i % kSlots;
-      step(i, st_k + slot * S::kGroupBytes, st_v + slot * S::kGroupBytes);
     }
   }
 
@@ -682,9 +673,8 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
 // third of its vector instructions): each wave loads its share of a group one
 // step ahead and stores it as operands, of which LDS holds this group's and the
 // next's.
-template <int D>
+template <int D, int kR>
 struct TileCfg {
-  static constexpr int kR = D <= 128 ? 32 : 16;
   static constexpr int kLaneGroups = kWave / kR;        // lanes of a row
   static constexpr int kBlocks = 4 / kLaneGroups;       // blocks of a group a lane holds
   static constexpr int kTiles = kGroup / kR;            // score tiles of a group
@@ -725,11 +715,11 @@ __device__ __forceinline__ v4f32 mfma_f16(v8f16 a, v8f16 b, v4f32 c) {
 // The keys of score tile q as an operand. Its rows are taken such that a lane's
 // values over the tiles are the tokens of its first block in order, then those
 // of its second.
-template <int D>
+template <int D, int kR>
 __device__ __forceinline__ void read_key_tile(const int8_t* st, int n, int g, int q,
-                                              v4i32 (&k)[TileCfg<D>::kC]) {
-  typedef TileCfg<D> Cfg;
-  const int8_t* p = st + (Cfg::kR == 32
+                                              v4i32 (&k)[TileCfg<D, kR>::kC]) {
+  typedef TileCfg<D, kR> Cfg;
+  const int8_t* p = st + (kR == 32
                               ? (2 * q + ((n >> 2) & 1)) * Stage<D>::kPitch + 64 * (n >> 3)
                               : (n >> 2) * Stage<D>::kPitch + 64 * q) + 16 * (n & 3);
 #pragma unroll
@@ -778,12 +768,12 @@ __device__ __forceinline__ Place place_of(const KvArgs& a, const AttnArgs& t, in
   return Place{b, __builtin_amdgcn_readlane(my_tiles, b) - 1 - in / s, in % s};
 }
 
-template <int D, bool kAlibi>
-__global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
+template <int D, int kR, bool kAlibi>
+__global__ __launch_bounds__((TileCfg<D, kR>::kThreads), 2) void k_kv_attn_tile(
     KvArgs a, RotaryArgs rot, AttnArgs t, int group, int tiles, int splits, int chunk) {
   typedef Stage<D> S;
-  typedef TileCfg<D> Cfg;
-  constexpr int kC = Cfg::kC, kR = Cfg::kR, kT = Cfg::kBlocks, kO = Cfg::kO;
+  typedef TileCfg<D, kR> Cfg;
+  constexpr int kC = Cfg::kC, kT = Cfg::kBlocks, kO = Cfg::kO;
   constexpr int kTiles = Cfg::kTiles, kValues = Cfg::kValues;
   // loads of a wave younger than the keys it waits for: the next group's keys
   // and its own values of that group
@@ -985,7 +975,7 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
 #pragma unroll
       for (int q = 0; q < kTiles; ++q) {
         v4i32 k[kC];
-        read_key_tile<D>(lds + gi_begin % Cfg::kKeyBuffers * S::kGroupBytes, n, g, q, k);
+        read_key_tile<D, kR>(lds + gi_begin % Cfg::kKeyBuffers * S::kGroupBytes, n, g, q, k);
         s[q] = products(k, [] {});
 #pragma unroll
         for (int e = 0; e < kValues; ++e) x[q * kValues + e] = (float)s[q][e];
@@ -1026,7 +1016,7 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
         v[i][0] = ld16v(st_v + i * 2048);
         v[i][1] = ld16v(st_v + i * 2048 + 1024);
       };
-      read_key_tile<D>(st_k, n, g, 0, k[0]);
+      read_key_tile<D, kR>(st_k, n, g, 0, k[0]);
 #pragma unroll
       for (int q = 0; q < kTiles; ++q) {
         if (q + 1 == kTiles)
@@ -1047,7 +1037,7 @@ __global__ __launch_bounds__(TileCfg<D>::kThreads, 2) void k_kv_attn_tile(
           }
           l += sum * of.inv_r;
         });
-        if (q + 1 < kTiles) read_key_tile<D>(st_k, n, g, q + 1, k[q + 1]);
+        if (q + 1 < kTiles) read_key_tile<D, kR>(st_k, n, g, q + 1, k[q + 1]);
         __builtin_amdgcn_sched_barrier(0);
       }
       factors((i + 1) & 15, next);
@@ -1212,46 +1202,53 @@ __global__ __launch_bounds__(kBlockThreads) void k_kv_attn_join(float* ws, int64
 }
 
 struct Plan {
-  bool shared;     // the kernel for many rows
+  bool shared, wide;   // the kernel for many rows; its waves of 32 rows
   int group, tile_rows, tiles, splits, chunk;
 };
 
 // Tiles of all sequences together, at most.
 int64_t most_tiles(const KvArgs& a, const Plan& p) {
-  return (int64_t)a.total_tokens * p.group / p.tile_rows + a.num_seqs;
+  return std::min((int64_t)p.tiles * a.num_seqs,
+                  (int64_t)a.total_tokens * p.group / p.tile_rows + a.num_seqs);
 }
 
 // Which kernel: up to 48 rows the one for few rows, each 16 of them another block
 // (8 sequences of up to 8191 tokens, 8 heads: 48 rows of 64 features 26 us against
-// 41, of 128 features 40 against 53; 64 rows 34 against 30 and 46 against 40); of
-// 256 features up to 32 (48 rows 82 us against 86, but 50 against 30 where one
-// sequence is alone).
-// Splits of the token axis: kResident blocks run at once (two a compute unit).
+// 31, of 80 features 36 against 40, of 128 alike; 64 rows 34 against 28 and 46
+// against 36 of 64 and 128); of 256 features up to 32 (48 rows 82 us against 86, but
+// 50 against 30 where one sequence is alone).
+// Waves of 32 rows where there is work for them, measured by the tokens that a
+// resident block of 128 rows would take: of 128 features, 32 heads, a prompt of
+// 2048 tokens (2048) 69 us against 73, of 1024 tokens (512) 41 against 33; of 80
+// features 24 heads of 4096 tokens (6144) 127 against 145, 32 of 2048 68 against
+// 58. 256 features have no room for them.
+// Splits of the token axis: two blocks run at once on a compute unit, one of 256
+// features (2048 tokens of 16 heads: 105 us when taken for two, 88 us).
 // For few rows, one round of them when there is little else to run, and chunks
-// of at most kMaxChunk, which evens out sequences of different lengths. For many
-// rows, no block longer than a fraction of a compute unit's whole share, the
-// smaller one when lengths may differ.
+// of at most kMaxChunk, which evens out sequences of different lengths (16 of up
+// to 4096 tokens and 64 of grouped heads: 68 and 124 us, with 8192 81 and 168, with
+// 1024 65 and 128). For many rows, whose queries cost a block about as much as 512
+// tokens do, only as many as fill one round (chunks of a quarter of that: 48 heads
+// of 4096 tokens 325 us against 261, a step of prompt chunks 240 against 195).
 Plan plan(const KvArgs& a, int q_heads) {
-  constexpr int64_t kResident = 2 * 256, kMinChunk = 4 * kGroup, kMaxChunk = 2048;
+  constexpr int64_t kMinChunk = 4 * kGroup, kMaxChunk = 2048;
+  const int64_t resident = (a.head_dim <= 128 ? 2 : 1) * 256;
   Plan p;
   p.group = q_heads / a.kv_heads;
   const int64_t rows = (int64_t)a.max_tokens * p.group;
-  p.shared = rows > (a.head_dim <= 128 ? 3 : 2) * kRows;
-  static_assert(TileCfg<64>::kBlockRows == 128 && TileCfg<80>::kBlockRows == 128 &&
-                    TileCfg<96>::kBlockRows == 128 && TileCfg<128>::kBlockRows == 128 &&
-                    TileCfg<256>::kBlockRows == 128, "one tile height");
-  p.tile_rows = p.shared ? 128 : kRows;
-  p.tiles = (int)((rows + p.tile_rows - 1) / p.tile_rows);
-  const int64_t blocks =
-      std::max<int64_t>(std::min<int64_t>((int64_t)p.tiles * a.num_seqs, most_tiles(a, p)) * a.kv_heads, 1);
+  const auto share = [&](int tile_rows) {   // the tokens that each resident block would take
+    p.tile_rows = tile_rows;
+    p.tiles = (int)((rows + tile_rows - 1) / tile_rows);
+    return (int64_t)a.len_cap * std::max<int64_t>(most_tiles(a, p) * a.kv_heads, 1) / resident;
+  };
   const int64_t len = (int64_t)a.len_cap + kGroup;   // a span starts at a whole group
-  int64_t chunk = len;
-  if (p.shared) {
-    const int64_t jobs = kResident * (a.num_seqs > 1 ? 8 : 4);
-    chunk = std::min(len, std::max((int64_t)a.len_cap * blocks / jobs, 2 * kMinChunk));
-  } else {
-    chunk = std::min(std::max((int64_t)a.len_cap * blocks / kResident, kMinChunk), kMaxChunk);
-  }
+  int64_t chunk;
+  p.shared = rows > (a.head_dim <= 128 ? 3 : 2) * kRows;
+  p.wide = p.shared && a.head_dim <= 128 && share(128) >= (a.head_dim < 128 ? 4096 : 1024);
+  if (p.shared)
+    chunk = std::min(len, std::max(share(p.wide || a.head_dim == 256 ? 128 : 64), 2 * kMinChunk));
+  else
+    chunk = std::min(std::max(share(kRows), kMinChunk), kMaxChunk);
   chunk = std::max(chunk, len / kMaxSplits + 1);
   chunk = (chunk + kGroup - 1) / kGroup * kGroup;
   p.chunk = (int)chunk;
@@ -1259,20 +1256,33 @@ Plan plan(const KvArgs& a, int q_heads) {
   return p;
 }
 
+// The kernel for many rows, kR a wave.
+template <int D, int kR>
+hipError_t launch_tiles(const KvArgs& a, const RotaryArgs& r, const AttnArgs& t, const Plan& p,
+                        hipStream_t s) {
+  typedef TileCfg<D, kR> Cfg;
+  if (p.tile_rows != Cfg::kBlockRows) return hipErrorInvalidValue;
+  const int64_t jobs = a.num_seqs <= kWave ? most_tiles(a, p) : (int64_t)p.tiles * a.num_seqs;
+  const int64_t blocks = jobs * p.splits * a.kv_heads;
+  if (blocks > INT32_MAX) return hipErrorInvalidValue;
+  if (t.slopes)
+    k_kv_attn_tile<D, kR, true><<<(uint32_t)blocks, Cfg::kThreads, 0, s>>>(
+        a, r, t, p.group, p.tiles, p.splits, p.chunk);
+  else
+    k_kv_attn_tile<D, kR, false><<<(uint32_t)blocks, Cfg::kThreads, 0, s>>>(
+        a, r, t, p.group, p.tiles, p.splits, p.chunk);
+  return hipGetLastError();
+}
+
 template <int D>
 hipError_t launch_d(const KvArgs& a, const RotaryArgs& r, const AttnArgs& t, hipStream_t s) {
   const Plan p = plan(a, t.q_heads);
+  hipError_t e;
   if (p.shared) {
-    int64_t jobs = (int64_t)p.tiles * a.num_seqs;
-    if (a.num_seqs <= kWave) jobs = std::min(jobs, most_tiles(a, p));
-    const int64_t blocks = jobs * p.splits * a.kv_heads;
-    if (blocks > INT32_MAX) return hipErrorInvalidValue;
-    if (t.slopes)
-      k_kv_attn_tile<D, true><<<(uint32_t)blocks, TileCfg<D>::kThreads, 0, s>>>(
-          a, r, t, p.group, p.tiles, p.splits, p.chunk);
+    if constexpr (D <= 128)
+      e = p.wide ? launch_tiles<D, 32>(a, r, t, p, s) : launch_tiles<D, 16>(a, r, t, p, s);
     else
-      k_kv_attn_tile<D, false><<<(uint32_t)blocks, TileCfg<D>::kThreads, 0, s>>>(
-          a, r, t, p.group, p.tiles, p.splits, p.chunk);
+      e = launch_tiles<D, 16>(a, r, t, p, s);
   } else {
     const dim3 grid((uint32_t)p.splits, (uint32_t)(p.tiles * a.kv_heads), (uint32_t)a.num_seqs);
     if (t.slopes)
@@ -1281,8 +1291,8 @@ hipError_t launch_d(const KvArgs& a, const RotaryArgs& r, const AttnArgs& t, hip
     else
       k_kv_attn_rows<D, false><<<grid, kBlockThreads, 0, s>>>(a, r, t, p.group, p.tiles, p.splits,
                                                               p.chunk);
+    e = hipGetLastError();
   }
-  hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits <= 1) return e;
   const int64_t rows = (int64_t)a.total_tokens * t.q_heads;
   if (p.splits <= kFewSplits) {
