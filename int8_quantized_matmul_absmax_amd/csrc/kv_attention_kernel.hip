@@ -15,11 +15,12 @@
 // and need the codes converted; 15 bits are finer than the fp16 the query came
 // in for all but the smallest features of a row.
 //
-// Softmax in base 2 with the running maximum m of each row. The value absmax
-// is folded into the weight: P = 2^(S - m + log2 r), r = absmax / ref, for one
-// ref a wave; O is then in units of ref / 127 and the row sum takes P / r.
-// P <= 2^kLazy is rounded to fp16 (2^-11 relative; below 2^-14 of the row's
-// maximum, 2^-25 absolute); all sums are fp32.
+// Softmax in base 2. The value absmax a of a block is folded into the weight,
+// P = 2^(S + log2 a - m), with the running maximum m over a row's S + log2 a, so
+// that the products sum the value codes as they are; the row sum takes P / a, and
+// O / (127 l) is the result. An a below 2^-40 counts as 2^-40, which an fp16
+// result cannot tell from it. P <= 2^kLazy is rounded to fp16 (2^-11 relative;
+// below 2^-14 of the row's largest, 2^-25 absolute); all sums are fp32.
 
 #include <algorithm>
 #include <type_traits>
@@ -33,10 +34,10 @@ namespace {
 constexpr int kGroup = 64;          // tokens of a step: four blocks
 constexpr int kRows = 16;           // rows of a tile
 constexpr float kLazy = 8.f;        // a row is rescaled when its maximum grew by more
-constexpr float kMinRatio = 0x1p-40f;   // weights of such values vanish in fp16 anyway
+constexpr float kMinAbsmax = 0x1p-40f;   // of values
 
 // The workspace of a launch with several splits: for each split and row the sum
-// O (not divided) and its maximum and row sum, and for each row the number of
+// O (of codes, not divided) and its maximum and row sum, and for each row the number of
 // splits that see some of it, written by the first.
 struct Parts {
   float* o;        // [splits][rows][D]
@@ -257,7 +258,7 @@ __device__ __forceinline__ void read_query(const int8_t* row, int g, v4i32* hi, 
 struct BlockList {
   int lin;            // -1 where there is no block to read
   float ks;           // key absmax / 127
-  float log_r, inv_r; // of the value absmax over the wave's ref
+  float log_a, inv_a; // of the value absmax
 };
 
 // ---- Codes through LDS. A group is staged as its four blocks, each as it lies
@@ -352,14 +353,14 @@ struct Row {
   float slope;   // * log2(e)
 };
 
-// A lane's factors of a group: weights are 2^(x f - m + log_r), and the row sum
-// takes them times inv_r.
+// A lane's factors of a block: weights are 2^(x f + log_a - m), and the row sum
+// takes them times inv_a.
 struct Scale {
-  float f, log_r, inv_r;
+  float f, log_a, inv_a;
 };
 
-// The logits' maximum over a lane's 16 tokens. A position bias goes into x in
-// units of f, its part common to the 16 into log_r. With `masked`, hidden
+// The maximum of a lane's 16 exponents. A position bias goes into x in units of
+// f, its part common to the 16 into log_a. With `masked`, hidden
 // tokens' x is -infinity, and a lane whose block its row does not see at all
 // drops the block's factors (they may be NaN).
 template <bool kAlibi>
@@ -369,13 +370,11 @@ __device__ __forceinline__ float logits(float* x, Scale* sc, const Row& row, int
   sc->f *= row.qf;
   sc->f = sc->f < kMinFactor ? kMinFactor : sc->f;   // (keeps a NaN)
   const int tok0 = t0 + 16 * g;
-  float base = 0.f;
   if (kAlibi) {
-    base = row.slope * (float)(tok0 - row.pos);
     const float step = row.slope * __builtin_amdgcn_rcpf(sc->f);
 #pragma unroll
     for (int e = 1; e < 16; ++e) x[e] = __builtin_fmaf(step, (float)e, x[e]);
-    sc->log_r += base;
+    sc->log_a += row.slope * (float)(tok0 - row.pos);
   }
   if (masked) {
     const int lo = row.lo - tok0, hi = row.hi - tok0;
@@ -384,13 +383,13 @@ __device__ __forceinline__ float logits(float* x, Scale* sc, const Row& row, int
     for (int e = 0; e < 16; ++e) x[e] = some && e >= lo && e < hi ? x[e] : -INFINITY;
     if (!some) {
       sc->f = 1.f;
-      sc->log_r = sc->inv_r = base = 0.f;
+      sc->log_a = sc->inv_a = 0.f;
     }
   }
   float top = fmaxf(x[0], x[1]);
 #pragma unroll
   for (int e = 2; e < 16; e += 2) top = fmaxf(fmaxf(top, x[e]), x[e + 1]);
-  return top * sc->f + base;
+  return top * sc->f + sc->log_a;
 }
 
 // Takes a row's new maximum (over the lanes that share it) into m and l; what
@@ -410,8 +409,11 @@ __device__ __forceinline__ void weights4(const float* x, float f, float off, flo
   *sum += (p[0] + p[1]) + (p[2] + p[3]);
 }
 __device__ __forceinline__ float weight_offset(float m, const Scale& sc) {
-  return (m == -INFINITY ? 0.f : m) - sc.log_r;
+  return (m == -INFINITY ? 0.f : m) - sc.log_a;
 }
+
+// What a row's sums over codes are multiplied by in the end (0: it saw nothing).
+__device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.0f / (127.0f * l); }
 
 // Four words of fp16 pairs as an MFMA operand.
 __device__ __forceinline__ v8f16 as_f16(const uint32_t* w) {
@@ -432,24 +434,12 @@ __device__ __forceinline__ void list_blocks(const KvArgs& a, int b, int h, int g
     *v_absmax = a.v_absmax[*lin];
   }
 }
-// The list's factors; true when ref grew, with what sums in its units are to be
-// multiplied by.
-__device__ __forceinline__ bool list_factors(float k_absmax, float v_absmax, float* ref,
-                                             float* rescale, BlockList* bl) {
-  float top = v_absmax;
-#pragma unroll
-  for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x, kWave));
-  const bool grown = top > *ref;
-  if (grown) {
-    *rescale = *ref / top;
-    *ref = top;
-  }
-  float ratio = v_absmax / (*ref > 0.f ? *ref : 1.f);
-  ratio = ratio < kMinRatio ? kMinRatio : ratio;   // (keeps a NaN)
+// The list's factors.
+__device__ __forceinline__ void list_factors(float k_absmax, float v_absmax, BlockList* bl) {
+  const float a = v_absmax < kMinAbsmax ? kMinAbsmax : v_absmax;   // (keeps a NaN)
   bl->ks = k_absmax / 127.0f;
-  bl->log_r = __builtin_amdgcn_logf(ratio);
-  bl->inv_r = 1.0f / ratio;
-  return grown;
+  bl->log_a = __builtin_amdgcn_logf(a);
+  bl->inv_a = 1.0f / a;
 }
 
 // ---- Few rows: each wave streams its own groups through its own part of
@@ -514,14 +504,14 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
   v4f32 o[kT];
 #pragma unroll
   for (int d = 0; d < kT; ++d) o[d] = v4f32{0.f, 0.f, 0.f, 0.f};
-  float m = -INFINITY, l = 0.f, ref = 0.f;
+  float m = -INFINITY, l = 0.f;
 
   const int gi_end = (end + kGroup - 1) / kGroup;
   const int gi_first = begin / kGroup + wave;
   int8_t* const st_k = lds + wave * (2 * S::kGroupBytes);
   int8_t* const st_v = st_k + S::kGroupBytes;
   BlockList bl;
-  float k_absmax, v_absmax, rescale;
+  float k_absmax, v_absmax;
   // absent blocks are masked; block 0 is read in their place
   auto load = [&](int i, const int8_t* codes, int8_t* dst) __attribute__((always_inline)) {
 #pragma unroll
@@ -561,10 +551,7 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
     }
     const uint64_t present = __ballot(bl.lin >= 0);
     const int count = min(16, (gi_end - gi0 + 3) / 4);
-    if (list_factors(k_absmax, v_absmax, &ref, &rescale, &bl)) {
-#pragma unroll
-      for (int d = 0; d < kT; ++d) o[d] *= rescale;
-    }
+    list_factors(k_absmax, v_absmax, &bl);
     for (int i = 0; i < count; ++i) {
       const uint32_t have = (uint32_t)(present >> (4 * i)) & 15u;
       const int t0 = (gi0 + 4 * i) * kGroup;
@@ -578,8 +565,8 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
       }
 #pragma unroll
       for (int e = 0; e < 16; ++e) x[e] = (float)s[e >> 2][e & 3];
-      Scale sc = {__shfl(bl.ks, 4 * i + g, kWave), __shfl(bl.log_r, 4 * i + g, kWave),
-                  __shfl(bl.inv_r, 4 * i + g, kWave)};
+      Scale sc = {__shfl(bl.ks, 4 * i + g, kWave), __shfl(bl.log_a, 4 * i + g, kWave),
+                  __shfl(bl.inv_a, 4 * i + g, kWave)};
       const float top = max_over_groups<4>(
           logits<kAlibi>(x, &sc, row, t0, g, t0 < all_lo || t0 + kGroup > all_hi || have != 15u,
                          (have >> g) & 1u));
@@ -592,7 +579,7 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
       float sum = 0.f;
 #pragma unroll
       for (int q = 0; q < 4; ++q) weights4(x + 4 * q, sc.f, off, &sum, p + 4 * q);
-      l += sum * sc.inv_r;
+      l += sum * sc.inv_a;
       uint32_t ph[8], pl[8];   // the weights in two parts of 11 bits
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -621,9 +608,8 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
   l += __shfl_xor(l, 16, kWave);
   l += __shfl_xor(l, 32, kWave);
   __syncthreads();   // every wave is done with the staged groups
-  const float unit = ref / 127.0f;
 #pragma unroll
-  for (int d = 0; d < kT; ++d) *reinterpret_cast<v4f32*>(&s_o[wave][n][16 * d + 4 * g]) = o[d] * unit;
+  for (int d = 0; d < kT; ++d) *reinterpret_cast<v4f32*>(&s_o[wave][n][16 * d + 4 * g]) = o[d];
   if (g == 0) {
     s_m[wave][n] = m;
     s_l[wave][n] = l;
@@ -648,7 +634,7 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
     const int rr = r_first + row;
     const int64_t out_row = (int64_t)(sq.row0 + rr / group) * t.q_heads + h * group + rr % group;
     if (only) {
-      const float inv = total == 0.f ? 0.f : 1.0f / total;
+      const float inv = inverse(total);
       *reinterpret_cast<uint2*>(t.out + out_row * D + d4) =
           make_uint2(f2h2(acc[0] * inv, acc[1] * inv), f2h2(acc[2] * inv, acc[3] * inv));
     } else {
@@ -808,7 +794,7 @@ __global__ __launch_bounds__((TileCfg<D, kR>::kThreads), 2) void k_kv_attn_tile(
   const bool works = w_first < rows;
 
   int lin, lin_next = -1;
-  float ka, va, ka_next = 0.f, va_next = 0.f, rescale, ref = 0.f;
+  float ka, va, ka_next = 0.f, va_next = 0.f;
   const int gi_begin = begin / kGroup, gi_end = (end + kGroup - 1) / kGroup;
   list_blocks(a, b, h, gi_begin, 1, end, lane, &lin, &ka, &va);
   // What follows takes group gi as the i-th (up to 31st) of the current and
@@ -926,12 +912,9 @@ __global__ __launch_bounds__((TileCfg<D, kR>::kThreads), 2) void k_kv_attn_tile(
   auto take_list = [&]() __attribute__((always_inline)) {
     BlockList bl;
     present = __ballot(lin >= 0);
-    if (list_factors(ka, va, &ref, &rescale, &bl)) {
-#pragma unroll
-      for (int d = 0; d < kO; ++d) o[d] *= rescale;
-    }
+    list_factors(ka, va, &bl);
     lds_store(reinterpret_cast<int8_t*>(s_factors + lane),
-              __builtin_bit_cast(v4i32, v4f32{bl.ks, bl.log_r, bl.inv_r, 0.f}));
+              __builtin_bit_cast(v4i32, v4f32{bl.ks, bl.log_a, bl.inv_a, 0.f}));
   };
   take_list();
   float x[16 * kT], top = -INFINITY;
@@ -1035,7 +1018,7 @@ __global__ __launch_bounds__((TileCfg<D, kR>::kThreads), 2) void k_kv_attn_tile(
             sum += p0 + p1;
             pw[w] = f2h2(p0, p1);
           }
-          l += sum * of.inv_r;
+          l += sum * of.inv_a;
         });
         if (q + 1 < kTiles) read_key_tile<D, kR>(st_k, n, g, q + 1, k[q + 1]);
         __builtin_amdgcn_sched_barrier(0);
@@ -1071,7 +1054,6 @@ __global__ __launch_bounds__((TileCfg<D, kR>::kThreads), 2) void k_kv_attn_tile(
   }
   wait_loads<0>();   // nothing may land in LDS after the block has ended
 
-  const float unit = ref / 127.0f;
   const Parts parts = parts_of(t.part, (int64_t)a.total_tokens * t.q_heads, splits, D);
   if constexpr (Cfg::kLaneGroups == 4) l += __shfl_xor(l, 16, kWave);
   l += __shfl_xor(l, 32, kWave);
@@ -1079,7 +1061,7 @@ __global__ __launch_bounds__((TileCfg<D, kR>::kThreads), 2) void k_kv_attn_tile(
   const int64_t out_row = (int64_t)(sq.row0 + i_row) * t.q_heads + head;
   // a lane's sums: of each output tile, runs of four features
   constexpr int kRuns = kR == 32 ? 4 : 1;
-  const float inv = l == 0.f ? 0.f : unit / l;
+  const float inv = inverse(l);
   const int64_t part = at.split * parts.rows + out_row;
 #pragma unroll
   for (int d = 0; d < kO; ++d)
@@ -1092,7 +1074,7 @@ __global__ __launch_bounds__((TileCfg<D, kR>::kThreads), 2) void k_kv_attn_tile(
         *reinterpret_cast<uint2*>(t.out + out_row * D + e0) =
             make_uint2(f2h2(y[0] * inv, y[1] * inv), f2h2(y[2] * inv, y[3] * inv));
       else
-        *reinterpret_cast<v4f32*>(parts.o + part * D + e0) = y * unit;
+        *reinterpret_cast<v4f32*>(parts.o + part * D + e0) = y;
     }
   if (g == 0 && !only) {
     parts.ml[part * 2] = m;
@@ -1133,7 +1115,7 @@ __global__ __launch_bounds__(kBlockThreads) void k_kv_attn_join_few(float* ws, i
     total += parts.ml[(p * rows + row) * 2 + 1] * w;
     acc += ld16f(parts.o + (p * rows + row) * D + d4) * w;
   }
-  acc *= total == 0.f ? 0.f : 1.0f / total;
+  acc *= inverse(total);
   *reinterpret_cast<uint2*>(out + row * D + d4) = make_uint2(f2h2(acc[0], acc[1]), f2h2(acc[2], acc[3]));
 }
 
@@ -1197,7 +1179,7 @@ __global__ __launch_bounds__(kBlockThreads) void k_kv_attn_join(float* ws, int64
     float acc = 0.f;
 #pragma unroll
     for (int i = 0; i < kSets; ++i) acc += s_sum[i][tid];
-    out[row * D + tid] = f2h(total == 0.f ? 0.f : acc / total);
+    out[row * D + tid] = f2h(acc * inverse(total));
   }
 }
 

@@ -66,7 +66,7 @@ def check_attention(i8, rng, lens, counts, heads=4, kv_heads=2, dim=64, page=32,
         q = rng.normal(0, 1.5, (total, heads, dim)).astype(np.float16)
     cos = sin = rot = None
     if rotary:
-        cos, sin = tables(rotary, max(lens) + 1)
+        cos, sin = tables(rotary, max(max(lens), max_len or 0) + 1)
         rot = i8.Rotary(dev(cos), dev(sin), interleaved)
     c, b = on_gpu(i8, cache, table, lens, counts, max_len=max(lens) if max_len is None else max_len)
     slopes = kw.get("slopes")
@@ -296,6 +296,80 @@ def test_attention_growing_maximum(gpu, count):
         cache["k_codes"][p, :, s] = np.abs(cache["k_codes"][p, :, s])
         cache["k_absmax"][p, :, s] = 0.01 * 1.5 ** (t // 16 if t < 250 else 25 - t // 16)
     check_attention(gpu, rng, [400], [count], cache=(cache, table))
+
+
+# A launch bound of 2^16 or 2^20 tokens calls for the widest tiles, whatever the
+# lengths.
+
+def widen(cache_and_table, page):
+    cache, table = cache_and_table
+    return cache, np.pad(table, ((0, 0), (0, (1 << 20) // page - table.shape[1])),
+                         constant_values=-1)
+
+
+@pytest.mark.parametrize("dim", [64, 80, 96, 128])
+@pytest.mark.parametrize("kw", [
+    {}, {"causal": False}, {"window": 1}, {"window": 37}, {"rotary": 32, "interleaved": True},
+    {"rotary": 64}, {"alibi": True}, {"alibi": True, "window": 100}, {"scale": 0.9}])
+def test_wide_tiles_chunks(gpu, dim, kw):
+    kw = dict(kw)
+    rng = np.random.default_rng(dim + 100 * len(kw))
+    lens, counts = [150, 33, 1, 0, 90, 64, 1200], [150, 1, 1, 0, 0, 17, 70]
+    if kw.pop("alibi", False):
+        kw["slopes"] = (2.0 ** -np.arange(1, 13)).astype(np.float32)
+    check_attention(gpu, rng, lens, counts, heads=12, kv_heads=4, dim=dim, page=64, max_len=1 << 16,
+                    cache=widen(make(rng, lens, 4, dim, 64), 64), **kw)
+
+
+@pytest.mark.parametrize("dim", [64, 96, 128])
+@pytest.mark.parametrize("count", [127, 128, 129, 255])
+def test_wide_tiles_row_counts(gpu, dim, count):
+    rng = np.random.default_rng(dim + count)
+    lens = [count + 77, count]
+    check_attention(gpu, rng, lens, [count, count], dim=dim, heads=4, kv_heads=4, page=32,
+                    max_len=1 << 20, cache=widen(make(rng, lens, 4, dim, 32), 32))
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_wide_tiles_values_and_logits_far_apart(gpu, dim):
+    """Values of blocks that differ by 2^60, and logits that grow by far more
+    than fp16 can hold."""
+    rng = np.random.default_rng(dim + 17)
+    lens = [400, 260]
+    cache, table = make(rng, lens, 4, dim, 32)
+    a = cache["v_absmax"]
+    a *= np.float32(2.0) ** rng.integers(-70, 8, a.shape).astype(np.float32)
+    a[rng.random(a.shape) < 0.2] = 0
+    check_attention(gpu, rng, lens, [200, 260], heads=4, kv_heads=4, dim=dim, scale=0.3,
+                    max_len=1 << 20, cache=widen((cache, table), 32))
+    cache, table = make(rng, lens, 4, dim, 32)
+    q = np.abs(rng.normal(0, 2, (460, 4, dim))).astype(np.float16)
+    for b in range(2):
+        for t in range(0, lens[b], 16):
+            p, s, _ = R.place(cache, table[b], t)
+            cache["k_codes"][p, :, s] = np.abs(cache["k_codes"][p, :, s])
+            cache["k_absmax"][p, :, s] = 0.01 * 1.5 ** (t // 16 if t < 250 else 25 - t // 16)
+    check_attention(gpu, rng, lens, [200, 260], heads=4, kv_heads=4, dim=dim, q=q,
+                    max_len=1 << 20, cache=widen((cache, table), 32))
+
+
+@pytest.mark.parametrize("which", ["k_absmax", "v_absmax"])
+def test_wide_tiles_nan_blocks_and_queries(gpu, which):
+    rng = np.random.default_rng(18)
+    lens, counts = [256], [256]
+    cache, table = widen(make(rng, lens, 4, 64, 64), 64)
+    q = rng.normal(0, 1, (256, 4, 64)).astype(np.float16)
+    q[3] = 0
+    want, bound = R.attention(cache, q, (table, lens, counts))
+    p, s, _ = R.place(cache, table[0], 160)
+    cache[which][p, 1:, s] = np.nan
+    q[40, 0, 7] = np.nan
+    c, b = on_gpu(gpu, cache, table, lens, counts, max_len=1 << 20)
+    got = host(c.attention(dev(q), b)).astype(np.float64)
+    bad = np.zeros((256, 4), bool)
+    bad[160:, 1:] = bad[40, 0] = True
+    assert np.isnan(got[bad]).all()
+    assert (np.abs(got - want) <= bound)[~bad].all()
 
 
 def test_attention_query_layouts(gpu):
