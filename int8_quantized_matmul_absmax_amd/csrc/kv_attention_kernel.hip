@@ -442,10 +442,16 @@ __device__ __forceinline__ void list_factors(float k_absmax, float v_absmax, Blo
   bl->inv_a = 1.0f / a;
 }
 
-// ---- Few rows: each wave streams its own groups through its own part of
+// ---- Few rows: bound by the cache's bytes, each read once for all the rows of
+// a key/value head. Each wave streams its own groups through its own part of
 // LDS, keys and values apart: a buffer is refilled as soon as it has been read,
-// so something is always in flight. The four waves of a block join through LDS,
-// the blocks of a row tile through the workspace and k_kv_attn_join.
+// so something is always in flight (a second pair of buffers changed nothing). The
+// four waves of a block join through LDS, the blocks of a row tile through the
+// workspace and the kernels below. The weights go to the second product in two
+// parts of fp16: there is time for it. One token over each of 64 sequences of up to
+// 8192, 64 heads on 8 of 128 features (595 MB): 119 us, 5.0 TB/s, and 5 us to join;
+// over one of 131071, 32 heads on 8 (268 MB): 51 us, 5.3 TB/s, and 5 us. A large
+// copy moves 5.2 TB/s on the same card.
 template <int D, bool kAlibi>
 __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_rows(KvArgs a, RotaryArgs rot,
                                                                 AttnArgs t, int group, int tiles,
@@ -652,13 +658,22 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
 
 // ---- Many rows: the waves of a block share each group, a wave takes kR rows: 32
 // by MFMAs of 32 x 32 (half the instructions of 16 x 16, which keep the vector
-// pipe from issuing; the two lanes of a row hold two blocks of a group each), or
-// for D = 256, whose sums would not leave room for them, 16 as above. Keys are
-// copied to LDS as they are, into the next of three buffers. Values are turned
-// into fp16 once for the block (converted by every wave for itself they were a
-// third of its vector instructions): each wave loads its share of a group one
-// step ahead and stores it as operands, of which LDS holds this group's and the
-// next's.
+// pipe from issuing; the two lanes of a row hold two blocks of a group each) or 16
+// as above, where there is not work enough (see the plan) and for D = 256, whose
+// sums of 32 rows would not leave room. Keys are copied to LDS as they are, into
+// the next of three buffers. Values are turned into fp16 once for the block
+// (converted by every wave for itself they were a third of its vector
+// instructions): each wave loads its share of a group one step ahead and stores it
+// as operands, of which LDS holds this group's and the next's.
+//
+// Bound by the issue of vector instructions, about 270 beside 32 MFMAs for a group
+// of 64 tokens, 32 rows and 128 features: exponentials, conversions, the joining of
+// the two parts of the scores. 4096 tokens of 96 heads of 128 (412 GFLOP): 520 us,
+// 0.79 PFLOP/s (a large fp16 product: 1.2); the vector pipe is busy for 0.63 of the
+// cycles at 2.05 GHz, the matrix pipe for 0.37, and the two hardly overlap. A step
+// of prompt chunks over prefixes of up to 8191 tokens, 32 heads on 8 of 64 (90
+// GFLOP): 182 us. What else it costs a block is its start, about 12 us for the
+// queries.
 template <int D, int kR>
 struct TileCfg {
   static constexpr int kLaneGroups = kWave / kR;        // lanes of a row
@@ -1087,7 +1102,8 @@ __global__ __launch_bounds__((TileCfg<D, kR>::kThreads), 2) void k_kv_attn_tile(
 // The splits' sums of a row, weighed by their maxima, into the output of rows
 // with more than one. (Rows of the packed tensor that belong to no sequence have
 // no count: what they are given is unspecified, and bounded by `splits`.)
-// Up to kFewSplits: a lane takes four features, a wave several rows.
+// Up to kFewSplits: a lane takes four features, a wave several rows. Bound by
+// latency: 4096 rows of 128 features and up to 4 splits 4.9 us (a block a row 15).
 constexpr int kFewSplits = 16;
 template <int D>
 __global__ __launch_bounds__(kBlockThreads) void k_kv_attn_join_few(float* ws, int64_t rows,
@@ -1121,7 +1137,7 @@ __global__ __launch_bounds__(kBlockThreads) void k_kv_attn_join_few(float* ws, i
 
 // More splits: one block a row. Threads take four features each, the groups of
 // threads that cover a row take the splits in turn, and the groups' sums are
-// added in a fixed order.
+// added in a fixed order. 32 rows of 128 features and 64 splits: 4.7 us.
 constexpr int kMaxSplits = 1024;
 template <int D>
 __global__ __launch_bounds__(kBlockThreads) void k_kv_attn_join(float* ws, int64_t rows, int splits,
