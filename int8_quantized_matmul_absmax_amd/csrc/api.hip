@@ -538,10 +538,12 @@ int rotary_check(const char* fn, const i8mm_rotary* r, const i8mm::KvArgs& a,
   return I8MM_OK;
 }
 
-// The queries that share a key/value head are rows, numbered in int32.
+// The queries that share a key/value head are rows, numbered in int32; the rows
+// of all heads are few enough for the workspace's bytes to stay in 64 bits.
 bool heads_ok(const i8mm::KvArgs& a, int64_t q_heads) {
   return q_heads > 0 && q_heads <= 65535 && q_heads % a.kv_heads == 0 &&
-         a.max_tokens <= INT32_MAX / 2 / (q_heads / a.kv_heads);
+         a.max_tokens <= INT32_MAX / 2 / (q_heads / a.kv_heads) &&
+         a.total_tokens <= (int64_t{1} << 40) / q_heads;
 }
 
 // 16-byte loads of 8 halfs at any token and head.
@@ -610,7 +612,8 @@ int int8_kv_cache_attention(const uint16_t* q, int64_t q_token_stride, int64_t q
   I8MM_TRY(rotary_check(fn, rotary, a, &r));
   if (!heads_ok(a, q_heads))
     return fail(I8MM_EINVAL, "%s: q_heads=%lld is not a multiple of %d key/value heads, or too many "
-                "for %d tokens a sequence", fn, (long long)q_heads, a.kv_heads, a.max_tokens);
+                "for %d tokens, %d a sequence", fn, (long long)q_heads, a.kv_heads,
+                a.total_tokens, a.max_tokens);
   I8MM_TRY(strides_check(fn, "q", q, a.total_tokens > 0, q_token_stride, q_head_stride));
   if (!std::isfinite(scale) || !(scale > 0.f))
     return fail(I8MM_EINVAL, "%s: scale is not finite and positive", fn);

@@ -1237,7 +1237,8 @@ Plan plan(const KvArgs& a, int q_heads) {
   const auto share = [&](int tile_rows) {   // the tokens that each resident block would take
     p.tile_rows = tile_rows;
     p.tiles = (int)((rows + tile_rows - 1) / tile_rows);
-    return (int64_t)a.len_cap * std::max<int64_t>(most_tiles(a, p) * a.kv_heads, 1) / resident;
+    const int64_t blocks = std::min<int64_t>(most_tiles(a, p) * a.kv_heads, INT32_MAX);
+    return (int64_t)a.len_cap * std::max<int64_t>(blocks, 1) / resident;
   };
   const int64_t len = (int64_t)a.len_cap + kGroup;   // a span starts at a whole group
   int64_t chunk;
