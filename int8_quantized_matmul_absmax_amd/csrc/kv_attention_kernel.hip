@@ -669,10 +669,10 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
 // Bound by the issue of vector instructions, about 270 beside 32 MFMAs for a group
 // of 64 tokens, 32 rows and 128 features: exponentials, conversions, the joining of
 // the two parts of the scores. 4096 tokens of 96 heads of 128 (412 GFLOP): 520 us,
-// 0.79 PFLOP/s (a large fp16 product: 1.2); the vector pipe is busy for 0.63 of the
-// cycles at 2.05 GHz, the matrix pipe for 0.37, and the two hardly overlap. A step
+// 0.79 PFLOP/s (a large fp16 product: 1.2); the vector pipe is busy for 0.62 of the
+// cycles at 2.05 GHz, the matrix pipe for 0.38, and the two hardly overlap. A step
 // of prompt chunks over prefixes of up to 8191 tokens, 32 heads on 8 of 64 (90
-// GFLOP): 182 us. What else it costs a block is its start, about 12 us for the
+// GFLOP): 175 us. What else it costs a block is its start, about 12 us for the
 // queries.
 template <int D, int kR>
 struct TileCfg {
