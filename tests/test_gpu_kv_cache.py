@@ -500,3 +500,35 @@ def test_empty_calls(gpu):
     c = gpu.Int8KVCache(1, 2, 64)
     c.append(e, e, b)
     assert c.attention(e, b).shape == (0, 2, 64) and c.read(b)[0].shape == (0, 2, 64)
+
+
+def test_offsets_beyond_32_bits(gpu):
+    """Pages more than 4 GiB into the cache, and tokens more than 4 GiB apart:
+    the results of a small cache and of packed tensors, bit for bit."""
+    rng = np.random.default_rng(21)
+    pages, heads, dim, page = 70000, 8, 128, 64          # 4.6 GB of codes each
+    lens, counts = [100, 37], [60, 37]
+    far = gpu.Int8KVCache(pages, heads, dim, page)
+    near = gpu.Int8KVCache(4, heads, dim, page)
+    cu = dev(np.array([0, 60, 97], np.int32))
+    b_near = gpu.KVBatch(dev(np.array([[0, 1], [2, 3]], np.int32)), dev(np.array(lens, np.int32)),
+                         cu, total_tokens=97, max_tokens=60)
+    b_far = gpu.KVBatch(dev(np.array([[pages - 1, 3], [pages - 2, 0]], np.int32)),
+                        dev(np.array(lens, np.int32)), cu, total_tokens=97, max_tokens=60)
+    x = [dev(rng.normal(0, 1, (97, heads, dim)).astype(np.float16)) for _ in range(3)]
+    step = (1 << 31) // 64 + 8                           # elements: 97 of them are 6.5 GB
+    room = torch.empty((96 * step + heads * dim,), dtype=torch.float16, device="cuda")
+    got = []
+    for cache, batch, spread in ((near, b_near, False), (far, b_far, True)):
+        cache.k_absmax.zero_()
+        cache.v_absmax.zero_()
+        cache.k_codes[batch.page_table.long().flatten()] = 0
+        cache.v_codes[batch.page_table.long().flatten()] = 0
+        q, k, v = x
+        if spread:
+            view = room.as_strided((97, heads, dim), (step, dim, 1))
+        cache.append(view.copy_(k) if spread else k, v, batch)
+        cache.append(k, view.copy_(v) if spread else v, batch)
+        got.append((*cache.read(batch), cache.attention(view.copy_(q) if spread else q, batch)))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
