@@ -471,13 +471,21 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
   float(*s_l)[kRows] = s_m + 4;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
-  const int split = blockIdx.x, h = blockIdx.y / tiles, b = blockIdx.z;
-  const int r_first = (blockIdx.y % tiles) * kRows;
+  const int h = blockIdx.x / tiles, b = blockIdx.y;
+  const int r_first = (blockIdx.x % tiles) * kRows;
   const KvSeq sq = kv_seq(a, b);
   const int rows = sq.n * group;
   if (r_first >= rows) return;
   const int r_last = min(r_first + kRows, rows) - 1;
   const Span span = row_span(t, sq, r_first / group, r_last / group);
+  // Whole chunks first, then what is left of each span together, since what starts
+  // last should be short: in the slab that the longest sequence's rest falls into
+  // (the last is for spans that begin inside a group). Against a sequence's chunks
+  // one after the other, 16 ragged sequences of 32 heads 65.1 us and 67.6, 64 of
+  // grouped heads 122.2 and 123.6; with 256 features 64 sequences 128 and 123.
+  const int whole = min((span.end - span.begin) / chunk, splits - 1), z = blockIdx.z;
+  if (z >= whole && z != max(whole, splits - 2)) return;
+  const int split = min(z, whole);
   const int begin = span.begin + split * chunk;
   // an empty span still has its outputs written, by split 0
   if (split > 0 && begin >= span.end) return;
@@ -1224,8 +1232,8 @@ int64_t most_tiles(const KvArgs& a, const Plan& p) {
 // features (2048 tokens of 16 heads: 105 us when taken for two, 88 us).
 // For few rows, one round of them when there is little else to run, and chunks
 // of at most kMaxChunk, which evens out sequences of different lengths (16 of up
-// to 4096 tokens and 64 of grouped heads: 68 and 124 us, with 8192 81 and 168, with
-// 1024 65 and 128). For many rows, whose queries cost a block about as much as 512
+// to 4096 tokens and 64 of grouped heads: 65 and 122 us, with 4096 65 and 129, with
+// 1024 63 and 131). For many rows, whose queries cost a block about as much as 512
 // tokens do, only as many as fill one round (chunks of a quarter of that: 48 heads
 // of 4096 tokens 325 us against 261, a step of prompt chunks 240 against 195).
 Plan plan(const KvArgs& a, int q_heads) {
@@ -1283,7 +1291,7 @@ hipError_t launch_d(const KvArgs& a, const RotaryArgs& r, const AttnArgs& t, hip
     else
       e = launch_tiles<D, 16>(a, r, t, p, s);
   } else {
-    const dim3 grid((uint32_t)p.splits, (uint32_t)(p.tiles * a.kv_heads), (uint32_t)a.num_seqs);
+    const dim3 grid((uint32_t)(p.tiles * a.kv_heads), (uint32_t)a.num_seqs, (uint32_t)p.splits);
     if (t.slopes)
       k_kv_attn_rows<D, true><<<grid, kBlockThreads, 0, s>>>(a, r, t, p.group, p.tiles, p.splits,
                                                              p.chunk);

@@ -11,7 +11,7 @@ import pytest
 
 from int8_quantized_matmul_absmax_amd import build as B
 
-# (a copy of the tree for a GPU machine may lack the host-only files)
+# (skipped where the host-only files are absent)
 H = pytest.importorskip("tests.test_host_sanitizers")
 
 DRIVER = os.path.join(H.HERE, "kv_sanitizer_driver.cpp")
