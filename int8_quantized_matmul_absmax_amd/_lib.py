@@ -116,6 +116,8 @@ def load_library(path=None):
     over from torch are then valid in the library.
     """
     global _lib
+    if _lib is not None:   # (every call comes here: no lock once it is loaded)
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -449,7 +449,7 @@ __device__ __forceinline__ void list_factors(float k_absmax, float v_absmax, Blo
 // four waves of a block join through LDS, the blocks of a row tile through the
 // workspace and the kernels below. The weights go to the second product in two
 // parts of fp16: there is time for it. One token over each of 64 sequences of up to
-// 8192, 64 heads on 8 of 128 features (595 MB): 119 us, 5.0 TB/s, and 5 us to join;
+// 8192, 64 heads on 8 of 128 features (595 MB): 117 us, 5.1 TB/s, and 5 us to join;
 // over one of 131071, 32 heads on 8 (268 MB): 51 us, 5.3 TB/s, and 5 us. A large
 // copy moves 5.2 TB/s on the same card.
 template <int D, bool kAlibi>
