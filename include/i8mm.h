@@ -401,7 +401,9 @@ typedef struct i8mm_kv_cache {
  * page_tokens), n to max_tokens and to the rows below total_tokens; a page
  * outside [0, num_pages) is absent (nothing is written to it, no query sees
  * its tokens, it reads as 0); a token at a negative position (n > L) is not
- * stored, sees nothing and reads as 0.
+ * stored, sees nothing and reads as 0. Rows that belong to no sequence (past
+ * cu_tokens[num_seqs], or tokens beyond max_tokens) are not stored and get 0
+ * from attention and read.
  *
  * page_table int32 [num_seqs, max_pages], seq_lens int32 [num_seqs],
  * cu_tokens int32 [num_seqs + 1] ascending from 0, or NULL for one new token
@@ -483,8 +485,7 @@ I8MM_API int int8_kv_cache_append(const uint16_t* k, int64_t k_token_stride, int
  * product of weight and value absmax of their row, to fp16 where max_tokens *
  * q_heads / kv_heads is more than 48 (32 for D = 256), to two parts of fp16 (22
  * bits) where it is not; a value absmax below 2^-40 counts as 2^-40. Results do
- * not depend on what ran before. What rows of `out` that belong to no sequence
- * (past cu_tokens[num_seqs]) get is unspecified.
+ * not depend on what ran before.
  * Errors: EINVAL, EALIGN, EWORKSPACE, ENODEVICE, ELAUNCH.
  */
 I8MM_API int int8_kv_cache_attention(const uint16_t* q, int64_t q_token_stride,

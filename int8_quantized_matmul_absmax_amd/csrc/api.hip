@@ -546,6 +546,12 @@ bool heads_ok(const i8mm::KvArgs& a, int64_t q_heads) {
          a.total_tokens <= (int64_t{1} << 40) / q_heads;
 }
 
+// All rows of an output, where none belongs to a sequence.
+int zero_halfs(const char* fn, uint16_t* p, int64_t count, i8mm_stream_t stream) {
+  return launched(i8mm::launch_fill_u32(reinterpret_cast<uint32_t*>(p), count / 2, 0u,
+                                        (hipStream_t)stream), fn);
+}
+
 // 16-byte loads of 8 halfs at any token and head.
 int strides_check(const char* fn, const char* name, const void* p, bool required, int64_t ts,
                   int64_t hs) {
@@ -586,8 +592,13 @@ int int8_kv_cache_read(const i8mm_kv_cache* cache, const i8mm_kv_batch* batch, u
   I8MM_TRY(kv_check(fn, cache, batch, &a));
   I8MM_TRY(check_ptr(fn, "k", k, false));
   I8MM_TRY(check_ptr(fn, "v", v, false));
-  if ((!k && !v) || a.total_tokens == 0 || a.max_tokens == 0) return ok();
+  if ((!k && !v) || a.total_tokens == 0) return ok();
   I8MM_TRY(check_device());
+  if (a.max_tokens == 0) {
+    if (k) I8MM_TRY(zero_halfs(fn, k, (int64_t)a.total_tokens * a.kv_heads * a.head_dim, stream));
+    if (v) I8MM_TRY(zero_halfs(fn, v, (int64_t)a.total_tokens * a.kv_heads * a.head_dim, stream));
+    return ok();
+  }
   I8MM_TRY(launched(i8mm::launch_kv_read(a, k, v, (hipStream_t)stream), fn));
   return ok();
 }
@@ -631,8 +642,12 @@ int int8_kv_cache_attention(const uint16_t* q, int64_t q_token_stride, int64_t q
     if ((reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0)
       return fail(I8MM_EALIGN, "%s: workspace is not 256-byte aligned", fn);
   }
-  if (a.total_tokens == 0 || a.max_tokens == 0) return ok();
+  if (a.total_tokens == 0) return ok();
   I8MM_TRY(check_device());
+  if (a.max_tokens == 0) {
+    I8MM_TRY(zero_halfs(fn, out, a.total_tokens * q_heads * a.head_dim, stream));
+    return ok();
+  }
   i8mm::AttnArgs t;
   t.q = q;
   t.q_ts = q_token_stride;

@@ -54,6 +54,17 @@ __host__ __device__ __forceinline__ Parts parts_of(float* ws, int64_t rows, int 
   return p;
 }
 
+// Row r of the packed queries, which belongs to no sequence: its outputs are 0,
+// and there is nothing to join.
+template <int D>
+__device__ __forceinline__ void zero_row(const KvArgs& a, const AttnArgs& t, int64_t r, int splits,
+                                         int lane) {
+  zero_bytes(t.out + r * t.q_heads * D, 2 * t.q_heads * D, lane);
+  if (splits <= 1) return;
+  const Parts parts = parts_of(t.part, (int64_t)a.total_tokens * t.q_heads, splits, D);
+  for (int h = lane; h < t.q_heads; h += kWave) parts.count[r * t.q_heads + h] = 0;
+}
+
 // Visible tokens [lo, hi) of the query at position pos.
 __device__ __forceinline__ int visible_hi(const AttnArgs& t, const KvSeq& sq, int pos) {
   return pos < 0 ? 0 : t.causal ? min(pos + 1, sq.len) : sq.len;
@@ -474,6 +485,10 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
   const int h = blockIdx.x / tiles, b = blockIdx.y;
   const int r_first = (blockIdx.x % tiles) * kRows;
   const KvSeq sq = kv_seq(a, b);
+  if (blockIdx.z == 0)
+    for (int64_t r = (int64_t)sq.row0 + sq.n + blockIdx.x * (kBlockThreads / kWave) + wave;
+         r < sq.stop; r += gridDim.x * (kBlockThreads / kWave))
+      zero_row<D>(a, t, r, splits, lane);
   const int rows = sq.n * group;
   if (r_first >= rows) return;
   const int r_last = min(r_first + kRows, rows) - 1;
@@ -777,9 +792,30 @@ __device__ __forceinline__ Place place_of(const KvArgs& a, const AttnArgs& t, in
   return Place{b, __builtin_amdgcn_readlane(my_tiles, b) - 1 - in / s, in % s};
 }
 
+// The rows that belong to no sequence, over the waves of kZeroBlocks blocks.
+constexpr int kZeroBlocks = 32;
+template <int D>
+__device__ __forceinline__ void zero_rows(const KvArgs& a, const AttnArgs& t, int splits, int w,
+                                          int waves, int lane) {
+  for (int b0 = 0; b0 < a.num_seqs; b0 += kWave) {
+    int begin = 0, end = 0;
+    if (b0 + lane < a.num_seqs) {
+      const KvSeq sq = kv_seq(a, b0 + lane);
+      begin = sq.row0 + sq.n;
+      end = sq.stop;
+    }
+    for (uint64_t some = __ballot(begin < end); some; some &= some - 1) {
+      const int i = __builtin_ctzll(some), stop = __builtin_amdgcn_readlane(end, i);
+      for (int64_t r = (int64_t)__builtin_amdgcn_readlane(begin, i) + w; r < stop; r += waves)
+        zero_row<D>(a, t, r, splits, lane);
+    }
+  }
+}
+
+// Blocks from `work` on are kZeroBlocks for zero_rows.
 template <int D, int kR, bool kAlibi>
 __global__ __launch_bounds__((TileCfg<D, kR>::kThreads), 2) void k_kv_attn_tile(
-    KvArgs a, RotaryArgs rot, AttnArgs t, int group, int tiles, int splits, int chunk) {
+    KvArgs a, RotaryArgs rot, AttnArgs t, int group, int tiles, int splits, int chunk, int work) {
   typedef Stage<D> S;
   typedef TileCfg<D, kR> Cfg;
   constexpr int kC = Cfg::kC, kT = Cfg::kBlocks, kO = Cfg::kO;
@@ -792,6 +828,11 @@ __global__ __launch_bounds__((TileCfg<D, kR>::kThreads), 2) void k_kv_attn_tile(
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane % kR, g = lane / kR;            // row, lane group
   const int n16 = lane & 15, g16 = lane >> 4;
+  if ((int)blockIdx.x >= work) {
+    zero_rows<D>(a, t, splits, ((int)blockIdx.x - work) * Cfg::kWaves + wave,
+                 kZeroBlocks * Cfg::kWaves, lane);
+    return;
+  }
   const int h = blockIdx.x % a.kv_heads;
   const Place at = place_of(a, t, blockIdx.x / a.kv_heads, group, Cfg::kBlockRows, tiles, splits,
                             chunk, lane);
@@ -1108,8 +1149,7 @@ __global__ __launch_bounds__((TileCfg<D, kR>::kThreads), 2) void k_kv_attn_tile(
 }
 
 // The splits' sums of a row, weighed by their maxima, into the output of rows
-// with more than one. (Rows of the packed tensor that belong to no sequence have
-// no count: what they are given is unspecified, and bounded by `splits`.)
+// with more than one.
 // Up to kFewSplits: a lane takes four features, a wave several rows. Bound by
 // latency: 4096 rows of 128 features and up to 4 splits 4.9 us (a block a row 15).
 constexpr int kFewSplits = 16;
@@ -1270,14 +1310,15 @@ hipError_t launch_tiles(const KvArgs& a, const RotaryArgs& r, const AttnArgs& t,
   typedef TileCfg<D, kR> Cfg;
   if (p.tile_rows != Cfg::kBlockRows) return hipErrorInvalidValue;
   const int64_t jobs = a.num_seqs <= kWave ? most_tiles(a, p) : (int64_t)p.tiles * a.num_seqs;
-  const int64_t blocks = jobs * p.splits * a.kv_heads;
+  const int64_t work = jobs * p.splits * a.kv_heads;
+  const int64_t blocks = work + (a.cu_tokens ? kZeroBlocks : 0);
   if (blocks > INT32_MAX) return hipErrorInvalidValue;
   if (t.slopes)
     k_kv_attn_tile<D, kR, true><<<(uint32_t)blocks, Cfg::kThreads, 0, s>>>(
-        a, r, t, p.group, p.tiles, p.splits, p.chunk);
+        a, r, t, p.group, p.tiles, p.splits, p.chunk, (int)work);
   else
     k_kv_attn_tile<D, kR, false><<<(uint32_t)blocks, Cfg::kThreads, 0, s>>>(
-        a, r, t, p.group, p.tiles, p.splits, p.chunk);
+        a, r, t, p.group, p.tiles, p.splits, p.chunk, (int)work);
   return hipGetLastError();
 }
 

@@ -12,9 +12,11 @@ constexpr int kTile = 256;                // bytes of a 16 x 16 code tile
 // What the kernels take from a sequence's entries, bounded as the header
 // says, so that no content of the arrays reaches past a buffer: new tokens
 // are positions [first, len) (first < 0 for tokens before the sequence), rows
-// row0 .. row0 + n - 1 of the packed tensors.
+// row0 .. row0 + n - 1 of the packed tensors. The rows after them up to `stop`
+// belong to no sequence: tokens beyond max_tokens and, after the last sequence,
+// the rest.
 struct KvSeq {
-  int row0, n, len, first;
+  int row0, n, len, first, stop;
 };
 __device__ __forceinline__ KvSeq kv_seq(const KvArgs& a, int b) {
   KvSeq s;
@@ -27,7 +29,14 @@ __device__ __forceinline__ KvSeq kv_seq(const KvArgs& a, int b) {
   s.n = min(hi - lo, a.max_tokens);
   s.len = min(max(a.seq_lens[b], 0), a.len_cap);
   s.first = s.len - s.n;
+  s.stop = a.cu_tokens && b == a.num_seqs - 1 ? a.total_tokens : hi;
   return s;
+}
+
+// A wave writes zeros to `bytes` (a multiple of 16).
+__device__ __forceinline__ void zero_bytes(void* p, int bytes, int lane) {
+  for (int i = lane * 16; i < bytes; i += kWave * 16)
+    *reinterpret_cast<v4i32*>(static_cast<int8_t*>(p) + i) = v4i32{0, 0, 0, 0};
 }
 
 // Number of block `blk` (16 tokens) of sequence b for head h among all blocks

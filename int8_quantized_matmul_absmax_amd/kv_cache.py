@@ -102,7 +102,8 @@ class KVBatch:
     total_tokens, max_tokens, max_len  the host's figures: rows of the packed
                tensors (default: num_seqs, without cu_tokens), and bounds on a
                sequence's new tokens (default: total_tokens) and on its length
-               (default: what its row of the page table has room for)."""
+               (default: what its row of the page table has room for). Rows that
+               belong to no sequence get 0 from attention and read."""
 
     def __init__(self, page_table, seq_lens, cu_tokens=None, total_tokens=None, max_tokens=None,
                  max_len=None):

@@ -1,0 +1,88 @@
+"""The paged 8-bit key/value cache where sizes and contents meet limits."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv_cache as R
+from tests.gpu_helpers import dev, host, note
+from tests.test_gpu_cached_attention import build, empty_cache
+from tests.test_gpu_kv_cache import make
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------- packed rows without a sequence
+
+def padded(i8, cache, table, lens, counts, extra, max_tokens, max_len):
+    """A batch with `extra` rows past the last sequence's, each sequence's new
+    tokens cut to max_tokens. Also the rows that belong to a sequence, and how
+    many of each sequence's do."""
+    c = i8.Int8KVCache.from_tensors(*(dev(cache[n]) for n in
+                                      ("k_codes", "k_absmax", "v_codes", "v_absmax")))
+    cu = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    b = i8.KVBatch(dev(table), dev(np.array(lens, np.int32)), dev(cu),
+                   total_tokens=int(cu[-1]) + extra, max_tokens=max_tokens, max_len=max_len)
+    kept = [min(n, max_tokens) for n in counts]
+    rows = np.concatenate([np.arange(s, s + n) for s, n in zip(cu, kept)]).astype(int)
+    return c, b, rows, kept
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("counts,max_tokens", [
+    ([1, 1, 1], 1), ([3, 0, 1], 3), ([70, 1, 33], 70), ([70, 1, 33], 40), ([9, 1, 2], 4),
+    ([5, 2, 90], 64)])
+@pytest.mark.parametrize("splits", [False, True])
+def test_rows_of_no_sequence_are_zero(gpu, dim, counts, max_tokens, splits):
+    """Rows past the last sequence's and tokens beyond max_tokens give 0 from
+    attention and read, whatever the outputs and the workspace held."""
+    rng = np.random.default_rng(dim + sum(counts) + max_tokens)
+    lens = [200, 1, 640]
+    heads, kv_heads = 4, 2
+    cache, table = make(rng, lens, kv_heads, dim, 64)
+    if splits:      # a bound far above the lengths: many splits, which only few sequences fill
+        table = np.pad(table, ((0, 0), (0, 256 - table.shape[1])), constant_values=-1)
+    c, b, rows, kept = padded(gpu, cache, table, lens, counts, 21, max_tokens,
+                              64 * table.shape[1])
+    total = b.total_tokens
+    q = rng.normal(0, 1, (total, heads, dim)).astype(np.float16)
+    want, bound = R.attention(cache, q[rows], (table, lens, kept))
+    owned = np.zeros(total, bool)
+    owned[rows] = True
+    wk, wv = R.read(cache, (table, lens, kept))
+    need = gpu.ops.int8_kv_cache_attention_workspace_bytes(c, b, heads)
+    lib = gpu.load_library()
+    note("rows of no sequence: dim=%d counts=%s max_tokens=%d" % (dim, counts, max_tokens))
+    for poison in (1, 65):       # of the workspace: counts far above the splits, floats 2e-38 and 12
+        ws = torch.full((max(need, 1),), poison, dtype=torch.uint8, device="cuda")
+        out = torch.full((total, heads, dim), 1000.0, dtype=torch.float16, device="cuda")
+        got = host(gpu.ops.int8_kv_cache_attention(dev(q), c, b, workspace=ws, out=out))
+        assert (np.abs(got[owned].astype(np.float64) - want) <= bound).all()
+        assert not got[~owned].any()
+    k, v = torch.full((2, total, kv_heads, dim), 1000.0, dtype=torch.float16, device="cuda")
+    assert lib.int8_kv_cache_read(c.ref, b.ref, k.data_ptr(), v.data_ptr(),
+                                  torch.cuda.current_stream().cuda_stream) == 0
+    assert np.array_equal(host(k)[rows], wk) and np.array_equal(host(v)[rows], wv)
+    assert not host(k)[~owned].any() and not host(v)[~owned].any()
+
+
+def test_layer_ignores_rows_of_no_sequence(gpu):
+    """The output projection picks its outlier columns over all rows: padded ones
+    give it zeros, so the rows of sequences do not depend on what memory held."""
+    rng = np.random.default_rng(3)
+    layer, seen, _ = build(gpu, rng, 256, 4, 2, 64)
+    table = np.arange(12, dtype=np.int32).reshape(2, 6)
+    x = np.zeros((64, 256), np.float16)
+    x[:31] = rng.normal(0, 1, (31, 256))
+    outs = []
+    for poison in (0.0, 1000.0):
+        cache, _ = empty_cache(gpu, 12, 2, 64, 32)
+        b = gpu.KVBatch(dev(table), dev(np.array([30, 1], np.int32)),
+                        dev(np.array([0, 30, 31], np.int32)), total_tokens=64, max_tokens=40)
+        # every block that the step may be given holds the poison
+        held = [torch.full((n,), poison, dtype=torch.float16, device="cuda")
+                for n in (64 * 256, 64 * 512, 1 << 18, 1 << 20) for _ in range(6)]
+        del held
+        outs.append(host(layer(dev(x), cache, b))[:31])
+        assert not host(seen["a"])[31:].any()
+    assert np.array_equal(*outs)
