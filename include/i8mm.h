@@ -467,7 +467,8 @@ I8MM_API int int8_kv_cache_append(const uint16_t* k, int64_t k_token_stride, int
  * at position p:
  *   S_t = scale * <q, k_t> - slope_h * (p - t),  O = sum_t softmax(S)_t v_t
  * over the visible tokens t < L: t <= p when causal, and t > p - window when
- * window > 0. A query that sees no token gets O = 0.
+ * window > 0. A query that sees no token gets O = 0; one with a NaN or an
+ * infinity gets NaN where it sees any.
  *
  *   q        fp16 [total_tokens, q_heads, D], strides as for append; rotated
  *            here when `rotary` is given.

@@ -241,7 +241,10 @@ __device__ __forceinline__ void store_query(const float (&x)[16], uint32_t top,
     lds_store(dst + e[r], hi);
     lds_store(dst + 64 * QueryCfg<D>::kC + e[r], lo);
   }
-  if (e[0] == 0) lds_store(factor, a * (1.0f / 16256.0f));
+  // An infinity leaves nothing of the row's integers to go by (inf * 0 in their
+  // place): its logits are NaN or infinities of either sign, its outputs NaN.
+  const float f = top < 0x7f800000u ? a * (1.0f / 16256.0f) : __builtin_nanf("");
+  if (e[0] == 0) lds_store(factor, f);
 }
 // kPasses rows of a lane together (their reductions overlap).
 template <int D, int kPasses>

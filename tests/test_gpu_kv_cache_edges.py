@@ -7,7 +7,7 @@ import torch
 from oracle import kv_cache as R
 from tests.gpu_helpers import dev, host, note
 from tests.test_gpu_cached_attention import build, empty_cache
-from tests.test_gpu_kv_cache import make
+from tests.test_gpu_kv_cache import make, on_gpu, tables
 
 pytestmark = pytest.mark.gpu
 
@@ -86,3 +86,33 @@ def test_layer_ignores_rows_of_no_sequence(gpu):
         outs.append(host(layer(dev(x), cache, b))[:31])
         assert not host(seen["a"])[31:].any()
     assert np.array_equal(*outs)
+
+
+# ---------------------------------------------------------- infinite queries
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("value", [np.inf, -np.inf, np.nan])
+@pytest.mark.parametrize("count,heads", [(1, 2), (60, 2), (200, 4)])
+def test_infinite_query_is_nan_whatever_the_keys(gpu, interleaved, value, count, heads):
+    """A rotated query with an infinity, over keys of one sign: its row is NaN
+    where it sees a token and 0 where it sees none; no other row changes."""
+    rng = np.random.default_rng(31)
+    lens, dim = [count + 3], 64
+    for sign in (1, -1):
+        cache, table = make(rng, lens, 1, dim, 64)
+        cache["k_codes"] = (sign * np.maximum(np.abs(cache["k_codes"]), 1)).astype(np.int8)
+        q = np.abs(rng.normal(0, 1, (count, heads, dim))).astype(np.float16)
+        cos, sin = tables(dim, lens[0] + 1)
+        rot = gpu.Rotary(dev(cos), dev(sin), interleaved)
+        want, bound = R.attention(cache, q, (table, lens, [count]), cos, sin, interleaved)
+        bad = np.zeros((count, heads), bool)
+        for i in {0, count // 2, count - 1}:
+            bad[i, i % heads] = True
+            q[i, i % heads, 6] = value
+        c, b = on_gpu(gpu, cache, table, lens, [count], max_len=lens[0])
+        got = host(c.attention(dev(q), b, rot)).astype(np.float64)
+        assert np.isnan(got[bad]).all()
+        assert (np.abs(got - want) <= bound)[~bad].all()
+        absent = np.full_like(table, -1)
+        c, b = on_gpu(gpu, cache, absent, lens, [count], max_len=lens[0])
+        assert not host(c.attention(dev(q), b, rot)).any()
