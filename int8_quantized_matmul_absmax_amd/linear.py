@@ -35,14 +35,20 @@ INT8_FORMAT = "llm-int8/per-output-row-absmax/v1"
 # workspace, not one per module. Calls on different streams get their own.
 # Each call takes the prefix of the layer's own size, so the layer's path
 # (and its result bits) do not depend on which layers ran before.
+# A call that is recorded into a graph gets one from the graph's own memory
+# pool instead, and nothing else keeps it: the shared one is replaced when a
+# larger call comes, and the graph's replays go on writing where it recorded.
 _WS_LOCK = threading.Lock()
 _WORKSPACES = {}
 
 
 def shared_workspace(device, nbytes):
     """The shared workspace of the current stream on `device`, grown to at
-    least nbytes (uint8 tensor)."""
+    least nbytes (uint8 tensor). While the stream is being captured, one of the
+    graph's own."""
     device = torch.device(device)
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty((max(int(nbytes), 1),), dtype=torch.uint8, device=device)
     key = (device.index, torch.cuda.current_stream(device).cuda_stream)
     with _WS_LOCK:
         ws = _WORKSPACES.get(key)

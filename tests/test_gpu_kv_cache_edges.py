@@ -116,3 +116,46 @@ def test_infinite_query_is_nan_whatever_the_keys(gpu, interleaved, value, count,
         absent = np.full_like(table, -1)
         c, b = on_gpu(gpu, cache, absent, lens, [count], max_len=lens[0])
         assert not host(c.attention(dev(q), b, rot)).any()
+
+
+# ------------------------------------------------------------ recorded steps
+
+def test_recorded_step_after_larger_calls(gpu):
+    """A recorded step, then larger eager calls on the stream it was recorded on,
+    which replace the stream's shared workspace: the replays give what they gave,
+    and write to nothing else."""
+    rng = np.random.default_rng(51)
+    layer, _, _ = build(gpu, rng, 256, 4, 2, 64)
+    cache, _ = empty_cache(gpu, 160, 2, 64, 64)
+    table = dev(np.arange(160, dtype=np.int32).reshape(2, 80))
+    prompt = gpu.KVBatch(table, dev(np.array([4000, 1500], np.int32)),
+                         dev(np.array([0, 4000, 5500], np.int32)), total_tokens=5500,
+                         max_tokens=4000)
+    tokens = gpu.KVBatch(table, dev(np.array([4001, 1501], np.int32)))
+    many = dev(rng.normal(0, 1, (5500, 256)).astype(np.float16))
+    x = dev(rng.normal(0, 1, (2, 256)).astype(np.float16))
+    layer(many, cache, prompt)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        want = layer(x, cache, tokens).clone()
+        layer(x, cache, tokens)
+    side.synchronize()
+    assert gpu.ops.int8_kv_cache_attention_workspace_bytes(cache, tokens, 4) > 0
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        y = layer(x, cache, tokens)
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            layer(many, cache, prompt)
+            layer(x, cache, tokens)
+            # whatever the stream's allocator has free now belongs to these
+            others = [torch.full((n,), 77, dtype=torch.uint8, device="cuda")
+                      for n in (1 << 10, 1 << 14, 1 << 17, 1 << 19, 1 << 20, 1 << 22, 1 << 24)
+                      for _ in range(4)]
+            y.fill_(5)
+            g.replay()
+        side.synchronize()
+        assert torch.equal(y, want)
+        assert all(bool((t == 77).all()) for t in others)
+        del others
