@@ -546,6 +546,11 @@ bool heads_ok(const i8mm::KvArgs& a, int64_t q_heads) {
          a.total_tokens <= (int64_t{1} << 40) / q_heads;
 }
 
+// No row of the packed tensors belongs to a sequence.
+bool no_tokens(const i8mm::KvArgs& a) {
+  return a.total_tokens == 0 || a.max_tokens == 0 || a.num_seqs == 0;
+}
+
 // All rows of an output, where none belongs to a sequence.
 int zero_halfs(const char* fn, uint16_t* p, int64_t count, i8mm_stream_t stream) {
   return launched(i8mm::launch_fill_u32(reinterpret_cast<uint32_t*>(p), count / 2, 0u,
@@ -577,7 +582,7 @@ int int8_kv_cache_append(const uint16_t* k, int64_t k_token_stride, int64_t k_he
   I8MM_TRY(rotary_check(fn, rotary, a, &r));
   I8MM_TRY(strides_check(fn, "k", k, a.total_tokens > 0, k_token_stride, k_head_stride));
   I8MM_TRY(strides_check(fn, "v", v, a.total_tokens > 0, v_token_stride, v_head_stride));
-  if (a.total_tokens == 0 || a.max_tokens == 0 || a.len_cap == 0 || a.num_pages == 0) return ok();
+  if (no_tokens(a) || a.len_cap == 0 || a.num_pages == 0) return ok();
   I8MM_TRY(check_device());
   I8MM_TRY(launched(i8mm::launch_kv_append(k, k_token_stride, k_head_stride, v, v_token_stride,
                                            v_head_stride, a, r, (hipStream_t)stream),
@@ -594,7 +599,7 @@ int int8_kv_cache_read(const i8mm_kv_cache* cache, const i8mm_kv_batch* batch, u
   I8MM_TRY(check_ptr(fn, "v", v, false));
   if ((!k && !v) || a.total_tokens == 0) return ok();
   I8MM_TRY(check_device());
-  if (a.max_tokens == 0) {
+  if (no_tokens(a)) {
     if (k) I8MM_TRY(zero_halfs(fn, k, (int64_t)a.total_tokens * a.kv_heads * a.head_dim, stream));
     if (v) I8MM_TRY(zero_halfs(fn, v, (int64_t)a.total_tokens * a.kv_heads * a.head_dim, stream));
     return ok();
@@ -644,7 +649,7 @@ int int8_kv_cache_attention(const uint16_t* q, int64_t q_token_stride, int64_t q
   }
   if (a.total_tokens == 0) return ok();
   I8MM_TRY(check_device());
-  if (a.max_tokens == 0) {
+  if (no_tokens(a)) {
     I8MM_TRY(zero_halfs(fn, out, a.total_tokens * q_heads * a.head_dim, stream));
     return ok();
   }

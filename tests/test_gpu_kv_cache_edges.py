@@ -159,3 +159,27 @@ def test_recorded_step_after_larger_calls(gpu):
         assert torch.equal(y, want)
         assert all(bool((t == 77).all()) for t in others)
         del others
+
+
+# ------------------------------------------------------------- empty batches
+
+@pytest.mark.parametrize("max_tokens", [0, 5])
+@pytest.mark.parametrize("seqs", [0, 2])
+def test_padding_alone(gpu, seqs, max_tokens):
+    """No sequences, or none with new tokens: append does nothing, every row of
+    attention and read is 0."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    c = gpu.Int8KVCache(2, 2, 64)
+    for t in (c.k_codes, c.v_codes, c.k_absmax, c.v_absmax):
+        t.fill_(3)
+    b = gpu.KVBatch(torch.zeros((seqs, 1), **i32), torch.full((seqs,), 9, **i32),
+                    torch.zeros((seqs + 1,), **i32), total_tokens=5, max_tokens=max_tokens)
+    x = torch.ones((5, 2, 64), dtype=torch.float16, device="cuda")
+    c.append(x, x, b)
+    assert all((t == 3).all() for t in (c.k_codes, c.v_codes, c.k_absmax, c.v_absmax))
+    out = torch.full((5, 4, 64), 7.0, dtype=torch.float16, device="cuda")
+    assert not c.attention(x.repeat(1, 2, 1), b, out=out).any()
+    held = [torch.full_like(x, 7.0) for _ in range(4)]     # what read is given next holds 7
+    del held
+    k, v = c.read(b)
+    assert k.shape == x.shape and not k.any() and not v.any()
