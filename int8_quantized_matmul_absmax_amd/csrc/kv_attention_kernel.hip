@@ -763,21 +763,53 @@ __device__ __forceinline__ void read_key_tile(const int8_t* st, int n, int g, in
 // (causal rows see more tokens the later they are): what starts last should be
 // short. Blocks without work come last: among the others, they upset the turns
 // in which blocks go to compute units (a step of mixed prompt chunks took
-// twice as long). A wave's lanes hold a sequence each; beyond 64 sequences
-// they are taken in order, each with the most tiles and splits there can be.
+// twice as long). A wave's lanes hold a sequence each, up to 64 of them.
 struct Place {
   int b, tile, split;   // b < 0: nothing to do
 };
+
+// More than 64 sequences are taken in order, split by split. Tiles of packed rows:
+// sequence b's begin at slot floor(cu_tokens[b] group / kTileRows) + b, so each
+// has room for its own and at most one is empty, and the sequence of a slot is
+// found by a search of 64 probes at once.
+template <int kTileRows>
+__host__ __device__ __forceinline__ int64_t first_slot(int64_t row, int group, int b) {
+  return row * group / kTileRows + b;
+}
+template <int kTileRows>
+__device__ __forceinline__ Place place_among_many(const KvArgs& a, int job, int group, int lane) {
+  const int slots = (int)first_slot<kTileRows>(a.total_tokens, group, a.num_seqs);
+  const int split = job / slots, slot = job - split * slots;
+  int b = 0;   // of [b, b + size), the last whose tiles begin at `slot` or before
+  for (int size = a.num_seqs; size > 0;) {
+    const int step = (size + kWave - 1) / kWave, ahead = lane * step;
+    bool before = false;
+    if (ahead < size) {
+      const int at = b + ahead;
+      const int row = a.cu_tokens ? min(max(a.cu_tokens[at], 0), a.total_tokens) : at;
+      before = first_slot<kTileRows>(row, group, at) <= slot;
+    }
+    const uint64_t some = __ballot(before);
+    if (!some) return Place{-1, 0, 0};
+    const int skip = (63 - __builtin_clzll(some)) * step;
+    b += skip;
+    size = step > 1 ? min(step, size - skip) : 0;
+  }
+  const KvSeq sq = kv_seq(a, b);
+  const int tile = slot - (int)first_slot<kTileRows>(sq.row0, group, b);
+  const int own = (int)(((int64_t)sq.n * group + kTileRows - 1) / kTileRows);
+  return tile < own ? Place{b, own - 1 - tile, split} : Place{-1, 0, 0};
+}
+
+template <int kTileRows>
 __device__ __forceinline__ Place place_of(const KvArgs& a, const AttnArgs& t, int job, int group,
-                                          int tile_rows, int tiles, int splits, int chunk,
-                                          int lane) {
-  if (a.num_seqs > kWave)
-    return Place{job / (tiles * splits), tiles - 1 - job % (tiles * splits) / splits, job % splits};
+                                          int chunk, int lane) {
+  if (a.num_seqs > kWave) return place_among_many<kTileRows>(a, job, group, lane);
   int my_tiles = 0, my_splits = 0, len = -1;
   if (lane < a.num_seqs) {
     const KvSeq sq = kv_seq(a, lane);
     len = sq.len;
-    my_tiles = (sq.n * group + tile_rows - 1) / tile_rows;
+    my_tiles = (sq.n * group + kTileRows - 1) / kTileRows;
     int seen = t.window > 0 ? min(len, t.window + sq.n) + kGroup : len;
     my_splits = max((seen + chunk - 1) / chunk, 1);
   }
@@ -818,7 +850,7 @@ __device__ __forceinline__ void zero_rows(const KvArgs& a, const AttnArgs& t, in
 // Blocks from `work` on are kZeroBlocks for zero_rows.
 template <int D, int kR, bool kAlibi>
 __global__ __launch_bounds__((TileCfg<D, kR>::kThreads), 2) void k_kv_attn_tile(
-    KvArgs a, RotaryArgs rot, AttnArgs t, int group, int tiles, int splits, int chunk, int work) {
+    KvArgs a, RotaryArgs rot, AttnArgs t, int group, int splits, int chunk, int work) {
   typedef Stage<D> S;
   typedef TileCfg<D, kR> Cfg;
   constexpr int kC = Cfg::kC, kT = Cfg::kBlocks, kO = Cfg::kO;
@@ -837,8 +869,8 @@ __global__ __launch_bounds__((TileCfg<D, kR>::kThreads), 2) void k_kv_attn_tile(
     return;
   }
   const int h = blockIdx.x % a.kv_heads;
-  const Place at = place_of(a, t, blockIdx.x / a.kv_heads, group, Cfg::kBlockRows, tiles, splits,
-                            chunk, lane);
+  const Place at =
+      place_of<Cfg::kBlockRows>(a, t, blockIdx.x / a.kv_heads, group, chunk, lane);
   const int b = at.b;
   if (b < 0) return;
   const KvSeq sq = kv_seq(a, b);
@@ -1312,16 +1344,18 @@ hipError_t launch_tiles(const KvArgs& a, const RotaryArgs& r, const AttnArgs& t,
                         hipStream_t s) {
   typedef TileCfg<D, kR> Cfg;
   if (p.tile_rows != Cfg::kBlockRows) return hipErrorInvalidValue;
-  const int64_t jobs = a.num_seqs <= kWave ? most_tiles(a, p) : (int64_t)p.tiles * a.num_seqs;
+  const int64_t jobs = a.num_seqs <= kWave
+                           ? most_tiles(a, p)
+                           : first_slot<Cfg::kBlockRows>(a.total_tokens, p.group, a.num_seqs);
   const int64_t work = jobs * p.splits * a.kv_heads;
   const int64_t blocks = work + (a.cu_tokens ? kZeroBlocks : 0);
-  if (blocks > INT32_MAX) return hipErrorInvalidValue;
+  if (blocks > UINT32_MAX / Cfg::kThreads) return hipErrorInvalidValue;
   if (t.slopes)
     k_kv_attn_tile<D, kR, true><<<(uint32_t)blocks, Cfg::kThreads, 0, s>>>(
-        a, r, t, p.group, p.tiles, p.splits, p.chunk, (int)work);
+        a, r, t, p.group, p.splits, p.chunk, (int)work);
   else
     k_kv_attn_tile<D, kR, false><<<(uint32_t)blocks, Cfg::kThreads, 0, s>>>(
-        a, r, t, p.group, p.tiles, p.splits, p.chunk, (int)work);
+        a, r, t, p.group, p.splits, p.chunk, (int)work);
   return hipGetLastError();
 }
 

@@ -7,7 +7,7 @@ import torch
 from oracle import kv_cache as R
 from tests.gpu_helpers import dev, host, note
 from tests.test_gpu_cached_attention import build, empty_cache
-from tests.test_gpu_kv_cache import make, on_gpu, tables
+from tests.test_gpu_kv_cache import check_attention, make, on_gpu, tables, widen
 
 pytestmark = pytest.mark.gpu
 
@@ -183,3 +183,73 @@ def test_padding_alone(gpu, seqs, max_tokens):
     del held
     k, v = c.read(b)
     assert k.shape == x.shape and not k.any() and not v.any()
+
+
+# ------------------------------------------------------------ many sequences
+
+def test_many_sequences_with_a_wide_bound(gpu):
+    """60000 single tokens whose launch bound is the packed rows' total: the work
+    is small, and so is the launch. Against the same sequences a few at a time."""
+    rng = np.random.default_rng(41)
+    seqs, total, heads, dim, page = 60000, 80000, 64, 64, 16
+    cache, _ = make(rng, [16 * 40], 1, dim, page, spare=0)
+    table = rng.integers(0, 40, (seqs, 1)).astype(np.int32)       # shared pages
+    lens = rng.integers(1, 17, seqs).astype(np.int32)
+    c = gpu.Int8KVCache.from_tensors(*(dev(cache[n]) for n in
+                                       ("k_codes", "k_absmax", "v_codes", "v_absmax")))
+    cu = torch.arange(seqs + 1, dtype=torch.int32, device="cuda")
+    b = gpu.KVBatch(dev(table), dev(lens), cu, total_tokens=total)
+    q = torch.randn((total, heads, dim), dtype=torch.float16, device="cuda",
+                    generator=torch.Generator("cuda").manual_seed(1))
+    note("60000 sequences")
+    got = c.attention(q, b)
+    assert not got[seqs:].any()
+    some = np.unique(np.concatenate([[0, 1, 63, 64, 65, 4095, 4096, seqs - 2, seqs - 1],
+                                     rng.integers(0, seqs, 40)]))
+    at = torch.from_numpy(some).cuda()
+    want, bound = R.attention(cache, host(q[at]), (table[some], lens[some], [1] * len(some)))
+    assert (np.abs(host(got[at]).astype(np.float64) - want) <= bound).all()
+
+
+@pytest.mark.parametrize("dim", [64, 96, 128, 256])
+@pytest.mark.parametrize("seqs", [65, 130, 300])
+@pytest.mark.parametrize("kw", [{}, {"window": 50}, {"wide": True}])
+def test_more_sequences_than_a_wave_has_lanes(gpu, dim, seqs, kw):
+    """Single tokens, chunks and sequences without new tokens, more than 64 of
+    them, over prefixes of several splits."""
+    kw = dict(kw)
+    rng = np.random.default_rng(seqs + dim)
+    counts = rng.choice([0, 1, 1, 1, 2], seqs)
+    counts[rng.choice(seqs, 3, replace=False)] = [40, 129, 90]
+    counts[-1] = 65
+    lens = counts + rng.integers(0, 30, seqs)
+    lens[[0, seqs // 2, seqs - 1]] += 1100
+    counts, lens = counts.tolist(), lens.tolist()
+    cache = make(rng, lens, 2, dim, 32)
+    if kw.pop("wide", False):
+        cache, kw["max_len"] = widen(cache, 32), 1 << 20
+    check_attention(gpu, rng, lens, counts, heads=4, dim=dim, page=32, cache=cache, **kw)
+
+
+@pytest.mark.parametrize("cut", [0, 7])
+def test_many_sequences_of_one_token_or_cut(gpu, cut):
+    """65 and more sequences without cu_tokens, and with new tokens beyond
+    max_tokens, of 64 query heads on one."""
+    rng = np.random.default_rng(61 + cut)
+    seqs, heads, dim = 90, 64, 64
+    lens = rng.integers(1, 200, seqs).tolist()
+    cache, table = make(rng, lens, 1, dim, 16)
+    if not cut:
+        q = rng.normal(0, 1, (seqs, heads, dim)).astype(np.float16)
+        c, _, _, _ = padded(gpu, cache, table, lens, [1] * seqs, 0, 1, 200)
+        b = gpu.KVBatch(dev(table), dev(np.array(lens, np.int32)), max_len=200)
+        rows, kept = np.arange(seqs), [1] * seqs
+    else:
+        counts = rng.integers(0, 2 * cut, seqs).tolist()
+        c, b, rows, kept = padded(gpu, cache, table, lens, counts, 3, cut, 200)
+        q = rng.normal(0, 1, (b.total_tokens, heads, dim)).astype(np.float16)
+    want, bound = R.attention(cache, q[rows], (table, lens, kept))
+    out = torch.full(q.shape, 9.0, dtype=torch.float16, device="cuda")
+    got = host(c.attention(dev(q), b, out=out)).astype(np.float64)
+    assert (np.abs(got[rows] - want) <= bound).all()
+    assert not np.delete(got, rows, axis=0).any()
