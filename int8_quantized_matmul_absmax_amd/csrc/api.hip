@@ -538,11 +538,13 @@ int rotary_check(const char* fn, const i8mm_rotary* r, const i8mm::KvArgs& a,
   return I8MM_OK;
 }
 
-// The queries that share a key/value head are rows, numbered in int32; the rows
-// of all heads are few enough for the workspace's bytes to stay in 64 bits.
+// The queries that share a key/value head are rows, numbered in int32, those of
+// a sequence up to half of it; the rows of all heads are few enough for the
+// workspace's bytes to stay in 64 bits.
 bool heads_ok(const i8mm::KvArgs& a, int64_t q_heads) {
   return q_heads > 0 && q_heads <= 65535 && q_heads % a.kv_heads == 0 &&
          a.max_tokens <= INT32_MAX / 2 / (q_heads / a.kv_heads) &&
+         a.total_tokens <= (INT32_MAX - 65536) / (q_heads / a.kv_heads) &&
          a.total_tokens <= (int64_t{1} << 40) / q_heads;
 }
 

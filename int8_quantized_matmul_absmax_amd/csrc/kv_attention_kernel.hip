@@ -54,15 +54,17 @@ __host__ __device__ __forceinline__ Parts parts_of(float* ws, int64_t rows, int 
   return p;
 }
 
-// Row r of the packed queries, which belongs to no sequence: its outputs are 0,
-// and there is nothing to join.
+// Rows [r, end) of a key/value head, counted on past a sequence's own, belong to
+// none: their outputs are 0, and there is nothing to join. One wave.
 template <int D>
-__device__ __forceinline__ void zero_row(const KvArgs& a, const AttnArgs& t, int64_t r, int splits,
-                                         int lane) {
-  zero_bytes(t.out + r * t.q_heads * D, 2 * t.q_heads * D, lane);
-  if (splits <= 1) return;
+__device__ __forceinline__ void zero_rows(const KvArgs& a, const AttnArgs& t, const KvSeq& sq, int h,
+                                          int group, int splits, int r, int end, int lane) {
   const Parts parts = parts_of(t.part, (int64_t)a.total_tokens * t.q_heads, splits, D);
-  for (int h = lane; h < t.q_heads; h += kWave) parts.count[r * t.q_heads + h] = 0;
+  for (; r < end; ++r) {
+    const int64_t row = (int64_t)(sq.row0 + r / group) * t.q_heads + h * group + r % group;
+    if (lane < D / 8) *reinterpret_cast<v4i32*>(t.out + row * D + lane * 8) = v4i32{0, 0, 0, 0};
+    if (splits > 1 && lane == 0) parts.count[row] = 0;
+  }
 }
 
 // Visible tokens [lo, hi) of the query at position pos.
@@ -488,11 +490,21 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
   const int h = blockIdx.x / tiles, b = blockIdx.y;
   const int r_first = (blockIdx.x % tiles) * kRows;
   const KvSeq sq = kv_seq(a, b);
-  if (blockIdx.z == 0)
-    for (int64_t r = (int64_t)sq.row0 + sq.n + blockIdx.x * (kBlockThreads / kWave) + wave;
-         r < sq.stop; r += gridDim.x * (kBlockThreads / kWave))
-      zero_row<D>(a, t, r, splits, lane);
   const int rows = sq.n * group;
+  if (sq.row0 + sq.n < sq.stop) {
+    // the rows after the sequence's that belong to none, over all its blocks: their
+    // outputs are 0, and there is nothing to join
+    const int64_t first = (int64_t)(sq.row0 + sq.n) * t.q_heads;
+    const int64_t past = (int64_t)sq.stop * t.q_heads;
+    const int64_t threads = (int64_t)gridDim.x * gridDim.z * kBlockThreads;
+    const int64_t at = ((int64_t)blockIdx.z * gridDim.x + blockIdx.x) * kBlockThreads + threadIdx.x;
+    for (int64_t i = first * (D / 8) + at; i < past * (D / 8); i += threads)
+      *reinterpret_cast<v4i32*>(t.out + i * 8) = v4i32{0, 0, 0, 0};
+    if (splits > 1) {
+      const Parts parts = parts_of(t.part, (int64_t)a.total_tokens * t.q_heads, splits, D);
+      for (int64_t i = first + at; i < past; i += threads) parts.count[i] = 0;
+    }
+  }
   if (r_first >= rows) return;
   const int r_last = min(r_first + kRows, rows) - 1;
   const Span span = row_span(t, sq, r_first / group, r_last / group);
@@ -768,6 +780,12 @@ struct Place {
   int b, tile, split;   // b < 0: nothing to do
 };
 
+// Tiles of a sequence and of the rows after it that belong to none.
+template <int kTileRows>
+__device__ __forceinline__ int tiles_of(const KvSeq& sq, int group) {
+  return ((sq.stop - sq.row0) * group + kTileRows - 1) / kTileRows;
+}
+
 // More than 64 sequences are taken in order, split by split. Tiles of packed rows:
 // sequence b's begin at slot floor(cu_tokens[b] group / kTileRows) + b, so each
 // has room for its own and at most one is empty, and the sequence of a slot is
@@ -797,19 +815,20 @@ __device__ __forceinline__ Place place_among_many(const KvArgs& a, int job, int 
   }
   const KvSeq sq = kv_seq(a, b);
   const int tile = slot - (int)first_slot<kTileRows>(sq.row0, group, b);
-  const int own = (int)(((int64_t)sq.n * group + kTileRows - 1) / kTileRows);
+  const int own = tiles_of<kTileRows>(sq, group);
   return tile < own ? Place{b, own - 1 - tile, split} : Place{-1, 0, 0};
 }
 
 template <int kTileRows>
 __device__ __forceinline__ Place place_of(const KvArgs& a, const AttnArgs& t, int job, int group,
                                           int chunk, int lane) {
-  if (a.num_seqs > kWave) return place_among_many<kTileRows>(a, job, group, lane);
+  // (marked as rare, or a step of chunks takes 2% longer)
+  if (__builtin_expect(a.num_seqs > kWave, 0)) return place_among_many<kTileRows>(a, job, group, lane);
   int my_tiles = 0, my_splits = 0, len = -1;
   if (lane < a.num_seqs) {
     const KvSeq sq = kv_seq(a, lane);
     len = sq.len;
-    my_tiles = (sq.n * group + kTileRows - 1) / kTileRows;
+    my_tiles = tiles_of<kTileRows>(sq, group);
     int seen = t.window > 0 ? min(len, t.window + sq.n) + kGroup : len;
     my_splits = max((seen + chunk - 1) / chunk, 1);
   }
@@ -827,30 +846,9 @@ __device__ __forceinline__ Place place_of(const KvArgs& a, const AttnArgs& t, in
   return Place{b, __builtin_amdgcn_readlane(my_tiles, b) - 1 - in / s, in % s};
 }
 
-// The rows that belong to no sequence, over the waves of kZeroBlocks blocks.
-constexpr int kZeroBlocks = 32;
-template <int D>
-__device__ __forceinline__ void zero_rows(const KvArgs& a, const AttnArgs& t, int splits, int w,
-                                          int waves, int lane) {
-  for (int b0 = 0; b0 < a.num_seqs; b0 += kWave) {
-    int begin = 0, end = 0;
-    if (b0 + lane < a.num_seqs) {
-      const KvSeq sq = kv_seq(a, b0 + lane);
-      begin = sq.row0 + sq.n;
-      end = sq.stop;
-    }
-    for (uint64_t some = __ballot(begin < end); some; some &= some - 1) {
-      const int i = __builtin_ctzll(some), stop = __builtin_amdgcn_readlane(end, i);
-      for (int64_t r = (int64_t)__builtin_amdgcn_readlane(begin, i) + w; r < stop; r += waves)
-        zero_row<D>(a, t, r, splits, lane);
-    }
-  }
-}
-
-// Blocks from `work` on are kZeroBlocks for zero_rows.
 template <int D, int kR, bool kAlibi>
 __global__ __launch_bounds__((TileCfg<D, kR>::kThreads), 2) void k_kv_attn_tile(
-    KvArgs a, RotaryArgs rot, AttnArgs t, int group, int splits, int chunk, int work) {
+    KvArgs a, RotaryArgs rot, AttnArgs t, int group, int splits, int chunk) {
   typedef Stage<D> S;
   typedef TileCfg<D, kR> Cfg;
   constexpr int kC = Cfg::kC, kT = Cfg::kBlocks, kO = Cfg::kO;
@@ -863,11 +861,6 @@ __global__ __launch_bounds__((TileCfg<D, kR>::kThreads), 2) void k_kv_attn_tile(
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane % kR, g = lane / kR;            // row, lane group
   const int n16 = lane & 15, g16 = lane >> 4;
-  if ((int)blockIdx.x >= work) {
-    zero_rows<D>(a, t, splits, ((int)blockIdx.x - work) * Cfg::kWaves + wave,
-                 kZeroBlocks * Cfg::kWaves, lane);
-    return;
-  }
   const int h = blockIdx.x % a.kv_heads;
   const Place at =
       place_of<Cfg::kBlockRows>(a, t, blockIdx.x / a.kv_heads, group, chunk, lane);
@@ -876,6 +869,11 @@ __global__ __launch_bounds__((TileCfg<D, kR>::kThreads), 2) void k_kv_attn_tile(
   const KvSeq sq = kv_seq(a, b);
   const int rows = sq.n * group;
   const int blk_first = at.tile * Cfg::kBlockRows;
+  const bool zeros = blk_first + Cfg::kBlockRows > rows && sq.row0 + sq.n < sq.stop && at.split == 0;
+  if (__builtin_expect(zeros, 0)) {
+    const int r = blk_first + wave * kR, all = (sq.stop - sq.row0) * group;
+    zero_rows<D>(a, t, sq, h, group, splits, max(r, rows), min(r + kR, all), lane);
+  }
   if (blk_first >= rows) return;
   const int blk_last = min(blk_first + Cfg::kBlockRows, rows) - 1;
   const Span span = row_span(t, sq, blk_first / group, blk_last / group);
@@ -1344,18 +1342,18 @@ hipError_t launch_tiles(const KvArgs& a, const RotaryArgs& r, const AttnArgs& t,
                         hipStream_t s) {
   typedef TileCfg<D, kR> Cfg;
   if (p.tile_rows != Cfg::kBlockRows) return hipErrorInvalidValue;
-  const int64_t jobs = a.num_seqs <= kWave
+  // (without cu_tokens every row belongs to a sequence)
+  const int64_t jobs = a.num_seqs <= kWave && !a.cu_tokens
                            ? most_tiles(a, p)
                            : first_slot<Cfg::kBlockRows>(a.total_tokens, p.group, a.num_seqs);
-  const int64_t work = jobs * p.splits * a.kv_heads;
-  const int64_t blocks = work + (a.cu_tokens ? kZeroBlocks : 0);
+  const int64_t blocks = jobs * p.splits * a.kv_heads;
   if (blocks > UINT32_MAX / Cfg::kThreads) return hipErrorInvalidValue;
   if (t.slopes)
     k_kv_attn_tile<D, kR, true><<<(uint32_t)blocks, Cfg::kThreads, 0, s>>>(
-        a, r, t, p.group, p.splits, p.chunk, (int)work);
+        a, r, t, p.group, p.splits, p.chunk);
   else
     k_kv_attn_tile<D, kR, false><<<(uint32_t)blocks, Cfg::kThreads, 0, s>>>(
-        a, r, t, p.group, p.splits, p.chunk, (int)work);
+        a, r, t, p.group, p.splits, p.chunk);
   return hipGetLastError();
 }
 
