@@ -16,11 +16,15 @@
 // in for all but the smallest features of a row.
 //
 // Softmax in base 2. The value absmax a of a block is folded into the weight,
-// P = 2^(S + log2 a - m), with the running maximum m over a row's S + log2 a, so
-// that the products sum the value codes as they are; the row sum takes P / a, and
+// P = 2^(S + log2 a - m), where m follows the running maximum of a row's S + log2 a,
+// so that the products sum the value codes as they are; the row sum takes P / a, and
 // O / (127 l) is the result. An a below 2^-40 counts as 2^-40, which an fp16
-// result cannot tell from it. P <= 2^kLazy is rounded to fp16 (2^-11 relative;
-// below 2^-14 of the row's largest, 2^-25 absolute); all sums are fp32.
+// result cannot tell from it. P is rounded to fp16, and the many small weights of
+// a long row count like its large ones only while they round as finely: m stays
+// kHead below the maximum that it was last raised to, so that P goes up to 2^15,
+// the rounding is 2^-11 relative down to 2^-21 of the row's largest weight and
+// 2^-32 of that below (with m at the maximum, 131000 weights of 2^-25.5 beside one
+// of 1 were lost: 0.3% of the result). All sums are fp32.
 
 #include <algorithm>
 #include <type_traits>
@@ -33,6 +37,7 @@ namespace {
 
 constexpr int kGroup = 64;          // tokens of a step: four blocks
 constexpr int kRows = 16;           // rows of a tile
+constexpr float kHead = 7.f;        // of m below a row's maximum
 constexpr float kLazy = 8.f;        // a row is rescaled when its maximum grew by more
 constexpr float kMinAbsmax = 0x1p-40f;   // of values
 
@@ -411,7 +416,7 @@ __device__ __forceinline__ float logits(float* x, Scale* sc, const Row& row, int
 // Takes a row's new maximum (over the lanes that share it) into m and l; what
 // its sums over earlier tokens are to be multiplied by.
 __device__ __forceinline__ float raise(float top, float* m, float* l) {
-  const float next = fmaxf(*m, top);
+  const float next = fmaxf(*m, top - kHead);
   const float alpha = next == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(*m - next);
   *m = next;
   *l *= alpha;
@@ -614,7 +619,7 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
       const float top = max_over_groups<4>(
           logits<kAlibi>(x, &sc, row, t0, g, t0 < all_lo || t0 + kGroup > all_hi || have != 15u,
                          (have >> g) & 1u));
-      if (__any(top > m + kLazy)) {
+      if (__any(top > m + (kHead + kLazy))) {
         const float alpha = raise(top, &m, &l);
 #pragma unroll
         for (int d = 0; d < kT; ++d) o[d] *= alpha;
@@ -1080,7 +1085,7 @@ __global__ __launch_bounds__((TileCfg<D, kR>::kThreads), 2) void k_kv_attn_tile(
     stage_keys(gi + 3, i + 3);
     v4f32 next[kT];
     if (works) {
-      if (__any(top > m + kLazy)) {
+      if (__any(top > m + (kHead + kLazy))) {
         const float alpha = raise(top, &m, &l);
 #pragma unroll
         for (int d = 0; d < kO; ++d) o[d] *= alpha;

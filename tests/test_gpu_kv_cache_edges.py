@@ -253,3 +253,30 @@ def test_many_sequences_of_one_token_or_cut(gpu, cut):
     got = host(c.attention(dev(q), b, out=out)).astype(np.float64)
     assert (np.abs(got[rows] - want) <= bound).all()
     assert not np.delete(got, rows, axis=0).any()
+
+
+# ---------------------------------------- weights far below a row's largest
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_many_small_weights_beside_a_large_one(gpu, dim):
+    """131000 tokens of weight 2^-25.5 beside one of weight 1, every value the
+    same: the result is that value. Rounded: the output (2^-11 relative) and the
+    weights (2^-11); a chain of binary32 sums over the tokens, 32 an addition,
+    above and below the line (2^-24 each). Together the small weights are 0.0027
+    of the sum, so they have to count on both sides."""
+    length, count = 131000, 64
+    page, pages = 64, -(-length // 64)
+    slots, tiles = page // 16, dim // 16
+    cache = {"k_codes": np.zeros((pages, 1, slots, tiles, 16, 16), np.int8),
+             "k_absmax": np.ones((pages, 1, slots), np.float32),
+             "v_codes": np.full((pages, 1, slots, tiles, 16, 16), 127, np.int8),
+             "v_absmax": np.ones((pages, 1, slots), np.float32)}
+    cache["k_codes"][0, 0, 0, 0, 0, 0] = 127                 # token 0, feature 0
+    table = np.full((1, 1 << 20), -1, np.int32)              # a bound of 2^26: few splits
+    table[0, :pages] = np.arange(pages)
+    q = np.zeros((count, 4, dim), np.float16)
+    q[:, :, 0] = 1
+    c, b = on_gpu(gpu, cache, table, [length], [count])
+    got = host(c.attention(dev(q), b, scale=25.5 * float(np.log(2)))).astype(np.float64)
+    tol = 2.0 ** -11 + 2.0 ** -11 + 2 * length / 32 * 2.0 ** -24
+    assert np.abs(got - 1).max() <= tol, np.abs(got - 1).max()
