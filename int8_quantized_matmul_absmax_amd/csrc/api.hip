@@ -534,6 +534,7 @@ int rotary_check(const char* fn, const i8mm_rotary* r, const i8mm::KvArgs& a,
                 (long long)r->positions, a.len_cap);
   I8MM_TRY(check_ptr(fn, "cos", r->cos, a.len_cap > 0));
   I8MM_TRY(check_ptr(fn, "sin", r->sin, a.len_cap > 0));
+  if (a.len_cap == 0) return I8MM_OK;   // no token has a position: the tables may be empty
   *out = i8mm::RotaryArgs{r->cos, r->sin, (int)r->dim, r->interleaved != 0};
   return I8MM_OK;
 }

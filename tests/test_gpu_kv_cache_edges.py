@@ -280,3 +280,19 @@ def test_many_small_weights_beside_a_large_one(gpu, dim):
     got = host(c.attention(dev(q), b, scale=25.5 * float(np.log(2)))).astype(np.float64)
     tol = 2.0 ** -11 + 2.0 ** -11 + 2 * length / 32 * 2.0 ** -24
     assert np.abs(got - 1).max() <= tol, np.abs(got - 1).max()
+
+
+@pytest.mark.parametrize("count", [1, 60])
+def test_empty_rotation_tables_are_not_read(gpu, count):
+    """Tables of no positions serve a batch without room for tokens: their
+    addresses are never followed."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    c = gpu.Int8KVCache(1, 2, 64)
+    b = gpu.KVBatch(torch.zeros((1, 1), **i32), torch.full((1,), 5, **i32),
+                    torch.tensor([0, count], **i32), total_tokens=count, max_len=0)
+    rot = gpu.Rotary(torch.zeros((0, 32), device="cuda"), torch.zeros((0, 32), device="cuda"))
+    rot._struct.cos = rot._struct.sin = 0x10000
+    x = torch.ones((count, 4, 64), dtype=torch.float16, device="cuda")
+    out = torch.full_like(x, 7.0)
+    assert not c.attention(x, b, rot, out=out).any()
+    c.append(x[:, :2], x[:, 2:], b, rot)
