@@ -1302,10 +1302,14 @@ int64_t most_tiles(const KvArgs& a, const Plan& p) {
 // against 36 of 64 and 128); of 256 features up to 32 (48 rows 82 us against 86, but
 // 50 against 30 where one sequence is alone).
 // Waves of 32 rows where there is work for them, measured by the tokens that a
-// resident block of 128 rows would take: of 128 features, 32 heads, a prompt of
-// 2048 tokens (2048) 69 us against 73, of 1024 tokens (512) 41 against 33; of 80
-// features 24 heads of 4096 tokens (6144) 127 against 145, 32 of 2048 68 against
-// 58. 256 features have no room for them.
+// resident block of 128 rows would take; the fewer features, the less a wave gains
+// from more rows (80 fill three output tiles of 32 to five sixths). Prompts of
+// 1024 to 4096 tokens, against waves of 16 rows, with that share: 128 features
+// (2048) 75 us and 81, (512) 43 and 35; 96 (2048) 70 and 80, (1024) 45 and 50, (512) 40
+// and 34; 80 (6144) 137 and 149, (4096) 101 and 112 or 114 and 105, (2048) 69 and
+// 68; 64 (24576) 357 and 361, (4096) 83 and 78, prompt chunks of 64 (9726) 175 and 185,
+// (5119) 146 and 127; between 8192 and 16384 either may win. 256 features have no
+// room for them.
 // Splits of the token axis: two blocks run at once on a compute unit, one of 256
 // features (2048 tokens of 16 heads: 105 us when taken for two, 88 us).
 // For few rows, one round of them when there is little else to run, and chunks
@@ -1329,7 +1333,7 @@ Plan plan(const KvArgs& a, int q_heads) {
   const int64_t len = (int64_t)a.len_cap + kGroup;   // a span starts at a whole group
   int64_t chunk;
   p.shared = rows > (a.head_dim <= 128 ? 3 : 2) * kRows;
-  p.wide = p.shared && a.head_dim <= 128 && share(128) >= (a.head_dim < 128 ? 4096 : 1024);
+  p.wide = p.shared && a.head_dim <= 128 && share(128) >= (a.head_dim == 64 ? 8192 : a.head_dim == 80 ? 4096 : 1024);
   if (p.shared)
     chunk = std::min(len, std::max(share(p.wide || a.head_dim == 256 ? 128 : 64), 2 * kMinChunk));
   else

@@ -87,11 +87,11 @@ def test_few_rows_with_several_block_lists(gpu, dim, kw):
 
 
 # Head size, rows of the batch, longest sequence, splits: waves of 16 rows, chunks
-# below and above a list of 1024 tokens; of 32 rows (12000 and 4096 rows).
+# below and above a list of 1024 tokens; of 32 rows (16000, 12000 and 4096 rows).
 @pytest.mark.parametrize("dim,rows,length,splits", [
     (64, 5600, 2300, 2), (80, 5600, 2300, 2), (96, 5600, 2300, 2), (128, 5600, 2300, 2),
     (64, 8192, 2300, 1), (256, 8192, 2300, 1), (256, 4500, 2300, 2), (256, 2048, 2300, 4),
-    (64, 12000, 6000, 2), (80, 12000, 6000, 2), (96, 12000, 6000, 2), (128, 4096, 4200, 4),
+    (64, 16000, 9000, 2), (80, 12000, 6000, 2), (96, 12000, 6000, 2), (128, 4096, 4200, 4),
     (128, 2000, 1500, 4), (64, 300, 1500, 4)])
 @pytest.mark.parametrize("kw", [{}, {"window": 1300}, {"alibi": True, "rotary": 32},
                                 {"causal": False}])
@@ -104,6 +104,20 @@ def test_many_rows_split_or_in_several_lists(gpu, dim, rows, length, splits, kw)
     if kw.pop("alibi", False):
         kw["slopes"] = np.array([0.02, 0.001, 0.1, 0.0], np.float32)
     check(gpu, rng, cache, table, lens, counts, 4, rows, length, lambda s: s == splits, **kw)
+
+
+@pytest.mark.parametrize("kw", [
+    {}, {"causal": False}, {"window": 1}, {"window": 37}, {"rotary": 32}, {"rotary": 64},
+    {"alibi": True}, {"alibi": True, "window": 100}])
+def test_waves_of_32_rows_of_64_features(gpu, kw):
+    """64 features take them under larger bounds than others do."""
+    kw = dict(kw)
+    rng = np.random.default_rng(64 + len(kw))
+    lens, counts = [150, 33, 1, 0, 90, 64, 1200], [150, 1, 1, 0, 0, 17, 70]
+    cache, table = widen(make(rng, lens, 4, 64, 64), 64)
+    if kw.pop("alibi", False):
+        kw["slopes"] = (2.0 ** -np.arange(1, 13)).astype(np.float32)
+    check(gpu, rng, cache, table, lens, counts, 12, 300, 1 << 18, lambda s: s < 16, **kw)
 
 
 @pytest.mark.parametrize("dim,kv_heads", [(64, 5), (80, 6), (96, 7), (128, 5), (256, 6)])
