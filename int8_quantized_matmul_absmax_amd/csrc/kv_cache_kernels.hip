@@ -336,9 +336,11 @@ hipError_t launch_kv_append(const uint16_t* k, int64_t k_ts, int64_t k_hs, const
   // Four heads a wave once there are waves enough: they share the rotation's
   // factors (4096 tokens of 96 heads of 128: 66 us, with one 83). With few tokens
   // the heads are what there is to run at once (16 tokens of 32 heads: 5.8 us with
-  // one, with four 13).
+  // one, with four 13). At 8256 waves, 2048 tokens of 32 heads, four take 18.0 us and
+  // one 20.5 (64 features 14.2 and 15.5, 256 38 and 50), at 4160 15.2 and 13.7 (12.4
+  // and 10.1, 22.5 and 27.9).
   const int64_t one = max_blocks(a) * a.kv_heads * 2 * a.num_seqs;
-  const int per_wave = one >= 32768 ? 4 : 1;
+  const int per_wave = one >= 8192 ? 4 : 1;
   const int64_t parts = (a.kv_heads + per_wave - 1) / per_wave;
   const int64_t tasks = max_blocks(a) * parts * 2;
   if (tasks > INT32_MAX - 4) return hipErrorInvalidValue;
