@@ -480,14 +480,14 @@ I8MM_API int int8_kv_cache_append(const uint16_t* k, int64_t k_token_stride, int
  *            aligned (NULL when that is 0). What it holds on entry does not
  *            matter.
  *
- * The query is taken as 15-bit integers over its row's absmax, so its product
- * with the key codes is an exact integer. The softmax and the sums over tokens
- * are fp32. The weights that meet the values, times their value absmax, are
- * rounded to fp16 where max_tokens * q_heads / kv_heads is more than 48 (32 for D
- * = 256), to two parts of fp16 (22 bits) where it is not, and to 2^-32 of the
- * largest of their row where that is coarser; a value absmax below 2^-40 counts as
- * 2^-40. Results do
- * not depend on what ran before.
+ * The query is taken as 15-bit integers over its row's absmax a (each feature
+ * within a / 32512), so its product with the key codes is an exact integer. The
+ * softmax and the sums over tokens are fp32. The weights that meet the values,
+ * times their value absmax, are rounded to fp16 where max_tokens * q_heads /
+ * kv_heads is more than 48 (32 for D = 256), to two parts of fp16 (22 bits) where
+ * it is not, and to 2^-32 of the largest of their row where that is coarser; a
+ * value absmax below 2^-40 counts as 2^-40. Results do not depend on what ran
+ * before.
  * Errors: EINVAL, EALIGN, EWORKSPACE, ENODEVICE, ELAUNCH.
  */
 I8MM_API int int8_kv_cache_attention(const uint16_t* q, int64_t q_token_stride,

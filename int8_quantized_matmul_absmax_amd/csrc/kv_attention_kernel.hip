@@ -11,9 +11,14 @@
 //
 // The query is a 15-bit integer, q = (128 hi + lo) a / 16256 over its row's
 // absmax a, with int8 hi and lo: two int8 MFMAs take the codes as they lie in
-// the cache and sum the product exactly. An fp16 MFMA would have half the rate
-// and need the codes converted; 15 bits are finer than the fp16 the query came
-// in for all but the smallest features of a row.
+// the cache and sum the product exactly. That is the matrix pipe's time of one
+// fp16 MFMA; it saves the conversion of the key codes and costs a shift and a
+// conversion for each score. It rounds every feature by up to a / 32512: finer
+// than the fp16 that the query came in for features above an eighth of a (a query
+// that is not rotated would be exact in fp16), coarser for the others, and beside
+// the rounding of the key codes little: over 2000 tokens of 128 features 5e-5 of
+// the result against 8e-3 for normal queries, 9e-4 against 4e-2 where one feature is
+// 50 times the others.
 //
 // Softmax in base 2. The value absmax a of a block is folded into the weight,
 // P = 2^(S + log2 a - m), where m follows the running maximum of a row's S + log2 a,
@@ -709,14 +714,15 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_row
 // instructions): each wave loads its share of a group one step ahead and stores it
 // as operands, of which LDS holds this group's and the next's.
 //
-// Bound by the issue of vector instructions, about 270 beside 32 MFMAs for a group
-// of 64 tokens, 32 rows and 128 features: exponentials, conversions, the joining of
-// the two parts of the scores. 4096 tokens of 96 heads of 128 (412 GFLOP): 520 us,
-// 0.79 PFLOP/s (a large fp16 product: 1.2); the vector pipe is busy for 0.62 of the
-// cycles at 2.05 GHz, the matrix pipe for 0.38, and the two hardly overlap. A step
-// of prompt chunks over prefixes of up to 8191 tokens, 32 heads on 8 of 64 (90
-// GFLOP): 175 us. What else it costs a block is its start, about 12 us for the
-// queries.
+// 4096 tokens of 96 heads of 128 (412 GFLOP): 520 to 550 us, 0.75 to 0.79 PFLOP/s (a
+// large fp16 product: 1.2). The vector pipe is busy for 0.62 of the cycles at 2.05
+// GHz (about 270 instructions beside 32 MFMAs for a group of 64 tokens, 32 rows and
+// 128 features: exponentials, conversions, the joining of the two parts of the
+// scores), the matrix pipe for 0.38. Neither is full: they take turns more than they
+// overlap, with two waves a SIMD and a barrier every 64 tokens. A step of prompt
+// chunks over prefixes of up to 8191 tokens, 32 heads on 8 of 64 (90 GFLOP): 178 us,
+// 0.63 and 0.20 of the cycles. What else it costs a block is its start, about 12 us for
+// the queries.
 template <int D, int kR>
 struct TileCfg {
   static constexpr int kLaneGroups = kWave / kR;        // lanes of a row

@@ -83,7 +83,8 @@ class Int8KVCache:
     def attention(self, q, batch, rotary=None, scale=None, causal=True, window=0,
                   alibi_slopes=None, out=None):
         """Attention of the batch's queries over the cached tokens. Its workspace
-        is the current stream's shared one, as for the linear layers."""
+        is the current stream's shared one (a graph's own while recording), as for
+        the linear layers."""
         return ops.int8_kv_cache_attention(q, self, batch, rotary, scale, causal, window,
                                            alibi_slopes, shared_workspace, out)
 
