@@ -514,6 +514,53 @@ I8MM_API size_t int8_kv_cache_attention_workspace_bytes(const i8mm_kv_cache* cac
 I8MM_API int int8_kv_cache_read(const i8mm_kv_cache* cache, const i8mm_kv_batch* batch,
                                 uint16_t* k, uint16_t* v, i8mm_stream_t stream);
 
+/*
+ * i8mm_beam_select: a beam search's choice of its next beams over beams and
+ * vocabulary, for a batch of searches of `beams` beams each.
+ *
+ * The candidates of a beam i that goes on are its words v, of value
+ *   scores[i] + logits[i][v] - log sum_u exp(logits[i][u]);
+ * a beam that has ended has one, itself, of value scores[i]. The `count` best of a
+ * search are written in order, equal values by beam and word. A word of logit
+ * -infinity is no candidate, and a beam whose score is not finite, or whose logits
+ * hold a NaN or +infinity, has none.
+ *
+ *   logits   fp16 (logits_fp32 == 0) or fp32 [batch * beams, vocab], rows
+ *            row_stride >= vocab elements apart, at any alignment of their type.
+ *   scores   fp32 [batch, beams]: what a beam's words have summed up to.
+ *   live     int32 [batch, beams], 0 for a beam that has ended (its logits are
+ *            not read), or NULL: all go on.
+ *   beams    up to I8MM_MAX_BEAMS; vocab up to I8MM_MAX_VOCAB; count
+ *            1 .. I8MM_MAX_BEAM_COUNT.
+ *   eos      the word that ends a beam, or -1.
+ *   out_scores   fp32 [batch, count] values.
+ *   out_tokens   int32 [batch, count]: the word; eos of a beam that had ended.
+ *   out_parents  int32 [batch, count]: the row of logits, search * beams + i.
+ *   out_live     int32 [batch, count]: 1, or 0 for a beam that has ended.
+ *   workspace    i8mm_beam_select_workspace_bytes(...) bytes, 256-byte
+ *            aligned. What it holds on entry does not matter.
+ * Places beyond the candidates get -infinity, -1, -1 and 0. All arrays of 32-bit
+ * elements are 4-byte aligned.
+ *
+ * Exponentials are fp32 (a row's sum is within 2^-18 of itself); values are
+ * compared in 64 bits and rounded to fp32 when they are written.
+ * Errors: EINVAL, EALIGN, EWORKSPACE, ENODEVICE, ELAUNCH.
+ */
+#define I8MM_MAX_BEAMS 1024
+#define I8MM_MAX_VOCAB (1 << 24)
+#define I8MM_MAX_BEAM_COUNT 64
+I8MM_API int i8mm_beam_select(const void* logits, int logits_fp32, int64_t row_stride,
+                              const float* scores, const int32_t* live, int64_t batch,
+                              int64_t beams, int64_t vocab, int64_t count, int32_t eos,
+                              float* out_scores, int32_t* out_tokens, int32_t* out_parents,
+                              int32_t* out_live, void* workspace, size_t workspace_bytes,
+                              i8mm_stream_t stream);
+
+/* Bytes of workspace i8mm_beam_select needs (0 if the sizes are invalid or
+ * there is nothing to do). Host-only, pure. */
+I8MM_API size_t i8mm_beam_select_workspace_bytes(int logits_fp32, int64_t batch, int64_t beams,
+                                                 int64_t vocab, int64_t count);
+
 /* Text of the last error raised on the calling host thread ("" if none). */
 I8MM_API const char* i8mm_last_error(void);
 

@@ -34,6 +34,8 @@ EXPORTS = (
     "int8_kv_cache_attention",
     "int8_kv_cache_attention_workspace_bytes",
     "int8_kv_cache_read",
+    "i8mm_beam_select",
+    "i8mm_beam_select_workspace_bytes",
     "i8mm_last_error",
     "i8mm_status_string",
 )
@@ -99,6 +101,9 @@ def _declare(lib):
                                      vp, ctypes.c_size_t, vp], i32),
         "int8_kv_cache_attention_workspace_bytes": ([cache, batch, i64], ctypes.c_size_t),
         "int8_kv_cache_read": ([cache, batch, vp, vp, vp], i32),
+        "i8mm_beam_select": ([vp, i32, i64, vp, vp, i64, i64, i64, i64, i32, vp, vp, vp, vp, vp,
+                              ctypes.c_size_t, vp], i32),
+        "i8mm_beam_select_workspace_bytes": ([i32, i64, i64, i64, i64], ctypes.c_size_t),
         "i8mm_last_error": ([], ctypes.c_char_p),
         "i8mm_status_string": ([i32], ctypes.c_char_p),
     }

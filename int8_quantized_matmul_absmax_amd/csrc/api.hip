@@ -672,3 +672,101 @@ int int8_kv_cache_attention(const uint16_t* q, int64_t q_token_stride, int64_t q
 }
 
 }  // extern "C"
+
+namespace {
+
+int beam_sizes(const char* fn, int fp32, int64_t batch, int64_t beams, int64_t vocab,
+               int64_t count, i8mm::BeamArgs* a) {
+  if (fp32 != 0 && fp32 != 1) return fail(I8MM_EINVAL, "%s: logits_fp32 is not 0 or 1", fn);
+  if (batch < 0 || beams < 0 || vocab < 0)
+    return fail(I8MM_EINVAL, "%s: negative size", fn);
+  // (rows are numbered in int32, and blocks of up to 65536 words of them launched)
+  if (beams > I8MM_MAX_BEAMS || vocab > I8MM_MAX_VOCAB ||
+      batch > (1 << 23) / std::max<int64_t>(beams, 1) / (vocab / 65536 + 1))
+    return fail(I8MM_EINVAL, "%s: more than %d beams, %d words or 2^23 rows of 65536 words", fn,
+                I8MM_MAX_BEAMS, I8MM_MAX_VOCAB);
+  if (count < 1 || count > I8MM_MAX_BEAM_COUNT)
+    return fail(I8MM_EINVAL, "%s: count=%lld is not 1 .. %d", fn, (long long)count,
+                I8MM_MAX_BEAM_COUNT);
+  a->fp32 = fp32;
+  a->batch = (int)batch;
+  a->beams = (int)beams;
+  a->vocab = vocab;
+  a->count = (int)count;
+  return I8MM_OK;
+}
+
+int check_ints(const char* fn, const char* name, const void* p, bool required) {
+  if (!p && required) return fail(I8MM_EINVAL, "%s: %s is NULL", fn, name);
+  if (!aligned4(p)) return fail(I8MM_EALIGN, "%s: %s is not 4-byte aligned", fn, name);
+  return I8MM_OK;
+}
+
+int check_scratch(const char* fn, const void* workspace, size_t bytes, size_t need) {
+  if (need == 0) return I8MM_OK;
+  if (!workspace || bytes < need)
+    return fail(I8MM_EWORKSPACE, "%s: workspace has %zu bytes, needs %zu", fn,
+                workspace ? bytes : (size_t)0, need);
+  if ((reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0)
+    return fail(I8MM_EALIGN, "%s: workspace is not 256-byte aligned", fn);
+  return I8MM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t i8mm_beam_select_workspace_bytes(int logits_fp32, int64_t batch, int64_t beams,
+                                        int64_t vocab, int64_t count) {
+  i8mm::BeamArgs a;
+  if (beam_sizes("i8mm_beam_select_workspace_bytes", logits_fp32, batch, beams, vocab, count, &a) !=
+      I8MM_OK)
+    return 0;
+  return batch == 0 ? 0 : i8mm::beam_workspace_bytes(a);
+}
+
+int i8mm_beam_select(const void* logits, int logits_fp32, int64_t row_stride, const float* scores,
+                     const int32_t* live, int64_t batch, int64_t beams, int64_t vocab,
+                     int64_t count, int32_t eos, float* out_scores, int32_t* out_tokens,
+                     int32_t* out_parents, int32_t* out_live, void* workspace,
+                     size_t workspace_bytes, i8mm_stream_t stream) {
+  const char* fn = "i8mm_beam_select";
+  i8mm::BeamArgs a;
+  I8MM_TRY(beam_sizes(fn, logits_fp32, batch, beams, vocab, count, &a));
+  const int64_t rows = batch * beams;
+  if (row_stride < vocab)
+    return fail(I8MM_EINVAL, "%s: row_stride=%lld is less than vocab=%lld", fn,
+                (long long)row_stride, (long long)vocab);
+  if (rows > 0 && row_stride > INT64_MAX / 8 / rows)
+    return fail(I8MM_EINVAL, "%s: rows beyond 64 bits", fn);
+  if (eos < -1 || (eos >= 0 && eos >= vocab))
+    return fail(I8MM_EINVAL, "%s: eos=%d is neither -1 nor one of %lld words", fn, eos,
+                (long long)vocab);
+  if (!logits && rows > 0 && vocab > 0) return fail(I8MM_EINVAL, "%s: logits is NULL", fn);
+  if (reinterpret_cast<uintptr_t>(logits) % (logits_fp32 ? 4 : 2) != 0)
+    return fail(I8MM_EALIGN, "%s: logits is not aligned to its elements", fn);
+  I8MM_TRY(check_ints(fn, "scores", scores, rows > 0));
+  I8MM_TRY(check_ints(fn, "live", live, false));
+  I8MM_TRY(check_ints(fn, "out_scores", out_scores, batch > 0));
+  I8MM_TRY(check_ints(fn, "out_tokens", out_tokens, batch > 0));
+  I8MM_TRY(check_ints(fn, "out_parents", out_parents, batch > 0));
+  I8MM_TRY(check_ints(fn, "out_live", out_live, batch > 0));
+  I8MM_TRY(check_scratch(fn, workspace, workspace_bytes,
+                         batch == 0 ? 0 : i8mm::beam_workspace_bytes(a)));
+  if (batch == 0) return ok();
+  I8MM_TRY(check_device());
+  a.logits = logits;
+  a.row_stride = row_stride;
+  a.scores = scores;
+  a.live = live;
+  a.out_scores = out_scores;
+  a.out_tokens = out_tokens;
+  a.out_parents = out_parents;
+  a.out_live = out_live;
+  a.ws = workspace;
+  a.eos = eos;
+  I8MM_TRY(launched(i8mm::launch_beam_select(a, (hipStream_t)stream), fn));
+  return ok();
+}
+
+}  // extern "C"

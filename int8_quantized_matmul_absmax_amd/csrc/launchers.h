@@ -137,6 +137,23 @@ size_t attn_workspace_bytes(const KvArgs& a, int q_heads);
 hipError_t launch_kv_attention(const KvArgs& a, const RotaryArgs& r, const AttnArgs& t,
                                hipStream_t s);
 
+// ---- a beam search's choice of its next beams (arguments as in the C ABI)
+struct BeamArgs {
+  const void* logits;
+  int64_t row_stride;
+  const float* scores;
+  const int32_t* live;        // or nullptr: all
+  float* out_scores;
+  int32_t* out_tokens;
+  int32_t* out_parents;
+  int32_t* out_live;
+  void* ws;
+  int64_t vocab;
+  int fp32, batch, beams, count, eos;
+};
+size_t beam_workspace_bytes(const BeamArgs& a);
+hipError_t launch_beam_select(const BeamArgs& a, hipStream_t s);
+
 hipError_t launch_gelu(const uint16_t* X, int64_t count, uint16_t* Y, hipStream_t s);
 
 }  // namespace i8mm

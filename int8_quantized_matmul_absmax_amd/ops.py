@@ -39,6 +39,14 @@ def _raw_stream(device):
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
+def _run(device, call, *args):
+    """call(*args, the current stream of `device`), checked, with `device` current."""
+    if torch._C._cuda_getDevice() == device.index:
+        return _lib.check(call(*args, _raw_stream(device)))
+    with torch.cuda.device(device):
+        return _lib.check(call(*args, _raw_stream(device)))
+
+
 def _need(t, name, dtype, ndim=None, shape=None, min_numel=None):
     """Type, dtype, contiguity and size of one tensor argument (no device check:
     _on_gpu does that for all arguments of a call together)."""
@@ -350,6 +358,22 @@ def _kv_args(cache, batch, rotary):
     return rotary.ref
 
 
+def _scratch(need, workspace, dev):
+    """Address and size of a workspace of `need` bytes: `workspace` is a uint8
+    tensor, or a function of the device and a number of bytes that gives one, or
+    None (allocated here)."""
+    if workspace is None or callable(workspace):
+        if not need:
+            return None, 0
+        workspace = workspace(dev, need) if workspace else \
+            torch.empty((need,), dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", torch.uint8, 1)
+        if workspace.device != dev:
+            raise ValueError("workspace is on %s, the call on %s" % (workspace.device, dev))
+    return workspace.data_ptr(), workspace.numel()
+
+
 def int8_kv_cache_append(k, v, cache, batch, rotary=None):
     """Quantize new keys (rotated first when `rotary` is given) and values into
     the cache. k, v fp16 [total_tokens, kv_heads, D]; the token and head strides
@@ -420,6 +444,57 @@ def int8_kv_cache_read(cache, batch):
     _lib.check(lib.int8_kv_cache_read(cache.ref, batch.ref, k.data_ptr(), v.data_ptr(),
                                       _raw_stream(cache.device)))
     return k, v
+
+
+# ---- a beam search over such caches
+
+def beam_select(logits, scores, live=None, eos=None, count=None, workspace=None):
+    """The next beams of a batch of beam searches: of each search the `count`
+    (default: beams) best of all its beams' words, by scores + log_softmax(logits),
+    equal ones by beam and word.
+
+    logits  fp16 or fp32 [batch, beams, vocab], words contiguous, rows evenly apart
+    scores  fp32 [batch, beams]; -inf for a beam that is not there (all but one at
+            the start of a search)
+    live    int32 [batch, beams], 0 for a beam that has ended: it stands for itself,
+            with its score and the word eos. None: all go on
+    eos     the word that ends a beam, None if none does
+    workspace  as for int8_kv_cache_attention
+
+    Returns scores fp32, tokens, parents (rows search * beams + beam: what
+    KVPages.step takes) and live int32, each [batch, count]; -inf, -1, -1 and 0
+    where there is no candidate left."""
+    lib = _lib.load_library()
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    if logits.dtype not in (torch.float16, torch.float32):
+        raise TypeError("logits must be torch.float16 or torch.float32, got %s" % logits.dtype)
+    if logits.dim() != 3:
+        raise ValueError("logits must have 3 dims, got %d" % logits.dim())
+    batch, beams, vocab = logits.shape
+    _need(scores, "scores", torch.float32, shape=(batch, beams))
+    if live is not None:
+        _need(live, "live", torch.int32, shape=(batch, beams))
+    bs, rs, ws = logits.stride()
+    if beams == 1:
+        rs = bs
+    if batch * beams <= 1:
+        rs = max(rs, vocab)
+    if logits.numel() and ((vocab > 1 and ws != 1) or (batch > 1 and bs != beams * rs) or rs < vocab):
+        raise ValueError("the words of logits must be contiguous and its rows evenly apart")
+    dev = _on_gpu(logits=logits, scores=scores, live=live)
+    count = beams if count is None else int(count)
+    fp32 = 1 if logits.dtype == torch.float32 else 0
+    ints = torch.empty((3, batch, max(count, 0)), dtype=torch.int32, device=dev)
+    out = torch.empty((batch, max(count, 0)), dtype=torch.float32, device=dev)
+    wp, wn = _scratch(lib.i8mm_beam_select_workspace_bytes(fp32, batch, beams, vocab, count),
+                      workspace, dev)
+    tokens, parents, alive = ints.unbind(0)
+    _run(dev, lib.i8mm_beam_select, logits.data_ptr(), fp32, max(rs, vocab), scores.data_ptr(),
+         None if live is None else live.data_ptr(), batch, beams, vocab, count,
+         -1 if eos is None else int(eos), out.data_ptr(), tokens.data_ptr(), parents.data_ptr(),
+         alive.data_ptr(), wp, wn)
+    return out, tokens, parents, alive
 
 
 OUTLIER_REGION_COLS = 512   # I8MM_OUTLIER_REGION_COLS
