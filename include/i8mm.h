@@ -515,6 +515,93 @@ I8MM_API int int8_kv_cache_read(const i8mm_kv_cache* cache, const i8mm_kv_batch*
                                 uint16_t* k, uint16_t* v, i8mm_stream_t stream);
 
 /*
+ * Pages of the cache. What belongs to a sequence is in the page table alone: a
+ * page that no row names is free, and one that several name is shared, which is
+ * right for tokens that none of them will change. The calls below make the next
+ * table from the last and say which pages are to be copied; int8_kv_cache_copy_pages
+ * does that for each cache (layer) that the table is for.
+ *
+ * i8mm_kv_pages_step: the page table of the next step, before its append: beams
+ * that go on from others, sequences that share a prompt, grow, are cut back, begin
+ * or end. Row i of the new table keeps k = min(keep[i], seq_lens[parents[i]])
+ * tokens of row parents[i] of the old one (none for a parent outside [0, num_seqs))
+ * and has room for new_tokens[i] after them:
+ *   - its length is min(k + new_tokens[i], max_pages * page_tokens), its first
+ *     ceil(k / page_tokens) pages are the parent's;
+ *   - where new tokens begin inside the last of them (k no multiple of page_tokens)
+ *     and other rows keep that page too, row i gets a copy of it, unless all of them
+ *     write to it and i is the first;
+ *   - tokens past them get pages that no row of the new table keeps, the lowest
+ *     first, rows in order, a row's copy before its new pages;
+ *   - entries past its length are -1.
+ * Parents' entries that are outside [0, num_pages) become -1 and are not copied.
+ * When no page is left entries are -1, and the tokens absent.
+ *
+ *   page_table  int32 [num_seqs, max_pages], seq_lens int32 [num_seqs] (cut to
+ *               0 .. max_pages * page_tokens).
+ *   parents     int32 [num_rows]: i8mm_beam_select's, for one.
+ *   keep        int32 [num_rows] (negative: none), or NULL: all tokens.
+ *   new_tokens  int32 [num_rows] (negative: none), or NULL: new_all each.
+ *   out_table   int32 [num_rows, max_pages], not overlapping page_table;
+ *   out_lens    int32 [num_rows], not overlapping seq_lens: what an i8mm_kv_batch
+ *               takes, the new tokens included.
+ *   copies      int32 [num_rows][3]: page, the page to copy it to, tokens that
+ *               count; rows in order, then rows of -1.
+ *   counts      int32 [2]: copies; pages that were wanting.
+ *   workspace   i8mm_kv_pages_workspace_bytes(num_rows, num_pages) bytes, 256-byte
+ *               aligned. What it holds on entry does not matter.
+ *
+ * num_seqs, num_rows up to 65535; max_pages * page_tokens up to 2^30;
+ * num_rows * (max_pages + 1) and num_pages below 2^31; page_tokens as in the cache.
+ * Errors: EINVAL, EALIGN, EWORKSPACE, ENODEVICE, ELAUNCH.
+ */
+I8MM_API int i8mm_kv_pages_step(const int32_t* page_table, const int32_t* seq_lens,
+                                int64_t num_seqs, int64_t max_pages, const int32_t* parents,
+                                const int32_t* keep, const int32_t* new_tokens, int64_t new_all,
+                                int64_t num_rows, int64_t num_pages, int64_t page_tokens,
+                                int32_t* out_table, int32_t* out_lens, int32_t* copies,
+                                int32_t* counts, void* workspace, size_t workspace_bytes,
+                                i8mm_stream_t stream);
+
+/* Bytes of workspace for i8mm_kv_pages_step and (num_rows 0)
+ * i8mm_kv_pages_compact; 0 also if the sizes are invalid. Host-only, pure. */
+I8MM_API size_t i8mm_kv_pages_workspace_bytes(int64_t num_rows, int64_t num_pages);
+
+/*
+ * i8mm_kv_pages_compact: the used pages to the front. With `live` pages named by
+ * rows of the table, the used pages at or past live go to the free ones below it,
+ * both in ascending order, and the table names their new places.
+ *
+ *   page_table, seq_lens, sizes  as for i8mm_kv_pages_step.
+ *   out_table   int32 [num_seqs, max_pages]; may be page_table.
+ *   copies      int32 [num_pages / 2][3], as for i8mm_kv_pages_step, of whole
+ *               pages. No page is both copied and copied to.
+ *   counts      int32 [2]: copies; live.
+ * Errors: EINVAL, EALIGN, EWORKSPACE, ENODEVICE, ELAUNCH.
+ */
+I8MM_API int i8mm_kv_pages_compact(const int32_t* page_table, const int32_t* seq_lens,
+                                   int64_t num_seqs, int64_t max_pages, int64_t num_pages,
+                                   int64_t page_tokens, int32_t* out_table, int32_t* copies,
+                                   int32_t* counts, void* workspace, size_t workspace_bytes,
+                                   i8mm_stream_t stream);
+
+/*
+ * int8_kv_cache_copy_pages: copies of a cache's pages: codes and absmaxes of the
+ * blocks that hold the first copies[i][2] tokens of page copies[i][0], to page
+ * copies[i][1]; the rest of that page stays as it was.
+ *   k_means  fp16 [num_pages, kv_heads, D] or NULL: the pages' mean keys, copied
+ *            with them.
+ *   copies   int32 [max_copies][3], count int32 [1] (both on the device, so that
+ *            nothing waits for the host): rows past count, of pages outside
+ *            [0, num_pages) or of a page to itself do nothing. A page that is copied
+ *            to must be in no other row.
+ * Errors: EINVAL, EALIGN, ENODEVICE, ELAUNCH.
+ */
+I8MM_API int int8_kv_cache_copy_pages(const i8mm_kv_cache* cache, uint16_t* k_means,
+                                      const int32_t* copies, const int32_t* count,
+                                      int64_t max_copies, i8mm_stream_t stream);
+
+/*
  * i8mm_beam_select: a beam search's choice of its next beams over beams and
  * vocabulary, for a batch of searches of `beams` beams each.
  *

@@ -23,7 +23,7 @@ def __getattr__(name):
     if name in ("ops", "linear", "synth", "kv_cache", "attention"):
         import importlib
         return importlib.import_module("." + name, __name__)
-    if name in ("Int8KVCache", "KVBatch", "Rotary"):
+    if name in ("Int8KVCache", "KVBatch", "KVPages", "PageCopies", "Rotary"):
         from . import kv_cache
         return getattr(kv_cache, name)
     if name == "Int8CachedAttention":

@@ -34,6 +34,10 @@ EXPORTS = (
     "int8_kv_cache_attention",
     "int8_kv_cache_attention_workspace_bytes",
     "int8_kv_cache_read",
+    "i8mm_kv_pages_step",
+    "i8mm_kv_pages_compact",
+    "i8mm_kv_pages_workspace_bytes",
+    "int8_kv_cache_copy_pages",
     "i8mm_beam_select",
     "i8mm_beam_select_workspace_bytes",
     "i8mm_last_error",
@@ -101,6 +105,12 @@ def _declare(lib):
                                      vp, ctypes.c_size_t, vp], i32),
         "int8_kv_cache_attention_workspace_bytes": ([cache, batch, i64], ctypes.c_size_t),
         "int8_kv_cache_read": ([cache, batch, vp, vp, vp], i32),
+        "i8mm_kv_pages_step": ([vp, vp, i64, i64, vp, vp, vp, i64, i64, i64, i64, vp, vp, vp, vp, vp,
+                                ctypes.c_size_t, vp], i32),
+        "i8mm_kv_pages_compact": ([vp, vp, i64, i64, i64, i64, vp, vp, vp, vp, ctypes.c_size_t, vp],
+                                  i32),
+        "i8mm_kv_pages_workspace_bytes": ([i64, i64], ctypes.c_size_t),
+        "int8_kv_cache_copy_pages": ([cache, vp, vp, vp, i64, vp], i32),
         "i8mm_beam_select": ([vp, i32, i64, vp, vp, i64, i64, i64, i64, i32, vp, vp, vp, vp, vp,
                               ctypes.c_size_t, vp], i32),
         "i8mm_beam_select_workspace_bytes": ([i32, i64, i64, i64, i64], ctypes.c_size_t),

@@ -459,8 +459,7 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 
 // Sizes of a cache and a batch, checked and narrowed into *a (pointers not
 // looked at).
-int kv_sizes(const char* fn, const i8mm_kv_cache* c, const i8mm_kv_batch* b, i8mm::KvArgs* a) {
-  if (!c || !b) return fail(I8MM_EINVAL, "%s: cache or batch is NULL", fn);
+int cache_sizes(const char* fn, const i8mm_kv_cache* c, i8mm::KvArgs* a) {
   if (c->num_pages < 0 || c->page_tokens <= 0 || c->page_tokens > 65536 || c->kv_heads <= 0)
     return fail(I8MM_EINVAL, "%s: cache of %lld pages of %lld tokens, %lld heads", fn,
                 (long long)c->num_pages, (long long)c->page_tokens, (long long)c->kv_heads);
@@ -475,6 +474,16 @@ int kv_sizes(const char* fn, const i8mm_kv_cache* c, const i8mm_kv_batch* b, i8m
   if (c->kv_heads > 65535 || slots > INT32_MAX / c->kv_heads ||
       c->num_pages > INT32_MAX / (slots * c->kv_heads))
     return fail(I8MM_EINVAL, "%s: more than 2^31 - 1 blocks or 65535 heads", fn);
+  a->num_pages = (int)c->num_pages;
+  a->slots = (int)slots;
+  a->kv_heads = (int)c->kv_heads;
+  a->head_dim = (int)c->head_dim;
+  return I8MM_OK;
+}
+
+int kv_sizes(const char* fn, const i8mm_kv_cache* c, const i8mm_kv_batch* b, i8mm::KvArgs* a) {
+  if (!c || !b) return fail(I8MM_EINVAL, "%s: cache or batch is NULL", fn);
+  I8MM_TRY(cache_sizes(fn, c, a));
   if (b->num_seqs < 0 || b->max_pages < 0 || b->total_tokens < 0 || b->max_tokens < 0 ||
       b->max_len < 0)
     return fail(I8MM_EINVAL, "%s: negative size in the batch", fn);
@@ -488,10 +497,6 @@ int kv_sizes(const char* fn, const i8mm_kv_cache* c, const i8mm_kv_batch* b, i8m
   // (no pages: every token is absent, as in sequences of length 0)
   const int64_t cap = c->num_pages > 0 ? std::min(b->max_len, room) : 0;
   if (cap > INT32_MAX / 2) return fail(I8MM_EINVAL, "%s: max_len beyond 2^30 tokens", fn);
-  a->num_pages = (int)c->num_pages;
-  a->slots = (int)slots;
-  a->kv_heads = (int)c->kv_heads;
-  a->head_dim = (int)c->head_dim;
   a->num_seqs = (int)b->num_seqs;
   a->max_pages = (int)b->max_pages;
   a->total_tokens = (int)b->total_tokens;
@@ -500,22 +505,27 @@ int kv_sizes(const char* fn, const i8mm_kv_cache* c, const i8mm_kv_batch* b, i8m
   return I8MM_OK;
 }
 
-int kv_check(const char* fn, const i8mm_kv_cache* c, const i8mm_kv_batch* b, i8mm::KvArgs* a) {
-  I8MM_TRY(kv_sizes(fn, c, b, a));
+int cache_pointers(const char* fn, const i8mm_kv_cache* c, i8mm::KvArgs* a) {
   const bool some = c->num_pages > 0;
   I8MM_TRY(check_ptr(fn, "k_codes", c->k_codes, some));
   I8MM_TRY(check_ptr(fn, "k_absmax", c->k_absmax, some));
   I8MM_TRY(check_ptr(fn, "v_codes", c->v_codes, some));
   I8MM_TRY(check_ptr(fn, "v_absmax", c->v_absmax, some));
+  a->k_codes = c->k_codes;
+  a->k_absmax = c->k_absmax;
+  a->v_codes = c->v_codes;
+  a->v_absmax = c->v_absmax;
+  return I8MM_OK;
+}
+
+int kv_check(const char* fn, const i8mm_kv_cache* c, const i8mm_kv_batch* b, i8mm::KvArgs* a) {
+  I8MM_TRY(kv_sizes(fn, c, b, a));
+  I8MM_TRY(cache_pointers(fn, c, a));
   if (!b->page_table && b->num_seqs * b->max_pages > 0)
     return fail(I8MM_EINVAL, "%s: page_table is NULL", fn);
   if (!b->seq_lens && b->num_seqs > 0) return fail(I8MM_EINVAL, "%s: seq_lens is NULL", fn);
   if (!aligned4(b->page_table) || !aligned4(b->seq_lens) || !aligned4(b->cu_tokens))
     return fail(I8MM_EALIGN, "%s: page_table, seq_lens or cu_tokens is not 4-byte aligned", fn);
-  a->k_codes = c->k_codes;
-  a->k_absmax = c->k_absmax;
-  a->v_codes = c->v_codes;
-  a->v_absmax = c->v_absmax;
   a->page_table = b->page_table;
   a->seq_lens = b->seq_lens;
   a->cu_tokens = b->cu_tokens;
@@ -766,6 +776,134 @@ int i8mm_beam_select(const void* logits, int logits_fp32, int64_t row_stride, co
   a.ws = workspace;
   a.eos = eos;
   I8MM_TRY(launched(i8mm::launch_beam_select(a, (hipStream_t)stream), fn));
+  return ok();
+}
+
+}  // extern "C"
+
+namespace {
+
+// Sizes of the calls on page tables, narrowed into *a.
+int pages_sizes(const char* fn, int64_t num_seqs, int64_t max_pages, int64_t num_rows,
+                int64_t num_pages, int64_t page_tokens, i8mm::PagesArgs* a) {
+  *a = i8mm::PagesArgs{};
+  if (num_seqs < 0 || max_pages < 0 || num_rows < 0 || num_pages < 0)
+    return fail(I8MM_EINVAL, "%s: negative size", fn);
+  if (page_tokens <= 0 || page_tokens > 65536)
+    return fail(I8MM_EINVAL, "%s: pages of %lld tokens", fn, (long long)page_tokens);
+  if (page_tokens % I8MM_KV_BLOCK != 0)
+    return fail(I8MM_EALIGN, "%s: page_tokens=%lld is not a multiple of %d", fn,
+                (long long)page_tokens, I8MM_KV_BLOCK);
+  if (num_seqs > 65535 || num_rows > 65535 || num_pages > INT32_MAX - 8192 ||
+      max_pages > (1 << 30) / page_tokens ||
+      std::max(num_seqs, num_rows) * (max_pages + 1) > INT32_MAX)
+    return fail(I8MM_EINVAL, "%s: more than 65535 sequences, 2^30 tokens of one or 2^31 pages", fn);
+  a->num_seqs = (int)num_seqs;
+  a->max_pages = (int)max_pages;
+  a->num_rows = (int)num_rows;
+  a->num_pages = (int)num_pages;
+  a->page_tokens = (int)page_tokens;
+  return I8MM_OK;
+}
+
+bool overlap(const void* p, int64_t p_bytes, const void* q, int64_t q_bytes) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && a < b + q_bytes && b < a + p_bytes;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t i8mm_kv_pages_workspace_bytes(int64_t num_rows, int64_t num_pages) {
+  i8mm::PagesArgs a;
+  if (pages_sizes("i8mm_kv_pages_workspace_bytes", 0, 0, num_rows, num_pages, I8MM_KV_BLOCK, &a) !=
+      I8MM_OK)
+    return 0;
+  return i8mm::kv_pages_workspace_bytes(a);
+}
+
+int i8mm_kv_pages_step(const int32_t* page_table, const int32_t* seq_lens, int64_t num_seqs,
+                       int64_t max_pages, const int32_t* parents, const int32_t* keep,
+                       const int32_t* new_tokens, int64_t new_all, int64_t num_rows,
+                       int64_t num_pages, int64_t page_tokens, int32_t* out_table,
+                       int32_t* out_lens, int32_t* copies, int32_t* counts, void* workspace,
+                       size_t workspace_bytes, i8mm_stream_t stream) {
+  const char* fn = "i8mm_kv_pages_step";
+  i8mm::PagesArgs a;
+  I8MM_TRY(pages_sizes(fn, num_seqs, max_pages, num_rows, num_pages, page_tokens, &a));
+  if (new_all < 0 || new_all > (1 << 30))
+    return fail(I8MM_EINVAL, "%s: %lld new tokens", fn, (long long)new_all);
+  I8MM_TRY(check_ints(fn, "page_table", page_table, num_seqs * max_pages > 0));
+  I8MM_TRY(check_ints(fn, "seq_lens", seq_lens, num_seqs > 0));
+  I8MM_TRY(check_ints(fn, "parents", parents, num_rows > 0));
+  I8MM_TRY(check_ints(fn, "keep", keep, false));
+  I8MM_TRY(check_ints(fn, "new_tokens", new_tokens, false));
+  I8MM_TRY(check_ints(fn, "out_table", out_table, num_rows * max_pages > 0));
+  I8MM_TRY(check_ints(fn, "out_lens", out_lens, num_rows > 0));
+  I8MM_TRY(check_ints(fn, "copies", copies, num_rows > 0));
+  I8MM_TRY(check_ints(fn, "counts", counts, true));
+  if (overlap(page_table, 4 * num_seqs * max_pages, out_table, 4 * num_rows * max_pages) ||
+      overlap(seq_lens, 4 * num_seqs, out_lens, 4 * num_rows))
+    return fail(I8MM_EINVAL, "%s: the new table or lengths overlap the old ones", fn);
+  I8MM_TRY(check_scratch(fn, workspace, workspace_bytes, i8mm::kv_pages_workspace_bytes(a)));
+  I8MM_TRY(check_device());
+  a.page_table = page_table;
+  a.seq_lens = seq_lens;
+  a.parents = parents;
+  a.keep = keep;
+  a.new_tokens = new_tokens;
+  a.new_all = (int)new_all;
+  a.out_table = out_table;
+  a.out_lens = out_lens;
+  a.copies = copies;
+  a.counts = counts;
+  I8MM_TRY(launched(i8mm::launch_kv_pages_step(a, workspace, (hipStream_t)stream), fn));
+  return ok();
+}
+
+int i8mm_kv_pages_compact(const int32_t* page_table, const int32_t* seq_lens, int64_t num_seqs,
+                          int64_t max_pages, int64_t num_pages, int64_t page_tokens,
+                          int32_t* out_table, int32_t* copies, int32_t* counts, void* workspace,
+                          size_t workspace_bytes, i8mm_stream_t stream) {
+  const char* fn = "i8mm_kv_pages_compact";
+  i8mm::PagesArgs a;
+  I8MM_TRY(pages_sizes(fn, num_seqs, max_pages, 0, num_pages, page_tokens, &a));
+  const int64_t entries = num_seqs * max_pages;
+  I8MM_TRY(check_ints(fn, "page_table", page_table, entries > 0));
+  I8MM_TRY(check_ints(fn, "seq_lens", seq_lens, num_seqs > 0));
+  I8MM_TRY(check_ints(fn, "out_table", out_table, entries > 0));
+  I8MM_TRY(check_ints(fn, "copies", copies, num_pages >= 2));
+  I8MM_TRY(check_ints(fn, "counts", counts, true));
+  if (out_table != page_table && overlap(page_table, 4 * entries, out_table, 4 * entries))
+    return fail(I8MM_EINVAL, "%s: the new table overlaps the old one without being it", fn);
+  I8MM_TRY(check_scratch(fn, workspace, workspace_bytes, i8mm::kv_pages_workspace_bytes(a)));
+  I8MM_TRY(check_device());
+  a.page_table = page_table;
+  a.seq_lens = seq_lens;
+  a.out_table = out_table;
+  a.copies = copies;
+  a.counts = counts;
+  I8MM_TRY(launched(i8mm::launch_kv_pages_compact(a, workspace, (hipStream_t)stream), fn));
+  return ok();
+}
+
+int int8_kv_cache_copy_pages(const i8mm_kv_cache* cache, uint16_t* k_means, const int32_t* copies,
+                             const int32_t* count, int64_t max_copies, i8mm_stream_t stream) {
+  const char* fn = "int8_kv_cache_copy_pages";
+  i8mm::KvArgs a = {};
+  if (!cache) return fail(I8MM_EINVAL, "%s: cache is NULL", fn);
+  I8MM_TRY(cache_sizes(fn, cache, &a));
+  I8MM_TRY(cache_pointers(fn, cache, &a));
+  I8MM_TRY(check_ptr(fn, "k_means", k_means, false));
+  if (max_copies < 0 || max_copies > INT32_MAX)
+    return fail(I8MM_EINVAL, "%s: %lld copies", fn, (long long)max_copies);
+  I8MM_TRY(check_ints(fn, "copies", copies, max_copies > 0));
+  I8MM_TRY(check_ints(fn, "count", count, max_copies > 0));
+  if (max_copies == 0 || a.num_pages == 0) return ok();
+  I8MM_TRY(check_device());
+  I8MM_TRY(launched(i8mm::launch_kv_copy_pages(a, k_means, copies, count, (int)max_copies,
+                                               (hipStream_t)stream), fn));
   return ok();
 }
 

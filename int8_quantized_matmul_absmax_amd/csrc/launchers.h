@@ -154,6 +154,26 @@ struct BeamArgs {
 size_t beam_workspace_bytes(const BeamArgs& a);
 hipError_t launch_beam_select(const BeamArgs& a, hipStream_t s);
 
+// ---- pages of the key/value cache (arguments as in the C ABI)
+struct PagesArgs {
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  const int32_t* parents;
+  const int32_t* keep;        // or nullptr: all tokens
+  const int32_t* new_tokens;  // or nullptr: new_all
+  int32_t* out_table;
+  int32_t* out_lens;
+  int32_t* copies;
+  int32_t* counts;
+  int num_seqs, max_pages, num_rows, num_pages, page_tokens, new_all;
+};
+size_t kv_pages_workspace_bytes(const PagesArgs& a);
+hipError_t launch_kv_pages_step(const PagesArgs& a, void* ws, hipStream_t s);
+hipError_t launch_kv_pages_compact(const PagesArgs& a, void* ws, hipStream_t s);
+// (of KvArgs the cache's part)
+hipError_t launch_kv_copy_pages(const KvArgs& a, uint16_t* means, const int32_t* copies,
+                                const int32_t* count, int most, hipStream_t s);
+
 hipError_t launch_gelu(const uint16_t* X, int64_t count, uint16_t* Y, hipStream_t s);
 
 }  // namespace i8mm

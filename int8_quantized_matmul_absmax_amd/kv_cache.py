@@ -34,10 +34,13 @@ class Int8KVCache:
     k_codes, v_codes  int8 [num_pages, kv_heads, page_tokens / 16, D / 16, 16, 16]
                       tiles: keys [token][feature], values [feature][token]
     k_absmax, v_absmax  fp32 [num_pages, kv_heads, page_tokens / 16]
+    k_means  None, or fp16 [num_pages, kv_heads, D]: the mean key of each page
+             (page_means=True), which select_pages goes by
 
-    Which page belongs to which sequence is the caller's to decide."""
+    Which page belongs to which sequence is the caller's to decide (KVPages)."""
 
-    def __init__(self, num_pages, kv_heads, head_dim, page_tokens=64, device="cuda"):
+    def __init__(self, num_pages, kv_heads, head_dim, page_tokens=64, device="cuda",
+                 page_means=False):
         if head_dim not in HEAD_DIMS:
             raise ValueError("head_dim must be one of %s, got %s" % (HEAD_DIMS, head_dim))
         if page_tokens <= 0 or page_tokens % BLOCK != 0:
@@ -47,16 +50,18 @@ class Int8KVCache:
         self._hold(torch.empty(tiles, dtype=torch.int8, device=device),
                    torch.empty(blocks, dtype=torch.float32, device=device),
                    torch.empty(tiles, dtype=torch.int8, device=device),
-                   torch.empty(blocks, dtype=torch.float32, device=device))
+                   torch.empty(blocks, dtype=torch.float32, device=device),
+                   torch.zeros(blocks[:2] + (head_dim,), dtype=torch.float16, device=device)
+                   if page_means else None)
 
     @classmethod
-    def from_tensors(cls, k_codes, k_absmax, v_codes, v_absmax):
+    def from_tensors(cls, k_codes, k_absmax, v_codes, v_absmax, k_means=None):
         """A cache over tensors of the layout above (shared, not copied)."""
         self = cls.__new__(cls)
-        self._hold(k_codes, k_absmax, v_codes, v_absmax)
+        self._hold(k_codes, k_absmax, v_codes, v_absmax, k_means)
         return self
 
-    def _hold(self, k_codes, k_absmax, v_codes, v_absmax):
+    def _hold(self, k_codes, k_absmax, v_codes, v_absmax, k_means=None):
         ops._need(k_codes, "k_codes", torch.int8, 6)
         pages, heads, slots, tiles = k_codes.shape[:4]
         if k_codes.shape[4:] != (16, 16) or tiles * 16 not in HEAD_DIMS or slots == 0 or heads == 0:
@@ -65,10 +70,13 @@ class Int8KVCache:
         ops._need(k_absmax, "k_absmax", torch.float32, shape=(pages, heads, slots))
         ops._need(v_codes, "v_codes", torch.int8, shape=k_codes.shape)
         ops._need(v_absmax, "v_absmax", torch.float32, shape=(pages, heads, slots))
+        if k_means is not None:
+            ops._need(k_means, "k_means", torch.float16, shape=(pages, heads, tiles * 16))
         self.device = ops._on_gpu(k_codes=k_codes, k_absmax=k_absmax, v_codes=v_codes,
-                                  v_absmax=v_absmax)
+                                  v_absmax=v_absmax, k_means=k_means)
         self.k_codes, self.k_absmax = k_codes, k_absmax
         self.v_codes, self.v_absmax = v_codes, v_absmax
+        self.k_means = k_means
         self.num_pages, self.kv_heads = pages, heads
         self.page_tokens, self.head_dim = slots * BLOCK, tiles * 16
         self._struct, self.ref = _struct(
@@ -91,6 +99,66 @@ class Int8KVCache:
     def read(self, batch):
         """Keys and values of the batch's tokens in fp16."""
         return ops.int8_kv_cache_read(self, batch)
+
+    def copy_pages(self, copies):
+        """The copies that a KVPages call asked for. The table it gave is right for
+        this cache after them."""
+        ops.int8_kv_cache_copy_pages(self, copies.pages, copies.counts)
+
+
+class PageCopies:
+    """Copies of pages that a KVPages call asks for, on the GPU: pages int32 [n, 3]
+    (page, page to copy it to, tokens that count), counts int32 [2], the number of
+    them first."""
+
+    def __init__(self, pages, counts):
+        self.pages, self.counts = pages, counts
+
+
+class KVPages:
+    """The pages of the caches of a model's layers, which share one page table. It
+    holds nothing but their number and size: a page is free when no row of the table
+    names it. Nothing waits for the host.
+
+        table, lens, copies = pool.step(table, lens, parents)
+        for cache in caches:
+            cache.copy_pages(copies)
+        batch = KVBatch(table, lens)"""
+
+    def __init__(self, num_pages, page_tokens=64):
+        if page_tokens <= 0 or page_tokens % BLOCK != 0:
+            raise ValueError("page_tokens must be a positive multiple of %d" % BLOCK)
+        if num_pages < 0:
+            raise ValueError("num_pages must not be negative")
+        self.num_pages, self.page_tokens = int(num_pages), int(page_tokens)
+
+    def empty_table(self, rows, max_tokens, device="cuda"):
+        """The table and lengths of `rows` sequences of no tokens, wide enough for
+        max_tokens."""
+        width = -(-int(max_tokens) // self.page_tokens)
+        return (torch.full((rows, width), -1, dtype=torch.int32, device=device),
+                torch.zeros((rows,), dtype=torch.int32, device=device))
+
+    def step(self, page_table, seq_lens, parents, new_tokens=1, keep=None):
+        """The table of the next step, its lengths (new tokens included) and the
+        copies to make before its append. Row i keeps the first keep[i] tokens (None:
+        all) of row parents[i] (-1: none) and has room for new_tokens (an int, or one
+        a row) after them: beams that go on from others, prompts that several
+        sequences share, growth, cutting back, beginning and, for rows that the new
+        table leaves out, ending are all this call. Pages that rows share are copied
+        for those about to write to them. copies.counts[1] says how many pages were
+        wanting; their tokens are absent."""
+        table, lens, pages, counts = ops.kv_pages_step(
+            page_table, seq_lens, parents, self.num_pages, self.page_tokens, new_tokens, keep,
+            shared_workspace)
+        return table, lens, PageCopies(pages, counts)
+
+    def compact(self, page_table, seq_lens):
+        """The used pages to the front of the caches: the table with their new places
+        and the copies to make. copies.counts[1] says how many are used."""
+        table, pages, counts = ops.kv_pages_compact(page_table, seq_lens, self.num_pages,
+                                                    self.page_tokens, shared_workspace)
+        return table, PageCopies(pages, counts)
 
 
 class KVBatch:

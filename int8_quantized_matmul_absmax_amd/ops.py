@@ -446,6 +446,79 @@ def int8_kv_cache_read(cache, batch):
     return k, v
 
 
+def kv_pages_step(page_table, seq_lens, parents, num_pages, page_tokens, new_tokens=1, keep=None,
+                  workspace=None):
+    """The page table of the next step: row i keeps the first keep[i] tokens (None:
+    all) of row parents[i] (none for a parent outside the table) and has room for
+    new_tokens (an int, or int32 [rows]) after them. All int32 on the GPU.
+
+    Returns the table [rows, max_pages], the lengths [rows] (new tokens included),
+    the copies to make before the next append [rows, 3] and counts [2]: copies, and
+    pages that were wanting (their tokens are absent)."""
+    lib = _lib.load_library()
+    _need(page_table, "page_table", torch.int32, 2)
+    seqs, width = page_table.shape
+    _need(seq_lens, "seq_lens", torch.int32, shape=(seqs,))
+    if isinstance(parents, torch.Tensor):
+        parents = parents.view(-1) if parents.is_contiguous() else parents
+    _need(parents, "parents", torch.int32, 1)
+    rows = parents.shape[0]
+    if keep is not None:
+        _need(keep, "keep", torch.int32, min_numel=rows)
+    each, new_all = None, 0
+    if isinstance(new_tokens, torch.Tensor):
+        _need(new_tokens, "new_tokens", torch.int32)
+        if new_tokens.numel() != rows:
+            raise ValueError("new_tokens must hold %d numbers, got %d" % (rows, new_tokens.numel()))
+        each = new_tokens
+    else:
+        new_all = int(new_tokens)
+    if keep is not None and keep.numel() != rows:
+        raise ValueError("keep must hold %d numbers, got %d" % (rows, keep.numel()))
+    dev = _on_gpu(page_table=page_table, seq_lens=seq_lens, parents=parents, keep=keep,
+                  new_tokens=each)
+    out = torch.empty((rows * (width + 4) + 2,), dtype=torch.int32, device=dev)
+    table, lens, copies, counts = out.split((rows * width, rows, 3 * rows, 2))
+    wp, wn = _scratch(lib.i8mm_kv_pages_workspace_bytes(rows, num_pages), workspace, dev)
+    _run(dev, lib.i8mm_kv_pages_step, page_table.data_ptr(), seq_lens.data_ptr(), seqs, width,
+         parents.data_ptr(), None if keep is None else keep.data_ptr(),
+         None if each is None else each.data_ptr(), new_all, rows, num_pages, page_tokens,
+         table.data_ptr(), lens.data_ptr(), copies.data_ptr(), counts.data_ptr(), wp, wn)
+    return table.view(rows, width), lens, copies.view(rows, 3), counts
+
+
+def kv_pages_compact(page_table, seq_lens, num_pages, page_tokens, workspace=None):
+    """The used pages to the front: the table with their new places, the copies to
+    make [num_pages // 2, 3] and counts [2]: copies, and used pages."""
+    lib = _lib.load_library()
+    _need(page_table, "page_table", torch.int32, 2)
+    seqs, width = page_table.shape
+    _need(seq_lens, "seq_lens", torch.int32, shape=(seqs,))
+    dev = _on_gpu(page_table=page_table, seq_lens=seq_lens)
+    most = max(int(num_pages) // 2, 0)
+    out = torch.empty((seqs * width + 3 * most + 2,), dtype=torch.int32, device=dev)
+    table, copies, counts = out.split((seqs * width, 3 * most, 2))
+    wp, wn = _scratch(lib.i8mm_kv_pages_workspace_bytes(0, num_pages), workspace, dev)
+    _run(dev, lib.i8mm_kv_pages_compact, page_table.data_ptr(), seq_lens.data_ptr(), seqs, width,
+         num_pages, page_tokens, table.data_ptr(), copies.data_ptr(), counts.data_ptr(), wp, wn)
+    return table.view(seqs, width), copies.view(most, 3), counts
+
+
+def int8_kv_cache_copy_pages(cache, copies, count):
+    """Copy a cache's pages (its mean keys, too, where it holds them): copies int32
+    [n, 3] of (page, page to copy it to, tokens that count), of which the first
+    `count` (int32, its first element) are made."""
+    lib = _lib.load_library()
+    _need(copies, "copies", torch.int32, 2)
+    if copies.shape[1] != 3:
+        raise ValueError("copies must be [n, 3], got %s" % (tuple(copies.shape),))
+    _need(count, "count", torch.int32, min_numel=1)
+    _on_gpu(cache=cache.k_codes, copies=copies, count=count)
+    _run(cache.device, lib.int8_kv_cache_copy_pages, cache.ref,
+         None if cache.k_means is None else cache.k_means.data_ptr(), copies.data_ptr(),
+         count.data_ptr(), copies.shape[0])
+
+
 # ---- a beam search over such caches
 
 def beam_select(logits, scores, live=None, eos=None, count=None, workspace=None):
