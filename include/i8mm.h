@@ -515,6 +515,72 @@ I8MM_API int int8_kv_cache_read(const i8mm_kv_cache* cache, const i8mm_kv_batch*
                                 uint16_t* k, uint16_t* v, i8mm_stream_t stream);
 
 /*
+ * Attention over some of the pages: for a long sequence a query reads the pages
+ * that a cheap score chooses for it. A page's mean key stands for it:
+ *   k_means  fp16 [num_pages, kv_heads, D], 16-byte aligned, beside the cache.
+ *
+ * int8_kv_cache_page_means: the mean keys of the pages that hold the batch's new
+ * tokens (after their append), over the tokens that the page then holds:
+ * fp16(fl32(sum_t k_t / n)), the sum of q * fl32(a / 127) in 64 bits.
+ * Errors: EINVAL, EALIGN, ENODEVICE, ELAUNCH.
+ */
+I8MM_API int int8_kv_cache_page_means(const i8mm_kv_cache* cache, const i8mm_kv_batch* batch,
+                                      uint16_t* k_means, i8mm_stream_t stream);
+
+/*
+ * int8_kv_cache_select_pages: for each new token, at position p, and key/value head,
+ * `count` of the pages 0 .. p / page_tokens of its sequence: the first `first` and
+ * the last `recent` of them, and of the others those of the largest score
+ *   <sum over the head's query heads of the rotated q, k_means of the page>
+ * (64-bit sums of the 16-bit values and 32-bit tables), equal ones by their number.
+ * A page that is absent, or whose score is NaN, counts as one of score -infinity.
+ *
+ *   q, rotary  as for int8_kv_cache_attention.
+ *   count      first + recent .. 2^30 / page_tokens; first >= 0, recent >= 1. A
+ *              sequence has at most I8MM_MAX_SELECT_PAGES pages beside the first and
+ *              the recent ones (by max_len).
+ *   pages      int32 [total_tokens, kv_heads, count], 4-byte aligned: numbers of
+ *              pages in the sequence, ascending, then -1 (all -1 for a token of no
+ *              sequence).
+ * Errors: EINVAL, EALIGN, ENODEVICE, ELAUNCH.
+ */
+#define I8MM_MAX_SELECT_PAGES 16384
+I8MM_API int int8_kv_cache_select_pages(const uint16_t* q, int64_t q_token_stride,
+                                        int64_t q_head_stride, int64_t q_heads,
+                                        const i8mm_kv_cache* cache, const uint16_t* k_means,
+                                        const i8mm_kv_batch* batch, const i8mm_rotary* rotary,
+                                        int64_t count, int64_t first, int64_t recent, int32_t* pages,
+                                        i8mm_stream_t stream);
+
+/*
+ * int8_kv_cache_attention_pages: int8_kv_cache_attention, causal, over the tokens of
+ * the listed pages alone.
+ *   pages    int32 [total_tokens, kv_heads, count], 4-byte aligned: numbers of pages
+ *            in the token's sequence, in any order; one that is negative, past the
+ *            token's own page or absent has no tokens, one listed twice counts twice.
+ *   count    1 .. 2^30 / page_tokens.
+ *   q, rotary, scale, out  as for int8_kv_cache_attention; a token that sees nothing
+ *            gets 0.
+ *   workspace  int8_kv_cache_attention_pages_workspace_bytes(...) bytes, 256-byte
+ *            aligned (NULL when that is 0). What it holds on entry does not matter.
+ * Roundings are int8_kv_cache_attention's, the weights' those of two parts of fp16.
+ * Errors: EINVAL, EALIGN, EWORKSPACE, ENODEVICE, ELAUNCH.
+ */
+I8MM_API int int8_kv_cache_attention_pages(const uint16_t* q, int64_t q_token_stride,
+                                           int64_t q_head_stride, int64_t q_heads,
+                                           const i8mm_kv_cache* cache, const i8mm_kv_batch* batch,
+                                           const i8mm_rotary* rotary, const int32_t* pages,
+                                           int64_t count, float scale, uint16_t* out,
+                                           void* workspace, size_t workspace_bytes,
+                                           i8mm_stream_t stream);
+
+/* Bytes of workspace int8_kv_cache_attention_pages needs (0 also if the sizes are
+ * invalid). Host-only, pure: it reads the structs' sizes, not their pointers. */
+I8MM_API size_t int8_kv_cache_attention_pages_workspace_bytes(const i8mm_kv_cache* cache,
+                                                              const i8mm_kv_batch* batch,
+                                                              int64_t q_heads, int64_t count);
+
+/*
  * Pages of the cache. What belongs to a sequence is in the page table alone: a
  * page that no row names is free, and one that several name is shared, which is
  * right for tokens that none of them will change. The calls below make the next

@@ -34,6 +34,10 @@ EXPORTS = (
     "int8_kv_cache_attention",
     "int8_kv_cache_attention_workspace_bytes",
     "int8_kv_cache_read",
+    "int8_kv_cache_page_means",
+    "int8_kv_cache_select_pages",
+    "int8_kv_cache_attention_pages",
+    "int8_kv_cache_attention_pages_workspace_bytes",
     "i8mm_kv_pages_step",
     "i8mm_kv_pages_compact",
     "i8mm_kv_pages_workspace_bytes",
@@ -105,6 +109,12 @@ def _declare(lib):
                                      vp, ctypes.c_size_t, vp], i32),
         "int8_kv_cache_attention_workspace_bytes": ([cache, batch, i64], ctypes.c_size_t),
         "int8_kv_cache_read": ([cache, batch, vp, vp, vp], i32),
+        "int8_kv_cache_page_means": ([cache, batch, vp, vp], i32),
+        "int8_kv_cache_select_pages": ([vp, i64, i64, i64, cache, vp, batch, rotary, i64, i64, i64, vp,
+                                        vp], i32),
+        "int8_kv_cache_attention_pages": ([vp, i64, i64, i64, cache, batch, rotary, vp, i64, f32, vp,
+                                           vp, ctypes.c_size_t, vp], i32),
+        "int8_kv_cache_attention_pages_workspace_bytes": ([cache, batch, i64, i64], ctypes.c_size_t),
         "i8mm_kv_pages_step": ([vp, vp, i64, i64, vp, vp, vp, i64, i64, i64, i64, vp, vp, vp, vp, vp,
                                 ctypes.c_size_t, vp], i32),
         "i8mm_kv_pages_compact": ([vp, vp, i64, i64, i64, i64, vp, vp, vp, vp, ctypes.c_size_t, vp],

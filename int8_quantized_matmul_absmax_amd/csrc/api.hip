@@ -559,6 +559,13 @@ bool heads_ok(const i8mm::KvArgs& a, int64_t q_heads) {
          a.total_tokens <= (int64_t{1} << 40) / q_heads;
 }
 
+int heads_check(const char* fn, const i8mm::KvArgs& a, int64_t q_heads) {
+  if (heads_ok(a, q_heads)) return I8MM_OK;
+  return fail(I8MM_EINVAL, "%s: q_heads=%lld is not a multiple of %d key/value heads, or too many "
+              "for %d tokens, %d a sequence", fn, (long long)q_heads, a.kv_heads, a.total_tokens,
+              a.max_tokens);
+}
+
 // No row of the packed tensors belongs to a sequence.
 bool no_tokens(const i8mm::KvArgs& a) {
   return a.total_tokens == 0 || a.max_tokens == 0 || a.num_seqs == 0;
@@ -639,10 +646,7 @@ int int8_kv_cache_attention(const uint16_t* q, int64_t q_token_stride, int64_t q
   i8mm::RotaryArgs r;
   I8MM_TRY(kv_check(fn, cache, batch, &a));
   I8MM_TRY(rotary_check(fn, rotary, a, &r));
-  if (!heads_ok(a, q_heads))
-    return fail(I8MM_EINVAL, "%s: q_heads=%lld is not a multiple of %d key/value heads, or too many "
-                "for %d tokens, %d a sequence", fn, (long long)q_heads, a.kv_heads,
-                a.total_tokens, a.max_tokens);
+  I8MM_TRY(heads_check(fn, a, q_heads));
   I8MM_TRY(strides_check(fn, "q", q, a.total_tokens > 0, q_token_stride, q_head_stride));
   if (!std::isfinite(scale) || !(scale > 0.f))
     return fail(I8MM_EINVAL, "%s: scale is not finite and positive", fn);
@@ -904,6 +908,119 @@ int int8_kv_cache_copy_pages(const i8mm_kv_cache* cache, uint16_t* k_means, cons
   I8MM_TRY(check_device());
   I8MM_TRY(launched(i8mm::launch_kv_copy_pages(a, k_means, copies, count, (int)max_copies,
                                                (hipStream_t)stream), fn));
+  return ok();
+}
+
+}  // extern "C"
+
+namespace {
+
+// A list of pages for each token and head.
+int count_check(const char* fn, const i8mm::KvArgs& a, int64_t count) {
+  if (count < 1 || count > (1 << 30) / (a.slots * I8MM_KV_BLOCK))
+    return fail(I8MM_EINVAL, "%s: lists of %lld pages of %d tokens", fn, (long long)count,
+                a.slots * I8MM_KV_BLOCK);
+  return I8MM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int int8_kv_cache_page_means(const i8mm_kv_cache* cache, const i8mm_kv_batch* batch,
+                             uint16_t* k_means, i8mm_stream_t stream) {
+  const char* fn = "int8_kv_cache_page_means";
+  i8mm::KvArgs a;
+  I8MM_TRY(kv_check(fn, cache, batch, &a));
+  I8MM_TRY(check_ptr(fn, "k_means", k_means, a.num_pages > 0));
+  if (no_tokens(a) || a.len_cap == 0) return ok();
+  I8MM_TRY(check_device());
+  I8MM_TRY(launched(i8mm::launch_kv_page_means(a, k_means, (hipStream_t)stream), fn));
+  return ok();
+}
+
+int int8_kv_cache_select_pages(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride,
+                               int64_t q_heads, const i8mm_kv_cache* cache, const uint16_t* k_means,
+                               const i8mm_kv_batch* batch, const i8mm_rotary* rotary, int64_t count,
+                               int64_t first, int64_t recent, int32_t* pages, i8mm_stream_t stream) {
+  const char* fn = "int8_kv_cache_select_pages";
+  i8mm::KvArgs a;
+  i8mm::RotaryArgs r;
+  I8MM_TRY(kv_check(fn, cache, batch, &a));
+  I8MM_TRY(rotary_check(fn, rotary, a, &r));
+  I8MM_TRY(heads_check(fn, a, q_heads));
+  I8MM_TRY(strides_check(fn, "q", q, a.total_tokens > 0, q_token_stride, q_head_stride));
+  I8MM_TRY(check_ptr(fn, "k_means", k_means, a.num_pages > 0));
+  I8MM_TRY(count_check(fn, a, count));
+  if (first < 0 || recent < 1 || first > count || recent > count - first)
+    return fail(I8MM_EINVAL, "%s: first=%lld and recent=%lld of count=%lld", fn, (long long)first,
+                (long long)recent, (long long)count);
+  const int64_t page_tokens = (int64_t)a.slots * I8MM_KV_BLOCK;
+  if ((a.len_cap + page_tokens - 1) / page_tokens - first - recent > I8MM_MAX_SELECT_PAGES)
+    return fail(I8MM_EINVAL, "%s: more than %d pages to choose from in %d tokens", fn,
+                I8MM_MAX_SELECT_PAGES, a.len_cap);
+  I8MM_TRY(check_ints(fn, "pages", pages, a.total_tokens > 0));
+  if (a.total_tokens == 0) return ok();
+  I8MM_TRY(check_device());
+  if (no_tokens(a)) {
+    I8MM_TRY(launched(i8mm::launch_fill_u32(reinterpret_cast<uint32_t*>(pages),
+                                            (int64_t)a.total_tokens * a.kv_heads * count, ~0u,
+                                            (hipStream_t)stream), fn));
+    return ok();
+  }
+  I8MM_TRY(launched(i8mm::launch_kv_select_pages(a, r, q, q_token_stride, q_head_stride, (int)q_heads,
+                                                 k_means, (int)count, (int)first, (int)recent, pages,
+                                                 (hipStream_t)stream), fn));
+  return ok();
+}
+
+size_t int8_kv_cache_attention_pages_workspace_bytes(const i8mm_kv_cache* cache,
+                                                     const i8mm_kv_batch* batch, int64_t q_heads,
+                                                     int64_t count) {
+  const char* fn = "int8_kv_cache_attention_pages_workspace_bytes";
+  i8mm::KvArgs a;
+  if (kv_sizes(fn, cache, batch, &a) != I8MM_OK || !heads_ok(a, q_heads) ||
+      count_check(fn, a, count) != I8MM_OK)
+    return 0;
+  return i8mm::attn_pages_workspace_bytes(a, (int)q_heads, (int)count);
+}
+
+int int8_kv_cache_attention_pages(const uint16_t* q, int64_t q_token_stride, int64_t q_head_stride,
+                                  int64_t q_heads, const i8mm_kv_cache* cache,
+                                  const i8mm_kv_batch* batch, const i8mm_rotary* rotary,
+                                  const int32_t* pages, int64_t count, float scale, uint16_t* out,
+                                  void* workspace, size_t workspace_bytes, i8mm_stream_t stream) {
+  const char* fn = "int8_kv_cache_attention_pages";
+  i8mm::KvArgs a;
+  i8mm::RotaryArgs r;
+  I8MM_TRY(kv_check(fn, cache, batch, &a));
+  I8MM_TRY(rotary_check(fn, rotary, a, &r));
+  I8MM_TRY(heads_check(fn, a, q_heads));
+  I8MM_TRY(strides_check(fn, "q", q, a.total_tokens > 0, q_token_stride, q_head_stride));
+  I8MM_TRY(count_check(fn, a, count));
+  I8MM_TRY(check_ints(fn, "pages", pages, a.total_tokens > 0));
+  if (!std::isfinite(scale) || !(scale > 0.f))
+    return fail(I8MM_EINVAL, "%s: scale is not finite and positive", fn);
+  I8MM_TRY(check_ptr(fn, "out", out, a.total_tokens > 0));
+  I8MM_TRY(check_scratch(fn, workspace, workspace_bytes,
+                         i8mm::attn_pages_workspace_bytes(a, (int)q_heads, (int)count)));
+  if (a.total_tokens == 0) return ok();
+  I8MM_TRY(check_device());
+  if (no_tokens(a) || a.len_cap == 0) {
+    I8MM_TRY(zero_halfs(fn, out, a.total_tokens * q_heads * a.head_dim, stream));
+    return ok();
+  }
+  i8mm::AttnArgs t = {};
+  t.q = q;
+  t.q_ts = q_token_stride;
+  t.q_hs = q_head_stride;
+  t.out = out;
+  t.part = static_cast<float*>(workspace);
+  t.scale_log2 = scale * 1.44269504088896340736f;
+  t.q_heads = (int)q_heads;
+  t.causal = 1;
+  I8MM_TRY(launched(i8mm::launch_kv_attention_pages(a, r, t, pages, (int)count, (hipStream_t)stream),
+                    fn));
   return ok();
 }
 

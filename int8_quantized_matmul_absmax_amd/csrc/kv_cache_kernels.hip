@@ -322,15 +322,6 @@ int64_t max_blocks(const KvArgs& a) { return ((int64_t)a.max_tokens + 2 * kKvBlo
 
 bool kv_head_dim_ok(int64_t D) { return D == 64 || D == 80 || D == 96 || D == 128 || D == 256; }
 
-#define I8MM_KV_DIMS(D, CALL) \
-  switch (D) {                \
-    case 64: { CALL(64); } break;   \
-    case 80: { CALL(80); } break;   \
-    case 96: { CALL(96); } break;   \
-    case 128: { CALL(128); } break; \
-    default: { CALL(256); } break;  \
-  }
-
 hipError_t launch_kv_append(const uint16_t* k, int64_t k_ts, int64_t k_hs, const uint16_t* v,
                             int64_t v_ts, int64_t v_hs, const KvArgs& a, const RotaryArgs& r,
                             hipStream_t s) {

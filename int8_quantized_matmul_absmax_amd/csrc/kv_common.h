@@ -88,4 +88,49 @@ __device__ __forceinline__ void rotate_half(const v4f32& c0, const v4f32& c1, co
   }
 }
 
+// The sequence whose rows token t is among: the last that begins at t or before.
+// 64 probes at once.
+__device__ __forceinline__ int sequence_of(const KvArgs& a, int t, int lane) {
+  if (!a.cu_tokens) return t;
+  int b = 0;
+  for (int size = a.num_seqs; size > 0;) {
+    const int step = (size + kWave - 1) / kWave, ahead = lane * step;
+    const bool before = ahead < size && a.cu_tokens[b + ahead] <= t;
+    const int n = __popcll(__ballot(before));
+    if (n == 0) break;
+    const int at = (n - 1) * step;
+    b += at;
+    size = step == 1 ? 0 : min(step, size - at);
+  }
+  return b;
+}
+
+// Exclusive prefix sum over the block's kWaves waves, and the total. Two barriers.
+template <int kWaves>
+__device__ __forceinline__ int block_prefix(int v, int* s_wave, int* total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int incl = wave_inclusive_scan_dpp(v);
+  if (lane == 63) s_wave[wave] = incl;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    const int s = s_wave[w];
+    before += w < wave ? s : 0;
+    all += s;
+  }
+  __syncthreads();
+  *total = all;
+  return before + incl - v;
+}
+
+#define I8MM_KV_DIMS(D, CALL) \
+  switch (D) {                \
+    case 64: { CALL(64); } break;   \
+    case 80: { CALL(80); } break;   \
+    case 96: { CALL(96); } break;   \
+    case 128: { CALL(128); } break; \
+    default: { CALL(256); } break;  \
+  }
+
 }  // namespace i8mm

@@ -66,24 +66,6 @@ __global__ __launch_bounds__(kBlockThreads) void k_kv_pages_keep(PagesArgs a, ui
     __hip_atomic_store(words + page, kRead, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// Exclusive prefix sum over the block's threads, and the total. Two barriers.
-__device__ __forceinline__ int block_prefix(int v, int* s_wave, int* total) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int incl = wave_inclusive_scan_dpp(v);
-  if (lane == 63) s_wave[wave] = incl;
-  __syncthreads();
-  int before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kOneWaves; ++w) {
-    const int s = s_wave[w];
-    before += w < wave ? s : 0;
-    all += s;
-  }
-  __syncthreads();
-  *total = all;
-  return before + incl - v;
-}
-
 // The first `want` pages whose word is 0, to list; how many there are of them.
 __device__ __forceinline__ int list_free(const uint32_t* words, int num_pages, int want,
                                          int32_t* list, int* s_wave) {
@@ -97,7 +79,7 @@ __device__ __forceinline__ int list_free(const uint32_t* words, int num_pages, i
 #pragma unroll
     for (int e = 0; e < 4; ++e) n += w[e] == 0;
     int total;
-    int at = found + block_prefix(n, s_wave, &total);
+    int at = found + block_prefix<kOneWaves>(n, s_wave, &total);
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       if (w[e] == 0) {
@@ -130,9 +112,9 @@ __global__ __launch_bounds__(kOneBlock) void k_kv_pages_give(PagesArgs a, const 
       need = copy + r.all_pages - r.pages;
     }
     int total;
-    const int at = want + block_prefix(need, s_wave, &total);
+    const int at = want + block_prefix<kOneWaves>(need, s_wave, &total);
     want += total;
-    const int rank = copies + block_prefix(copy, s_wave, &total);
+    const int rank = copies + block_prefix<kOneWaves>(copy, s_wave, &total);
     copies += total;
     if (i < a.num_rows) places[i] = int2{at, copy ? rank : -1};
   }
@@ -161,7 +143,7 @@ __global__ __launch_bounds__(kOneBlock) void k_kv_pages_give(PagesArgs a, const 
       for (int j = r.pages; j < r.all_pages; ++j, ++at) row[j] = at < have ? list[at] : -1;
     }
     int total;
-    block_prefix(made, s_wave, &total);
+    block_prefix<kOneWaves>(made, s_wave, &total);
     done += total;
   }
   // (copies are made in the order of the rows until the pages run out)
@@ -192,7 +174,7 @@ __global__ __launch_bounds__(kOneBlock) void k_kv_pages_plan(PagesArgs a, uint32
   int live = 0, total;
   for (int p0 = 0; p0 < a.num_pages; p0 += kOneBlock) {
     const int p = p0 + tid;
-    block_prefix(p < a.num_pages && words[p] != 0, s_wave, &total);
+    block_prefix<kOneWaves>(p < a.num_pages && words[p] != 0, s_wave, &total);
     live += total;
   }
   list_free(words, live, live, list, s_wave);
@@ -200,7 +182,7 @@ __global__ __launch_bounds__(kOneBlock) void k_kv_pages_plan(PagesArgs a, uint32
   for (int p0 = 0; p0 < a.num_pages; p0 += kOneBlock) {
     const int p = p0 + tid;
     const bool used = p < a.num_pages && words[p] != 0, moved = used && p >= live;
-    const int rank = moves + block_prefix(moved, s_wave, &total);
+    const int rank = moves + block_prefix<kOneWaves>(moved, s_wave, &total);
     moves += total;
     if (used) words[p] = moved ? (uint32_t)list[rank] : (uint32_t)p;
     if (moved) {

@@ -154,6 +154,17 @@ struct BeamArgs {
 size_t beam_workspace_bytes(const BeamArgs& a);
 hipError_t launch_beam_select(const BeamArgs& a, hipStream_t s);
 
+// Attention over the `count` pages that each token and key/value head lists.
+size_t attn_pages_workspace_bytes(const KvArgs& a, int q_heads, int count);
+hipError_t launch_kv_attention_pages(const KvArgs& a, const RotaryArgs& r, const AttnArgs& t,
+                                     const int32_t* chosen, int count, hipStream_t s);
+// Mean keys of the pages that hold the batch's new tokens, and the choice of pages.
+constexpr int kMaxSelectPages = I8MM_MAX_SELECT_PAGES;
+hipError_t launch_kv_page_means(const KvArgs& a, uint16_t* means, hipStream_t s);
+hipError_t launch_kv_select_pages(const KvArgs& a, const RotaryArgs& r, const uint16_t* q, int64_t q_ts,
+                                  int64_t q_hs, int q_heads, const uint16_t* means, int count, int first,
+                                  int recent, int32_t* out, hipStream_t s);
+
 // ---- pages of the key/value cache (arguments as in the C ABI)
 struct PagesArgs {
   const int32_t* page_table;

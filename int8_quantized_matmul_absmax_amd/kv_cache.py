@@ -96,6 +96,23 @@ class Int8KVCache:
         return ops.int8_kv_cache_attention(q, self, batch, rotary, scale, causal, window,
                                            alibi_slopes, shared_workspace, out)
 
+    def update_means(self, batch):
+        """The mean keys of the pages that hold the batch's new tokens, after their
+        append."""
+        ops.int8_kv_cache_page_means(self, batch)
+
+    def select_pages(self, q, batch, count, rotary=None, first=1, recent=1):
+        """The pages that each new token and key/value head attends to, by its
+        queries' products with the pages' mean keys: int32 [total_tokens, kv_heads,
+        count]."""
+        return ops.int8_kv_cache_select_pages(q, self, batch, count, rotary, first, recent)
+
+    def attention_pages(self, q, pages, batch, rotary=None, scale=None, out=None):
+        """Attention of the batch's queries over the tokens of the pages listed for
+        each. Its workspace as for attention."""
+        return ops.int8_kv_cache_attention_pages(q, pages, self, batch, rotary, scale,
+                                                 shared_workspace, out)
+
     def read(self, batch):
         """Keys and values of the batch's tokens in fp16."""
         return ops.int8_kv_cache_read(self, batch)

@@ -446,6 +446,69 @@ def int8_kv_cache_read(cache, batch):
     return k, v
 
 
+def _means_of(cache):
+    if cache.k_means is None:
+        raise ValueError("the cache holds no mean keys (page_means=True)")
+    return cache.k_means.data_ptr()
+
+
+def int8_kv_cache_page_means(cache, batch):
+    """Mean keys (cache.k_means) of the pages that hold the batch's new tokens, after
+    their append."""
+    lib = _lib.load_library()
+    _kv_args(cache, batch, None)
+    _run(cache.device, lib.int8_kv_cache_page_means, cache.ref, batch.ref, _means_of(cache))
+
+
+def int8_kv_cache_select_pages(q, cache, batch, count, rotary=None, first=1, recent=1, out=None):
+    """The pages that each new token and key/value head attends to: int32
+    [total_tokens, kv_heads, count] numbers of pages in the sequence, ascending, then
+    -1. Always the first `first` and the newest `recent`, the others by the product
+    of the head's queries (q fp16 [total_tokens, q_heads, D], rotated here when
+    `rotary` is given) with the page's mean key."""
+    lib = _lib.load_library()
+    rot = _kv_args(cache, batch, rotary)
+    means = _means_of(cache)
+    qp, qts, qhs = _need_heads(q, "q", batch.total_tokens, None, cache.head_dim, cache.device)
+    shape = (batch.total_tokens, cache.kv_heads, max(int(count), 0))
+    if out is None:
+        out = torch.empty(shape, dtype=torch.int32, device=cache.device)
+    else:
+        _need(out, "out", torch.int32, shape=shape)
+        _on_gpu(q=q, out=out)
+    _run(cache.device, lib.int8_kv_cache_select_pages, qp, qts, qhs, q.shape[1], cache.ref, means,
+         batch.ref, rot, count, first, recent, out.data_ptr())
+    return out
+
+
+def int8_kv_cache_attention_pages(q, pages, cache, batch, rotary=None, scale=None, workspace=None,
+                                  out=None):
+    """Causal attention of the queries q fp16 [total_tokens, q_heads, D] over the
+    tokens of the listed pages: pages int32 [total_tokens, kv_heads, count], as
+    int8_kv_cache_select_pages gives them. scale and workspace as for
+    int8_kv_cache_attention."""
+    lib = _lib.load_library()
+    rot = _kv_args(cache, batch, rotary)
+    dev, D = cache.device, cache.head_dim
+    qp, qts, qhs = _need_heads(q, "q", batch.total_tokens, None, D, dev)
+    heads = q.shape[1]
+    _need(pages, "pages", torch.int32, 3)
+    count = pages.shape[2]
+    if pages.shape[:2] != (batch.total_tokens, cache.kv_heads):
+        raise ValueError("pages must be [%d, %d, count], got %s"
+                         % (batch.total_tokens, cache.kv_heads, tuple(pages.shape)))
+    if out is None:
+        out = q.new_empty(q.shape)
+    else:
+        _need(out, "out", torch.float16, shape=q.shape)
+    _on_gpu(q=q, pages=pages, out=out)
+    wp, wn = _scratch(lib.int8_kv_cache_attention_pages_workspace_bytes(cache.ref, batch.ref, heads,
+                                                                        count), workspace, dev)
+    _run(dev, lib.int8_kv_cache_attention_pages, qp, qts, qhs, heads, cache.ref, batch.ref, rot,
+         pages.data_ptr(), count, 1.0 / math.sqrt(D) if scale is None else scale, out.data_ptr(), wp, wn)
+    return out
+
+
 def kv_pages_step(page_table, seq_lens, parents, num_pages, page_tokens, new_tokens=1, keep=None,
                   workspace=None):
     """The page table of the next step: row i keeps the first keep[i] tokens (None:

@@ -101,6 +101,14 @@ def values(cache, which, table_row, t):
     return get_rows(cache, which, page, slot)[:, row].astype(F) * step[:, None]
 
 
+def values64(cache, which, table_row, t):
+    """Codes times the binary32 step, exact in binary64, of token t."""
+    page, slot, row = place(cache, table_row, t)
+    step = (cache[which + "_absmax"][page, :, slot] / F(127)).astype(np.float64)
+    with np.errstate(invalid="ignore"):
+        return get_rows(cache, which, page, slot)[:, row].astype(np.float64) * step[:, None]
+
+
 def read(cache, batch):
     """Keys and values of the batch's tokens, fp16 [tokens, heads, D]."""
     table, lens, counts = batch
