@@ -20,12 +20,15 @@ def ensure_built():
 
 def __getattr__(name):
     # ops and the module are imported on first use (they import torch)
-    if name in ("ops", "linear", "synth", "kv_cache", "attention"):
+    if name in ("ops", "linear", "synth", "kv_cache", "attention", "beam"):
         import importlib
         return importlib.import_module("." + name, __name__)
-    if name in ("Int8KVCache", "KVBatch", "KVPages", "PageCopies", "Rotary"):
+    if name in ("Int8KVCache", "KVBatch", "KVPages", "PageChoice", "PageCopies", "Rotary"):
         from . import kv_cache
         return getattr(kv_cache, name)
+    if name == "BeamSearch":
+        from .beam import BeamSearch
+        return BeamSearch
     if name == "Int8CachedAttention":
         from .attention import Int8CachedAttention
         return Int8CachedAttention

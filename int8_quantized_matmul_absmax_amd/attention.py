@@ -5,7 +5,8 @@ A step takes the batch's new tokens through the fused query/key/value
 projection (an Int8Linear), stores their keys and values in the layer's
 Int8KVCache, attends over what the cache then holds, and takes the result
 through the output projection. Prompt chunks, single tokens and mixtures of
-both are one call: the KVBatch says which rows belong to which sequence.
+both are one call: the KVBatch says which rows belong to which sequence. Over long
+sequences a step may attend to some pages of the cache only (a PageChoice).
 
     attn = Int8CachedAttention(4096, 32, kv_heads=8)
     attn.quantize_(w_qkv, w_out)
@@ -47,8 +48,13 @@ class Int8CachedAttention(torch.nn.Module):
         self.out.quantize_(w_out, b_out)
         return self
 
-    def forward(self, x, cache, batch, rotary=None, scale=None, window=0, alibi_slopes=None):
-        """x fp16 [total_tokens, hidden], the batch's new tokens -> the same shape."""
+    def forward(self, x, cache, batch, rotary=None, scale=None, window=0, alibi_slopes=None,
+                choice=None):
+        """x fp16 [total_tokens, hidden], the batch's new tokens -> the same shape.
+        choice (a PageChoice): each token attends to that many pages of its sequence,
+        by a cache that holds mean keys, and not to all; without window and slopes."""
+        if choice is not None and (window or alibi_slopes is not None):
+            raise ValueError("a choice of pages has neither a window nor position biases")
         if (cache.kv_heads, cache.head_dim) != (self.kv_heads, self.head_dim):
             raise ValueError("cache of %d heads of %d, layer of %d of %d"
                              % (cache.kv_heads, cache.head_dim, self.kv_heads, self.head_dim))
@@ -59,6 +65,10 @@ class Int8CachedAttention(torch.nn.Module):
         y = self.qkv(x).view(batch.total_tokens, self.heads + 2 * self.kv_heads, self.head_dim)
         q, k, v = y.split((self.heads, self.kv_heads, self.kv_heads), dim=1)
         cache.append(k, v, batch, rotary)
-        a = cache.attention(q, batch, rotary, scale=scale, window=window,
-                            alibi_slopes=alibi_slopes)
+        if choice is None:
+            a = cache.attention(q, batch, rotary, scale=scale, window=window,
+                                alibi_slopes=alibi_slopes)
+        else:
+            pages = cache.select_pages(q, batch, choice.count, rotary, choice.first, choice.recent)
+            a = cache.attention_pages(q, pages, batch, rotary, scale=scale)
         return self.out(a.view(batch.total_tokens, self.heads * self.head_dim))

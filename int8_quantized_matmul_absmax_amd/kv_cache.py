@@ -10,6 +10,7 @@ is made, so that the calls of a step's layers check only what is new to them.
     y = cache.attention(q, batch, rotary)
 """
 
+import collections
 import ctypes
 
 import torch
@@ -85,8 +86,11 @@ class Int8KVCache:
             page_tokens=self.page_tokens, kv_heads=heads, head_dim=self.head_dim)
 
     def append(self, k, v, batch, rotary=None):
-        """Store the batch's new keys (rotated) and values."""
+        """Store the batch's new keys (rotated) and values; a cache that holds mean
+        keys brings them up to date."""
         ops.int8_kv_cache_append(k, v, self, batch, rotary)
+        if self.k_means is not None:
+            ops.int8_kv_cache_page_means(self, batch)
 
     def attention(self, q, batch, rotary=None, scale=None, causal=True, window=0,
                   alibi_slopes=None, out=None):
@@ -97,8 +101,8 @@ class Int8KVCache:
                                            alibi_slopes, shared_workspace, out)
 
     def update_means(self, batch):
-        """The mean keys of the pages that hold the batch's new tokens, after their
-        append."""
+        """The mean keys of the pages that hold the batch's tokens (append does this
+        for its own; for keys that came into the cache another way)."""
         ops.int8_kv_cache_page_means(self, batch)
 
     def select_pages(self, q, batch, count, rotary=None, first=1, recent=1):
@@ -121,6 +125,11 @@ class Int8KVCache:
         """The copies that a KVPages call asked for. The table it gave is right for
         this cache after them."""
         ops.int8_kv_cache_copy_pages(self, copies.pages, copies.counts)
+
+
+class PageChoice(collections.namedtuple("PageChoice", "count first recent", defaults=(1, 1))):
+    """How many pages a query attends to, and how many of them are always the first
+    and the newest."""
 
 
 class PageCopies:

@@ -584,6 +584,8 @@ def int8_kv_cache_copy_pages(cache, copies, count):
 
 # ---- a beam search over such caches
 
+MAX_BEAM_COUNT = 64    # I8MM_MAX_BEAM_COUNT
+
 def beam_select(logits, scores, live=None, eos=None, count=None, workspace=None):
     """The next beams of a batch of beam searches: of each search the `count`
     (default: beams) best of all its beams' words, by scores + log_softmax(logits),
