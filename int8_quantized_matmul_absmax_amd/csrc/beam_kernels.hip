@@ -21,7 +21,10 @@ namespace {
 
 constexpr int kWaves = kBlockThreads / kWave;
 constexpr int kVectors = 4;   // 16-byte loads a lane takes at once
+// log2(e) to 24 bits, and what it is off by relative to itself.
 constexpr float kLog2E = 1.44269504088896340736f;
+constexpr double kLn2 = 0.693147180559945309417;
+constexpr double kOff = (double)kLog2E * kLn2 - 1.0;
 
 // 16 bytes of a row, which begins at any element.
 struct __attribute__((packed, aligned(2))) Loose16 {
@@ -47,6 +50,10 @@ struct Best {
   __device__ __forceinline__ bool takes(float x, uint32_t at) const {
     return x > last_v || (x == last_v && at < last_i);
   }
+  // (of words from i0 on, which may be before the piece's first: -infinity is none)
+  __device__ __forceinline__ bool may_take(float x, int i0) const {
+    return x > last_v || (x == last_v && i0 < (int)last_i && x > -INFINITY);
+  }
   // (uniform x and at that the list takes)
   __device__ __forceinline__ void insert(float x, uint32_t at, int lane, int count) {
     const int place = __popcll(__ballot(v > x || (v == x && i < at)));
@@ -59,23 +66,8 @@ struct Best {
   }
 };
 
-// A value that at least `count` lanes' x reach (-infinity where fewer are more
-// than that), within 2^-7 of the largest such: the order of floats as integers,
-// its upper 16 bits searched bit by bit.
-__device__ __forceinline__ float reached_by(float x, int count) {
-  const uint32_t b = __builtin_bit_cast(uint32_t, x);
-  const uint32_t key = (b ^ ((uint32_t)((int)b >> 31) | 0x80000000u)) >> 16;
-  uint32_t t = 0;
-#pragma unroll
-  for (uint32_t bit = 0x8000u; bit; bit >>= 1)
-    if (__popcll(__ballot(key >= (t | bit))) >= count) t |= bit;
-  if (t <= 0x007fu) return -INFINITY;
-  t <<= 16;
-  return __builtin_bit_cast(float, t & 0x80000000u ? t ^ 0x80000000u : ~t);
-}
-
-// What a piece leaves: its maximum and sum, then `count` values and as many
-// indices, best first.
+// What a piece leaves: its base and its sum (the logits' exponentials add up to sum
+// times 2^base for fp16, e^base for fp32), then `count` values and as many indices, best first.
 struct Pieces {
   float2* sum;      // [rows][pieces]
   float* value;     // [rows][pieces][count]
@@ -89,132 +81,288 @@ __host__ __device__ __forceinline__ Pieces pieces_of(void* ws, int64_t rows, int
   return p;
 }
 
-// One block a piece. A wave takes 4 KB at a time; its first 4 KB set a floor for
-// its list, what `count` of its lanes' maxima reach, so that the list starts with
-// about `count` insertions.
+// The order of floats as integers, zeros of both signs equal.
+__device__ __forceinline__ uint32_t order_of(float x) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, x + 0.0f);
+  return b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float of_order(uint32_t k) {
+  return __builtin_bit_cast(float, k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
+// 2^d, or e^d of a base in the logits' own units.
+__device__ __forceinline__ float power_of(float d, bool natural) {
+  return __builtin_amdgcn_exp2f(natural ? d * kLog2E : d);
+}
+
+// A value that at least `count` of the block's x reach (-infinity where fewer are
+// more than that), within 2^-7 of the largest such: the order of floats, its upper 16
+// bits searched bit by bit. One barrier.
+__device__ __forceinline__ float reached_by(float x, int count, float* s_x) {
+  s_x[threadIdx.x] = x;
+  lds_only_barrier();
+  uint32_t key[kWaves];
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) key[w] = order_of(s_x[w * kWave + (threadIdx.x & 63)]) >> 16;
+  uint32_t t = 0;
+#pragma unroll
+  for (uint32_t bit = 0x8000u; bit; bit >>= 1) {
+    int n = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) n += __popcll(__ballot(key[w] >= (t | bit)));
+    if (n >= count) t |= bit;
+  }
+  return t <= 0x007fu ? -INFINITY : of_order(t << 16);
+}
+
+// A value that `count` of the block's words reach: the last place of any wave's list,
+// or a `count`-th of each: the least of the waves' values at place count / kWaves. What
+// a wave reads may be older than what others have written since: floors only rise.
+__device__ __forceinline__ float shared_floor(const volatile float* s_last,
+                                              const volatile float* s_share) {
+  float any = s_last[0], all = s_share[0];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) {
+    any = fmaxf(any, s_last[w]);
+    all = fminf(all, s_share[w]);
+  }
+  return fmaxf(any, all);
+}
+
+// A lane's 16 bytes of a row, and their greatest element.
 template <bool kHalf>
+struct Words {
+  static constexpr int kV = kHalf ? 8 : 4;
+  v4i32 raw;
+  __device__ __forceinline__ float at(int e) const {
+    if constexpr (kHalf)
+      return h2f(((uint32_t)raw[e >> 1] >> (16 * (e & 1))) & 0xffffu);
+    else
+      return __builtin_bit_cast(float, (uint32_t)raw[e]);
+  }
+  __device__ __forceinline__ float most() const {
+    if constexpr (kHalf) {
+      v2f16 m = __builtin_bit_cast(v2f16, (uint32_t)raw[0]);
+#pragma unroll
+      for (int e = 1; e < 4; ++e)
+        m = __builtin_elementwise_max(m, __builtin_bit_cast(v2f16, (uint32_t)raw[e]));
+      return fmaxf((float)m[0], (float)m[1]);
+    } else {
+      return fmaxf(fmaxf(at(0), at(1)), fmaxf(at(2), at(3)));
+    }
+  }
+  // 2^(x L - b) of element e, for fp32 2^((x - b) L)
+  __device__ __forceinline__ float power(int e, float b) const {
+    float y;
+    if constexpr (kHalf) {
+      if (e & 1)
+        asm("v_fma_mix_f32 %0, %1, %2, -%3 op_sel:[1,0,0] op_sel_hi:[1,0,0]"
+            : "=v"(y) : "v"(raw[e >> 1]), "s"(kLog2E), "v"(b));
+      else
+        asm("v_fma_mix_f32 %0, %1, %2, -%3 op_sel:[0,0,0] op_sel_hi:[1,0,0]"
+            : "=v"(y) : "v"(raw[e >> 1]), "s"(kLog2E), "v"(b));
+    } else {
+      y = (at(e) - b) * kLog2E;
+    }
+    return __builtin_amdgcn_exp2f(y);
+  }
+  // Words from i on. A row's last ones are taken by a lane that begins before them:
+  // `drop` of its words are another's, and -infinity here.
+  __device__ __forceinline__ void load(const int8_t* row, int i) {
+    raw = reinterpret_cast<const Loose16*>(row + (int64_t)i * (16 / kV))->x;
+  }
+  __device__ __forceinline__ void drop(int n) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (kHalf) {
+        const uint32_t w = (uint32_t)raw[e];
+        const uint32_t lo = 2 * e < n ? 0xfc00u : w & 0xffffu;
+        raw[e] = (int)((2 * e + 1 < n ? 0xfc000000u : w & 0xffff0000u) | lo);
+      } else {
+        raw[e] = e < n ? (int)0xff800000u : raw[e];
+      }
+    }
+  }
+  // Of a row of fewer than kV words, the first n.
+  __device__ __forceinline__ void load_few(const int8_t* row, int n) {
+#pragma unroll
+    for (int e = 0; e < kV; ++e) {
+      if constexpr (kHalf) {
+        const uint32_t h = e < n ? reinterpret_cast<const uint16_t*>(row)[e] : 0xfc00u;
+        raw[e >> 1] = (int)(e & 1 ? (uint32_t)raw[e >> 1] | h << 16 : h);
+      } else {
+        raw[e] = e < n ? reinterpret_cast<const int32_t*>(row)[e] : (int)0xff800000u;
+      }
+    }
+  }
+};
+
+// One block a piece. A wave takes 4 KB at a time, the next in flight meanwhile.
+//
+// Exponentials are 2^(x L - b) with L = log2(e) to 24 bits and any b near the maximum:
+// one fma that takes x in its 16 bits, whose rounding matters little where the result
+// is large, and b is known exactly. L is log2(e) (1 + kOff), so what is summed are
+// exponentials of x (1 + kOff), and their logarithm is off by kOff times the mean of
+// x under the softmax; the join takes kOff times the maximum off instead. Of fp32
+// logits, whose product with L may overflow, (x - b) L with b the maximum itself.
+//
+// What costs most beside them is the list: an insertion and the search for what to
+// insert, about 100 instructions where 64 words cost 7. So the block's first 16 KB
+// set a floor, what `count` of its lanes' maxima reach, and later its waves' lists set
+// one together: little is inserted that is not among the block's best.
+template <bool kHalf, bool kFew>
 __global__ __launch_bounds__(kBlockThreads) void k_beam_rows(BeamArgs a, int pieces, int piece) {
-  constexpr int kV = kHalf ? 8 : 4, kStep = kVectors * kWave * kV;
-  __shared__ float s_v[kWaves][kWave], s_m[kWaves], s_l[kWaves];
-  __shared__ uint32_t s_i[kWaves][kWave];
+  typedef Words<kHalf> W;
+  constexpr int kV = W::kV, kStep = kVectors * kWave * kV;
+  __shared__ float s_x[kBlockThreads], s_b[kWaves], s_l[kWaves];
+  __shared__ uint64_t s_key[kWaves * kWave];
+  __shared__ float s_last[kWaves], s_share[kWaves];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row = blockIdx.x / pieces, at_piece = blockIdx.x % pieces;
   if (a.live && a.live[row] == 0) return;   // the join reads nothing of it
   const int64_t begin = (int64_t)at_piece * piece;
   const int n = (int)min((int64_t)piece, a.vocab - begin);
-  const uint16_t* const p16 = static_cast<const uint16_t*>(a.logits) + row * a.row_stride + begin;
-  const float* const p32 = static_cast<const float*>(a.logits) + row * a.row_stride + begin;
+  const int8_t* const words =
+      static_cast<const int8_t*>(a.logits) + (row * a.row_stride + begin) * (kHalf ? 2 : 4);
+  if (threadIdx.x < kWaves) s_last[threadIdx.x] = s_share[threadIdx.x] = -INFINITY;
+  // (reached_by's barrier comes before their use)
 
   Best best;
-  float m = -INFINITY, l = 0.f;
-  for (int at = wave * kStep; at < n; at += kWaves * kStep) {
-    float x[kVectors][kV], top[kVectors];
-    int i0[kVectors];
+  float b = 0.f, l = 0.f;   // of the lane: l 2^b
+  bool any = false;
+  float floor = -INFINITY;
+  W x[kVectors], ahead[kVectors];
+  // (before the piece's first word for a short piece, never before the row's)
+  auto first = [&](int at, int u) __attribute__((always_inline)) {
+    return min(at + (u * kWave + lane) * kV, n - kV);
+  };
+  auto load = [&](W (&to)[kVectors], int at) __attribute__((always_inline)) {
+    if constexpr (kFew) return;
 #pragma unroll
-    for (int u = 0; u < kVectors; ++u) {
-      i0[u] = at + (u * kWave + lane) * kV;
-      if (i0[u] + kV <= n) {
-        v4i32 t;
-        if constexpr (kHalf) {
-          t = reinterpret_cast<const Loose16*>(p16 + i0[u])->x;
+    for (int u = 0; u < kVectors; ++u) to[u].load(words, first(at, u));
+  };
+  int at = wave * kStep;
+  load(x, at);
+  for (bool start = true; start || at < n; start = false, at += kWaves * kStep) {
+    load(ahead, at + kWaves * kStep);   // (past the end, the last words again)
+    if constexpr (kFew) {
 #pragma unroll
-          for (int e = 0; e < kV; ++e)
-            x[u][e] = h2f(((uint32_t)t[e >> 1] >> (16 * (e & 1))) & 0xffffu);
-        } else {
-          t = reinterpret_cast<const Loose16*>(p32 + i0[u])->x;
+      for (int u = 0; u < kVectors; ++u)
+        x[u].load_few(words, wave == 0 && lane == 0 && u == 0 ? n : 0);
+    } else if (at + kStep > n) {
 #pragma unroll
-          for (int e = 0; e < kV; ++e) x[u][e] = __builtin_bit_cast(float, (uint32_t)t[e]);
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < kV; ++e)
-          x[u][e] = i0[u] + e >= n ? -INFINITY : kHalf ? h2f(p16[i0[u] + e]) : p32[i0[u] + e];
-      }
+      for (int u = 0; u < kVectors; ++u) x[u].drop(at + (u * kWave + lane) * kV - first(at, u));
     }
+    float top[kVectors];
 #pragma unroll
-    for (int u = 0; u < kVectors; ++u) {
-      top[u] = x[u][0];
-#pragma unroll
-      for (int e = 1; e < kV; ++e) top[u] = fmaxf(top[u], x[u][e]);
-    }
+    for (int u = 0; u < kVectors; ++u) top[u] = x[u].most();
     const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+    if (start) floor = reached_by(most, a.count, s_x);
+    else floor = fmaxf(floor, shared_floor(s_last, s_share));
+
     // A NaN or +infinity makes the sum NaN, and the row one without candidates.
-    const float next = fmaxf(m, most), base = next == -INFINITY ? 0.f : next;
-    l *= __builtin_amdgcn_exp2f((m - base) * kLog2E);
+    const float next = kHalf ? most * kLog2E : most;
+    if (most > -INFINITY && (!any || next > b)) {
+      l *= any ? power_of(b - next, !kHalf) : 0.f;
+      b = next;
+      any = true;
+    }
     float sum[kVectors];
 #pragma unroll
     for (int u = 0; u < kVectors; ++u) {
       sum[u] = 0.f;
 #pragma unroll
-      for (int e = 0; e < kV; ++e) sum[u] += __builtin_amdgcn_exp2f((x[u][e] - base) * kLog2E);
+      for (int e = 0; e < kV; ++e)
+        sum[u] += x[u].power(e, b);
     }
     l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-    m = next;
 
-    const float floor = at == wave * kStep ? reached_by(most, a.count) : -INFINITY;
-    if (!__any(most >= floor && best.takes(most, (uint32_t)i0[0]))) continue;
+    const auto index = [&](int u) __attribute__((always_inline)) {
+      return kFew ? 0 : first(at, u);
+    };
+    if (__any(most >= floor && best.may_take(most, index(0)))) {
 #pragma unroll
-    for (int u = 0; u < kVectors; ++u) {
-      if (!__any(top[u] >= floor && best.takes(top[u], (uint32_t)i0[u]))) continue;
+      for (int u = 0; u < kVectors; ++u) {
+        // lanes' best words, then their next ones, while they are taken
+        const int i0 = index(u);
+        float most = top[u];
+        uint64_t those = __ballot(most >= floor && best.may_take(most, i0));
+        if (!those) continue;
+        float y[kV];
 #pragma unroll
-      for (int e = 0; e < kV; ++e) {
-        const uint32_t mine = (uint32_t)(i0[u] + e);
-        uint64_t those = __ballot(x[u][e] >= floor && best.takes(x[u][e], mine));
-        while (those) {
-          const int from = __builtin_ctzll(those);
-          those &= those - 1;
-          const float v = lane_float(x[u][e], from);
-          const uint32_t i = (uint32_t)__builtin_amdgcn_readlane((int)mine, from);
-          if (best.takes(v, i)) best.insert(v, i, lane, a.count);
+        for (int e = 0; e < kV; ++e) y[e] = x[u].at(e);
+        for (int round = 0; round < kV && those; ++round) {
+          int at_most = 0;
+#pragma unroll
+          for (int e = kV - 1; e > 0; --e) at_most = y[e] == most ? e : at_most;
+          at_most = y[0] == most ? 0 : at_most;
+          do {
+            const int from = __builtin_ctzll(those);
+            those &= those - 1;
+            const float v = lane_float(most, from);
+            const uint32_t i = (uint32_t)__builtin_amdgcn_readlane(i0 + at_most, from);
+            if (best.takes(v, i)) best.insert(v, i, lane, a.count);
+          } while (those);
+          most = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < kV; ++e) {
+            y[e] = e == at_most ? -INFINITY : y[e];
+            most = fmaxf(most, y[e]);
+          }
+          those = __ballot(most >= floor && best.may_take(most, i0));
         }
       }
+      if (lane == 0) {
+        s_last[wave] = best.last_v;
+        s_share[wave] = lane_float(best.v, (a.count + kWaves - 1) / kWaves - 1);
+      }
     }
+#pragma unroll
+    for (int u = 0; u < kVectors; ++u) x[u] = ahead[u];
   }
 
   // the wave's sum, then the block's
-  float top = m;
+  const float mine = any ? b : -INFINITY;
+  float top = mine;
 #pragma unroll
   for (int d = 1; d < kWave; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, kWave));
-  const float base = top == -INFINITY ? 0.f : top;
-  l *= __builtin_amdgcn_exp2f((m - base) * kLog2E);
+  l *= any ? power_of(mine - top, !kHalf) : 1.f;   // (nothing: 0, or a NaN)
 #pragma unroll
   for (int d = 1; d < kWave; d <<= 1) l += __shfl_xor(l, d, kWave);
-  s_v[wave][lane] = best.v;
-  s_i[wave][lane] = best.i;
   if (lane == 0) {
-    s_m[wave] = top;
+    s_b[wave] = top;
     s_l[wave] = l;
   }
+  // keys: the greater the better, 0 in empty places
+  if (lane < a.count)
+    s_key[wave * a.count + lane] =
+        best.v > -INFINITY ? (uint64_t)order_of(best.v) << 32 | ~best.i : 0;
   __syncthreads();
-  // An entry's place is the number of entries before it.
   const Pieces out = pieces_of(a.ws, (int64_t)a.batch * a.beams, pieces, a.count);
   const int64_t part = (int64_t)row * pieces + at_piece;
+  // An entry's place is the number of entries before it; lanes share an entry.
   const int entries = kWaves * a.count;
-  if ((int)threadIdx.x < entries) {
-    const int w = threadIdx.x / a.count, j = threadIdx.x % a.count;
-    const float v = s_v[w][j];
-    const uint32_t i = s_i[w][j];
-    int place = j;
-    for (int o = 0; o < kWaves; ++o) {
-      if (o == w) continue;
-      for (int k = 0; k < a.count; ++k) {
-        const float ov = s_v[o][k];
-        // (empty places are equal: those of earlier waves come first)
-        place += ov > v || (ov == v && (s_i[o][k] < i || (s_i[o][k] == i && o < w)));
-      }
-    }
-    if (place < a.count) {
-      out.value[part * a.count + place] = v;
-      out.index[part * a.count + place] = i + (uint32_t)begin;
-    }
+  int lanes = 1;
+  while (2 * lanes * entries <= kBlockThreads) lanes *= 2;
+  const int entry = threadIdx.x / lanes;
+  int place = 0;
+  const uint64_t key = entry < entries ? s_key[entry] : 0;
+  for (int o = threadIdx.x % lanes; o < entries; o += lanes) {
+    const uint64_t other = s_key[o];
+    place += other > key || (other == key && o < entry);   // (empty places are equal)
+  }
+  for (int d = 1; d < lanes; d <<= 1) place += __shfl_xor(place, d, kWave);
+  if (entry < entries && threadIdx.x % lanes == 0 && place < a.count) {
+    out.value[part * a.count + place] = key ? of_order((uint32_t)(key >> 32)) : -INFINITY;
+    out.index[part * a.count + place] = key ? ~(uint32_t)key + (uint32_t)begin : 0;
   }
   if (threadIdx.x == 0) {
-    float t = s_m[0], sum = 0.f;
+    float t = s_b[0], sum = 0.f;
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) t = fmaxf(t, s_m[w]);
-    const float b = t == -INFINITY ? 0.f : t;
+    for (int w = 1; w < kWaves; ++w) t = fmaxf(t, s_b[w]);
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) sum += s_l[w] * __builtin_amdgcn_exp2f((s_m[w] - b) * kLog2E);
+    for (int w = 0; w < kWaves; ++w)
+      sum += s_b[w] > -INFINITY ? s_l[w] * power_of(s_b[w] - t, !kHalf) : s_l[w];
     out.sum[part] = float2{t, sum};
   }
 }
@@ -245,104 +393,166 @@ __device__ __forceinline__ bool before(double v, int64_t at, double w, int64_t b
 }
 
 // One block a search.
+//
+// A beam's base, what its logits are added to: its score less the logarithm, of which
+// the integer part and the 24-bit logarithm of the rest are put together in 64 bits.
+// A candidate's place is the number of candidates before it, counted over all pairs of
+// up to kJoinEntries; more of them first become the lists of the block's waves.
+constexpr int kJoinFew = 64;
 constexpr int kJoinThreads = 1024, kJoinWaves = kJoinThreads / kWave;
+constexpr int kJoinEntries = kJoinWaves * I8MM_MAX_BEAM_COUNT;
 __global__ __launch_bounds__(kJoinThreads) void k_beam_join(BeamArgs a, int pieces) {
-  extern __shared__ double s_base[];   // [beams]: what a beam's logits are added to
-  __shared__ double s_v[kJoinWaves][kWave];
-  __shared__ int64_t s_at[kJoinWaves][kWave];
+  extern __shared__ double s_base[];   // [beams]
+  __shared__ double s_v[kJoinEntries];
+  __shared__ int64_t s_at[kJoinEntries];
+  __shared__ int s_count;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int b = blockIdx.x;
   const Pieces in = pieces_of(a.ws, (int64_t)a.batch * a.beams, pieces, a.count);
   for (int i = wave; i < a.beams; i += kJoinWaves) {
     const int64_t row = (int64_t)b * a.beams + i;
     const float s = a.scores[row];
-    const double score = fabsf(s) < INFINITY ? (double)s : no_value();
-    if (a.live && a.live[row] == 0) {
-      if (lane == 0) s_base[i] = score;
-      continue;
-    }
-    float top = -INFINITY;
-    bool nan = false;
-    for (int p = lane; p < pieces; p += kWave) {
-      const float2 s = in.sum[row * pieces + p];
-      top = fmaxf(top, s.x);
-      nan |= !(s.y >= 0.f);
-    }
+    const bool ended = a.live && a.live[row] == 0;
+    double base = fabsf(s) < INFINITY ? (double)s : no_value();
+    if (!ended) {
+      float top = -INFINITY, sum = 0.f;
+      for (int p = lane; p < pieces; p += kWave) {
+        const float2 x = in.sum[row * pieces + p];
+        const float next = fmaxf(top, x.x);
+        sum = sum * (top > -INFINITY ? power_of(top - next, a.fp32) : 1.f) +
+              x.y * (x.x > -INFINITY ? power_of(x.x - next, a.fp32) : 1.f);
+        top = next;
+      }
+      float all = top;
 #pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, kWave));
-    double sum = 0.0;
-    for (int p = lane; p < pieces; p += kWave) {
-      const float2 s = in.sum[row * pieces + p];
-      if (s.y > 0.f) sum += (double)s.y * exp((double)s.x - (double)top);
-    }
+      for (int d = 1; d < kWave; d <<= 1) all = fmaxf(all, __shfl_xor(all, d, kWave));
+      double total = (double)(sum * (top > -INFINITY ? power_of(top - all, a.fp32) : 1.f));
 #pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) sum += __shfl_xor(sum, d, kWave);
-    const bool empty = __any(nan) || !(top > -INFINITY);
-    if (lane == 0) s_base[i] = empty ? no_value() : score - (double)top - log(sum);
+      for (int d = 1; d < kWave; d <<= 1) total += __shfl_xor(total, d, kWave);
+      const int e = __builtin_amdgcn_frexp_exp(total);
+      const float rest = __builtin_amdgcn_logf((float)__builtin_amdgcn_frexp_mant(total));
+      base -= ((double)e + (double)rest) * kLn2;
+      base -= a.fp32 ? (double)all : (double)all * (kLn2 - kLn2 * kOff);
+      if (!(total > 0.0) || !(total < 1e300)) base = no_value();
+    }
+    if (lane == 0) s_base[i] = base;
   }
   __syncthreads();
 
   const double none = no_value();
-  double best = none, last = none;   // as in the rows' lists
-  int64_t best_at = 0, last_at = 0;
   // (no words: a beam that has ended still has its one candidate)
   const int per_beam = max(pieces * a.count, 1), all = a.beams * per_beam;
   const int64_t words = max(a.vocab, (int64_t)1);
-  for (int e0 = wave * kWave; e0 < all; e0 += kJoinThreads) {
-    double v = none;
-    int64_t at = 0;
-    const int e = e0 + lane, i = e / per_beam, k = e % per_beam;
-    if (e < all) {
-      const int64_t row = (int64_t)b * a.beams + i;
-      if (a.live && a.live[row] == 0) {
-        if (k == 0) {
-          v = s_base[i];
-          at = i * words + max(a.eos, 0);
-        }
-      } else if (s_base[i] > none) {
-        v = s_base[i] + (double)in.value[row * per_beam + k];
-        at = i * words + in.index[row * per_beam + k];
+  auto candidate = [&](int e, double* v, int64_t* at) __attribute__((always_inline)) {
+    *v = none;
+    *at = 0;
+    const int i = e / per_beam, k = e % per_beam;
+    if (e >= all || !(s_base[i] > none)) return;
+    const int64_t row = (int64_t)b * a.beams + i;
+    if (a.live && a.live[row] == 0) {
+      if (k > 0) return;
+      *v = s_base[i];
+      *at = i * words + max(a.eos, 0);
+    } else {
+      const double x = s_base[i] + (double)in.value[row * per_beam + k];
+      if (!(x > none)) return;   // (an empty place)
+      *v = x;
+      *at = i * words + in.index[row * per_beam + k];
+    }
+  };
+  // Of more than kJoinFew, only those are counted that reach the last place of the list
+  // with the best one: that list alone has `count` of them.
+  double least = none;
+  if (all > kJoinFew) {
+    const int lists = pieces > 0 ? a.beams * pieces : 0;
+    for (int e = threadIdx.x; e < lists; e += kJoinThreads) {
+      double v;
+      int64_t at;
+      candidate(e * a.count + a.count - 1, &v, &at);
+      least = v > least ? v : least;
+    }
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+      const double o = __shfl_xor(least, d, kWave);
+      least = o > least ? o : least;
+    }
+    if (lane == 0) s_v[wave] = least;
+    if (threadIdx.x == 0) s_count = 0;
+    __syncthreads();
+    least = s_v[0];
+#pragma unroll
+    for (int w = 1; w < kJoinWaves; ++w) least = s_v[w] > least ? s_v[w] : least;
+    __syncthreads();
+    for (int e0 = 0; e0 < all; e0 += kJoinThreads) {
+      double v;
+      int64_t at;
+      candidate(e0 + threadIdx.x, &v, &at);
+      const bool some = v > none && v >= least;
+      const uint64_t those = __ballot(some);
+      int to = 0;
+      if (lane == 0 && those) to = atomicAdd(&s_count, __popcll(those));
+      to = __builtin_amdgcn_readfirstlane(to) + __popcll(those & ((1ull << lane) - 1));
+      if (some && to < kJoinEntries) {
+        s_v[to] = v;
+        s_at[to] = at;
       }
     }
-    uint64_t those = __ballot(v > none && before(v, at, last, last_at));
-    while (those) {
-      const int from = __builtin_ctzll(those);
-      those &= those - 1;
-      const double w = lane_double(v, from);
-      const int64_t w_at = (int64_t)lane_word((uint64_t)at, from);
-      if (!before(w, w_at, last, last_at)) continue;
-      const int place = __popcll(__ballot(before(best, best_at, w, w_at)));
-      const double up =
-          __builtin_bit_cast(double, word_from_lane_below(__builtin_bit_cast(uint64_t, best)));
-      const int64_t up_at = (int64_t)word_from_lane_below((uint64_t)best_at);
-      best = lane < place ? best : lane == place ? w : up;
-      best_at = lane < place ? best_at : lane == place ? w_at : up_at;
-      last = lane_double(best, a.count - 1);
-      last_at = (int64_t)lane_word((uint64_t)best_at, a.count - 1);
+    __syncthreads();
+  }
+  int entries = all > kJoinFew ? s_count : all;
+  if (all <= kJoinFew) {
+    if ((int)threadIdx.x < all) candidate(threadIdx.x, &s_v[threadIdx.x], &s_at[threadIdx.x]);
+  } else if (entries > kJoinEntries) {
+    entries = kJoinWaves * a.count;
+    double best = none, last = none;   // as in the rows' lists
+    int64_t best_at = 0, last_at = 0;
+    for (int e0 = wave * kWave; e0 < all; e0 += kJoinThreads) {
+      double v;
+      int64_t at;
+      candidate(e0 + lane, &v, &at);
+      uint64_t those = __ballot(v > none && before(v, at, last, last_at));
+      while (those) {
+        const int from = __builtin_ctzll(those);
+        those &= those - 1;
+        const double w = lane_double(v, from);
+        const int64_t w_at = (int64_t)lane_word((uint64_t)at, from);
+        if (!before(w, w_at, last, last_at)) continue;
+        const int place = __popcll(__ballot(before(best, best_at, w, w_at)));
+        const double up =
+            __builtin_bit_cast(double, word_from_lane_below(__builtin_bit_cast(uint64_t, best)));
+        const int64_t up_at = (int64_t)word_from_lane_below((uint64_t)best_at);
+        best = lane < place ? best : lane == place ? w : up;
+        best_at = lane < place ? best_at : lane == place ? w_at : up_at;
+        last = lane_double(best, a.count - 1);
+        last_at = (int64_t)lane_word((uint64_t)best_at, a.count - 1);
+      }
+    }
+    if (lane < a.count) {
+      s_v[wave * a.count + lane] = best;
+      s_at[wave * a.count + lane] = best_at;
     }
   }
-  s_v[wave][lane] = best;
-  s_at[wave][lane] = best_at;
   __syncthreads();
-  for (int e = threadIdx.x; e < kJoinWaves * a.count; e += kJoinThreads) {
-    const int w = e / a.count, j = e % a.count;
-    const double v = s_v[w][j];
-    const int64_t at = s_at[w][j];
-    int place = j;
-    for (int o = 0; o < kJoinWaves; ++o) {
-      if (o == w) continue;
-      for (int k = 0; k < a.count; ++k) {
-        const double ov = s_v[o][k];
-        const int64_t o_at = s_at[o][k];
-        // (empty places are equal: those of earlier waves come first)
-        place += before(ov, o_at, v, at) || (ov == v && o_at == at && o < w);
-      }
-    }
-    if (place >= a.count) continue;
+  int lanes = 1;   // that share an entry
+  while (2 * lanes * entries <= kJoinThreads && lanes < 16) lanes *= 2;
+  const int entry = threadIdx.x / lanes;
+  const double v = entry < entries ? s_v[entry] : none;
+  const int64_t at = entry < entries ? s_at[entry] : 0;
+  int place = 0;
+#pragma unroll 4
+  for (int o = threadIdx.x % lanes; o < entries; o += lanes) {
+    const double ov = s_v[o];
+    const int64_t o_at = s_at[o];
+    // (empty places are equal)
+    place += ov > v || (ov == v && (o_at < at || (o_at == at && o < entry)));
+  }
+  for (int d = 1; d < lanes; d <<= 1) place += __shfl_xor(place, d, kWave);
+  if (threadIdx.x % lanes == 0 && place < a.count && (entry < entries)) {
     const bool found = v > none;
     const int64_t i = at / words;
     const int64_t to = (int64_t)b * a.count + place;
     const int64_t row = (int64_t)b * a.beams + i;
+    // (where none is found, at is 0 and the row the search's first)
     const bool ended = a.live && a.live[row] == 0;
     const int token = ended ? a.eos : (int)(at - i * words);
     a.out_scores[to] = (float)v;
@@ -350,13 +560,22 @@ __global__ __launch_bounds__(kJoinThreads) void k_beam_join(BeamArgs a, int piec
     a.out_parents[to] = found ? (int)row : -1;
     a.out_live[to] = found && token != a.eos;
   }
+  // places that no entry is left for
+  for (int j = entries + threadIdx.x; j < a.count; j += kJoinThreads) {
+    const int64_t to = (int64_t)b * a.count + j;
+    a.out_scores[to] = -INFINITY;
+    a.out_tokens[to] = a.out_parents[to] = -1;
+    a.out_live[to] = 0;
+  }
 }
 
-// Pieces: about four blocks a compute unit, and at least a step of each wave. At
+// Pieces: about four blocks a compute unit, and at least a step of each wave: 512 rows
+// of 131072 fp16 words 33 us, with eight blocks a compute unit 37 and sixteen 41. At
 // most kPieceMost words: a lane's 32-bit sum then takes eight parts of 32 terms
-// (16 of 16 for fp32), which keeps its error below 2^-18: 10 and 16 roundings of
-// sums, as many of rescaling, the exponential's 2^-23, and its argument's, 2^-24 of
-// itself, which terms that matter have below the logarithm of their number.
+// (16 of 16 for fp32), which keeps its error below 2^-18: in units of 2^-24, 10 and
+// 16 roundings of sums and joins, up to twice 16 of rescaling, the exponential's 2 and
+// its argument's, which for terms that matter is below the logarithm of their number
+// times log2(e), 24.
 constexpr int64_t kPieceMost = 65536;
 struct Plan {
   int pieces, piece;
@@ -385,10 +604,11 @@ hipError_t launch_beam_select(const BeamArgs& a, hipStream_t s) {
   const int64_t blocks = (int64_t)a.batch * a.beams * p.pieces;
   if (blocks > INT32_MAX / kBlockThreads) return hipErrorInvalidValue;
   if (blocks > 0) {
-    if (a.fp32)
-      k_beam_rows<false><<<(uint32_t)blocks, kBlockThreads, 0, s>>>(a, p.pieces, p.piece);
-    else
-      k_beam_rows<true><<<(uint32_t)blocks, kBlockThreads, 0, s>>>(a, p.pieces, p.piece);
+    // (fewer words than 16 bytes hold: a kernel that does not load so many)
+    const bool few = a.vocab < (a.fp32 ? 4 : 8);
+    auto* const rows = a.fp32 ? few ? k_beam_rows<false, true> : k_beam_rows<false, false>
+                              : few ? k_beam_rows<true, true> : k_beam_rows<true, false>;
+    rows<<<(uint32_t)blocks, kBlockThreads, 0, s>>>(a, p.pieces, p.piece);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
