@@ -37,5 +37,6 @@ def __getattr__(name):
         return Int8Linear
     from . import ops as _ops
     if hasattr(_ops, name):
-        return getattr(_ops, name)
+        globals()[name] = getattr(_ops, name)   # (found at once from then on)
+        return globals()[name]
     raise AttributeError(name)

@@ -49,7 +49,10 @@ def shared_workspace(device, nbytes):
     device = torch.device(device)
     if torch.cuda.is_current_stream_capturing():
         return torch.empty((max(int(nbytes), 1),), dtype=torch.uint8, device=device)
-    key = (device.index, torch.cuda.current_stream(device).cuda_stream)
+    if device.type == "cuda" and device.index is not None:
+        key = (device.index, ops._raw_stream(device))
+    else:
+        key = (device.index, torch.cuda.current_stream(device).cuda_stream)
     with _WS_LOCK:
         ws = _WORKSPACES.get(key)
         if ws is None or ws.numel() < nbytes:

@@ -541,7 +541,7 @@ def kv_pages_step(page_table, seq_lens, parents, num_pages, page_tokens, new_tok
     dev = _on_gpu(page_table=page_table, seq_lens=seq_lens, parents=parents, keep=keep,
                   new_tokens=each)
     out = torch.empty((rows * (width + 4) + 2,), dtype=torch.int32, device=dev)
-    table, lens, copies, counts = out.split((rows * width, rows, 3 * rows, 2))
+    table, lens, copies, counts = out.split_with_sizes((rows * width, rows, 3 * rows, 2))
     wp, wn = _scratch(lib.i8mm_kv_pages_workspace_bytes(rows, num_pages), workspace, dev)
     _run(dev, lib.i8mm_kv_pages_step, page_table.data_ptr(), seq_lens.data_ptr(), seqs, width,
          parents.data_ptr(), None if keep is None else keep.data_ptr(),
@@ -560,7 +560,7 @@ def kv_pages_compact(page_table, seq_lens, num_pages, page_tokens, workspace=Non
     dev = _on_gpu(page_table=page_table, seq_lens=seq_lens)
     most = max(int(num_pages) // 2, 0)
     out = torch.empty((seqs * width + 3 * most + 2,), dtype=torch.int32, device=dev)
-    table, copies, counts = out.split((seqs * width, 3 * most, 2))
+    table, copies, counts = out.split_with_sizes((seqs * width, 3 * most, 2))
     wp, wn = _scratch(lib.i8mm_kv_pages_workspace_bytes(0, num_pages), workspace, dev)
     _run(dev, lib.i8mm_kv_pages_compact, page_table.data_ptr(), seq_lens.data_ptr(), seqs, width,
          num_pages, page_tokens, table.data_ptr(), copies.data_ptr(), counts.data_ptr(), wp, wn)
