@@ -27,8 +27,9 @@ constexpr uint32_t kRead = 0xffffffffu;
 // out with a block after it. A step of 4 rows of 17 entries 4.4 us against 7.7, 64 of
 // 128 7.1 and 10.9, 256 of 64 10.3 and 13.0, 256 of 131 14.5 and 11.7, 512 of 128 24.9
 // and 18.2; a compaction 5.6 and 9.6, 7.0 and 11.4, 11.9 and 16.8, 16.9 and 11.6, 32 and
-// 25 (recorded; an eager launch saved is 2 to 3 us of the host's besides).
-constexpr int kOneRows = 1024, kOnePages = 16384, kOneEntries = 24576;
+// 25. That is recorded; an eager launch saved is 2 to 3 us of the host's, and 256 rows
+// of 131 with their copies in two layers 27.7 us against 30.9.
+constexpr int kOneRows = 1024, kOnePages = 16384, kOneEntries = 40960;
 
 // What row i of a step takes of its parent.
 struct Row {

@@ -14,69 +14,103 @@ namespace i8mm {
 
 namespace {
 
-// Mean keys: one wave a page and head. Lane (t, c) of 16 x 4 takes token t of each
-// block and the 16 features of tiles c, c + 4, ...; sums are 64-bit, a code's product
-// with its block's 32-bit step exact in them.
+// A double of another lane by a DPP move.
+template <int kControl>
+__device__ __forceinline__ double dpp_double(double x) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo =
+      (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, kControl, 0xf, 0xf, false);
+  const uint32_t hi =
+      (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), kControl, 0xf, 0xf, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// The sum over 8, 16 or 32 neighbouring lanes, in each of them: within quads
+// (quad_perm), then with the mirror image in eight lanes and in sixteen.
+template <int kLanes>
+__device__ __forceinline__ double sum_of_lanes(double x) {
+  x += dpp_double<0xb1>(x);
+  x += dpp_double<0x4e>(x);
+  x += dpp_double<0x141>(x);
+  if constexpr (kLanes >= 16) x += dpp_double<0x140>(x);
+  if constexpr (kLanes >= 32) x += __shfl_xor(x, 16, kWave);
+  return x;
+}
+
+// Mean keys: one wave a page, head and 64 features (four tiles). Lane (t, c) of 16 x 4
+// takes token t of each block and the 16 features of its tile; sums are 64-bit, a code's
+// product with its block's 32-bit step exact in them. Eight blocks are loaded at once:
+// with few pages to do, what counts is how often a wave waits.
 template <int D>
 __global__ __launch_bounds__(kBlockThreads) void k_kv_page_means(KvArgs a, uint16_t* means, int tasks) {
+  constexpr int kParts = (D + 63) / 64, kBlocks = 8;
   const int lane = threadIdx.x & 63;
   const int task = blockIdx.x * (kBlockThreads / kWave) +
                    __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (task >= tasks) return;
-  const int b = blockIdx.y, h = task % a.kv_heads;
+  const int b = blockIdx.y, part = task % kParts, h = task / kParts % a.kv_heads;
   const KvSeq sq = kv_seq(a, b);
   if (sq.n <= 0) return;
   const int page_tokens = a.slots * kKvBlock;
-  const int j = max(sq.first, 0) / page_tokens + task / a.kv_heads;
+  const int j = max(sq.first, 0) / page_tokens + task / kParts / a.kv_heads;
   const int held = min(sq.len - j * page_tokens, page_tokens);
   if (held <= 0) return;
   const int page = a.page_table[(int64_t)b * a.max_pages + j];
   if ((uint32_t)page >= (uint32_t)a.num_pages) return;
   const int64_t head = (int64_t)page * a.kv_heads + h;
   const int blocks = (held + kKvBlock - 1) / kKvBlock;
-  const int t = lane & 15;
-  const int8_t* const codes = a.k_codes + head * a.slots * (kKvBlock * D);
+  const int t = lane & 15, c = 4 * part + (lane >> 4);
+  const bool here = c < D / 16;
+  const int8_t* const codes =
+      a.k_codes + head * a.slots * (kKvBlock * D) + min(c, D / 16 - 1) * kTile + t * 16;
   const float* const absmax = a.k_absmax + head * a.slots;
-  for (int c = lane >> 4; c < (D / 16 + 3) / 4 * 4; c += 4) {
-    const bool here = c < D / 16;
-    double sum[16];
+  double sum[16];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) sum[e] = 0.0;
-    for (int s = 0; s < blocks; ++s) {
-      const double step = (double)(absmax[s] / 127.0f);
-      v4i32 w = {0, 0, 0, 0};
-      if (here) w = ld16v(codes + (int64_t)s * (kKvBlock * D) + c * kTile + t * 16);
-      if (s * kKvBlock + t >= held) continue;
+  for (int e = 0; e < 16; ++e) sum[e] = 0.0;
+  for (int s0 = 0; s0 < blocks; s0 += kBlocks) {
+    v4i32 w[kBlocks];
+    float a_block[kBlocks];
+#pragma unroll
+    for (int u = 0; u < kBlocks; ++u) {
+      const int s = min(s0 + u, blocks - 1);
+      a_block[u] = absmax[s];
+      w[u] = ld16v(codes + (int64_t)s * (kKvBlock * D));
+    }
+#pragma unroll
+    for (int u = 0; u < kBlocks; ++u) {
+      if (s0 + u >= blocks) continue;
+      // (a token past the end may hold anything in a block that counts)
+      const double step = (s0 + u) * kKvBlock + t < held ? (double)(a_block[u] / 127.0f) : 0.0;
 #pragma unroll
       for (int e = 0; e < 16; ++e)
-        sum[e] += step * (double)(int8_t)((uint32_t)w[e >> 2] >> (8 * (e & 3)));
+        sum[e] += step * (double)(int8_t)((uint32_t)w[u][e >> 2] >> (8 * (e & 3)));
     }
+  }
+  uint32_t o[8];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
+  for (int e = 0; e < 16; ++e) sum[e] = sum_of_lanes<16>(sum[e]);
 #pragma unroll
-      for (int d = 1; d < 16; d <<= 1) sum[e] += __shfl_xor(sum[e], d, kWave);
-    }
-    if (here && t == 0) {
-      uint32_t o[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        o[e] = f2h2((float)(sum[2 * e] / held), (float)(sum[2 * e + 1] / held));
-      uint16_t* const dst = means + head * D + 16 * c;
-      *reinterpret_cast<v4i32*>(dst) = v4i32{(int)o[0], (int)o[1], (int)o[2], (int)o[3]};
-      *reinterpret_cast<v4i32*>(dst + 8) = v4i32{(int)o[4], (int)o[5], (int)o[6], (int)o[7]};
-    }
+  for (int e = 0; e < 8; ++e) o[e] = f2h2((float)(sum[2 * e] / held), (float)(sum[2 * e + 1] / held));
+  if (here && t == 0) {
+    uint16_t* const dst = means + head * D + 16 * c;
+    *reinterpret_cast<v4i32*>(dst) = v4i32{(int)o[0], (int)o[1], (int)o[2], (int)o[3]};
+    *reinterpret_cast<v4i32*>(dst + 8) = v4i32{(int)o[4], (int)o[5], (int)o[6], (int)o[7]};
   }
 }
 
-// The order of doubles as integers, NaN as -infinity: 0x000f... for that.
+// The order of doubles as integers, NaN as -infinity, which is kNoScore.
+constexpr uint64_t kNoScore = 0x000fffffffffffffull;
 __device__ __forceinline__ uint64_t score_key(double x) {
   const uint64_t b = __builtin_bit_cast(uint64_t, x);
-  if ((b << 1) > (0x7ffull << 53)) return 0x000fffffffffffffull;
+  if ((b << 1) > (0x7ffull << 53)) return kNoScore;
   return b ^ ((uint64_t)((int64_t)b >> 63) | (1ull << 63));
 }
 
 // One block a token and head. Keys of all candidate pages stand in LDS; the least of
 // the chosen is found digit by digit, from histograms of 256.
+//
+// A page's mean is taken by kLanes lanes, eight features each. What a block waits for
+// is kept to a few times: a group of lanes loads as many entries of the page table at
+// once, then the means of kAhead pages.
 template <int D, int kThreads>
 __global__ __launch_bounds__(kThreads) void k_kv_select_pages(KvArgs a, RotaryArgs rot,
                                                               const uint16_t* q, int64_t q_ts,
@@ -85,9 +119,10 @@ __global__ __launch_bounds__(kThreads) void k_kv_select_pages(KvArgs a, RotaryAr
                                                               int first, int recent, int32_t* out) {
   constexpr int kWaves = kThreads / kWave;
   constexpr int kLanes = D == 64 ? 8 : D <= 128 ? 16 : 32;   // of a page
+  constexpr int kGroups = kThreads / kLanes, kAhead = 8;
   extern __shared__ uint64_t s_key[];
   __shared__ double s_sum[D], s_q[D];
-  __shared__ int s_hist[256], s_wave[kWaves], s_pick[2];
+  __shared__ int s_hist[3][256], s_wave[kWaves];
   const int tid = threadIdx.x, lane = tid & 63;
   const int token = blockIdx.x / a.kv_heads, h = blockIdx.x % a.kv_heads;
   const int b = sequence_of(a, token, lane);
@@ -100,15 +135,26 @@ __global__ __launch_bounds__(kThreads) void k_kv_select_pages(KvArgs a, RotaryAr
     for (int j = tid; j < count; j += kThreads) line[j] = j < seen ? j : -1;
     return;
   }
+  const int candidates = seen - first - recent, want = count - first - recent;
+  for (int j = tid; j < first; j += kThreads) line[j] = j;
+  for (int j = tid; j < recent; j += kThreads) line[count - recent + j] = seen - recent + j;
 
   // the sum of the head's queries, rotated
   for (int d = tid; d < D; d += kThreads) {
+    const uint16_t* const row = q + (int64_t)token * q_ts + (int64_t)h * group * q_hs + d;
     double x = 0.0;
-    const uint16_t* row = q + (int64_t)token * q_ts + (int64_t)h * group * q_hs + d;
-    for (int g = 0; g < group; ++g) x += (double)h2f(row[g * q_hs]);
+    for (int g0 = 0; g0 < group; g0 += 8) {
+      uint32_t v[8];
+#pragma unroll
+      for (int g = 0; g < 8; ++g) v[g] = row[min(g0 + g, group - 1) * q_hs];
+#pragma unroll
+      for (int g = 0; g < 8; ++g)
+        if (g0 + g < group) x += (double)h2f(v[g]);
+    }
     s_sum[d] = x;
   }
-  __syncthreads();
+  for (int x = tid; x < 256; x += kThreads) s_hist[0][x] = 0;
+  lds_only_barrier();
   for (int d = tid; d < D; d += kThreads) {
     double x = s_sum[d];
     if (rot.cos && d < rot.dim) {
@@ -122,80 +168,94 @@ __global__ __launch_bounds__(kThreads) void k_kv_select_pages(KvArgs a, RotaryAr
     }
     s_q[d] = x;
   }
-  __syncthreads();
+  lds_only_barrier();
 
   // keys of the pages first .. seen - recent - 1
-  const int candidates = seen - first - recent, want = count - first - recent;
-  const int part = lane % kLanes;
+  const int part = tid % kLanes, mine = tid / kLanes;
+  const bool here = 8 * part < D;
   double qd[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) qd[e] = 8 * part + e < D ? s_q[8 * part + e] : 0.0;
-  for (int c0 = tid / kLanes; c0 < candidates; c0 += kThreads / kLanes) {
-    const int page = a.page_table[(int64_t)b * a.max_pages + first + c0];
-    double s = 0.0;
-    if ((uint32_t)page < (uint32_t)a.num_pages && 8 * part < D) {
-      const v4i32 w = ld16v(means + ((int64_t)page * a.kv_heads + h) * D + 8 * part);
+  for (int e = 0; e < 8; ++e) qd[e] = here ? s_q[8 * part + e] : 0.0;
+  const int32_t* const entries = a.page_table + (int64_t)b * a.max_pages + first;
+  for (int c0 = 0; c0 < candidates; c0 += kThreads) {
+    const int c_entry = c0 + part * kGroups + mine;
+    const int entry = c_entry < candidates ? entries[c_entry] : -1;
+#pragma unroll 1
+    for (int k0 = 0; k0 < kLanes && c0 + k0 * kGroups < candidates; k0 += kAhead) {
+      v4i32 w[kAhead];
+      int page[kAhead];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        s = __builtin_fma(qd[e], (double)h2f(((uint32_t)w[e >> 1] >> (16 * (e & 1))) & 0xffffu), s);
+      for (int u = 0; u < kAhead; ++u) {
+        page[u] = __shfl(entry, (lane - part) + k0 + u, kWave);
+        w[u] = v4i32{0, 0, 0, 0};
+        if (here && (uint32_t)page[u] < (uint32_t)a.num_pages)
+          w[u] = ld16v(means + ((int64_t)page[u] * a.kv_heads + h) * D + 8 * part);
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        double s = 0.0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          s = __builtin_fma(qd[e], (double)h2f(((uint32_t)w[u][e >> 1] >> (16 * (e & 1))) & 0xffffu), s);
+        s = sum_of_lanes<kLanes>(s);
+        const int c = c0 + (k0 + u) * kGroups + mine;
+        if (part == 0 && c < candidates)
+          s_key[c] = (uint32_t)page[u] < (uint32_t)a.num_pages ? score_key(s) : kNoScore;
+      }
     }
-#pragma unroll
-    for (int d = 1; d < kLanes; d <<= 1) s += __shfl_xor(s, d, kWave);
-    if (part == 0)
-      s_key[c0] = (uint32_t)page < (uint32_t)a.num_pages ? score_key(s) : score_key(__builtin_nan(""));
   }
-  __syncthreads();
+  lds_only_barrier();
 
-  // the key of place `want`, and how many of its equals are chosen
+  // the key of place `want`, and how many of its equals are chosen. (Every wave reads
+  // the histogram for itself; the next one is cleared two barriers before it is read.)
   uint64_t least = want > 0 ? 0 : ~0ull;
   int left = want;
-  for (int shift = 56; shift >= 0 && want > 0; shift -= 8) {
-    for (int x = tid; x < 256; x += kThreads) s_hist[x] = 0;
-    __syncthreads();
+  for (int digit = 0; digit < 8 && want > 0; ++digit) {
+    const int shift = 56 - 8 * digit;
+    int* const hist = s_hist[digit % 3];
+    for (int x = tid; x < 256; x += kThreads) s_hist[(digit + 1) % 3][x] = 0;
     for (int c = tid; c < candidates; c += kThreads) {
       const uint64_t k = s_key[c];
-      if (shift == 56 || (k >> (shift + 8)) == (least >> (shift + 8)))
-        atomicAdd(&s_hist[(int)(k >> shift) & 255], 1);
+      if (digit == 0 || (k >> (shift + 8)) == (least >> (shift + 8)))
+        atomicAdd(&hist[(int)(k >> shift) & 255], 1);
     }
-    __syncthreads();
-    if (tid < kWave) {
-      // digits from the highest down, four a lane
-      int n[4], sum = 0;
+    lds_only_barrier();
+    // digits from the highest down, four a lane
+    int n[4], sum = 0, pick = -1, rest = 0, many = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        n[e] = s_hist[255 - (4 * lane + e)];
-        sum += n[e];
-      }
-      int before = wave_inclusive_scan_dpp(sum) - sum;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (before < left && left <= before + n[e]) {
-          s_pick[0] = 255 - (4 * lane + e);
-          s_pick[1] = left - before;
-        }
-        before += n[e];
-      }
+    for (int e = 0; e < 4; ++e) {
+      n[e] = hist[255 - (4 * lane + e)];
+      sum += n[e];
     }
-    __syncthreads();
-    least |= (uint64_t)s_pick[0] << shift;
-    left = s_pick[1];
+    int before = wave_inclusive_scan_dpp(sum) - sum;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (before < left && left <= before + n[e]) {
+        pick = 255 - (4 * lane + e);
+        rest = left - before;
+        many = n[e];
+      }
+      before += n[e];
+    }
+    const int from = __builtin_ctzll(__ballot(pick >= 0));
+    least |= (uint64_t)__builtin_amdgcn_readlane(pick, from) << shift;
+    left = __builtin_amdgcn_readlane(rest, from);
+    if (left == __builtin_amdgcn_readlane(many, from)) break;   // all that begin with these digits
   }
 
-  // the chosen in ascending order: the first, the best, the newest
-  for (int j = tid; j < first; j += kThreads) line[j] = j;
-  for (int j = tid; j < recent; j += kThreads) line[count - recent + j] = seen - recent + j;
-  int placed = first, equals = 0;
+  // The chosen in ascending order between the first and the newest. A page's place:
+  // those above the least before it, and of those that are equal at most `left`. (After
+  // an early end none is equal but by chance, and then all are chosen.)
+  int placed = 0;   // above the least, and equals in the upper half
   for (int c0 = 0; c0 < candidates; c0 += kThreads) {
     const int c = c0 + tid;
     const uint64_t k = c < candidates ? s_key[c] : 0;
-    const bool equal = c < candidates && k == least;
+    const int above = c < candidates && k > least, equal = c < candidates && k == least;
     int total;
-    const int rank = equals + block_prefix<kWaves>(equal, s_wave, &total);
-    equals += total;
-    const bool take = c < candidates && (k > least || (equal && rank < left));
-    const int at = placed + block_prefix<kWaves>(take, s_wave, &total);
+    const int at = placed + block_prefix<kWaves>(above | equal << 16, s_wave, &total);
     placed += total;
-    if (take) line[at] = first + c;
+    const int equals = at >> 16;
+    if (above || (equal && equals < left)) line[first + (at & 0xffff) + min(equals, left)] = first + c;
   }
 }
 
@@ -205,7 +265,7 @@ hipError_t launch_kv_page_means(const KvArgs& a, uint16_t* means, hipStream_t s)
   const int64_t page_tokens = (int64_t)a.slots * kKvBlock;
   // pages that the new tokens of one sequence can touch
   const int64_t pages = std::min<int64_t>((a.max_tokens + 2 * page_tokens - 2) / page_tokens, a.max_pages);
-  const int64_t tasks = pages * a.kv_heads;
+  const int64_t tasks = pages * a.kv_heads * ((a.head_dim + 63) / 64);
   if (tasks > INT32_MAX - 4) return hipErrorInvalidValue;
   if (tasks == 0) return hipSuccess;
   const dim3 grid((uint32_t)((tasks + 3) / 4), (uint32_t)a.num_seqs);
