@@ -33,6 +33,10 @@ __device__ __forceinline__ KvSeq kv_seq(const KvArgs& a, int b) {
   return s;
 }
 
+__device__ __forceinline__ int page_or_none(const KvArgs& a, int page) {
+  return (uint32_t)page < (uint32_t)a.num_pages ? page : -1;
+}
+
 // A wave writes zeros to `bytes` (a multiple of 16).
 __device__ __forceinline__ void zero_bytes(void* p, int bytes, int lane) {
   for (int i = lane * 16; i < bytes; i += kWave * 16)

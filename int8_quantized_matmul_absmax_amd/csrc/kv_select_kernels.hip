@@ -24,16 +24,33 @@ __device__ __forceinline__ double dpp_double(double x) {
       (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), kControl, 0xf, 0xf, false);
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
-// The sum over 8, 16 or 32 neighbouring lanes, in each of them: within quads
-// (quad_perm), then with the mirror image in eight lanes and in sixteen.
-template <int kLanes>
+// The sum over 16 neighbouring lanes, in each of them: within quads (quad_perm), then
+// with the mirror image in eight lanes and in sixteen.
 __device__ __forceinline__ double sum_of_lanes(double x) {
   x += dpp_double<0xb1>(x);
   x += dpp_double<0x4e>(x);
   x += dpp_double<0x141>(x);
-  if constexpr (kLanes >= 16) x += dpp_double<0x140>(x);
-  if constexpr (kLanes >= 32) x += __shfl_xor(x, 16, kWave);
+  x += dpp_double<0x140>(x);
   return x;
+}
+// Of kN (8 or 16) values in each of kN lanes, lane i gets the sum of the i-th: halves
+// are exchanged with the mirror image, of which a lane keeps the half that its own
+// number is in. 15 additions for 16 sums, by sum_of_lanes they would be 64.
+template <int kControl, int kN>
+__device__ __forceinline__ void exchange_halves(double* x, bool upper) {
+#pragma unroll
+  for (int k = 0; k < kN / 2; ++k) {
+    const double keep = upper ? x[k + kN / 2] : x[k], give = upper ? x[k] : x[k + kN / 2];
+    x[k] = keep + dpp_double<kControl>(give);
+  }
+}
+template <int kN>
+__device__ __forceinline__ double spread_sums(double* x, int lane) {
+  if constexpr (kN == 16) exchange_halves<0x140, 16>(x, lane & 8);   // lane ^ 15
+  exchange_halves<0x141, 8>(x, lane & 4);                            // lane ^ 7
+  exchange_halves<0x1b, 4>(x, lane & 2);                             // lane ^ 3
+  exchange_halves<0xb1, 2>(x, lane & 1);                             // lane ^ 1
+  return x[0];
 }
 
 // Mean keys: one wave a page, head and 64 features (four tiles). Lane (t, c) of 16 x 4
@@ -87,7 +104,7 @@ __global__ __launch_bounds__(kBlockThreads) void k_kv_page_means(KvArgs a, uint1
   }
   uint32_t o[8];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) sum[e] = sum_of_lanes<16>(sum[e]);
+  for (int e = 0; e < 16; ++e) sum[e] = sum_of_lanes(sum[e]);
 #pragma unroll
   for (int e = 0; e < 8; ++e) o[e] = f2h2((float)(sum[2 * e] / held), (float)(sum[2 * e + 1] / held));
   if (here && t == 0) {
@@ -110,7 +127,7 @@ __device__ __forceinline__ uint64_t score_key(double x) {
 //
 // A page's mean is taken by kLanes lanes, eight features each. What a block waits for
 // is kept to a few times: a group of lanes loads as many entries of the page table at
-// once, then the means of kAhead pages.
+// once, then the means of kAhead pages; kBatch pages' sums are made together.
 template <int D, int kThreads>
 __global__ __launch_bounds__(kThreads) void k_kv_select_pages(KvArgs a, RotaryArgs rot,
                                                               const uint16_t* q, int64_t q_ts,
@@ -119,7 +136,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_select_pages(KvArgs a, RotaryAr
                                                               int first, int recent, int32_t* out) {
   constexpr int kWaves = kThreads / kWave;
   constexpr int kLanes = D == 64 ? 8 : D <= 128 ? 16 : 32;   // of a page
-  constexpr int kGroups = kThreads / kLanes, kAhead = 8;
+  constexpr int kGroups = kThreads / kLanes, kBatch = kLanes < 16 ? kLanes : 16, kAhead = 8;
   extern __shared__ uint64_t s_key[];
   __shared__ double s_sum[D], s_q[D];
   __shared__ int s_hist[3][256], s_wave[kWaves];
@@ -178,30 +195,34 @@ __global__ __launch_bounds__(kThreads) void k_kv_select_pages(KvArgs a, RotaryAr
   for (int e = 0; e < 8; ++e) qd[e] = here ? s_q[8 * part + e] : 0.0;
   const int32_t* const entries = a.page_table + (int64_t)b * a.max_pages + first;
   for (int c0 = 0; c0 < candidates; c0 += kThreads) {
-    const int c_entry = c0 + part * kGroups + mine;
-    const int entry = c_entry < candidates ? entries[c_entry] : -1;
+    const int c = c0 + part * kGroups + mine;
+    const int entry = c < candidates ? page_or_none(a, entries[c]) : -1;
 #pragma unroll 1
-    for (int k0 = 0; k0 < kLanes && c0 + k0 * kGroups < candidates; k0 += kAhead) {
-      v4i32 w[kAhead];
-      int page[kAhead];
+    for (int k0 = 0; k0 < kLanes && c0 + k0 * kGroups < candidates; k0 += kBatch) {
+      double s[kBatch];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        page[u] = __shfl(entry, (lane - part) + k0 + u, kWave);
-        w[u] = v4i32{0, 0, 0, 0};
-        if (here && (uint32_t)page[u] < (uint32_t)a.num_pages)
-          w[u] = ld16v(means + ((int64_t)page[u] * a.kv_heads + h) * D + 8 * part);
+      for (int u0 = 0; u0 < kBatch; u0 += kAhead) {
+        v4i32 w[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const int page = __shfl(entry, (lane - part) + k0 + u0 + u, kWave);
+          w[u] = v4i32{0, 0, 0, 0};
+          if (here && page >= 0) w[u] = ld16v(means + ((int64_t)page * a.kv_heads + h) * D + 8 * part);
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          s[u0 + u] = 0.0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            s[u0 + u] = __builtin_fma(
+                qd[e], (double)h2f(((uint32_t)w[u][e >> 1] >> (16 * (e & 1))) & 0xffffu), s[u0 + u]);
+        }
       }
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        double s = 0.0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          s = __builtin_fma(qd[e], (double)h2f(((uint32_t)w[u][e >> 1] >> (16 * (e & 1))) & 0xffffu), s);
-        s = sum_of_lanes<kLanes>(s);
-        const int c = c0 + (k0 + u) * kGroups + mine;
-        if (part == 0 && c < candidates)
-          s_key[c] = (uint32_t)page[u] < (uint32_t)a.num_pages ? score_key(s) : kNoScore;
-      }
+      // (each lane now gets the score of its own entry)
+      double mine_sum = spread_sums<kBatch>(s, lane);
+      if constexpr (kLanes == 32) mine_sum += __shfl_xor(mine_sum, 16, kWave);
+      if (part / kBatch == k0 / kBatch && c < candidates)
+        s_key[c] = entry >= 0 ? score_key(mine_sum) : kNoScore;
     }
   }
   lds_only_barrier();
