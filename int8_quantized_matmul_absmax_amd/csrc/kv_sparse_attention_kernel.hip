@@ -1,10 +1,9 @@
 // Attention over chosen pages of the paged 8-bit key/value cache.
 //
 // Each token and key/value head has its own list of pages, so its rows are only the
-// query heads that share the head: a block takes up to 16 of them, its waves stream
-// the pages' blocks through LDS as the dense kernel for few rows does, with the same
-// arithmetic. A list's tokens are counted on from page to page: groups of 64 of them
-// may begin inside one page and end in another.
+// query heads that share the head. The arithmetic is the dense kernels', the weights
+// in two parts of fp16 as for few rows. A list's tokens are counted on from page to
+// page: groups of 64 of them may begin inside one page and end in another.
 
 #include "kv_attention_common.h"
 
@@ -12,6 +11,21 @@ namespace i8mm {
 
 namespace {
 
+// Entries of a list up to the last page that may be visible.
+__device__ __forceinline__ int entries_of(const int32_t* list, int count, int seen_pages, int lane) {
+  int entries = 0;
+  for (int e0 = 0; e0 < count; e0 += kWave) {
+    const int e = e0 + lane;
+    const uint64_t there = __ballot(e < count && (uint32_t)list[min(e, count - 1)] < (uint32_t)seen_pages);
+    if (there) entries = e0 + 64 - __builtin_clzll(there);
+  }
+  return entries;
+}
+
+// ---- Few tokens: a block takes up to 16 rows, its four waves share a list, and a list
+// may be split. 64 tokens with lists of 64 pages of 16 tokens, 64 heads on 8 of 128
+// features (131 MB): 25.8 us, 5.1 TB/s; one token, 16 pages of 128 tokens, 32 heads on
+// 8: 7.6 us and 4.2 to join.
 template <int D>
 __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_pages(
     KvArgs a, RotaryArgs rot, AttnArgs t, const int32_t* chosen, int count, int group, int tiles,
@@ -45,16 +59,10 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_pag
   const int64_t out_row0 = (int64_t)token * t.q_heads + h * group;
   const Parts parts = parts_of(t.part, (int64_t)a.total_tokens * t.q_heads, splits, D);
 
-  // entries of the list up to the last page that may be visible
   const int32_t* const list = chosen + ((int64_t)token * a.kv_heads + h) * count;
   const int page_tokens = a.slots * kKvBlock;
   const int seen_pages = belongs ? pos / page_tokens + 1 : 0;
-  int entries = 0;
-  for (int e0 = 0; e0 < count; e0 += kWave) {
-    const int e = e0 + lane;
-    const uint64_t there = __ballot(e < count && (uint32_t)list[min(e, count - 1)] < (uint32_t)seen_pages);
-    if (there) entries = e0 + 64 - __builtin_clzll(there);
-  }
+  const int entries = entries_of(list, count, seen_pages, lane);
   const int all = entries * page_tokens;
   const int begin = split * chunk, end = min(begin + chunk, all);
   const bool only = all <= chunk;
@@ -236,9 +244,239 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_pag
   }
 }
 
+// ---- Many tokens: a wave takes a token and head by itself, and nothing is joined.
+// Bound by the vector pipe (exponentials, conversions), of whose lanes a group of four
+// query heads would use a quarter: so kCls groups of 64 tokens are done at once, each
+// with 16 / kCls of the MFMA's columns. A group's products take queries and weights
+// that are zero outside its own columns, so scores of all of them add up in one set of
+// registers, and a column's sums are those of every kCls-th group, with a maximum and a
+// row sum of its own. The columns of a row are joined at the end.
+//
+// A wave's stages, keys of kCls groups and then their values, go through two buffers
+// of its part of LDS, each refilled as soon as it has been read (with 64 features
+// three and four take the room of a third block a compute unit: 180 us, so 165).
+//
+// 1367 tokens with lists of 32 pages of 48 tokens, 32 heads on 8 of 64 features (what
+// the lists name, 3.2 GB, comes from the L2s): 166 us, 19 TB/s, against 212 by the
+// kernel above; of 128 features 263 us, 24 TB/s, against 361: what the L2s give.
+template <int D, int kCls>
+struct WaveCfg {
+  typedef Stage<D> S;
+  static constexpr int kCols = kRows / kCls;
+  static constexpr int kWaves = 4;
+  static constexpr int kStageLoads = 4 * S::kLoads;
+  static constexpr int kQueryBytes = kCols * (QueryCfg<D>::kRowBytes + 16);
+  static constexpr int kBuffers = 2;
+  static constexpr int kWaveBytes = (kBuffers * S::kGroupBytes + kQueryBytes + 15) / 16 * 16;
+};
+
+template <int D, int kCls>
+__global__ __launch_bounds__(kBlockThreads, D == 64 ? 3 : D <= 128 ? 2 : 1) void k_kv_attn_pages_wave(
+    KvArgs a, RotaryArgs rot, AttnArgs t, const int32_t* chosen, int count, int group) {
+  typedef WaveCfg<D, kCls> Cfg;
+  typedef Stage<D> S;
+  typedef QueryCfg<D> Q;
+  constexpr int kC = (D + 63) / 64, kT = D / 16, kCols = Cfg::kCols, kBuffers = Cfg::kBuffers;
+  constexpr int kAhead = (kBuffers - 1) * Cfg::kStageLoads;
+  constexpr int kListGroups = 16;
+  __shared__ __attribute__((aligned(1024))) int8_t lds[Cfg::kWaves * Cfg::kWaveBytes];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = lane & 15, g = lane >> 4, cls = n / kCols, r = n % kCols;
+  // heads first: blocks go to the 8 XCDs in turn, and a head's share an L2
+  const int h = blockIdx.x % a.kv_heads, token = blockIdx.x / a.kv_heads * Cfg::kWaves + wave;
+  if (token >= a.total_tokens) return;
+  int8_t* const ring = lds + wave * Cfg::kWaveBytes;
+  int8_t* const lds_q = ring + kBuffers * S::kGroupBytes;
+  float* const s_qf = reinterpret_cast<float*>(lds_q + kCols * Q::kRowBytes);
+  const int b = sequence_of(a, token, lane);
+  const KvSeq sq = kv_seq(a, b);
+  const int i_token = token - sq.row0;
+  // (a token of no sequence, or before one, sees nothing)
+  const bool belongs = i_token >= 0 && i_token < sq.n && sq.first + i_token >= 0;
+  const int pos = belongs ? sq.first + i_token : 0;
+  const int32_t* const list = chosen + ((int64_t)token * a.kv_heads + h) * count;
+  const int seen_pages = belongs ? pos / (a.slots * kKvBlock) + 1 : 0;
+  const int entries = entries_of(list, count, seen_pages, lane);
+  const int blocks = entries * a.slots, groups = (blocks + 3) / 4;
+
+  // the queries: columns past the group's rows repeat the last
+  constexpr int kPasses = (kCols + Q::kPassRows - 1) / Q::kPassRows;
+  QueryLoads q_in[kPasses];
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    const int rr = min(p * Q::kPassRows + lane / Q::kLanes, group - 1);
+    load_query<D>(t.q + (int64_t)token * t.q_ts + (int64_t)(h * group + rr) * t.q_hs, pos, rot, t.q,
+                  lane, q_in[p]);
+  }
+  float x_in[kPasses][16];
+  uint32_t x_top[kPasses];
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) x_top[p] = rotate_query<D>(q_in[p], belongs, rot, lane, x_in[p]);
+  row_absmax<D>(x_top);
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    const int rr = p * Q::kPassRows + lane / Q::kLanes;
+    if (rr < kCols) store_query<D>(x_in[p], x_top[p], rot, lane, lds_q + rr * Q::kRowBytes, s_qf + rr);
+  }
+  wait_lds_reads();   // (the wave's own stores)
+  v4i32 qh[kC], ql[kC];
+  read_query<D>(lds_q + r * Q::kRowBytes, g, qh, ql);
+  Row row;
+  row.pos = pos;
+  row.lo = 0;
+  row.slope = 0.f;
+  row.qf = s_qf[r] * t.scale_log2;
+
+  v4f32 o[kT];
+#pragma unroll
+  for (int d = 0; d < kT; ++d) o[d] = v4f32{0.f, 0.f, 0.f, 0.f};
+  float m = -INFINITY, l = 0.f;
+  for (int gi0 = 0; gi0 < groups; gi0 += kListGroups) {
+    // lane 4 i + j: block j of group gi0 + i
+    BlockList bl;
+    float k_absmax = 0.f, v_absmax = 0.f;
+    int room = 0;   // tokens of the block that are visible
+    bl.lin = -1;
+    const int c = 4 * gi0 + lane;
+    if (c < blocks) {
+      const int e = c / a.slots, page = list[e];
+      if ((uint32_t)page < (uint32_t)seen_pages) {
+        const int blk = page * a.slots + (c - e * a.slots);
+        room = max(min(pos + 1 - blk * kKvBlock, kKvBlock), 0);
+        if (room > 0) bl.lin = kv_block(a, b, h, blk);
+      }
+    }
+    if (bl.lin >= 0) {
+      k_absmax = a.k_absmax[bl.lin];
+      v_absmax = a.v_absmax[bl.lin];
+    } else {
+      room = 0;
+    }
+    const uint64_t whole = __ballot(room == kKvBlock);
+    const int sets = (min(kListGroups, groups - gi0) + kCls - 1) / kCls;
+    const int stages = sets * 2 * kCls;
+    // stage s: of set s / (2 kCls), keys of its kCls groups, then their values; past the
+    // last, block 0 again, so that the waits can count
+    auto load = [&](int s, int buffer) __attribute__((always_inline)) {
+      const int in_set = s % (2 * kCls);
+      const int i = s < stages ? s / (2 * kCls) * kCls + in_set % kCls : 0;
+      const int8_t* const codes = in_set < kCls ? a.k_codes : a.v_codes;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        stage_block<D>(codes, max(__builtin_amdgcn_readlane(bl.lin, 4 * i + j), 0),
+                       ring + buffer * S::kGroupBytes + j * S::kPitch, lane);
+    };
+    int s = 0, buffer = 0;
+#pragma unroll
+    for (int u = 0; u < kBuffers; ++u) load(u, u);
+    list_factors(k_absmax, v_absmax, &bl);
+    auto next = [&]() __attribute__((always_inline)) {
+      wait_lds_reads();
+      load(s + kBuffers, buffer);
+      ++s;
+      buffer = buffer + 1 == kBuffers ? 0 : buffer + 1;
+    };
+    for (int set = 0; set < sets; ++set) {
+      v4i32 hi[4], lo[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) hi[q] = lo[q] = v4i32{0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < kCls; ++k) {
+        const int mine = cls == k ? -1 : 0;
+        const int8_t* const st = ring + buffer * S::kGroupBytes;
+        wait_loads<kAhead>();
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const v4i32 keys = read_keys<D>(st, n, g, c, q);
+            hi[q] = __builtin_amdgcn_mfma_i32_16x16x64_i8(keys, qh[c] & mine, hi[q], 0, 0, 0);
+            lo[q] = __builtin_amdgcn_mfma_i32_16x16x64_i8(keys, ql[c] & mine, lo[q], 0, 0, 0);
+          }
+        next();
+      }
+      float x[16], p[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] = (float)((hi[e >> 2][e & 3] << 7) + lo[e >> 2][e & 3]);
+      const int at = 4 * (set * kCls + cls) + g;
+      Scale sc = {__shfl(bl.ks, at, kWave), __shfl(bl.log_a, at, kWave), __shfl(bl.inv_a, at, kWave)};
+      row.hi = __shfl(room, at, kWave);
+      constexpr uint64_t kAll = (1ull << (4 * kCls)) - 1;
+      const bool masked = ((whole >> (4 * kCls * set)) & kAll) != kAll;
+      const float top = max_over_groups<4>(logits<false>(x, &sc, row, -16 * g, g, masked, true));
+      if (__any(top > m + (kHead + kLazy))) {
+        const float alpha = raise(top, &m, &l);
+#pragma unroll
+        for (int d = 0; d < kT; ++d) o[d] *= alpha;
+      }
+      const float off = weight_offset(m, sc);
+      float sum = 0.f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) weights4(x + 4 * q, sc.f, off, &sum, p + 4 * q);
+      l += sum * sc.inv_a;
+      v4i32 ph[2], pl[2];   // the weights in two parts of 11 bits
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t w = f2h2(p[2 * e], p[2 * e + 1]);
+        ph[e >> 2][e & 3] = (int)w;
+        pl[e >> 2][e & 3] = (int)f2h2(p[2 * e] - h2f(w & 0xffffu), p[2 * e + 1] - h2f(w >> 16));
+      }
+#pragma unroll
+      for (int k = 0; k < kCls; ++k) {
+        const int mine = cls == k ? -1 : 0;
+        const int8_t* const st = ring + buffer * S::kGroupBytes;
+        const v8f16 p0h = __builtin_bit_cast(v8f16, ph[0] & mine), p1h = __builtin_bit_cast(v8f16, ph[1] & mine);
+        const v8f16 p0l = __builtin_bit_cast(v8f16, pl[0] & mine), p1l = __builtin_bit_cast(v8f16, pl[1] & mine);
+        wait_loads<kAhead>();
+#pragma unroll
+        for (int d = 0; d < kT; ++d) {
+          v8f16 v0, v1;
+          codes_to_f16(read_values<D>(st, n, g, d), &v0, &v1);
+          o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, p0h, o[d], 0, 0, 0);
+          o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, p1h, o[d], 0, 0, 0);
+          o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, p0l, o[d], 0, 0, 0);
+          o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, p1l, o[d], 0, 0, 0);
+        }
+        next();
+      }
+    }
+    wait_loads<0>();   // (of the next list, or the end: nothing may land in LDS after it)
+  }
+
+  // join the row's columns
+  float top = m;
+#pragma unroll
+  for (int d = kCols; d < kRows; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, kWave));
+  const float w = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top);
+  l *= w;
+#pragma unroll
+  for (int d = kCols; d < kWave; d <<= 1) l += __shfl_xor(l, d, kWave);
+  const float inv = inverse(l);
+  uint16_t* const out = t.out + ((int64_t)token * t.q_heads + h * group + r) * D;
+#pragma unroll
+  for (int d = 0; d < kT; ++d) {
+    v4f32 y = o[d] * w;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+#pragma unroll
+      for (int x = kCols; x < kRows; x <<= 1) y[e] += __shfl_xor(y[e], x, kWave);
+    }
+    if (cls == 0 && r < group)
+      *reinterpret_cast<uint2*>(out + 16 * d + 4 * g) =
+          make_uint2(f2h2(y[0] * inv, y[1] * inv), f2h2(y[2] * inv, y[3] * inv));
+  }
+}
+
+// The kernel for many tokens from kManyWaves of its waves on, where up to eight query
+// heads share a key/value head (lists as above, this one and the one for few): 2048
+// waves of 128 features 161 us and 147, 2216 of 64 47 and 50, of 128 96 and 93, 3768
+// 83 and 84, 157 and 170, of 256 335 and 382, 5088 of 64, 80 and 128 104 and 115, 152
+// and 153, 200 and 220.
+constexpr int kManyWaves = 2560;
 // Splits of a list's tokens, as for few rows of the dense attention.
 struct Plan {
   int group, tiles, splits, chunk;
+  bool wave;   // the kernel for many tokens
 };
 Plan plan(const KvArgs& a, int q_heads, int count) {
   constexpr int64_t kMinChunk = 4 * kGroup, kMaxChunk = 2048, kMaxSplits = 1024;
@@ -246,6 +484,12 @@ Plan plan(const KvArgs& a, int q_heads, int count) {
   Plan p;
   p.group = q_heads / a.kv_heads;
   p.tiles = (p.group + kRows - 1) / kRows;
+  p.wave = p.group <= 8 && (int64_t)a.total_tokens * a.kv_heads >= kManyWaves;
+  if (p.wave) {
+    p.splits = 1;
+    p.chunk = 0;
+    return p;
+  }
   const int64_t tokens = (int64_t)count * a.slots * kKvBlock;
   const int64_t blocks = (int64_t)a.total_tokens * a.kv_heads * p.tiles;
   int64_t chunk = std::min<int64_t>(std::max(tokens * blocks / resident, kMinChunk), kMaxChunk);
@@ -260,6 +504,13 @@ template <int D>
 hipError_t launch_d(const KvArgs& a, const RotaryArgs& r, const AttnArgs& t, const int32_t* chosen,
                     int count, hipStream_t s) {
   const Plan p = plan(a, t.q_heads, count);
+  if (p.wave) {
+    const int64_t blocks = ((int64_t)a.total_tokens + 3) / 4 * a.kv_heads;
+    if (blocks > UINT32_MAX / kBlockThreads) return hipErrorInvalidValue;
+    auto* const kernel = p.group <= 4 ? k_kv_attn_pages_wave<D, 4> : k_kv_attn_pages_wave<D, 2>;
+    kernel<<<(uint32_t)blocks, kBlockThreads, 0, s>>>(a, r, t, chosen, count, p.group);
+    return hipGetLastError();
+  }
   const int64_t blocks = (int64_t)a.total_tokens * a.kv_heads * p.tiles * p.splits;
   if (blocks > UINT32_MAX / kBlockThreads) return hipErrorInvalidValue;
   k_kv_attn_pages<D><<<(uint32_t)blocks, kBlockThreads, 0, s>>>(a, r, t, chosen, count, p.group, p.tiles,

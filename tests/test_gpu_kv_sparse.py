@@ -223,6 +223,77 @@ def test_lists_of_any_kind(gpu, dim):
     assert not got.any()
 
 
+@pytest.mark.parametrize("dim,rotary,interleaved", [
+    (64, 64, False), (80, 0, False), (96, 96, True), (128, 64, False), (256, 256, False)])
+@pytest.mark.parametrize("group", [1, 3, 4, 5, 8])
+def test_many_tokens(gpu, dim, rotary, interleaved, group):
+    """Enough tokens for a wave each: chunks and single tokens, lists longer than the
+    wave's list of blocks and lists that end inside a set of groups."""
+    rng = np.random.default_rng(dim + group)
+    note("many tokens %s" % ((dim, rotary, interleaved, group),))
+    lens, counts = [190, 1, 150, 0, 40, 301], [150, 1, 131, 0, 37, 6]
+    check_attention(gpu, rng, lens, counts, 8 * group, 8, dim, 16, 7, rotary, interleaved)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("group", [2, 7])
+def test_many_tokens_lists_of_any_kind(gpu, dim, group):
+    rng = np.random.default_rng(dim + group)
+    lens, counts = [1300, 270, 9], [3, 80, 3]
+    cache, table = make(rng, lens, 32, dim, 48)
+    table[0, 3], table[1, 2] = -1, 10 ** 9
+    check_attention(gpu, rng, lens, counts, 32 * group, 32, dim, 48, 30, junk=True, cache=(cache, table))
+    none = np.full((86, 32, 2), -1, np.int32)
+    got = check_attention(gpu, rng, lens, counts, 32 * group, 32, dim, 48, 2, chosen=none,
+                          cache=(cache, table))
+    assert not got.any()
+
+
+def test_many_tokens_some_of_no_sequence(gpu):
+    """Rows past the sequences, beyond max_tokens, before a sequence; special queries."""
+    rng = np.random.default_rng(22)
+    lens, counts, heads, kv = [100, 3], [40, 30], 64, 32
+    cache, table = make(rng, lens, kv, 64, 16, poison=False)
+    c, _ = on_gpu(gpu, cache, table, lens, counts)
+    cu = torch.tensor([0, 40, 70], dtype=torch.int32, device="cuda")
+    b = gpu.KVBatch(dev(table), dev(np.array(lens, np.int32)), cu, total_tokens=90, max_tokens=35,
+                    max_len=100)
+    q = rng.normal(0, 1, (90, heads, 64)).astype(np.float16)
+    q[3, 5, 7], q[4, 6, 8] = np.nan, np.inf
+    cos, sin = tables(64, 100)
+    chosen = np.sort(rng.integers(-1, 7, (90, kv, 4)).astype(np.int32), axis=2)
+    out = torch.full((90, heads, 64), float("nan"), dtype=torch.float16, device="cuda")
+    c.attention_pages(dev(q), dev(chosen), b, gpu.Rotary(dev(cos), dev(sin)), out=out)
+    got = host(out).astype(np.float64)
+    assert np.isnan(got[3, 5]).all() and np.isnan(got[4, 6]).all()
+    q[3, 5], q[4, 6] = 0, 0
+    got[3, 5] = got[4, 6] = 0
+    # the first sequence's rows are tokens 65 .. 99 of 35, the second's -27 .. 2 of 30
+    want, bound = R.attention_pages(cache, q[:35], (table, [100], [35]), chosen[:35], cos, sin)
+    want[3, 5] = want[4, 6] = 0
+    assert (np.abs(got[:35] - want) <= bound).all()
+    assert not got[35:67].any() and not got[70:].any()
+    want, bound = R.attention_pages(cache, q[67:70], (table[1:], [3], [3]), chosen[67:70], cos, sin)
+    assert (np.abs(got[67:70] - want) <= bound).all()
+
+
+def test_both_kernels_agree(gpu):
+    """The same tokens alone and among many: each within its bound of the reference, so
+    within both of each other."""
+    rng = np.random.default_rng(23)
+    lens, counts = [400] * 3, [100] * 3
+    cache, table = make(rng, lens, 16, 64, 16)
+    q = rng.normal(0, 1.5, (300, 64, 64)).astype(np.float16)
+    chosen = chosen_for(rng, lens, counts, 16, 16, 9)
+    c, b = on_gpu(gpu, cache, table, lens, counts, max_len=400)
+    many = host(c.attention_pages(dev(q), dev(chosen), b)).astype(np.float64)
+    last = [99, 199, 299]
+    one = gpu.KVBatch(b.page_table, b.seq_lens, max_len=400)
+    few = host(c.attention_pages(dev(q[last]), dev(chosen[last]), one)).astype(np.float64)
+    _, bound = R.attention_pages(cache, q[last], (table, lens, [1] * 3), chosen[last])
+    assert (np.abs(many[last] - few) <= 2 * bound).all()
+
+
 def test_long_lists_are_split(gpu):
     """Lists of many splits, and of more than the joins of few take."""
     rng = np.random.default_rng(9)
