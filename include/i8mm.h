@@ -521,7 +521,8 @@ I8MM_API int int8_kv_cache_read(const i8mm_kv_cache* cache, const i8mm_kv_batch*
  *
  * int8_kv_cache_page_means: the mean keys of the pages that hold the batch's new
  * tokens (after their append), over the tokens that the page then holds:
- * fp16(fl32(sum_t k_t / n)), the sum of q * fl32(a / 127) in 64 bits.
+ * fp16(fl32(sum_t k_t / n)), the sum of q * fl32(a / 127) in 64 bits. (Sequences that
+ * share a page and hold different numbers of its tokens race for its mean.)
  * Errors: EINVAL, EALIGN, ENODEVICE, ELAUNCH.
  */
 I8MM_API int int8_kv_cache_page_means(const i8mm_kv_cache* cache, const i8mm_kv_batch* batch,

@@ -35,9 +35,7 @@ class BeamSearch:
         if beams < 1 or beams > ops.MAX_BEAM_COUNT:
             raise ValueError("beams must be 1 .. %d, got %s" % (ops.MAX_BEAM_COUNT, beams))
         for c in caches:
-            if c.page_tokens != pool.page_tokens or c.num_pages < pool.num_pages:
-                raise ValueError("a cache of %d pages of %d tokens, the pool of %d of %d"
-                                 % (c.num_pages, c.page_tokens, pool.num_pages, pool.page_tokens))
+            pool.check(c)
         self.pool, self.caches, self.beams, self.eos = pool, list(caches), int(beams), eos
         self.max_len = max_len
         self.page_table, self.seq_lens = page_table, seq_lens

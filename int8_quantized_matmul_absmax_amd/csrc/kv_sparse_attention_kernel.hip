@@ -492,7 +492,11 @@ Plan plan(const KvArgs& a, int q_heads, int count) {
   }
   const int64_t tokens = (int64_t)count * a.slots * kKvBlock;
   const int64_t blocks = (int64_t)a.total_tokens * a.kv_heads * p.tiles;
-  int64_t chunk = std::min<int64_t>(std::max(tokens * blocks / resident, kMinChunk), kMaxChunk);
+  // (with blocks for two rounds there is nothing to fill, and sums to join would take
+  // room for every one of their rows)
+  int64_t chunk = tokens;
+  if (blocks < 2 * resident)
+    chunk = std::min<int64_t>(std::max(tokens * blocks / resident, kMinChunk), kMaxChunk);
   chunk = std::max(chunk, tokens / kMaxSplits + 1);
   chunk = (chunk + kGroup - 1) / kGroup * kGroup;
   p.chunk = (int)chunk;

@@ -124,6 +124,7 @@ class Int8KVCache:
     def copy_pages(self, copies):
         """The copies that a KVPages call asked for. The table it gave is right for
         this cache after them."""
+        copies.pool.check(self)
         ops.int8_kv_cache_copy_pages(self, copies.pages, copies.counts)
 
 
@@ -133,12 +134,12 @@ class PageChoice(collections.namedtuple("PageChoice", "count first recent", defa
 
 
 class PageCopies:
-    """Copies of pages that a KVPages call asks for, on the GPU: pages int32 [n, 3]
-    (page, page to copy it to, tokens that count), counts int32 [2], the number of
-    them first."""
+    """Copies of pages that a KVPages call (of `pool`) asks for, on the GPU: pages int32
+    [n, 3] (page, page to copy it to, tokens that count), counts int32 [2], the number
+    of them first."""
 
-    def __init__(self, pages, counts):
-        self.pages, self.counts = pages, counts
+    def __init__(self, pages, counts, pool):
+        self.pages, self.counts, self.pool = pages, counts, pool
 
 
 class KVPages:
@@ -157,6 +158,13 @@ class KVPages:
         if num_pages < 0:
             raise ValueError("num_pages must not be negative")
         self.num_pages, self.page_tokens = int(num_pages), int(page_tokens)
+
+    def check(self, cache):
+        """Refuses a cache that this pool's tables are not right for."""
+        if cache.page_tokens != self.page_tokens or cache.num_pages < self.num_pages:
+            raise ValueError("a cache of %d pages of %d tokens, the pool of %d of %d"
+                             % (cache.num_pages, cache.page_tokens, self.num_pages,
+                                self.page_tokens))
 
     def empty_table(self, rows, max_tokens, device="cuda"):
         """The table and lengths of `rows` sequences of no tokens, wide enough for
@@ -177,14 +185,14 @@ class KVPages:
         table, lens, pages, counts = ops.kv_pages_step(
             page_table, seq_lens, parents, self.num_pages, self.page_tokens, new_tokens, keep,
             shared_workspace)
-        return table, lens, PageCopies(pages, counts)
+        return table, lens, PageCopies(pages, counts, self)
 
     def compact(self, page_table, seq_lens):
         """The used pages to the front of the caches: the table with their new places
         and the copies to make. copies.counts[1] says how many are used."""
         table, pages, counts = ops.kv_pages_compact(page_table, seq_lens, self.num_pages,
                                                     self.page_tokens, shared_workspace)
-        return table, PageCopies(pages, counts)
+        return table, PageCopies(pages, counts, self)
 
 
 class KVBatch:

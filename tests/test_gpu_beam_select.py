@@ -14,11 +14,12 @@ pytestmark = pytest.mark.gpu
 SUM = 2.0 ** -18
 
 
-def check(i8, x, scores, live=None, eos=2, count=None, workspace=None):
+def check(i8, x, scores, live=None, eos=2, count=None, workspace=None, equal_beams=False):
     count = x.shape[1] if count is None else count
     *want, gap = R.select(x if isinstance(x, np.ndarray) else host(x), scores, live, eos, count)
-    # each value may be off by SUM: no choice that this could turn
-    assert gap.min() > 2 * SUM, gap.min()
+    # each value may be off by SUM: no choice that this could turn (equal beams' sums
+    # are equal, whatever they are off by)
+    assert gap.min() > 2 * SUM or equal_beams, gap.min()
     out = i8.beam_select(dev(x) if isinstance(x, np.ndarray) else x, dev(scores),
                          None if live is None else dev(live),
                          eos=None if eos < 0 else eos, count=count, workspace=workspace)
@@ -118,6 +119,35 @@ def test_sorted_rows(gpu, order):
     y[0, 0, 800:808] = np.arange(8)[::order]
     y[0, 0, 2848:2856] = 10 + np.arange(8)[::order]
     check(gpu, y, np.zeros((1, 1), np.float32), None, eos=-1, count=30)
+
+
+def test_no_beams_no_words(gpu):
+    """Searches of no beams or no words: ended beams alone, or nothing."""
+    for half in (np.float16, np.float32):
+        got = check(gpu, np.zeros((2, 0, 50), half), np.zeros((2, 0), np.float32), None, count=3)
+        assert (got[2] == -1).all()
+        live = np.array([[0, 1, 0]], np.int32)
+        got = check(gpu, np.zeros((1, 3, 0), half), np.array([[-2, 0, -1]], np.float32), live, eos=-1,
+                    count=4)
+        assert got[2].tolist() == [[2, 0, -1, -1]] and (got[1] == -1).all()
+        many = -np.arange(300, dtype=np.float32)[None]
+        got = check(gpu, np.zeros((1, 300, 0), half), many, np.zeros((1, 300), np.int32), eos=-1, count=5)
+        assert got[2].tolist() == [[0, 1, 2, 3, 4]]
+    assert gpu.beam_select(torch.zeros((0, 3, 9), device="cuda"),
+                           torch.zeros((0, 3), device="cuda"))[0].shape == (0, 3)
+
+
+@pytest.mark.parametrize("count", [1, 32, 64])
+def test_joins_of_many_lists(gpu, count):
+    """More entries than a join takes at once: many beams of many pieces, values of all
+    beams close together and beams that lead by far."""
+    rng = np.random.default_rng(count + 100)
+    x = rng.normal(0, 2.5, (1, 40, 70000)).astype(np.float16)
+    for spread in (0.0, 30.0):
+        scores = (-spread * rng.random((1, 40))).astype(np.float32)
+        check(gpu, x, scores, None, eos=-1, count=count)
+    x = np.broadcast_to(rng.normal(0, 2.5, (1, 1, 30000)).astype(np.float16), (1, 40, 30000)).copy()
+    check(gpu, x, np.zeros((1, 40), np.float32), None, eos=-1, count=count, equal_beams=True)
 
 
 def test_large_and_small_logits(gpu):

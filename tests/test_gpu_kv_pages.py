@@ -197,6 +197,10 @@ def test_copies_beyond_32_bit_offsets(gpu):
 
 def test_refused_tensors(gpu):
     c = gpu.Int8KVCache(4, 1, 64, 16)
+    for pool in (gpu.KVPages(4, 32), gpu.KVPages(5, 16)):
+        copies = pool.step(ints([[0]]), ints([9]), ints([0, 0]))[2]
+        with pytest.raises(ValueError):
+            c.copy_pages(copies)
     with pytest.raises(ValueError):
         gpu.ops.int8_kv_cache_copy_pages(c, ints([[0, 1]]), ints([1]))
     with pytest.raises(ValueError):
