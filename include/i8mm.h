@@ -615,8 +615,9 @@ I8MM_API size_t int8_kv_cache_attention_pages_workspace_bytes(const i8mm_kv_cach
  *   copies      int32 [num_rows][3]: page, the page to copy it to, tokens that
  *               count; rows in order, then rows of -1.
  *   counts      int32 [2]: copies; pages that were wanting.
- *   workspace   i8mm_kv_pages_workspace_bytes(num_rows, num_pages) bytes, 256-byte
- *               aligned. What it holds on entry does not matter.
+ *   workspace   i8mm_kv_pages_workspace_bytes(num_rows, max_pages, num_pages) bytes,
+ *               256-byte aligned (NULL when that is 0). What it holds on entry does
+ *               not matter.
  *
  * num_seqs, num_rows up to 65535; max_pages * page_tokens up to 2^30;
  * num_rows * (max_pages + 1) and num_pages below 2^31; page_tokens as in the cache.
@@ -630,9 +631,10 @@ I8MM_API int i8mm_kv_pages_step(const int32_t* page_table, const int32_t* seq_le
                                 int32_t* counts, void* workspace, size_t workspace_bytes,
                                 i8mm_stream_t stream);
 
-/* Bytes of workspace for i8mm_kv_pages_step and (num_rows 0)
+/* Bytes of workspace for i8mm_kv_pages_step and (num_rows its num_seqs)
  * i8mm_kv_pages_compact; 0 also if the sizes are invalid. Host-only, pure. */
-I8MM_API size_t i8mm_kv_pages_workspace_bytes(int64_t num_rows, int64_t num_pages);
+I8MM_API size_t i8mm_kv_pages_workspace_bytes(int64_t num_rows, int64_t max_pages,
+                                              int64_t num_pages);
 
 /*
  * i8mm_kv_pages_compact: the used pages to the front. With `live` pages named by

@@ -119,7 +119,7 @@ def _declare(lib):
                                 ctypes.c_size_t, vp], i32),
         "i8mm_kv_pages_compact": ([vp, vp, i64, i64, i64, i64, vp, vp, vp, vp, ctypes.c_size_t, vp],
                                   i32),
-        "i8mm_kv_pages_workspace_bytes": ([i64, i64], ctypes.c_size_t),
+        "i8mm_kv_pages_workspace_bytes": ([i64, i64, i64], ctypes.c_size_t),
         "int8_kv_cache_copy_pages": ([cache, vp, vp, vp, i64, vp], i32),
         "i8mm_beam_select": ([vp, i32, i64, vp, vp, i64, i64, i64, i64, i32, vp, vp, vp, vp, vp,
                               ctypes.c_size_t, vp], i32),

@@ -819,12 +819,12 @@ bool overlap(const void* p, int64_t p_bytes, const void* q, int64_t q_bytes) {
 
 extern "C" {
 
-size_t i8mm_kv_pages_workspace_bytes(int64_t num_rows, int64_t num_pages) {
+size_t i8mm_kv_pages_workspace_bytes(int64_t num_rows, int64_t max_pages, int64_t num_pages) {
   i8mm::PagesArgs a;
-  if (pages_sizes("i8mm_kv_pages_workspace_bytes", 0, 0, num_rows, num_pages, I8MM_KV_BLOCK, &a) !=
-      I8MM_OK)
+  if (pages_sizes("i8mm_kv_pages_workspace_bytes", 0, max_pages, num_rows, num_pages, I8MM_KV_BLOCK,
+                  &a) != I8MM_OK)
     return 0;
-  return i8mm::kv_pages_workspace_bytes(a);
+  return i8mm::kv_pages_workspace_bytes(a, a.num_rows);
 }
 
 int i8mm_kv_pages_step(const int32_t* page_table, const int32_t* seq_lens, int64_t num_seqs,
@@ -850,7 +850,8 @@ int i8mm_kv_pages_step(const int32_t* page_table, const int32_t* seq_lens, int64
   if (overlap(page_table, 4 * num_seqs * max_pages, out_table, 4 * num_rows * max_pages) ||
       overlap(seq_lens, 4 * num_seqs, out_lens, 4 * num_rows))
     return fail(I8MM_EINVAL, "%s: the new table or lengths overlap the old ones", fn);
-  I8MM_TRY(check_scratch(fn, workspace, workspace_bytes, i8mm::kv_pages_workspace_bytes(a)));
+  I8MM_TRY(check_scratch(fn, workspace, workspace_bytes,
+                         i8mm::kv_pages_workspace_bytes(a, a.num_rows)));
   I8MM_TRY(check_device());
   a.page_table = page_table;
   a.seq_lens = seq_lens;
@@ -881,7 +882,8 @@ int i8mm_kv_pages_compact(const int32_t* page_table, const int32_t* seq_lens, in
   I8MM_TRY(check_ints(fn, "counts", counts, true));
   if (out_table != page_table && overlap(page_table, 4 * entries, out_table, 4 * entries))
     return fail(I8MM_EINVAL, "%s: the new table overlaps the old one without being it", fn);
-  I8MM_TRY(check_scratch(fn, workspace, workspace_bytes, i8mm::kv_pages_workspace_bytes(a)));
+  I8MM_TRY(check_scratch(fn, workspace, workspace_bytes,
+                         i8mm::kv_pages_workspace_bytes(a, a.num_seqs)));
   I8MM_TRY(check_device());
   a.page_table = page_table;
   a.seq_lens = seq_lens;

@@ -420,9 +420,10 @@ int64_t pad4(int64_t n) { return (n + 3) / 4 * 4; }
 
 }  // namespace
 
-// words [num_pages], list [num_pages], places [num_rows]
-size_t kv_pages_workspace_bytes(const PagesArgs& a) {
-  return (size_t)(2 * pad4(a.num_pages) + 2 * (int64_t)a.num_rows) * 4;
+// words [num_pages], list [num_pages], places [rows]
+size_t kv_pages_workspace_bytes(const PagesArgs& a, int rows) {
+  if (one_block(a, rows)) return 0;
+  return (size_t)(2 * pad4(a.num_pages) + 2 * (int64_t)rows) * 4;
 }
 
 hipError_t launch_kv_pages_step(const PagesArgs& a, void* ws, hipStream_t s) {

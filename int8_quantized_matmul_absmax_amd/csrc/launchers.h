@@ -178,7 +178,7 @@ struct PagesArgs {
   int32_t* counts;
   int num_seqs, max_pages, num_rows, num_pages, page_tokens, new_all;
 };
-size_t kv_pages_workspace_bytes(const PagesArgs& a);
+size_t kv_pages_workspace_bytes(const PagesArgs& a, int rows);   // of the step or the compaction
 hipError_t launch_kv_pages_step(const PagesArgs& a, void* ws, hipStream_t s);
 hipError_t launch_kv_pages_compact(const PagesArgs& a, void* ws, hipStream_t s);
 // (of KvArgs the cache's part)

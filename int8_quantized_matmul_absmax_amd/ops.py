@@ -58,7 +58,7 @@ def _need(t, name, dtype, ndim=None, shape=None, min_numel=None):
         raise ValueError("%s must be contiguous" % name)
     if ndim is not None and t.dim() != ndim:
         raise ValueError("%s must have %d dims, got %d" % (name, ndim, t.dim()))
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     if min_numel is not None and t.numel() < min_numel:
         raise ValueError("%s must hold at least %d elements, got %d" % (name, min_numel, t.numel()))
@@ -522,32 +522,32 @@ def kv_pages_step(page_table, seq_lens, parents, num_pages, page_tokens, new_tok
     _need(page_table, "page_table", torch.int32, 2)
     seqs, width = page_table.shape
     _need(seq_lens, "seq_lens", torch.int32, shape=(seqs,))
-    if isinstance(parents, torch.Tensor):
-        parents = parents.view(-1) if parents.is_contiguous() else parents
-    _need(parents, "parents", torch.int32, 1)
-    rows = parents.shape[0]
-    if keep is not None:
-        _need(keep, "keep", torch.int32, min_numel=rows)
+    _need(parents, "parents", torch.int32)
+    rows = parents.numel()
     each, new_all = None, 0
     if isinstance(new_tokens, torch.Tensor):
         _need(new_tokens, "new_tokens", torch.int32)
-        if new_tokens.numel() != rows:
-            raise ValueError("new_tokens must hold %d numbers, got %d" % (rows, new_tokens.numel()))
         each = new_tokens
     else:
         new_all = int(new_tokens)
-    if keep is not None and keep.numel() != rows:
-        raise ValueError("keep must hold %d numbers, got %d" % (rows, keep.numel()))
+    if keep is not None:
+        _need(keep, "keep", torch.int32)
+    for name, t in (("new_tokens", each), ("keep", keep)):
+        if t is not None and t.numel() != rows:
+            raise ValueError("%s must hold %d numbers, got %d" % (name, rows, t.numel()))
     dev = _on_gpu(page_table=page_table, seq_lens=seq_lens, parents=parents, keep=keep,
                   new_tokens=each)
     out = torch.empty((rows * (width + 4) + 2,), dtype=torch.int32, device=dev)
-    table, lens, copies, counts = out.split_with_sizes((rows * width, rows, 3 * rows, 2))
-    wp, wn = _scratch(lib.i8mm_kv_pages_workspace_bytes(rows, num_pages), workspace, dev)
+    at = rows * width
+    table, lens = out.as_strided((rows, width), (width, 1)), out.as_strided((rows,), (1,), at)
+    copies = out.as_strided((rows, 3), (3, 1), at + rows)
+    counts = out.as_strided((2,), (1,), at + 4 * rows)
+    wp, wn = _scratch(lib.i8mm_kv_pages_workspace_bytes(rows, width, num_pages), workspace, dev)
     _run(dev, lib.i8mm_kv_pages_step, page_table.data_ptr(), seq_lens.data_ptr(), seqs, width,
          parents.data_ptr(), None if keep is None else keep.data_ptr(),
          None if each is None else each.data_ptr(), new_all, rows, num_pages, page_tokens,
          table.data_ptr(), lens.data_ptr(), copies.data_ptr(), counts.data_ptr(), wp, wn)
-    return table.view(rows, width), lens, copies.view(rows, 3), counts
+    return table, lens, copies, counts
 
 
 def kv_pages_compact(page_table, seq_lens, num_pages, page_tokens, workspace=None):
@@ -560,11 +560,13 @@ def kv_pages_compact(page_table, seq_lens, num_pages, page_tokens, workspace=Non
     dev = _on_gpu(page_table=page_table, seq_lens=seq_lens)
     most = max(int(num_pages) // 2, 0)
     out = torch.empty((seqs * width + 3 * most + 2,), dtype=torch.int32, device=dev)
-    table, copies, counts = out.split_with_sizes((seqs * width, 3 * most, 2))
-    wp, wn = _scratch(lib.i8mm_kv_pages_workspace_bytes(0, num_pages), workspace, dev)
+    table = out.as_strided((seqs, width), (width, 1))
+    copies = out.as_strided((most, 3), (3, 1), seqs * width)
+    counts = out.as_strided((2,), (1,), seqs * width + 3 * most)
+    wp, wn = _scratch(lib.i8mm_kv_pages_workspace_bytes(seqs, width, num_pages), workspace, dev)
     _run(dev, lib.i8mm_kv_pages_compact, page_table.data_ptr(), seq_lens.data_ptr(), seqs, width,
          num_pages, page_tokens, table.data_ptr(), copies.data_ptr(), counts.data_ptr(), wp, wn)
-    return table.view(seqs, width), copies.view(most, 3), counts
+    return table, copies, counts
 
 
 def int8_kv_cache_copy_pages(cache, copies, count):
@@ -623,11 +625,11 @@ def beam_select(logits, scores, live=None, eos=None, count=None, workspace=None)
     dev = _on_gpu(logits=logits, scores=scores, live=live)
     count = beams if count is None else int(count)
     fp32 = 1 if logits.dtype == torch.float32 else 0
-    ints = torch.empty((3, batch, max(count, 0)), dtype=torch.int32, device=dev)
+    tokens, parents, alive = torch.empty((3, batch, max(count, 0)), dtype=torch.int32,
+                                         device=dev).unbind(0)
     out = torch.empty((batch, max(count, 0)), dtype=torch.float32, device=dev)
     wp, wn = _scratch(lib.i8mm_beam_select_workspace_bytes(fp32, batch, beams, vocab, count),
                       workspace, dev)
-    tokens, parents, alive = ints.unbind(0)
     _run(dev, lib.i8mm_beam_select, logits.data_ptr(), fp32, max(rs, vocab), scores.data_ptr(),
          None if live is None else live.data_ptr(), batch, beams, vocab, count,
          -1 if eos is None else int(eos), out.data_ptr(), tokens.data_ptr(), parents.data_ptr(),

@@ -61,13 +61,13 @@ int main() {
           int64_t size[] = {3, 5, 4, 20, 64, 1};   // seqs, width, rows, pages, page_tokens, new
           size[f] = u;
           size[g] = w;
-          (void)i8mm_kv_pages_workspace_bytes(size[2], size[3]);
+          (void)i8mm_kv_pages_workspace_bytes(size[2], size[1], size[3]);
           expect(i8mm_kv_pages_step(ints, ints, size[0], size[1], ints, ints, nullptr, size[5], size[2],
                                     size[3], size[4], other, other, other, nullptr, floats, 1ull << 62,
                                     nullptr) < 0, "step counts");
           expect(i8mm_kv_pages_compact(ints, ints, size[0], size[1], size[3], size[4], ints, ints, nullptr,
                                        floats, 1ull << 62, nullptr) < 0, "compact counts");
-          if (i8mm_kv_pages_workspace_bytes(size[2], size[3]) > 0)
+          if (i8mm_kv_pages_workspace_bytes(size[2], size[1], size[3]) > 0)
             expect(i8mm_kv_pages_step(ints, ints, size[0], size[1], ints, ints, nullptr, size[5], size[2],
                                       size[3], size[4], other, other, other, other, nullptr, 0,
                                       nullptr) < 0, "step workspace");

@@ -213,25 +213,27 @@ def test_refused_tensors(gpu):
 
 
 def test_workspace_contents_do_not_matter(gpu):
-    table, lens, parents = [[0, 1, 2], [0, 1, 3]], [40, 47], [0, 0, 1, -1]
-    need = gpu.load_library().i8mm_kv_pages_workspace_bytes(4, 11)
-    want = R.step(table, lens, parents, [3] * 4, None, 11, 16, 3)
+    table, lens, parents, pages = [[0, 1, 2], [0, 1, 19999]], [40, 47], [0, 0, 1, -1], 20000
+    need = gpu.load_library().i8mm_kv_pages_workspace_bytes(4, 3, pages)
+    want = R.step(table, lens, parents, [3] * 4, None, pages, 16, 3)
+    assert need > 0
     for fill in (0, 255, 1, 128):
         ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
-        t, n, copies, counts = gpu.ops.kv_pages_step(ints(table), ints(lens), ints(parents), 11, 16, 3,
+        t, n, copies, counts = gpu.ops.kv_pages_step(ints(table), ints(lens), ints(parents), pages, 16, 3,
                                                      workspace=ws)
         assert host(t).tolist() == want[0] and host(n).tolist() == want[1]
         ws.fill_(fill)
-        t, _, _ = gpu.ops.kv_pages_compact(ints(table), ints(lens), 11, 16, workspace=ws)
-        assert host(t).tolist() == R.compact(table, lens, 11, 16)[0]
+        t, _, _ = gpu.ops.kv_pages_compact(ints(table), ints(lens), pages, 16, workspace=ws)
+        assert host(t).tolist() == R.compact(table, lens, pages, 16)[0]
 
 
-def test_recorded_steps(gpu):
+@pytest.mark.parametrize("pages", [60, 17000])
+def test_recorded_steps(gpu, pages):
     """A step, its copies and a compaction recorded once, replayed with other
-    tables, with eager calls in between."""
+    tables, with eager calls in between; in one launch each and in several."""
     rng = random.Random(5)
     nrng = np.random.default_rng(5)
-    page, pages, width, rows = 16, 60, 6, 5
+    page, width, rows = 16, 6, 5
     pool = gpu.KVPages(pages, page)
     cache = noise(nrng, pages, 2, page, 64, True)
     c = gpu_cache(gpu, cache)

@@ -53,8 +53,8 @@ BAD = [
     (dict(out=None), _lib.I8MM_EINVAL), (dict(out=ODD), _lib.I8MM_EALIGN),
     (dict(out=A + 4), _lib.I8MM_EINVAL), (dict(copies=None), _lib.I8MM_EINVAL),
     (dict(counts=None), _lib.I8MM_EINVAL), (dict(counts=ODD), _lib.I8MM_EALIGN),
-    (dict(ws=None), _lib.I8MM_EWORKSPACE), (dict(wn=79), _lib.I8MM_EWORKSPACE),
-    (dict(ws=A + 16), _lib.I8MM_EALIGN)]
+    (dict(ws=None, pages=20000), _lib.I8MM_EWORKSPACE), (dict(wn=79, pages=20000), _lib.I8MM_EWORKSPACE),
+    (dict(ws=A + 16, pages=20000), _lib.I8MM_EALIGN)]
 
 
 @pytest.mark.parametrize("kw,status", BAD)
@@ -98,11 +98,12 @@ def test_nothing_to_copy_needs_no_device(lib):
 
 
 def test_workspace_sizes(lib):
+    """None for what one block does, room for a word, an entry and a place each beyond."""
     size = lib.i8mm_kv_pages_workspace_bytes
-    assert size(-1, 4) == size(4, -1) == size(65536, 4) == size(0, 1 << 31) == 0
-    for rows in (0, 1, 65535):
-        for pages in (0, 1, 5, 1 << 20):
-            assert size(rows, pages) >= 8 * (rows + pages)
+    assert size(-1, 4, 4) == size(4, -1, 4) == size(4, 4, -1) == size(65536, 4, 4) == 0
+    assert size(0, 0, 1 << 31) == 0 and size(4, 17, 80) == 0
+    for rows, width, pages in ((2000, 10, 100), (500, 1000, 100), (1, 1, 1 << 20), (65535, 100, 0)):
+        assert size(rows, width, pages) >= 8 * (rows + pages)
 
 
 def test_binding_refusals():
