@@ -609,15 +609,15 @@ I8MM_API size_t int8_kv_cache_attention_pages_workspace_bytes(const i8mm_kv_cach
  *   parents     int32 [num_rows]: i8mm_beam_select's, for one.
  *   keep        int32 [num_rows] (negative: none), or NULL: all tokens.
  *   new_tokens  int32 [num_rows] (negative: none), or NULL: new_all each.
- *   out_table   int32 [num_rows, max_pages], not overlapping page_table;
- *   out_lens    int32 [num_rows], not overlapping seq_lens: what an i8mm_kv_batch
- *               takes, the new tokens included.
+ *   out_table   int32 [num_rows, max_pages], out_lens int32 [num_rows]: what an
+ *               i8mm_kv_batch takes, the new tokens included.
  *   copies      int32 [num_rows][3]: page, the page to copy it to, tokens that
  *               count; rows in order, then rows of -1.
  *   counts      int32 [2]: copies; pages that were wanting.
  *   workspace   i8mm_kv_pages_workspace_bytes(num_rows, max_pages, num_pages) bytes,
  *               256-byte aligned (NULL when that is 0). What it holds on entry does
  *               not matter.
+ * An output that overlaps an input or another output is refused (EINVAL).
  *
  * num_seqs, num_rows up to 65535; max_pages * page_tokens up to 2^30;
  * num_rows * (max_pages + 1) and num_pages below 2^31; page_tokens as in the cache.
@@ -642,7 +642,8 @@ I8MM_API size_t i8mm_kv_pages_workspace_bytes(int64_t num_rows, int64_t max_page
  * both in ascending order, and the table names their new places.
  *
  *   page_table, seq_lens, sizes  as for i8mm_kv_pages_step.
- *   out_table   int32 [num_seqs, max_pages]; may be page_table.
+ *   out_table   int32 [num_seqs, max_pages]; may be page_table (no other output
+ *               may overlap an input or another output).
  *   copies      int32 [num_pages / 2][3], as for i8mm_kv_pages_step, of whole
  *               pages. No page is both copied and copied to.
  *   counts      int32 [2]: copies; live.
@@ -696,7 +697,8 @@ I8MM_API int int8_kv_cache_copy_pages(const i8mm_kv_cache* cache, uint16_t* k_me
  *   workspace    i8mm_beam_select_workspace_bytes(...) bytes, 256-byte
  *            aligned. What it holds on entry does not matter.
  * Places beyond the candidates get -infinity, -1, -1 and 0. All arrays of 32-bit
- * elements are 4-byte aligned.
+ * elements are 4-byte aligned; an output that overlaps scores, live or another
+ * output is refused (EINVAL).
  *
  * Exponentials are fp32 (a row's sum is within 2^-18 of itself); values are
  * compared in 64 bits and rounded to fp32 when they are written.

@@ -55,6 +55,8 @@ class Int8CachedAttention(torch.nn.Module):
         by a cache that holds mean keys, and not to all; without window and slopes."""
         if choice is not None and (window or alibi_slopes is not None):
             raise ValueError("a choice of pages has neither a window nor position biases")
+        if choice is not None and cache.k_means is None:
+            raise ValueError("the cache holds no mean keys (page_means=True)")
         if (cache.kv_heads, cache.head_dim) != (self.kv_heads, self.head_dim):
             raise ValueError("cache of %d heads of %d, layer of %d of %d"
                              % (cache.kv_heads, cache.head_dim, self.kv_heads, self.head_dim))

@@ -28,7 +28,8 @@ class BeamSearch:
     max_len: a bound on the sequences' lengths for KVBatch.
 
     page_table, seq_lens, scores, live: of the rows as they stand, ended beams
-    included; batch: the KVBatch of the tokens that the last step chose."""
+    included; batch: the KVBatch of the tokens that the last step chose; wanting: int32
+    on the GPU, how many pages it found no room for (their tokens are absent)."""
 
     def __init__(self, pool, caches, page_table, seq_lens, beams, eos=None, max_len=None):
         searches = page_table.shape[0]
@@ -41,7 +42,7 @@ class BeamSearch:
         self.page_table, self.seq_lens = page_table, seq_lens
         self.scores = torch.zeros((searches, 1), dtype=torch.float32, device=page_table.device)
         self.live = torch.ones((searches, 1), dtype=torch.int32, device=page_table.device)
-        self.batch = None
+        self.batch = self.wanting = None
         self._history = []
 
     def step(self, logits):
@@ -57,7 +58,7 @@ class BeamSearch:
         # a beam that has ended has no new token: a sequence of length 0 stores nothing
         self.batch = KVBatch(self.page_table, self.seq_lens * self.live.view(-1),
                              max_len=self.max_len)
-        self.wanting = copies.counts[1]   # pages that were wanting
+        self.wanting = copies.counts[1]
         self._history.append((tokens, parents))
         return tokens
 

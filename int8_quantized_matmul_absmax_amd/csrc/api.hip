@@ -8,6 +8,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 
 #include <hip/hip_runtime.h>
 
@@ -689,6 +690,27 @@ int int8_kv_cache_attention(const uint16_t* q, int64_t q_token_stride, int64_t q
 
 namespace {
 
+// Arrays of 32-bit elements, and whether any that is written shares memory with one that
+// is read or with another that is written.
+struct Words32 {
+  const void* p;
+  int64_t n;
+};
+bool overlap(const Words32& x, const Words32& y) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+  return x.p && y.p && x.n > 0 && y.n > 0 && a < b + 4 * (uintptr_t)y.n && b < a + 4 * (uintptr_t)x.n;
+}
+int check_apart(const char* fn, std::initializer_list<Words32> written,
+                std::initializer_list<Words32> read) {
+  for (const Words32* w = written.begin(); w != written.end(); ++w) {
+    bool shared = false;
+    for (const Words32& r : read) shared = shared || overlap(*w, r);
+    for (const Words32* o = w + 1; o != written.end(); ++o) shared = shared || overlap(*w, *o);
+    if (shared) return fail(I8MM_EINVAL, "%s: an output overlaps an input or another output", fn);
+  }
+  return I8MM_OK;
+}
+
 int beam_sizes(const char* fn, int fp32, int64_t batch, int64_t beams, int64_t vocab,
                int64_t count, i8mm::BeamArgs* a) {
   if (fp32 != 0 && fp32 != 1) return fail(I8MM_EINVAL, "%s: logits_fp32 is not 0 or 1", fn);
@@ -767,6 +789,9 @@ int i8mm_beam_select(const void* logits, int logits_fp32, int64_t row_stride, co
   I8MM_TRY(check_ints(fn, "out_live", out_live, batch > 0));
   I8MM_TRY(check_scratch(fn, workspace, workspace_bytes,
                          batch == 0 ? 0 : i8mm::beam_workspace_bytes(a)));
+  I8MM_TRY(check_apart(fn, {{out_scores, batch * count}, {out_tokens, batch * count},
+                            {out_parents, batch * count}, {out_live, batch * count}},
+                       {{scores, rows}, {live, rows}}));
   if (batch == 0) return ok();
   I8MM_TRY(check_device());
   a.logits = logits;
@@ -810,11 +835,6 @@ int pages_sizes(const char* fn, int64_t num_seqs, int64_t max_pages, int64_t num
   return I8MM_OK;
 }
 
-bool overlap(const void* p, int64_t p_bytes, const void* q, int64_t q_bytes) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return p && q && a < b + q_bytes && b < a + p_bytes;
-}
-
 }  // namespace
 
 extern "C" {
@@ -847,11 +867,12 @@ int i8mm_kv_pages_step(const int32_t* page_table, const int32_t* seq_lens, int64
   I8MM_TRY(check_ints(fn, "out_lens", out_lens, num_rows > 0));
   I8MM_TRY(check_ints(fn, "copies", copies, num_rows > 0));
   I8MM_TRY(check_ints(fn, "counts", counts, true));
-  if (overlap(page_table, 4 * num_seqs * max_pages, out_table, 4 * num_rows * max_pages) ||
-      overlap(seq_lens, 4 * num_seqs, out_lens, 4 * num_rows))
-    return fail(I8MM_EINVAL, "%s: the new table or lengths overlap the old ones", fn);
   I8MM_TRY(check_scratch(fn, workspace, workspace_bytes,
                          i8mm::kv_pages_workspace_bytes(a, a.num_rows)));
+  I8MM_TRY(check_apart(fn, {{out_table, num_rows * max_pages}, {out_lens, num_rows},
+                            {copies, 3 * num_rows}, {counts, 2}},
+                       {{page_table, num_seqs * max_pages}, {seq_lens, num_seqs}, {parents, num_rows},
+                        {keep, num_rows}, {new_tokens, num_rows}}));
   I8MM_TRY(check_device());
   a.page_table = page_table;
   a.seq_lens = seq_lens;
@@ -880,10 +901,12 @@ int i8mm_kv_pages_compact(const int32_t* page_table, const int32_t* seq_lens, in
   I8MM_TRY(check_ints(fn, "out_table", out_table, entries > 0));
   I8MM_TRY(check_ints(fn, "copies", copies, num_pages >= 2));
   I8MM_TRY(check_ints(fn, "counts", counts, true));
-  if (out_table != page_table && overlap(page_table, 4 * entries, out_table, 4 * entries))
-    return fail(I8MM_EINVAL, "%s: the new table overlaps the old one without being it", fn);
   I8MM_TRY(check_scratch(fn, workspace, workspace_bytes,
                          i8mm::kv_pages_workspace_bytes(a, a.num_seqs)));
+  // (a table is renamed entry by entry, in place too)
+  I8MM_TRY(check_apart(fn, {{out_table, entries}, {copies, num_pages / 2 * 3}, {counts, 2}},
+                       {{out_table == page_table ? nullptr : page_table, entries},
+                        {seq_lens, num_seqs}}));
   I8MM_TRY(check_device());
   a.page_table = page_table;
   a.seq_lens = seq_lens;

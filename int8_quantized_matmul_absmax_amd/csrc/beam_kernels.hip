@@ -602,7 +602,7 @@ size_t beam_workspace_bytes(const BeamArgs& a) {
 hipError_t launch_beam_select(const BeamArgs& a, hipStream_t s) {
   const Plan p = plan(a);
   const int64_t blocks = (int64_t)a.batch * a.beams * p.pieces;
-  if (blocks > INT32_MAX / kBlockThreads) return hipErrorInvalidValue;
+  if (blocks > UINT32_MAX / kBlockThreads) return hipErrorInvalidValue;
   if (blocks > 0) {
     // (fewer words than 16 bytes hold: a kernel that does not load so many)
     const bool few = a.vocab < (a.fp32 ? 4 : 8);

@@ -46,6 +46,21 @@ def test_refused(lib, kw, status):
     assert lib.i8mm_last_error().startswith(b"i8mm_beam_select: ")
 
 
+APART = [A + 4096 * i for i in range(6)]   # scores, live and the outputs
+
+
+@pytest.mark.parametrize("i,j", [(i, j) for i in range(2, 6) for j in range(i)])
+def test_outputs_apart(lib, i, j):
+    """No output overlaps another or an input, not by its last element either (18
+    candidates): the next beams are not written over the last."""
+    size = 4 * 2 * (3 if j < 2 else 9)
+    for at in (APART[j], APART[j] + size - 4, APART[j] - 4 * 17):
+        p = list(APART)
+        p[i] = at
+        assert call(lib, scores=p[0], live=p[1], count=9, outs=p[2:]) == _lib.I8MM_EINVAL
+        assert b"overlaps" in lib.i8mm_last_error()
+
+
 def test_nothing_to_do_needs_no_device(lib):
     assert call(lib, batch=0, logits=None, scores=None, outs=(None,) * 4, ws=None, wn=0) == _lib.I8MM_OK
     assert lib.i8mm_beam_select_workspace_bytes(0, 0, 3, 100, 3) == 0

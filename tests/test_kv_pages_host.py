@@ -77,6 +77,24 @@ def test_refused_steps(lib, kw, status):
     assert call_step(lib, **kw) == status
 
 
+def test_outputs_apart(lib):
+    """No output overlaps another or an input, but for a compacted table that is the
+    old one."""
+    names = ("table", "lens", "parents", "keep", "new", "out", "out_lens", "copies", "counts")
+    apart = {name: (2 + i) << 16 for i, name in enumerate(names)}
+    for j, name in enumerate(names[5:], 5):
+        for other in names[:j]:
+            assert call_step(lib, **dict(apart, **{name: apart[other]})) == _lib.I8MM_EINVAL
+            assert b"overlaps" in lib.i8mm_last_error()
+    names = ("table", "lens", "out", "copies", "counts")
+    apart = {name: apart[name] for name in names}
+    for j, name in enumerate(names[2:], 2):
+        for other in names[:j]:
+            if (name, other) != ("out", "table"):
+                assert call_compact(lib, **dict(apart, **{name: apart[other]})) == _lib.I8MM_EINVAL
+                assert b"overlaps" in lib.i8mm_last_error()
+
+
 @pytest.mark.parametrize("kw,status", [
     (dict(num_pages=-1), _lib.I8MM_EINVAL), (dict(page_tokens=24), _lib.I8MM_EALIGN),
     (dict(head_dim=72), _lib.I8MM_EINVAL), (dict(kv_heads=0), _lib.I8MM_EINVAL),
