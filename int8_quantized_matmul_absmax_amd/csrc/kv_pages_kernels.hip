@@ -162,8 +162,16 @@ __device__ __forceinline__ void give_pages(const PagesArgs& a, const uint32_t* w
       extra = r.all_pages - r.pages;
       if (extra > 0) row[first] = at < have ? list[at] : -1;
     }
-    // rows with more new pages than one: a wave's lanes together
-    uint64_t long_rows = __ballot(extra > 1);
+    // Rows with more new pages than one: by a thread each, or each in turn by a wave's
+    // lanes. A turn takes the time of four pages of a thread: 190 rows of 6 pages 18.2 us
+    // in turn and 9.3 by their threads, 64 of 42 18.7 and 11.4.
+    const int few = 4 * __popcll(__ballot(extra > 1));
+    if (extra > 1 && extra <= few) {
+      int32_t* const row = a.out_table + (int64_t)i * a.max_pages + first;
+#pragma unroll 4
+      for (int j = 1; j < extra; ++j) row[j] = at + j < have ? list[at + j] : -1;
+    }
+    uint64_t long_rows = __ballot(extra > few && extra > 1);
     while (long_rows) {
       const int from = __builtin_ctzll(long_rows);
       long_rows &= long_rows - 1;

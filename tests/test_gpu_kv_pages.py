@@ -117,6 +117,18 @@ def test_a_long_prompt_and_many_pages(gpu):
                   1510)
 
 
+@pytest.mark.parametrize("rows", [3, 70])
+def test_rows_of_few_and_of_many_new_pages(gpu, rows):
+    """Side by side, until the pages run out."""
+    rng = np.random.default_rng(rows)
+    new = [int(n) for n in rng.choice([0, 1, 17, 40, 100, 300, 4000], rows)]
+    new[1] = 4700
+    table, lens = rng.permutation(1500)[:10].reshape(1, 10), [150]
+    table = np.concatenate([table, np.full((1, 290), -1)], axis=1).astype(np.int32)
+    for pages in (20000, 1510, 1700):
+        check_step(gpu, table, lens, [0] * rows, new, None, pages, 16, 300)
+
+
 @pytest.mark.parametrize("rows,width,page", [(1, 1, 16), (3, 5, 32), (40, 300, 16), (300, 40, 64)])
 def test_compact(gpu, rows, width, page):
     rng = random.Random(rows)
