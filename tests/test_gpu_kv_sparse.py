@@ -107,6 +107,12 @@ def test_select_many_pages(gpu):
         check_select(gpu, rng, [16 * pages - 5], [2], 4, 2, 64, 16, count, first=1, recent=2)
 
 
+def test_select_many_blocks(gpu):
+    """The same for more blocks than compute units."""
+    rng = np.random.default_rng(41)
+    check_select(gpu, rng, [16 * 600 - 5], [40], 8, 8, 64, 16, 33, first=1, recent=2)
+
+
 def test_select_the_most_pages(gpu):
     """As many candidates as are allowed; the reference is torch's sort."""
     pages, kv_heads, dim, count = 16386, 1, 64, 50
@@ -221,6 +227,15 @@ def test_lists_of_any_kind(gpu, dim):
     none = np.full((4, 2, 3), -1, np.int32)
     got = check_attention(gpu, rng, [300, 300], [2, 2], 4, 2, dim, 16, 3, chosen=none, cache=(cache, table))
     assert not got.any()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_lists_longer_than_their_sequence(gpu, dim):
+    """Pages listed many times: the last split of a list takes what is left of it."""
+    rng = np.random.default_rng(dim + 5)
+    chosen = rng.integers(-2, 40, (3, 2, 200)).astype(np.int32)
+    chosen[1, 0, 30:] = -1
+    check_attention(gpu, rng, [600, 40], [2, 1], 6, 2, dim, 16, 200, chosen=chosen)
 
 
 @pytest.mark.parametrize("dim,rotary,interleaved", [
