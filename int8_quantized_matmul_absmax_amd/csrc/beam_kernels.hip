@@ -11,6 +11,7 @@
 // exponentials are 32-bit within a lane and 64-bit from there on.
 
 #include <algorithm>
+#include <type_traits>
 
 #include "device_common.h"
 #include "launchers.h"
@@ -24,6 +25,7 @@ constexpr int kVectors = 4;   // 16-byte loads a lane takes at once
 // log2(e) to 24 bits, and what it is off by relative to itself.
 constexpr float kLog2E = 1.44269504088896340736f;
 constexpr double kLn2 = 0.693147180559945309417;
+constexpr float kLeastWord = -3.402823466e38f;   // of fp32
 constexpr double kOff = (double)kLog2E * kLn2 - 1.0;
 
 // 16 bytes of a row, which begins at any element.
@@ -38,33 +40,6 @@ __device__ __forceinline__ uint32_t from_lane_below(uint32_t x) {
 __device__ __forceinline__ float lane_float(float x, int lane) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
 }
-
-// The best of a row's piece, over the lanes of a wave: lane j holds the j-th.
-// Equal values stand in the order of their index. Empty places hold -infinity and
-// index 0, which nothing that is a candidate (more than -infinity) comes after.
-struct Best {
-  float v = -INFINITY;
-  uint32_t i = 0;
-  float last_v = -INFINITY;   // of place count - 1: what a candidate has to beat
-  uint32_t last_i = 0;
-  __device__ __forceinline__ bool takes(float x, uint32_t at) const {
-    return x > last_v || (x == last_v && at < last_i);
-  }
-  // (of words from i0 on, which may be before the piece's first: -infinity is none)
-  __device__ __forceinline__ bool may_take(float x, int i0) const {
-    return x > last_v || (x == last_v && i0 < (int)last_i && x > -INFINITY);
-  }
-  // (uniform x and at that the list takes)
-  __device__ __forceinline__ void insert(float x, uint32_t at, int lane, int count) {
-    const int place = __popcll(__ballot(v > x || (v == x && i < at)));
-    const float up = __builtin_bit_cast(float, from_lane_below(__builtin_bit_cast(uint32_t, v)));
-    const uint32_t up_i = from_lane_below(i);
-    v = lane < place ? v : lane == place ? x : up;
-    i = lane < place ? i : lane == place ? at : up_i;
-    last_v = lane_float(v, count - 1);
-    last_i = (uint32_t)__builtin_amdgcn_readlane((int)i, count - 1);
-  }
-};
 
 // What a piece leaves: its base and its sum (the logits' exponentials add up to sum
 // times 2^base for fp16, e^base for fp32), then `count` values and as many indices, best first.
@@ -90,43 +65,91 @@ __device__ __forceinline__ float of_order(uint32_t k) {
   return __builtin_bit_cast(float, k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
+// A word's key: its value, then its index, lower ones first. Keys are unique; kNoKey is
+// not less than that of a word of -infinity.
+__device__ __forceinline__ uint64_t key_of(float x, int i) {
+  return (uint64_t)order_of(x) << 32 | (uint32_t)~i;
+}
+constexpr uint64_t kNoKey = 0x007fffffffffffffull;
+__device__ __forceinline__ int lanes_before(uint64_t mask) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
+                                   __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+}
+
+// A wave's words that may be among the piece's best, in any order, in LDS. When there is
+// no room for more they become their `count` best, and what a word has to beat the least
+// of those.
+constexpr int kHold = 256;
+struct Hold {
+  uint64_t* key;
+  int n = 0;
+  uint64_t least = kNoKey;
+  __device__ __forceinline__ void shrink(int count, int lane) {
+    uint64_t k[kHold / kWave];
+#pragma unroll
+    for (int j = 0; j < kHold / kWave; ++j)
+      k[j] = j * kWave + lane < n ? key[j * kWave + lane] : 0;
+    // the key of place `count`, bit by bit: of the values, then, of more words of the last
+    // value than there are places, of the indices (below 2^17: a piece's)
+    auto reach = [&](uint64_t least) __attribute__((always_inline)) {
+      int n = 0;
+#pragma unroll
+      for (int j = 0; j < kHold / kWave; ++j) n += __popcll(__ballot(k[j] >= least));
+      return n;
+    };
+    uint64_t t = 0;
+#pragma unroll 1
+    for (uint64_t bit = 1ull << 63; bit > 0xffffffffull; bit >>= 1)
+      if (reach(t | bit) >= count) t |= bit;
+    if (reach(t) > count) {
+      t |= 0xfffe0000u;
+#pragma unroll 1
+      for (uint64_t bit = 0x10000; bit; bit >>= 1)
+        if (reach(t | bit) >= count) t |= bit;
+    }
+    least = t;
+    n = 0;
+#pragma unroll
+    for (int j = 0; j < kHold / kWave; ++j) {
+      const uint64_t those = __ballot(k[j] >= t);
+      if (k[j] >= t) key[n + lanes_before(those)] = k[j];
+      n += __popcll(those);
+    }
+  }
+  // (the wave together; `some`: of lanes that have one)
+  __device__ __forceinline__ void add(bool some, uint64_t k, int count, int lane) {
+    uint64_t those = __ballot(some && k > least);
+    if (n + __popcll(those) > kHold) {
+      shrink(count, lane);
+      those = __ballot(some && k > least);
+    }
+    if (some && k > least) key[n + lanes_before(those)] = k;
+    n += __popcll(those);
+  }
+};
+
 // 2^d, or e^d of a base in the logits' own units.
 __device__ __forceinline__ float power_of(float d, bool natural) {
   return __builtin_amdgcn_exp2f(natural ? d * kLog2E : d);
 }
 
-// A value that at least `count` of the block's x reach (-infinity where fewer are
-// more than that), within 2^-7 of the largest such: the order of floats, its upper 16
-// bits searched bit by bit. One barrier.
-__device__ __forceinline__ float reached_by(float x, int count, float* s_x) {
-  s_x[threadIdx.x] = x;
-  lds_only_barrier();
-  uint32_t key[kWaves];
+// A value that `count` of kN x of each lane reach (-infinity where fewer are more than
+// that), within 2^-7 of the largest such: the order of floats, its upper 16 bits searched
+// bit by bit.
+template <int kN>
+__device__ __forceinline__ float reached_by(const float (&x)[kN], int count) {
+  uint32_t key[kN];
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) key[w] = order_of(s_x[w * kWave + (threadIdx.x & 63)]) >> 16;
+  for (int w = 0; w < kN; ++w) key[w] = order_of(x[w]) >> 16;
   uint32_t t = 0;
 #pragma unroll
   for (uint32_t bit = 0x8000u; bit; bit >>= 1) {
     int n = 0;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) n += __popcll(__ballot(key[w] >= (t | bit)));
+    for (int w = 0; w < kN; ++w) n += __popcll(__ballot(key[w] >= (t | bit)));
     if (n >= count) t |= bit;
   }
   return t <= 0x007fu ? -INFINITY : of_order(t << 16);
-}
-
-// A value that `count` of the block's words reach: the last place of any wave's list,
-// or a `count`-th of each: the least of the waves' values at place count / kWaves. What
-// a wave reads may be older than what others have written since: floors only rise.
-__device__ __forceinline__ float shared_floor(const volatile float* s_last,
-                                              const volatile float* s_share) {
-  float any = s_last[0], all = s_share[0];
-#pragma unroll
-  for (int w = 1; w < kWaves; ++w) {
-    any = fmaxf(any, s_last[w]);
-    all = fminf(all, s_share[w]);
-  }
-  return fmaxf(any, all);
 }
 
 // A lane's 16 bytes of a row, and their greatest element.
@@ -139,6 +162,16 @@ struct Words {
       return h2f(((uint32_t)raw[e >> 1] >> (16 * (e & 1))) & 0xffffu);
     else
       return __builtin_bit_cast(float, (uint32_t)raw[e]);
+  }
+  // (a lane's own e)
+  __device__ __forceinline__ float pick(int e) const {
+    const int w = kHalf ? e >> 1 : e;
+    const uint32_t lo = (uint32_t)(w & 1 ? raw[1] : raw[0]), hi = (uint32_t)(w & 1 ? raw[3] : raw[2]);
+    const uint32_t x = w & 2 ? hi : lo;
+    if constexpr (kHalf)
+      return h2f((x >> (16 * (e & 1))) & 0xffffu);
+    else
+      return __builtin_bit_cast(float, x);
   }
   __device__ __forceinline__ float most() const {
     if constexpr (kHalf) {
@@ -206,17 +239,17 @@ struct Words {
 // x under the softmax; the join takes kOff times the maximum off instead. Of fp32
 // logits, whose product with L may overflow, (x - b) L with b the maximum itself.
 //
-// What costs most beside them is the list: an insertion and the search for what to
-// insert, about 100 instructions where 64 words cost 7. So the block's first 16 KB
-// set a floor, what `count` of its lanes' maxima reach, and later its waves' lists set
-// one together: little is inserted that is not among the block's best.
+// The best words are held unsorted until the end. What keeps them few is a floor, a value
+// that `count` of the block's words reach: the block's first 16 KB set one, what `count`
+// of its lanes' maxima reach; later it is the least of what a wave's share of `count` of
+// its lanes' maxima reach, over the waves. (XX)
 template <bool kHalf, bool kFew>
 __global__ __launch_bounds__(kBlockThreads) void k_beam_rows(BeamArgs a, int pieces, int piece) {
   typedef Words<kHalf> W;
   constexpr int kV = W::kV, kStep = kVectors * kWave * kV;
-  __shared__ float s_x[kBlockThreads], s_b[kWaves], s_l[kWaves];
-  __shared__ uint64_t s_key[kWaves * kWave];
-  __shared__ float s_last[kWaves], s_share[kWaves];
+  __shared__ float s_x[kBlockThreads], s_b[kWaves], s_l[kWaves], s_share[kWaves];
+  __shared__ uint64_t s_key[kWaves][kHold];
+  __shared__ int s_n[kWaves];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row = blockIdx.x / pieces, at_piece = blockIdx.x % pieces;
   if (a.live && a.live[row] == 0) return;   // the join reads nothing of it
@@ -224,13 +257,13 @@ __global__ __launch_bounds__(kBlockThreads) void k_beam_rows(BeamArgs a, int pie
   const int n = (int)min((int64_t)piece, a.vocab - begin);
   const int8_t* const words =
       static_cast<const int8_t*>(a.logits) + (row * a.row_stride + begin) * (kHalf ? 2 : 4);
-  if (threadIdx.x < kWaves) s_last[threadIdx.x] = s_share[threadIdx.x] = -INFINITY;
-  // (reached_by's barrier comes before their use)
+  if (threadIdx.x < kWaves) s_share[threadIdx.x] = -INFINITY;
 
-  Best best;
+  Hold hold;
+  hold.key = s_key[wave];
   float b = 0.f, l = 0.f;   // of the lane: l 2^b
   bool any = false;
-  float floor = -INFINITY;
+  float floor = -INFINITY, top_so_far = -INFINITY;
   W x[kVectors], ahead[kVectors];
   // (before the piece's first word for a short piece, never before the row's)
   auto first = [&](int at, int u) __attribute__((always_inline)) {
@@ -257,8 +290,24 @@ __global__ __launch_bounds__(kBlockThreads) void k_beam_rows(BeamArgs a, int pie
 #pragma unroll
     for (int u = 0; u < kVectors; ++u) top[u] = x[u].most();
     const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-    if (start) floor = reached_by(most, a.count, s_x);
-    else floor = fmaxf(floor, shared_floor(s_last, s_share));
+    top_so_far = fmaxf(top_so_far, most);
+    if (start) {
+      s_x[threadIdx.x] = most;
+      lds_only_barrier();
+      float all[kWaves];
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) all[w] = s_x[w * kWave + lane];
+      floor = fmaxf(reached_by(all, a.count), kLeastWord);
+    } else {
+      // (what a wave reads may be older than what others have written since: they only
+      // rise. Not volatile: that is a load which waits for the logits in flight, too.)
+      float least = INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w)
+        least = fminf(least, __hip_atomic_load(&s_share[w], __ATOMIC_RELAXED,
+                                               __HIP_MEMORY_SCOPE_WORKGROUP));
+      floor = fmaxf(floor, least);
+    }
 
     // A NaN or +infinity makes the sum NaN, and the row one without candidates.
     const float next = kHalf ? most * kLog2E : most;
@@ -280,42 +329,23 @@ __global__ __launch_bounds__(kBlockThreads) void k_beam_rows(BeamArgs a, int pie
     const auto index = [&](int u) __attribute__((always_inline)) {
       return kFew ? 0 : first(at, u);
     };
-    if (__any(most >= floor && best.may_take(most, index(0)))) {
+    if (__any(most >= floor)) {
 #pragma unroll
       for (int u = 0; u < kVectors; ++u) {
-        // lanes' best words, then their next ones, while they are taken
-        const int i0 = index(u);
-        float most = top[u];
-        uint64_t those = __ballot(most >= floor && best.may_take(most, i0));
-        if (!those) continue;
-        float y[kV];
+        if (!__any(top[u] >= floor)) continue;
+        uint32_t those = 0;   // of the lane's words, a bit each
 #pragma unroll
-        for (int e = 0; e < kV; ++e) y[e] = x[u].at(e);
-        for (int round = 0; round < kV && those; ++round) {
-          int at_most = 0;
-#pragma unroll
-          for (int e = kV - 1; e > 0; --e) at_most = y[e] == most ? e : at_most;
-          at_most = y[0] == most ? 0 : at_most;
-          do {
-            const int from = __builtin_ctzll(those);
-            those &= those - 1;
-            const float v = lane_float(most, from);
-            const uint32_t i = (uint32_t)__builtin_amdgcn_readlane(i0 + at_most, from);
-            if (best.takes(v, i)) best.insert(v, i, lane, a.count);
-          } while (those);
-          most = -INFINITY;
-#pragma unroll
-          for (int e = 0; e < kV; ++e) {
-            y[e] = e == at_most ? -INFINITY : y[e];
-            most = fmaxf(most, y[e]);
-          }
-          those = __ballot(most >= floor && best.may_take(most, i0));
+        for (int e = 0; e < kV; ++e) those |= x[u].at(e) >= floor ? 1u << e : 0u;
+        while (__any(those != 0)) {
+          const int e = those ? __builtin_ctz(those) : 0;
+          hold.add(those != 0, key_of(x[u].pick(e), index(u) + e), a.count, lane);
+          those &= those - 1;   // (of none, none)
         }
       }
-      if (lane == 0) {
-        s_last[wave] = best.last_v;
-        s_share[wave] = lane_float(best.v, (a.count + kWaves - 1) / kWaves - 1);
-      }
+      const float own[1] = {top_so_far};
+      const float reached = reached_by(own, (a.count + kWaves - 1) / kWaves);
+      if (lane == 0)
+        __hip_atomic_store(&s_share[wave], reached, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
     }
 #pragma unroll
     for (int u = 0; u < kVectors; ++u) x[u] = ahead[u];
@@ -333,28 +363,47 @@ __global__ __launch_bounds__(kBlockThreads) void k_beam_rows(BeamArgs a, int pie
     s_b[wave] = top;
     s_l[wave] = l;
   }
-  // keys: the greater the better, 0 in empty places
-  if (lane < a.count)
-    s_key[wave * a.count + lane] =
-        best.v > -INFINITY ? (uint64_t)order_of(best.v) << 32 | ~best.i : 0;
+  if (lane == 0) s_n[wave] = hold.n;
   __syncthreads();
+  if (s_n[0] + s_n[1] + s_n[2] + s_n[3] > kBlockThreads) {
+    // (count of each wave's are at most a block's threads)
+    __syncthreads();
+    if (hold.n > a.count) hold.shrink(a.count, lane);
+    if (lane == 0) s_n[wave] = hold.n;
+    __syncthreads();
+  }
   const Pieces out = pieces_of(a.ws, (int64_t)a.batch * a.beams, pieces, a.count);
   const int64_t part = (int64_t)row * pieces + at_piece;
   // An entry's place is the number of entries before it; lanes share an entry.
-  const int entries = kWaves * a.count;
-  int lanes = 1;
-  while (2 * lanes * entries <= kBlockThreads) lanes *= 2;
-  const int entry = threadIdx.x / lanes;
-  int place = 0;
-  const uint64_t key = entry < entries ? s_key[entry] : 0;
-  for (int o = threadIdx.x % lanes; o < entries; o += lanes) {
-    const uint64_t other = s_key[o];
-    place += other > key || (other == key && o < entry);   // (empty places are equal)
+  int n_of[kWaves], entries = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    n_of[w] = __builtin_amdgcn_readfirstlane(s_n[w]);
+    entries += n_of[w];
   }
+  int lanes = 1;
+  while (2 * lanes * entries <= kBlockThreads && lanes < kWave) lanes *= 2;
+  int of_wave = 0, entry = threadIdx.x / lanes;
+  const bool some = entry < entries;
+#pragma unroll
+  for (int w = 0; w < kWaves - 1; ++w)
+    if (of_wave == w && entry >= n_of[w]) {
+      entry -= n_of[w];
+      ++of_wave;
+    }
+  const uint64_t key = some ? s_key[of_wave][entry] : 0;
+  int place = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w)
+    for (int o = threadIdx.x % lanes; o < n_of[w]; o += lanes) place += s_key[w][o] > key;
   for (int d = 1; d < lanes; d <<= 1) place += __shfl_xor(place, d, kWave);
-  if (entry < entries && threadIdx.x % lanes == 0 && place < a.count) {
-    out.value[part * a.count + place] = key ? of_order((uint32_t)(key >> 32)) : -INFINITY;
-    out.index[part * a.count + place] = key ? ~(uint32_t)key + (uint32_t)begin : 0;
+  if (some && threadIdx.x % lanes == 0 && place < a.count) {
+    out.value[part * a.count + place] = of_order((uint32_t)(key >> 32));
+    out.index[part * a.count + place] = ~(uint32_t)key + (uint32_t)begin;
+  }
+  for (int j = entries + threadIdx.x; j < a.count; j += kBlockThreads) {
+    out.value[part * a.count + j] = -INFINITY;
+    out.index[part * a.count + j] = 0;
   }
   if (threadIdx.x == 0) {
     float t = s_b[0], sum = 0.f;
@@ -392,17 +441,35 @@ __device__ __forceinline__ bool before(double v, int64_t at, double w, int64_t b
   return v > w || (v == w && at < bt);
 }
 
+// The upper bits of a value's order, and the least value that has them.
+constexpr int kHeadBits = 24;
+__device__ __forceinline__ uint32_t head_of(double x) {
+  const uint32_t b = (uint32_t)(__builtin_bit_cast(uint64_t, x) >> 32);
+  return (b ^ ((uint32_t)((int)b >> 31) | 0x80000000u)) >> (32 - kHeadBits);
+}
+__device__ __forceinline__ double of_head(uint32_t k) {
+  const uint32_t o = k << (32 - kHeadBits);
+  const bool positive = o & 0x80000000u;
+  const uint32_t high = positive ? o ^ 0x80000000u : ~o, low = positive ? 0u : 0xffffffffu;
+  return __builtin_bit_cast(double, (uint64_t)high << 32 | low);
+}
+
 // One block a search.
 //
 // A beam's base, what its logits are added to: its score less the logarithm, of which
 // the integer part and the 24-bit logarithm of the rest are put together in 64 bits.
 // A candidate's place is the number of candidates before it, counted over all pairs of
 // up to kJoinEntries; more of them first become the lists of the block's waves.
+// (Fewer than kJoinFew are counted at once: 4 beams of 4 pieces' 4 10.5 us in all, with a
+// bound for them first 11.8; 13 pieces' 16 17.9 and 17.2.)
 constexpr int kJoinFew = 64;
+constexpr int kJoinMany = 128;
+constexpr int kJoinAhead = 4;   // candidates of a thread in flight
 constexpr int kJoinThreads = 1024, kJoinWaves = kJoinThreads / kWave;
 constexpr int kJoinEntries = kJoinWaves * I8MM_MAX_BEAM_COUNT;
 __global__ __launch_bounds__(kJoinThreads) void k_beam_join(BeamArgs a, int pieces) {
-  extern __shared__ double s_base[];   // [beams]
+  extern __shared__ double s_base[];   // [beams], then whether they have ended
+  int* const s_ended = reinterpret_cast<int*>(s_base + a.beams);
   __shared__ double s_v[kJoinEntries];
   __shared__ int64_t s_at[kJoinEntries];
   __shared__ int s_count;
@@ -435,7 +502,10 @@ __global__ __launch_bounds__(kJoinThreads) void k_beam_join(BeamArgs a, int piec
       base -= a.fp32 ? (double)all : (double)all * (kLn2 - kLn2 * kOff);
       if (!(total > 0.0) || !(total < 1e300)) base = no_value();
     }
-    if (lane == 0) s_base[i] = base;
+    if (lane == 0) {
+      s_base[i] = base;
+      s_ended[i] = ended;
+    }
   }
   __syncthreads();
 
@@ -443,25 +513,25 @@ __global__ __launch_bounds__(kJoinThreads) void k_beam_join(BeamArgs a, int piec
   // (no words: a beam that has ended still has its one candidate)
   const int per_beam = max(pieces * a.count, 1), all = a.beams * per_beam;
   const int64_t words = max(a.vocab, (int64_t)1);
+  // (loaded whether it is one or not, so that several can be in flight)
+  const int64_t first = (int64_t)b * all;
   auto candidate = [&](int e, double* v, int64_t* at) __attribute__((always_inline)) {
-    *v = none;
-    *at = 0;
-    const int i = e / per_beam, k = e % per_beam;
-    if (e >= all || !(s_base[i] > none)) return;
-    const int64_t row = (int64_t)b * a.beams + i;
-    if (a.live && a.live[row] == 0) {
-      if (k > 0) return;
-      *v = s_base[i];
-      *at = i * words + max(a.eos, 0);
-    } else {
-      const double x = s_base[i] + (double)in.value[row * per_beam + k];
-      if (!(x > none)) return;   // (an empty place)
-      *v = x;
-      *at = i * words + in.index[row * per_beam + k];
-    }
+    const int c = min(e, all - 1), i = c / per_beam;
+    const double base = s_base[i];
+    const bool ended = s_ended[i];
+    const float x = pieces > 0 ? in.value[first + c] : 0.f;
+    const int word = pieces > 0 ? (int)in.index[first + c] : 0;
+    const double own = c == i * per_beam ? base : none;
+    const double sum = ended ? own : base + (double)x;
+    const bool some = e < all && sum > none;   // (not of an empty place, or a row without candidates)
+    *v = some ? sum : none;
+    *at = some ? i * words + (ended ? max(a.eos, 0) : word) : 0;
   };
   // Of more than kJoinFew, only those are counted that reach the last place of the list
-  // with the best one: that list alone has `count` of them.
+  // with the best one: that list alone has `count` of them. If they are still more than
+  // kJoinMany, as of many lists that are alike, only those that reach what `count` of 64
+  // groups' best reach (groups of a lane of each wave, another one in each: a list's best
+  // stand in neighbouring lanes).
   double least = none;
   if (all > kJoinFew) {
     const int lists = pieces > 0 ? a.beams * pieces : 0;
@@ -483,21 +553,53 @@ __global__ __launch_bounds__(kJoinThreads) void k_beam_join(BeamArgs a, int piec
 #pragma unroll
     for (int w = 1; w < kJoinWaves; ++w) least = s_v[w] > least ? s_v[w] : least;
     __syncthreads();
-    for (int e0 = 0; e0 < all; e0 += kJoinThreads) {
-      double v;
-      int64_t at;
-      candidate(e0 + threadIdx.x, &v, &at);
-      const bool some = v > none && v >= least;
-      const uint64_t those = __ballot(some);
-      int to = 0;
-      if (lane == 0 && those) to = atomicAdd(&s_count, __popcll(those));
-      to = __builtin_amdgcn_readfirstlane(to) + __popcll(those & ((1ull << lane) - 1));
-      if (some && to < kJoinEntries) {
-        s_v[to] = v;
-        s_at[to] = at;
+    double mine = none;   // the best of the thread's
+    auto sweep = [&](auto ahead) __attribute__((always_inline)) {
+      constexpr int kN = decltype(ahead)::value;
+      for (int e0 = 0; e0 < all; e0 += kN * kJoinThreads) {
+        double v[kN];
+        int64_t at[kN];
+#pragma unroll
+        for (int u = 0; u < kN; ++u)
+          candidate(e0 + u * kJoinThreads + threadIdx.x, &v[u], &at[u]);
+#pragma unroll
+        for (int u = 0; u < kN; ++u) {
+          mine = v[u] > mine ? v[u] : mine;
+          const bool some = v[u] > none && v[u] >= least;
+          const uint64_t those = __ballot(some);
+          if (!those) continue;
+          int to = 0;
+          if (lane == 0) to = atomicAdd(&s_count, __popcll(those));
+          to = __builtin_amdgcn_readfirstlane(to) + lanes_before(those);
+          if (some && to < kJoinEntries) {
+            s_v[to] = v[u];
+            s_at[to] = at[u];
+          }
+        }
       }
+    };
+    for (int round = 0;; ++round) {
+      if (all <= kJoinThreads)
+        sweep(std::integral_constant<int, 1>());
+      else
+        sweep(std::integral_constant<int, kJoinAhead>());
+      __syncthreads();
+      if (round == 1 || s_count <= kJoinMany) break;
+      uint32_t* const s_head = reinterpret_cast<uint32_t*>(s_v);
+      __syncthreads();
+      s_head[threadIdx.x] = head_of(mine);
+      if (threadIdx.x == 0) s_count = 0;
+      __syncthreads();
+      uint32_t head = 0, t = 0;
+#pragma unroll
+      for (int w = 0; w < kJoinWaves; ++w) head = max(head, s_head[w * kWave + ((lane + 5 * w) & 63)]);
+#pragma unroll 1
+      for (uint32_t bit = 1u << (kHeadBits - 1); bit; bit >>= 1)
+        if (__popcll(__ballot(head >= (t | bit))) >= a.count) t |= bit;
+      const double reached = of_head(t);   // (a NaN if fewer groups have one)
+      least = reached > least ? reached : least;
+      __syncthreads();
     }
-    __syncthreads();
   }
   int entries = all > kJoinFew ? s_count : all;
   if (all <= kJoinFew) {
@@ -612,7 +714,7 @@ hipError_t launch_beam_select(const BeamArgs& a, hipStream_t s) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  k_beam_join<<<(uint32_t)a.batch, kJoinThreads, a.beams * sizeof(double), s>>>(a, p.pieces);
+  k_beam_join<<<(uint32_t)a.batch, kJoinThreads, a.beams * 12, s>>>(a, p.pieces);
   return hipGetLastError();
 }
 
