@@ -121,6 +121,22 @@ def test_sorted_rows(gpu, order):
     check(gpu, y, np.zeros((1, 1), np.float32), None, eos=-1, count=30)
 
 
+@pytest.mark.parametrize("half", [True, False])
+@pytest.mark.parametrize("count", [1, 64])
+def test_long_pieces_of_many_good_words(gpu, half, count):
+    """So many rows that a piece is all of one, of words that reach what has been seen
+    before them: ascending, equal, of a few values; and the least that fp32 holds."""
+    rng = np.random.default_rng(count)
+    kinds = np.stack([np.linspace(-8, 8, 20001), np.linspace(8, -8, 20001), np.full(20001, -3.0),
+                      rng.integers(0, 3, 20001), np.arange(20001) // 2500])
+    if not half:
+        kinds[2] = np.finfo(np.float32).min
+        kinds[2, 50] = -np.inf
+    x = np.tile(kinds.astype(np.float16 if half else np.float32), (210, 1)).reshape(1050, 1, -1)
+    scores = (-6 * rng.random((1050, 1))).astype(np.float32)
+    check(gpu, x, scores, None, eos=-1, count=count)
+
+
 def test_no_beams_no_words(gpu):
     """Searches of no beams or no words: ended beams alone, or nothing."""
     for half in (np.float16, np.float32):
