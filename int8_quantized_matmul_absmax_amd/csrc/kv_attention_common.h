@@ -494,11 +494,12 @@ __global__ __launch_bounds__(kBlockThreads) void k_kv_attn_join(float* ws, int64
   }
 }
 
-// The join of a launch's splits, if there are any.
+// The join of a launch's splits, if there are any; up to `few` by several rows a block.
 template <int D>
-hipError_t launch_join(float* part, int64_t rows, int splits, uint16_t* out, hipStream_t s) {
+hipError_t launch_join(float* part, int64_t rows, int splits, uint16_t* out, hipStream_t s,
+                       int few = kFewSplits) {
   if (splits <= 1) return hipSuccess;
-  if (splits <= kFewSplits) {
+  if (splits <= few) {
     constexpr int kBlockRows = kBlockThreads / kWave * (kWave / (D / 4));
     if (rows > (int64_t)INT32_MAX * kBlockRows) return hipErrorInvalidValue;
     k_kv_attn_join_few<D><<<(uint32_t)((rows + kBlockRows - 1) / kBlockRows), kBlockThreads, 0, s>>>(

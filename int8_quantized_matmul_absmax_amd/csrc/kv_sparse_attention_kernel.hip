@@ -25,7 +25,7 @@ __device__ __forceinline__ int entries_of(const int32_t* list, int count, int se
 // ---- Few tokens: a block takes up to 16 rows, its four waves share a list, and a list
 // may be split. 64 tokens with lists of 64 pages of 16 tokens, 64 heads on 8 of 128
 // features (131 MB): 25.8 us, 5.1 TB/s; one token, 16 pages of 128 tokens, 32 heads on
-// 8: 7.6 us and 4.2 to join.
+// 8: 7.8 us and 3.6 to join.
 template <int D>
 __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_pages(
     KvArgs a, RotaryArgs rot, AttnArgs t, const int32_t* chosen, int count, int group, int tiles,
@@ -482,6 +482,10 @@ struct Plan {
 Plan plan(const KvArgs& a, int q_heads, int count) {
   constexpr int64_t kMinChunk = 4 * kGroup, kMaxChunk = 2048, kMaxSplits = 1024;
   const int64_t resident = (a.head_dim <= 128 ? 2 : 1) * 256;
+  // Up to two chunks are not worth a join of up to 128 features: 32 rows of 512 tokens of
+  // 128 features 8.8 us and 9.6 in two splits, 768 tokens 10.3 and 9.9 in three; of 256
+  // features 512 tokens 12.2 and 11.7.
+  const int64_t kWhole = a.head_dim <= 128 ? 2 * kMinChunk : kMinChunk;
   Plan p;
   p.group = q_heads / a.kv_heads;
   p.tiles = (p.group + kRows - 1) / kRows;
@@ -500,8 +504,12 @@ Plan plan(const KvArgs& a, int q_heads, int count) {
   // (with blocks for two rounds there is nothing to fill, and sums to join would take
   // room for every one of their rows)
   int64_t chunk = tokens;
-  if (blocks < 2 * resident)
-    chunk = std::min<int64_t>(std::max(tokens * blocks / resident, kMinChunk), kMaxChunk);
+  if (blocks < 2 * resident && tokens > kWhole) {
+    // (no more splits than are resident at once: 96 blocks of 4096 tokens in six splits
+    // 29.5 us, in five 25.6; of 256 features 40 of 4096 in seven 32.0, in six 25.0)
+    const int64_t splits = std::max<int64_t>(resident / std::max<int64_t>(blocks, 1), 1);
+    chunk = std::min(std::max((tokens + splits - 1) / splits, kMinChunk), kMaxChunk);
+  }
   chunk = std::max(chunk, tokens / kMaxSplits + 1);
   chunk = (chunk + kGroup - 1) / kGroup * kGroup;
   p.chunk = (int)chunk;
@@ -526,7 +534,10 @@ hipError_t launch_d(const KvArgs& a, const RotaryArgs& r, const AttnArgs& t, con
                                                                 p.splits, p.chunk);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  return launch_join<D>(t.part, (int64_t)a.total_tokens * t.q_heads, p.splits, t.out, s);
+  // (of few rows a block each is faster from five splits on: 32 rows of 8 splits 11.6 us
+  // and 10.4, of 16 14.7 and 10.9, 512 of 16 13.3 and 11.9, 1024 of 8 21.9 and 22.0)
+  const int64_t rows = (int64_t)a.total_tokens * t.q_heads;
+  return launch_join<D>(t.part, rows, p.splits, t.out, s, rows < 1024 ? 4 : kFewSplits);
 }
 
 }  // namespace

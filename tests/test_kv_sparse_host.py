@@ -105,6 +105,14 @@ def test_nothing_to_do_needs_no_device(lib):
     assert call_attention(lib, cache(), batch(**none), q=None, pages=None, out=None, ws=None, wn=0) == 0
 
 
+def test_no_tokens_of_long_sequences(lib):
+    """Nothing to split, however long the lists are."""
+    for tokens in (0, 2):
+        b = batch(num_seqs=tokens, total_tokens=tokens, cu_tokens=None, max_pages=5000, max_len=320000)
+        need = lib.int8_kv_cache_attention_pages_workspace_bytes(cache(num_pages=9000), b, 4, 4000)
+        assert (need > 0) == (tokens > 0)
+
+
 def test_binding_refusals():
     class Cache:
         device, k_means, kv_heads, head_dim, ref = torch.device("cpu"), None, 2, 64, None
