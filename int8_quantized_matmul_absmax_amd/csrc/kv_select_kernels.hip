@@ -56,7 +56,8 @@ __device__ __forceinline__ double spread_sums(double* x, int lane) {
 // Mean keys: one wave a page, head and 64 features (four tiles). Lane (t, c) of 16 x 4
 // takes token t of each block and the 16 features of its tile; sums are 64-bit, a code's
 // product with its block's 32-bit step exact in them. Eight blocks are loaded at once:
-// with few pages to do, what counts is how often a wave waits.
+// with few pages to do, what counts is how often a wave waits (one page of 128 tokens of 8
+// heads of 128 features 5.5 us, 64 pages of 16 5.2).
 template <int D>
 __global__ __launch_bounds__(kBlockThreads) void k_kv_page_means(KvArgs a, uint16_t* means, int tasks) {
   constexpr int kParts = (D + 63) / 64, kBlocks = 8;
@@ -127,7 +128,9 @@ __device__ __forceinline__ uint64_t score_key(double x) {
 //
 // A page's mean is taken by kLanes lanes, eight features each. What a block waits for
 // is kept to a few times: a group of lanes loads as many entries of the page table at
-// once, then the means of kAhead pages; kBatch pages' sums are made together.
+// once, then the means of kAhead pages; kBatch pages' sums are made together. One token
+// over 1024 pages, 8 heads of 128 features: 12.9 us, of which the scores 6 (64-bit sums
+// of eight blocks) and the rest waits; 64 tokens over up to 512 pages 15.1.
 template <int D, int kThreads>
 __global__ __launch_bounds__(kThreads) void k_kv_select_pages(KvArgs a, RotaryArgs rot,
                                                               const uint16_t* q, int64_t q_ts,
