@@ -187,6 +187,14 @@ def test_alignment_and_strides(gpu, half, shift):
     check(gpu, view, scores, live, count=9)
 
 
+def test_rows_beyond_32_bit_offsets(gpu):
+    """Rows more than 2^31 bytes apart."""
+    x, scores, live = inputs(31, 1, 3, 5000, dead=False)
+    wide = torch.empty((1, 3, (1 << 30) + 5000), dtype=torch.float16, device="cuda")[:, :, :5000]
+    wide.copy_(dev(x))
+    check(gpu, wide, scores, live, count=6)
+
+
 def test_workspace_contents_do_not_matter(gpu):
     x, scores, live = inputs(21, 2, 3, 40000)
     need = gpu.load_library().i8mm_beam_select_workspace_bytes(0, 2, 3, 40000, 6)

@@ -331,6 +331,29 @@ def test_every_page_equals_the_dense_attention(gpu):
     assert (np.abs(got - dense) <= 2 * bound).all()
 
 
+def test_beyond_32_bit_offsets(gpu):
+    """Pages past 2^31 bytes of codes: as the same pages at the front of a small cache."""
+    rng = np.random.default_rng(77)
+    pages, n, dim, kv, page = 34000, 12, 128, 8, 64
+    small = gpu.Int8KVCache(n, kv, dim, page, page_means=True)
+    big = gpu.Int8KVCache(pages, kv, dim, page, page_means=True)
+    order = rng.permutation(n)
+    table = torch.from_numpy(order.reshape(1, n).astype(np.int32)).cuda()
+    lens = torch.tensor([n * page - 5], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, n * page - 5], dtype=torch.int32, device="cuda")
+    k, v = (dev(rng.normal(0, 1, (n * page - 5, kv, dim)).astype(np.float16)) for _ in range(2))
+    q = dev(rng.normal(0, 1.5, (1, 4 * kv, dim)).astype(np.float16))
+    found = []
+    for cache, shift in ((small, 0), (big, pages - n)):
+        cache.append(k, v, gpu.KVBatch(table + shift, lens, cu, n * page - 5, n * page - 5))
+        one = gpu.KVBatch(table + shift, lens)
+        chosen = cache.select_pages(q, one, 5, first=1, recent=2)
+        found.append((cache.k_means[shift:shift + n].clone(), chosen, cache.attention_pages(q, chosen, one)))
+    for a, b in zip(*found):
+        assert torch.equal(a, b)
+    assert found[0][2].abs().sum() > 0
+
+
 def test_rows_of_no_sequence(gpu):
     """Rows past the last sequence, tokens beyond max_tokens and at negative
     positions: 0, and a choice of -1."""
