@@ -609,8 +609,9 @@ I8MM_API size_t int8_kv_cache_attention_pages_workspace_bytes(const i8mm_kv_cach
  *   parents     int32 [num_rows]: i8mm_beam_select's, for one.
  *   keep        int32 [num_rows] (negative: none), or NULL: all tokens.
  *   new_tokens  int32 [num_rows] (negative: none), or NULL: new_all each.
- *   out_table   int32 [num_rows, max_pages], out_lens int32 [num_rows]: what an
- *               i8mm_kv_batch takes, the new tokens included.
+ *   out_table   int32 [num_rows, max_pages], out_lens int32 [num_rows]: the new tokens
+ *               included, what an i8mm_kv_batch takes if all of them have room in their
+ *               rows (i8mm_kv_pages_step_batch tells).
  *   copies      int32 [num_rows][3]: page, the page to copy it to, tokens that
  *               count; rows in order, then rows of -1.
  *   counts      int32 [2]: copies; pages that were wanting.
@@ -631,7 +632,28 @@ I8MM_API int i8mm_kv_pages_step(const int32_t* page_table, const int32_t* seq_le
                                 int32_t* counts, void* workspace, size_t workspace_bytes,
                                 i8mm_stream_t stream);
 
-/* Bytes of workspace for i8mm_kv_pages_step and (num_rows its num_seqs)
+/*
+ * i8mm_kv_pages_step_batch: i8mm_kv_pages_step, and the lengths for the append after it.
+ * A row at the end of its table has no position for a new token, and an i8mm_kv_batch of
+ * out_lens would store that token over its last one, in a page that others may share.
+ *   max_len     the batches' (>= 0): lengths are cut to it where it is less than
+ *               max_pages * page_tokens.
+ *   batch_lens  int32 [num_rows]: out_lens, but 0 (a sequence that stores nothing and
+ *               sees nothing) for a row that has no new tokens or no room for all of them
+ *               (of the latter's tokens only the k that it keeps are there).
+ *   full        int32 [1]: how many rows have no room for all of their new tokens.
+ * Errors: EINVAL, EALIGN, EWORKSPACE, ENODEVICE, ELAUNCH.
+ */
+I8MM_API int i8mm_kv_pages_step_batch(const int32_t* page_table, const int32_t* seq_lens,
+                                      int64_t num_seqs, int64_t max_pages, const int32_t* parents,
+                                      const int32_t* keep, const int32_t* new_tokens,
+                                      int64_t new_all, int64_t num_rows, int64_t num_pages,
+                                      int64_t page_tokens, int64_t max_len, int32_t* out_table,
+                                      int32_t* out_lens, int32_t* batch_lens, int32_t* full,
+                                      int32_t* copies, int32_t* counts, void* workspace,
+                                      size_t workspace_bytes, i8mm_stream_t stream);
+
+/* Bytes of workspace for i8mm_kv_pages_step (_batch) and (num_rows its num_seqs)
  * i8mm_kv_pages_compact; 0 also if the sizes are invalid. Host-only, pure. */
 I8MM_API size_t i8mm_kv_pages_workspace_bytes(int64_t num_rows, int64_t max_pages,
                                               int64_t num_pages);

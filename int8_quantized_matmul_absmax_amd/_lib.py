@@ -39,6 +39,7 @@ EXPORTS = (
     "int8_kv_cache_attention_pages",
     "int8_kv_cache_attention_pages_workspace_bytes",
     "i8mm_kv_pages_step",
+    "i8mm_kv_pages_step_batch",
     "i8mm_kv_pages_compact",
     "i8mm_kv_pages_workspace_bytes",
     "int8_kv_cache_copy_pages",
@@ -117,6 +118,8 @@ def _declare(lib):
         "int8_kv_cache_attention_pages_workspace_bytes": ([cache, batch, i64, i64], ctypes.c_size_t),
         "i8mm_kv_pages_step": ([vp, vp, i64, i64, vp, vp, vp, i64, i64, i64, i64, vp, vp, vp, vp, vp,
                                 ctypes.c_size_t, vp], i32),
+        "i8mm_kv_pages_step_batch": ([vp, vp, i64, i64, vp, vp, vp, i64, i64, i64, i64, i64, vp, vp, vp,
+                                      vp, vp, vp, vp, ctypes.c_size_t, vp], i32),
         "i8mm_kv_pages_compact": ([vp, vp, i64, i64, i64, i64, vp, vp, vp, vp, ctypes.c_size_t, vp],
                                   i32),
         "i8mm_kv_pages_workspace_bytes": ([i64, i64, i64], ctypes.c_size_t),

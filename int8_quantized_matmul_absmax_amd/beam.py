@@ -25,11 +25,14 @@ from .linear import shared_workspace
 class BeamSearch:
     """pool and caches: the pages and the layers' caches that page_table (one row a
     search, its prompt's) is for. eos: the word that ends a beam, None if none does.
-    max_len: a bound on the sequences' lengths for KVBatch.
+    max_len: a bound on the sequences' lengths for KVBatch (None: the table's width).
 
     page_table, seq_lens, scores, live: of the rows as they stand, ended beams
     included; batch: the KVBatch of the tokens that the last step chose; wanting: int32
-    on the GPU, how many pages it found no room for (their tokens are absent)."""
+    on the GPU, how many pages it found no room for (their tokens are absent); full:
+    int32 on the GPU, how many beams had no room for their token in the table or below
+    max_len. Such a beam keeps its tokens, but the new one is not stored and sees
+    nothing: a search ends where full is not 0."""
 
     def __init__(self, pool, caches, page_table, seq_lens, beams, eos=None, max_len=None):
         searches = page_table.shape[0]
@@ -42,7 +45,7 @@ class BeamSearch:
         self.page_table, self.seq_lens = page_table, seq_lens
         self.scores = torch.zeros((searches, 1), dtype=torch.float32, device=page_table.device)
         self.live = torch.ones((searches, 1), dtype=torch.int32, device=page_table.device)
-        self.batch = self.wanting = None
+        self.batch = self.wanting = self.full = None
         self._history = []
 
     def step(self, logits):
@@ -52,13 +55,12 @@ class BeamSearch:
         self.scores, tokens, parents, self.live = ops.beam_select(
             logits, self.scores, self.live, self.eos, self.beams, shared_workspace)
         self.page_table, self.seq_lens, copies = self.pool.step(
-            self.page_table, self.seq_lens, parents, new_tokens=self.live)
+            self.page_table, self.seq_lens, parents, new_tokens=self.live, max_len=self.max_len)
         for c in self.caches:
             c.copy_pages(copies)
-        # a beam that has ended has no new token: a sequence of length 0 stores nothing
-        self.batch = KVBatch(self.page_table, self.seq_lens * self.live.view(-1),
-                             max_len=self.max_len)
-        self.wanting = copies.counts[1]
+        # (a beam that has ended, or is full, has length 0 there: it stores nothing)
+        self.batch = KVBatch(self.page_table, copies.batch_lens, max_len=self.max_len)
+        self.wanting, self.full = copies.counts[1], copies.full[0]
         self._history.append((tokens, parents))
         return tokens
 

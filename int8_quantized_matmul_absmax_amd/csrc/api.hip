@@ -847,17 +847,22 @@ size_t i8mm_kv_pages_workspace_bytes(int64_t num_rows, int64_t max_pages, int64_
   return i8mm::kv_pages_workspace_bytes(a, a.num_rows);
 }
 
-int i8mm_kv_pages_step(const int32_t* page_table, const int32_t* seq_lens, int64_t num_seqs,
-                       int64_t max_pages, const int32_t* parents, const int32_t* keep,
-                       const int32_t* new_tokens, int64_t new_all, int64_t num_rows,
-                       int64_t num_pages, int64_t page_tokens, int32_t* out_table,
-                       int32_t* out_lens, int32_t* copies, int32_t* counts, void* workspace,
-                       size_t workspace_bytes, i8mm_stream_t stream) {
-  const char* fn = "i8mm_kv_pages_step";
+}  // extern "C"
+
+namespace {
+
+// A step of the page tables; batch_lens and full are there or not together.
+int pages_step(const char* fn, const int32_t* page_table, const int32_t* seq_lens, int64_t num_seqs,
+               int64_t max_pages, const int32_t* parents, const int32_t* keep,
+               const int32_t* new_tokens, int64_t new_all, int64_t num_rows, int64_t num_pages,
+               int64_t page_tokens, int64_t max_len, bool batch, int32_t* out_table,
+               int32_t* out_lens, int32_t* batch_lens, int32_t* full, int32_t* copies,
+               int32_t* counts, void* workspace, size_t workspace_bytes, i8mm_stream_t stream) {
   i8mm::PagesArgs a;
   I8MM_TRY(pages_sizes(fn, num_seqs, max_pages, num_rows, num_pages, page_tokens, &a));
   if (new_all < 0 || new_all > (1 << 30))
     return fail(I8MM_EINVAL, "%s: %lld new tokens", fn, (long long)new_all);
+  if (max_len < 0) return fail(I8MM_EINVAL, "%s: max_len=%lld", fn, (long long)max_len);
   I8MM_TRY(check_ints(fn, "page_table", page_table, num_seqs * max_pages > 0));
   I8MM_TRY(check_ints(fn, "seq_lens", seq_lens, num_seqs > 0));
   I8MM_TRY(check_ints(fn, "parents", parents, num_rows > 0));
@@ -865,12 +870,14 @@ int i8mm_kv_pages_step(const int32_t* page_table, const int32_t* seq_lens, int64
   I8MM_TRY(check_ints(fn, "new_tokens", new_tokens, false));
   I8MM_TRY(check_ints(fn, "out_table", out_table, num_rows * max_pages > 0));
   I8MM_TRY(check_ints(fn, "out_lens", out_lens, num_rows > 0));
+  I8MM_TRY(check_ints(fn, "batch_lens", batch_lens, batch && num_rows > 0));
+  I8MM_TRY(check_ints(fn, "full", full, batch));
   I8MM_TRY(check_ints(fn, "copies", copies, num_rows > 0));
   I8MM_TRY(check_ints(fn, "counts", counts, true));
   I8MM_TRY(check_scratch(fn, workspace, workspace_bytes,
                          i8mm::kv_pages_workspace_bytes(a, a.num_rows)));
   I8MM_TRY(check_apart(fn, {{out_table, num_rows * max_pages}, {out_lens, num_rows},
-                            {copies, 3 * num_rows}, {counts, 2}},
+                            {batch_lens, num_rows}, {full, 1}, {copies, 3 * num_rows}, {counts, 2}},
                        {{page_table, num_seqs * max_pages}, {seq_lens, num_seqs}, {parents, num_rows},
                         {keep, num_rows}, {new_tokens, num_rows}}));
   I8MM_TRY(check_device());
@@ -882,10 +889,41 @@ int i8mm_kv_pages_step(const int32_t* page_table, const int32_t* seq_lens, int64
   a.new_all = (int)new_all;
   a.out_table = out_table;
   a.out_lens = out_lens;
+  a.batch_lens = batch_lens;
+  a.full = full;
+  a.max_len = (int)std::min<int64_t>(max_len, INT32_MAX);
   a.copies = copies;
   a.counts = counts;
   I8MM_TRY(launched(i8mm::launch_kv_pages_step(a, workspace, (hipStream_t)stream), fn));
   return ok();
+}
+
+}  // namespace
+
+extern "C" {
+
+int i8mm_kv_pages_step(const int32_t* page_table, const int32_t* seq_lens, int64_t num_seqs,
+                       int64_t max_pages, const int32_t* parents, const int32_t* keep,
+                       const int32_t* new_tokens, int64_t new_all, int64_t num_rows,
+                       int64_t num_pages, int64_t page_tokens, int32_t* out_table,
+                       int32_t* out_lens, int32_t* copies, int32_t* counts, void* workspace,
+                       size_t workspace_bytes, i8mm_stream_t stream) {
+  return pages_step("i8mm_kv_pages_step", page_table, seq_lens, num_seqs, max_pages, parents, keep,
+                    new_tokens, new_all, num_rows, num_pages, page_tokens, INT32_MAX, false, out_table,
+                    out_lens, nullptr, nullptr, copies, counts, workspace, workspace_bytes, stream);
+}
+
+int i8mm_kv_pages_step_batch(const int32_t* page_table, const int32_t* seq_lens, int64_t num_seqs,
+                             int64_t max_pages, const int32_t* parents, const int32_t* keep,
+                             const int32_t* new_tokens, int64_t new_all, int64_t num_rows,
+                             int64_t num_pages, int64_t page_tokens, int64_t max_len,
+                             int32_t* out_table, int32_t* out_lens, int32_t* batch_lens,
+                             int32_t* full, int32_t* copies, int32_t* counts, void* workspace,
+                             size_t workspace_bytes, i8mm_stream_t stream) {
+  return pages_step("i8mm_kv_pages_step_batch", page_table, seq_lens, num_seqs, max_pages, parents,
+                    keep, new_tokens, new_all, num_rows, num_pages, page_tokens, max_len, true,
+                    out_table, out_lens, batch_lens, full, copies, counts, workspace, workspace_bytes,
+                    stream);
 }
 
 int i8mm_kv_pages_compact(const int32_t* page_table, const int32_t* seq_lens, int64_t num_seqs,

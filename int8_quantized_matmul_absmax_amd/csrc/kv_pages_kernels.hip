@@ -38,9 +38,11 @@ struct Row {
   int all_pages;
   int rest;        // tokens kept in the last of `pages`, 0 if they fill it
   bool writes;     // to that page
+  bool full;       // not all of its new tokens have room
 };
-__device__ __forceinline__ Row step_row(const PagesArgs& a, int i, int* len) {
-  const int limit = a.max_pages * a.page_tokens;
+// (*batch_len: its length in a batch of the new tokens)
+__device__ __forceinline__ Row step_row(const PagesArgs& a, int i, int* len, int* batch_len) {
+  const int limit = min(a.max_pages * a.page_tokens, a.max_len);
   Row r;
   r.parent = a.parents[i];
   if ((uint32_t)r.parent >= (uint32_t)a.num_seqs) r.parent = -1;
@@ -53,13 +55,16 @@ __device__ __forceinline__ Row step_row(const PagesArgs& a, int i, int* len) {
   r.all_pages = (*len + a.page_tokens - 1) / a.page_tokens;
   r.rest = kept - kept / a.page_tokens * a.page_tokens;
   r.writes = r.rest != 0 && *len > kept;
+  r.full = more > limit - kept;
+  *batch_len = more > 0 && !r.full ? *len : 0;
   return r;
 }
 __device__ __forceinline__ int4 packed(const Row& r) {
-  return make_int4(r.parent, r.pages, r.all_pages, r.rest | (r.writes ? 1 << 30 : 0));
+  return make_int4(r.parent, r.pages, r.all_pages,
+                   r.rest | (r.writes ? 1 << 30 : 0) | (r.full ? 1 << 29 : 0));
 }
 __device__ __forceinline__ Row unpacked(const int4& p) {
-  return Row{p.x, p.y, p.z, p.w & 0xffff, (p.w >> 30) != 0};
+  return Row{p.x, p.y, p.z, p.w & 0xffff, (p.w & 1 << 30) != 0, (p.w & 1 << 29) != 0};
 }
 
 __device__ __forceinline__ int page_or_none(const PagesArgs& a, int page) {
@@ -70,8 +75,8 @@ __device__ __forceinline__ int page_or_none(const PagesArgs& a, int page) {
 __global__ __launch_bounds__(kBlockThreads) void k_kv_pages_keep(PagesArgs a, uint32_t* words) {
   const int i = blockIdx.y, j = blockIdx.x * kBlockThreads + threadIdx.x;
   if (j >= a.max_pages) return;
-  int len;
-  const Row r = step_row(a, i, &len);
+  int len, batch_len;
+  const Row r = step_row(a, i, &len, &batch_len);
   int page = -1;
   if (j < r.pages) page = page_or_none(a, a.page_table[(int64_t)r.parent * a.max_pages + j]);
   a.out_table[(int64_t)i * a.max_pages + j] = page;
@@ -117,12 +122,13 @@ template <class RowOf>
 __device__ __forceinline__ void give_pages(const PagesArgs& a, const uint32_t* words, int32_t* list,
                                            int2* places, int* s_wave, RowOf row_of) {
   const int tid = threadIdx.x, lane = tid & 63;
-  int want = 0, copies = 0;
+  int want = 0, copies = 0, full = 0;
   for (int i0 = 0; i0 < a.num_rows; i0 += kOneBlock) {
     const int i = i0 + tid;
-    int copy = 0, need = 0;
+    int copy = 0, need = 0, no_room = 0;
     if (i < a.num_rows) {
       const Row r = row_of(i);
+      no_room = r.full;
       if (r.writes) {
         const int page = a.out_table[(int64_t)i * a.max_pages + r.pages - 1];
         copy = page >= 0 && words[page] != (uint32_t)(a.num_rows - i);
@@ -132,8 +138,10 @@ __device__ __forceinline__ void give_pages(const PagesArgs& a, const uint32_t* w
     int total;
     const int at = want + block_prefix<kOneWaves>(need, s_wave, &total);
     want += total;
-    const int rank = copies + block_prefix<kOneWaves>(copy, s_wave, &total);
-    copies += total;
+    // (both counts are a block's threads at most)
+    const int rank = copies + (block_prefix<kOneWaves>(copy | no_room << 16, s_wave, &total) & 0xffff);
+    copies += total & 0xffff;
+    full += total >> 16;
     if (i < a.num_rows) places[i] = int2{at, copy ? rank : -1};
   }
   const int have = list_free(words, a.num_pages, want, list, s_wave);
@@ -192,6 +200,7 @@ __device__ __forceinline__ void give_pages(const PagesArgs& a, const uint32_t* w
   if (tid == 0) {
     a.counts[0] = done;
     a.counts[1] = want - have;
+    if (a.full) a.full[0] = full;
   }
 }
 
@@ -199,13 +208,14 @@ __global__ __launch_bounds__(kOneBlock) void k_kv_pages_give(PagesArgs a, const 
                                                              int32_t* list, int2* places) {
   __shared__ int s_wave[kOneWaves];
   for (int i = threadIdx.x; i < a.num_rows; i += kOneBlock) {
-    int len;
-    step_row(a, i, &len);
+    int len, batch_len;
+    step_row(a, i, &len, &batch_len);
     a.out_lens[i] = len;
+    if (a.batch_lens) a.batch_lens[i] = batch_len;
   }
   give_pages(a, words, list, places, s_wave, [&](int i) {
-    int len;
-    return step_row(a, i, &len);
+    int len, batch_len;
+    return step_row(a, i, &len, &batch_len);
   });
 }
 
@@ -243,9 +253,10 @@ __global__ __launch_bounds__(kOneBlock) void k_kv_pages_step_one(PagesArgs a) {
   int32_t* const list = reinterpret_cast<int32_t*>(words + a.num_pages);
   const int tid = threadIdx.x;
   if (tid < a.num_rows) {
-    int len;
-    rows[tid] = packed(step_row(a, tid, &len));
+    int len, batch_len;
+    rows[tid] = packed(step_row(a, tid, &len, &batch_len));
     a.out_lens[tid] = len;
+    if (a.batch_lens) a.batch_lens[tid] = batch_len;
   }
   for (int p = tid; p < a.num_pages; p += kOneBlock) words[p] = 0;
   __syncthreads();

@@ -176,7 +176,9 @@ struct PagesArgs {
   int32_t* out_lens;
   int32_t* copies;
   int32_t* counts;
-  int num_seqs, max_pages, num_rows, num_pages, page_tokens, new_all;
+  int32_t* batch_lens;        // or nullptr, then full too
+  int32_t* full;
+  int num_seqs, max_pages, num_rows, num_pages, page_tokens, new_all, max_len;
 };
 size_t kv_pages_workspace_bytes(const PagesArgs& a, int rows);   // of the step or the compaction
 hipError_t launch_kv_pages_step(const PagesArgs& a, void* ws, hipStream_t s);

@@ -136,10 +136,15 @@ class PageChoice(collections.namedtuple("PageChoice", "count first recent", defa
 class PageCopies:
     """Copies of pages that a KVPages call (of `pool`) asks for, on the GPU: pages int32
     [n, 3] (page, page to copy it to, tokens that count), counts int32 [2], the number
-    of them first."""
+    of them first, and then, of a step, the pages that were wanting, of a compaction, the
+    pages in use.
 
-    def __init__(self, pages, counts, pool):
+    Of a step also batch_lens int32 [rows], the lengths for a KVBatch of the new tokens,
+    and full int32 [1], the rows that had no room for all of theirs."""
+
+    def __init__(self, pages, counts, pool, batch_lens=None, full=None):
         self.pages, self.counts, self.pool = pages, counts, pool
+        self.batch_lens, self.full = batch_lens, full
 
 
 class KVPages:
@@ -150,7 +155,7 @@ class KVPages:
         table, lens, copies = pool.step(table, lens, parents)
         for cache in caches:
             cache.copy_pages(copies)
-        batch = KVBatch(table, lens)"""
+        batch = KVBatch(table, copies.batch_lens)"""
 
     def __init__(self, num_pages, page_tokens=64):
         if page_tokens <= 0 or page_tokens % BLOCK != 0:
@@ -173,7 +178,7 @@ class KVPages:
         return (torch.full((rows, width), -1, dtype=torch.int32, device=device),
                 torch.zeros((rows,), dtype=torch.int32, device=device))
 
-    def step(self, page_table, seq_lens, parents, new_tokens=1, keep=None):
+    def step(self, page_table, seq_lens, parents, new_tokens=1, keep=None, max_len=None):
         """The table of the next step, its lengths (new tokens included) and the
         copies to make before its append. Row i keeps the first keep[i] tokens (None:
         all) of row parents[i] (-1: none) and has room for new_tokens (an int, or one
@@ -181,11 +186,17 @@ class KVPages:
         sequences share, growth, cutting back, beginning and, for rows that the new
         table leaves out, ending are all this call. Pages that rows share are copied
         for those about to write to them. copies.counts[1] says how many pages were
-        wanting; their tokens are absent."""
-        table, lens, pages, counts = ops.kv_pages_step(
+        wanting; their tokens are absent.
+
+        The KVBatch of the new tokens takes copies.batch_lens: a row without new tokens
+        has length 0 there, and so has one without room for all of them in the table (or
+        below max_len, the batches'), whose tokens would be stored over its last ones, in
+        pages that it may share. copies.full says how many those are; what the table
+        holds of them stays."""
+        table, lens, pages, counts, batch_lens, full = ops.kv_pages_step(
             page_table, seq_lens, parents, self.num_pages, self.page_tokens, new_tokens, keep,
-            shared_workspace)
-        return table, lens, PageCopies(pages, counts, self)
+            shared_workspace, max_len, True)
+        return table, lens, PageCopies(pages, counts, self, batch_lens, full)
 
     def compact(self, page_table, seq_lens):
         """The used pages to the front of the caches: the table with their new places

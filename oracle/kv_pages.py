@@ -2,9 +2,23 @@
 with no GPU code. Tables are lists of rows of page numbers."""
 
 
-def step(table, lens, parents, new, keep, num_pages, page, width):
+def batch_lens(lens, parents, new, keep, limit):
+    """-> (the rows' lengths in a batch of the new tokens: 0 where they have none or, of
+    `limit` tokens, no room for all of them; how many have no room)."""
+    out, full = [], 0
+    for i, parent in enumerate(parents):
+        k = min(max(lens[parent], 0), limit) if 0 <= parent < len(lens) else 0
+        if keep is not None:
+            k = min(k, max(keep[i], 0))
+        fits = k + max(new[i], 0) <= limit
+        out.append(k + new[i] if fits and new[i] > 0 else 0)
+        full += not fits
+    return out, full
+
+
+def step(table, lens, parents, new, keep, num_pages, page, width, max_len=None):
     """-> (table of `width` entries a row, lengths, copies, wanting)."""
-    limit = width * page
+    limit = width * page if max_len is None else min(width * page, max_len)
     rows = []
     for i, parent in enumerate(parents):
         known = 0 <= parent < len(table)
