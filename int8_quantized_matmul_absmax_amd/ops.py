@@ -358,20 +358,23 @@ def _kv_args(cache, batch, rotary):
     return rotary.ref
 
 
-def _scratch(need, workspace, dev):
-    """Address and size of a workspace of `need` bytes: `workspace` is a uint8
-    tensor, or a function of the device and a number of bytes that gives one, or
-    None (allocated here)."""
+def _scratch(workspace, dev, size, *args):
+    """A workspace of size(*args) bytes, its address and its size: `workspace` is a
+    uint8 tensor, or a function of the device and a number of bytes that gives one, or
+    None (allocated here). The caller keeps the tensor until its call returns: memory
+    that nothing holds could be given to another thread's call, or back to the device,
+    before the kernels that use it are on the stream."""
     if workspace is None or callable(workspace):
+        need = size(*args)
         if not need:
-            return None, 0
+            return None, None, 0
         workspace = workspace(dev, need) if workspace else \
             torch.empty((need,), dtype=torch.uint8, device=dev)
     else:
         _need(workspace, "workspace", torch.uint8, 1)
         if workspace.device != dev:
             raise ValueError("workspace is on %s, the call on %s" % (workspace.device, dev))
-    return workspace.data_ptr(), workspace.numel()
+    return workspace, workspace.data_ptr(), workspace.numel()
 
 
 def int8_kv_cache_append(k, v, cache, batch, rotary=None):
@@ -416,17 +419,8 @@ def int8_kv_cache_attention(q, cache, batch, rotary=None, scale=None, causal=Tru
     else:
         _need(out, "out", torch.float16, shape=q.shape)
         _on_gpu(q=q, out=out)
-    wp, wn = None, 0
-    if workspace is None or callable(workspace):
-        wn = lib.int8_kv_cache_attention_workspace_bytes(cache.ref, batch.ref, heads)
-        if wn:
-            workspace = workspace(dev, wn) if workspace else \
-                torch.empty((wn,), dtype=torch.uint8, device=dev)
-            wp = workspace.data_ptr()
-    else:
-        _need(workspace, "workspace", torch.uint8, 1)
-        _on_gpu(q=q, workspace=workspace)
-        wp, wn = workspace.data_ptr(), workspace.numel()
+    held, wp, wn = _scratch(workspace, dev, lib.int8_kv_cache_attention_workspace_bytes, cache.ref,
+                            batch.ref, heads)
     _lib.check(lib.int8_kv_cache_attention(
         qp, qts, qhs, heads, cache.ref, batch.ref, rot,
         1.0 / math.sqrt(D) if scale is None else scale, 1 if causal else 0, window, slopes,
@@ -502,8 +496,8 @@ def int8_kv_cache_attention_pages(q, pages, cache, batch, rotary=None, scale=Non
     else:
         _need(out, "out", torch.float16, shape=q.shape)
     _on_gpu(q=q, pages=pages, out=out)
-    wp, wn = _scratch(lib.int8_kv_cache_attention_pages_workspace_bytes(cache.ref, batch.ref, heads,
-                                                                        count), workspace, dev)
+    held, wp, wn = _scratch(workspace, dev, lib.int8_kv_cache_attention_pages_workspace_bytes,
+                            cache.ref, batch.ref, heads, count)
     _run(dev, lib.int8_kv_cache_attention_pages, qp, qts, qhs, heads, cache.ref, batch.ref, rot,
          pages.data_ptr(), count, 1.0 / math.sqrt(D) if scale is None else scale, out.data_ptr(), wp, wn)
     return out
@@ -544,7 +538,7 @@ def kv_pages_step(page_table, seq_lens, parents, num_pages, page_tokens, new_tok
     table, lens = out.as_strided((rows, width), (width, 1)), out.as_strided((rows,), (1,), at)
     copies = out.as_strided((rows, 3), (3, 1), at + rows)
     counts = out.as_strided((2,), (1,), at + 4 * rows)
-    wp, wn = _scratch(lib.i8mm_kv_pages_workspace_bytes(rows, width, num_pages), workspace, dev)
+    held, wp, wn = _scratch(workspace, dev, lib.i8mm_kv_pages_workspace_bytes, rows, width, num_pages)
     full = out.as_strided((1,), (1,), at + 4 * rows + 2)
     batch_lens = out.as_strided((rows,), (1,), at + 4 * rows + 3)
     _run(dev, lib.i8mm_kv_pages_step_batch, page_table.data_ptr(), seq_lens.data_ptr(), seqs, width,
@@ -568,7 +562,7 @@ def kv_pages_compact(page_table, seq_lens, num_pages, page_tokens, workspace=Non
     table = out.as_strided((seqs, width), (width, 1))
     copies = out.as_strided((most, 3), (3, 1), seqs * width)
     counts = out.as_strided((2,), (1,), seqs * width + 3 * most)
-    wp, wn = _scratch(lib.i8mm_kv_pages_workspace_bytes(seqs, width, num_pages), workspace, dev)
+    held, wp, wn = _scratch(workspace, dev, lib.i8mm_kv_pages_workspace_bytes, seqs, width, num_pages)
     _run(dev, lib.i8mm_kv_pages_compact, page_table.data_ptr(), seq_lens.data_ptr(), seqs, width,
          num_pages, page_tokens, table.data_ptr(), copies.data_ptr(), counts.data_ptr(), wp, wn)
     return table, copies, counts
@@ -633,8 +627,8 @@ def beam_select(logits, scores, live=None, eos=None, count=None, workspace=None)
     tokens, parents, alive = torch.empty((3, batch, max(count, 0)), dtype=torch.int32,
                                          device=dev).unbind(0)
     out = torch.empty((batch, max(count, 0)), dtype=torch.float32, device=dev)
-    wp, wn = _scratch(lib.i8mm_beam_select_workspace_bytes(fp32, batch, beams, vocab, count),
-                      workspace, dev)
+    held, wp, wn = _scratch(workspace, dev, lib.i8mm_beam_select_workspace_bytes, fp32, batch, beams,
+                            vocab, count)
     _run(dev, lib.i8mm_beam_select, logits.data_ptr(), fp32, max(rs, vocab), scores.data_ptr(),
          None if live is None else live.data_ptr(), batch, beams, vocab, count,
          -1 if eos is None else int(eos), out.data_ptr(), tokens.data_ptr(), parents.data_ptr(),
