@@ -32,20 +32,22 @@ INT8_FORMAT = "llm-int8/per-output-row-absmax/v1"
 # (outlier flags and columns, row scales, int8 codes, gathered outlier
 # activations, and the region of recovered outlier weights, room for 512
 # columns per output row). A model then holds one layer's worth of
-# workspace, not one per module. Calls on different streams get their own.
+# workspace, not one per module. Calls on different streams get their own, and so do
+# those of different host threads: a call is several launches, and the launches of two
+# threads' calls on one stream may alternate.
 # Each call takes the prefix of the layer's own size, so the layer's path
 # (and its result bits) do not depend on which layers ran before.
 # A call that is recorded into a graph gets one from the graph's own memory
 # pool instead, and nothing else keeps it: the shared one is replaced when a
 # larger call comes, and the graph's replays go on writing where it recorded.
-_WS_LOCK = threading.Lock()
-_WORKSPACES = {}
+_WORKSPACES = {}                 # the main thread's
+_OF_THREAD = threading.local()   # another's, until it ends
 
 
 def shared_workspace(device, nbytes):
-    """The shared workspace of the current stream on `device`, grown to at
-    least nbytes (uint8 tensor). While the stream is being captured, one of the
-    graph's own."""
+    """The calling thread's shared workspace of the current stream on `device`,
+    grown to at least nbytes (uint8 tensor). While the stream is being captured,
+    one of the graph's own."""
     device = torch.device(device)
     if torch.cuda.is_current_stream_capturing():
         return torch.empty((max(int(nbytes), 1),), dtype=torch.uint8, device=device)
@@ -53,12 +55,14 @@ def shared_workspace(device, nbytes):
         key = (device.index, ops._raw_stream(device))
     else:
         key = (device.index, torch.cuda.current_stream(device).cuda_stream)
-    with _WS_LOCK:
-        ws = _WORKSPACES.get(key)
-        if ws is None or ws.numel() < nbytes:
-            ws = torch.empty((max(int(nbytes), 1),), dtype=torch.uint8, device=device)
-            _WORKSPACES[key] = ws
-        return ws
+    if threading.get_ident() == threading.main_thread().ident:
+        held = _WORKSPACES
+    else:
+        held = _OF_THREAD.__dict__.setdefault("held", {})
+    ws = held.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = held[key] = torch.empty((max(int(nbytes), 1),), dtype=torch.uint8, device=device)
+    return ws
 
 
 def save_int8_weight(path, Wq, sw, bias=None, threshold=ops.DEFAULT_THRESHOLD):
