@@ -540,6 +540,7 @@ I8MM_API int int8_kv_cache_page_means(const i8mm_kv_cache* cache, const i8mm_kv_
  *   count      first + recent .. 2^30 / page_tokens; first >= 0, recent >= 1. A
  *              sequence has at most I8MM_MAX_SELECT_PAGES pages beside the first and
  *              the recent ones (by max_len).
+ *   total_tokens * kv_heads is at most 2^24 - 1.
  *   pages      int32 [total_tokens, kv_heads, count], 4-byte aligned: numbers of
  *              pages in the sequence, ascending, then -1 (all -1 for a token of no
  *              sequence).

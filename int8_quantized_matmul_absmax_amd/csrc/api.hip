@@ -1022,6 +1022,9 @@ int int8_kv_cache_select_pages(const uint16_t* q, int64_t q_token_stride, int64_
   if ((a.len_cap + page_tokens - 1) / page_tokens - first - recent > I8MM_MAX_SELECT_PAGES)
     return fail(I8MM_EINVAL, "%s: more than %d pages to choose from in %d tokens", fn,
                 I8MM_MAX_SELECT_PAGES, a.len_cap);
+  if (!no_tokens(a) && (int64_t)a.total_tokens * a.kv_heads > i8mm::max_grid(256))
+    return fail(I8MM_EINVAL, "%s: %d tokens of %d heads are more than 2^24 - 1 lists", fn,
+                a.total_tokens, a.kv_heads);
   I8MM_TRY(check_ints(fn, "pages", pages, a.total_tokens > 0));
   if (a.total_tokens == 0) return ok();
   I8MM_TRY(check_device());

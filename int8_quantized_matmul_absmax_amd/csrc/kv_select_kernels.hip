@@ -308,20 +308,13 @@ hipError_t launch_kv_select_pages(const KvArgs& a, const RotaryArgs& r, const ui
   if (candidates > kMaxSelectPages) return hipErrorInvalidValue;
   const int group = q_heads / a.kv_heads;
   const size_t lds = (size_t)candidates * 8;
-#define CALL_T(D, T)                                                                             \
-  do {                                                                                           \
-    if (blocks > UINT32_MAX / T) return hipErrorInvalidValue;                                    \
-    k_kv_select_pages<D, T><<<(uint32_t)blocks, T, lds, s>>>(a, r, q, q_ts, q_hs, group, means,  \
-                                                             count, first, recent, out);         \
-  } while (0)
-  // 1024 threads a block where a compute unit has one: of few blocks, and where keys fill
-  // its LDS (means and choice, with 256 and 1024 threads). 8 blocks of 509 candidates
-  // 15.4 and 16.1 us, of 1021 21.0 and 17.6, of 2045 31.2 and 23.0; 256 of 1021 27.7 and
-  // 24.4, 320 32.4 and 35.1, 512 35.2 and 39.6; 2048 of 4093 105 and 107, of 8189 170 and
-  // 121; 16384 of 1997 516 and 778.
-  const bool large = candidates > 512 && (blocks <= 256 || candidates > 4096);
+#define CALL_T(D, T)                                                                            \
+  k_kv_select_pages<D, T><<<(uint32_t)blocks, T, lds, s>>>(a, r, q, q_ts, q_hs, group, means,   \
+                                                           count, first, recent, out)
+  const int threads = select_threads(blocks, candidates);
+  if (blocks > max_grid(threads)) return hipErrorInvalidValue;
 #define CALL(D) \
-  if (large) CALL_T(D, 1024); else CALL_T(D, 256)
+  if (threads == 1024) CALL_T(D, 1024); else CALL_T(D, 256)
   I8MM_KV_DIMS(a.head_dim, CALL)
 #undef CALL
 #undef CALL_T

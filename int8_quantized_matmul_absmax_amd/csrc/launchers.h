@@ -160,6 +160,17 @@ hipError_t launch_kv_attention_pages(const KvArgs& a, const RotaryArgs& r, const
                                      const int32_t* chosen, int count, hipStream_t s);
 // Mean keys of the pages that hold the batch's new tokens, and the choice of pages.
 constexpr int kMaxSelectPages = I8MM_MAX_SELECT_PAGES;
+// Threads of a launch along x stay below 2^32.
+constexpr int64_t max_grid(int threads) { return (((int64_t)1 << 32) - 1) / threads; }
+// Threads of a block of the choice, given its blocks and the candidates of one: 1024
+// where a compute unit has one block, which is with few blocks, and where keys fill its LDS
+// (means and choice, with 256 and 1024 threads). 8 blocks of 509 candidates 15.4 and
+// 16.1 us, of 1021 21.0 and 17.6, of 2045 31.2 and 23.0; 256 of 1021 27.7 and 24.4, 320 32.4
+// and 35.1, 512 35.2 and 39.6; 2048 of 4093 105 and 107, of 8189 170 and 121; 16384 of
+// 1997 516 and 778. And 256 for blocks that would be too many for a launch with 1024.
+constexpr int select_threads(int64_t blocks, int64_t candidates) {
+  return candidates > 512 && (blocks <= 256 || candidates > 4096) && blocks <= max_grid(1024) ? 1024 : 256;
+}
 hipError_t launch_kv_page_means(const KvArgs& a, uint16_t* means, hipStream_t s);
 hipError_t launch_kv_select_pages(const KvArgs& a, const RotaryArgs& r, const uint16_t* q, int64_t q_ts,
                                   int64_t q_hs, int q_heads, const uint16_t* means, int count, int first,

@@ -1,0 +1,30 @@
+"""Sizes past what one launch takes are refused by the checks, and those up to it are not
+(no GPU: what passes the checks finds no device)."""
+
+import pytest
+import torch
+
+import int8_quantized_matmul_absmax_amd as i8
+from int8_quantized_matmul_absmax_amd import _lib
+from tests.test_kv_cache_host import batch, cache
+from tests.test_kv_sparse_host import call_select
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are not memory")
+    return i8.ensure_built()
+
+
+@pytest.mark.parametrize("pages", [100, 8200])
+@pytest.mark.parametrize("heads,tokens", [(1, (1 << 24) - 1), (32, (1 << 19) - 1), (32, 131073), (5, 3355443)])
+def test_choice(lib, pages, heads, tokens):
+    c = cache(kv_heads=heads, page_tokens=16)
+    sizes = dict(max_tokens=4, max_pages=pages, max_len=1 << 20)
+    assert call_select(lib, c, batch(total_tokens=tokens, **sizes), heads=heads) == _lib.I8MM_ENODEVICE
+    if (tokens + 1) * heads > (1 << 24) - 1:
+        assert call_select(lib, c, batch(total_tokens=tokens + 1, **sizes), heads=heads) == _lib.I8MM_EINVAL
+        assert b"2^24" in lib.i8mm_last_error()
+    none = batch(total_tokens=(1 << 24) + 1, **dict(sizes, max_tokens=0))
+    assert call_select(lib, c, none, heads=heads) == _lib.I8MM_ENODEVICE
