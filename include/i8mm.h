@@ -522,7 +522,9 @@ I8MM_API int int8_kv_cache_read(const i8mm_kv_cache* cache, const i8mm_kv_batch*
  * int8_kv_cache_page_means: the mean keys of the pages that hold the batch's new
  * tokens (after their append), over the tokens that the page then holds:
  * fp16(fl32(sum_t k_t / n)), the sum of q * fl32(a / 127) in 64 bits. (Sequences that
- * share a page and hold different numbers of its tokens race for its mean.)
+ * share a page and hold different numbers of its tokens race for its mean.) The pages
+ * that max_tokens tokens can touch, times kv_heads, times ceil(D / 64), are at most
+ * 2^26 - 4.
  * Errors: EINVAL, EALIGN, ENODEVICE, ELAUNCH.
  */
 I8MM_API int int8_kv_cache_page_means(const i8mm_kv_cache* cache, const i8mm_kv_batch* batch,
@@ -561,6 +563,9 @@ I8MM_API int int8_kv_cache_select_pages(const uint16_t* q, int64_t q_token_strid
  *            in the token's sequence, in any order; one that is negative, past the
  *            token's own page or absent has no tokens, one listed twice counts twice.
  *   count    1 .. 2^30 / page_tokens.
+ *   total_tokens * kv_heads is at most 2^26 - 4 * kv_heads, and with more than eight
+ *            query heads a key/value head times ceil(q_heads / kv_heads / 16) at most
+ *            2^24 - 1.
  *   q, rotary, scale, out  as for int8_kv_cache_attention; a token that sees nothing
  *            gets 0.
  *   workspace  int8_kv_cache_attention_pages_workspace_bytes(...) bytes, 256-byte

@@ -997,6 +997,9 @@ int int8_kv_cache_page_means(const i8mm_kv_cache* cache, const i8mm_kv_batch* ba
   I8MM_TRY(kv_check(fn, cache, batch, &a));
   I8MM_TRY(check_ptr(fn, "k_means", k_means, a.num_pages > 0));
   if (no_tokens(a) || a.len_cap == 0) return ok();
+  if ((i8mm::page_means_tasks(a) + 3) / 4 > i8mm::max_grid(256))
+    return fail(I8MM_EINVAL, "%s: %d new tokens of a sequence touch too many pages of %d heads", fn,
+                a.max_tokens, a.kv_heads);
   I8MM_TRY(check_device());
   I8MM_TRY(launched(i8mm::launch_kv_page_means(a, k_means, (hipStream_t)stream), fn));
   return ok();
@@ -1068,6 +1071,9 @@ int int8_kv_cache_attention_pages(const uint16_t* q, int64_t q_token_stride, int
   if (!std::isfinite(scale) || !(scale > 0.f))
     return fail(I8MM_EINVAL, "%s: scale is not finite and positive", fn);
   I8MM_TRY(check_ptr(fn, "out", out, a.total_tokens > 0));
+  if (!no_tokens(a) && a.len_cap > 0 && !i8mm::attn_pages_fits(a, (int)q_heads, (int)count))
+    return fail(I8MM_EINVAL, "%s: too many lists, %d tokens of %d heads of %lld queries", fn,
+                a.total_tokens, a.kv_heads, (long long)(q_heads / a.kv_heads));
   I8MM_TRY(check_scratch(fn, workspace, workspace_bytes,
                          i8mm::attn_pages_workspace_bytes(a, (int)q_heads, (int)count)));
   if (a.total_tokens == 0) return ok();

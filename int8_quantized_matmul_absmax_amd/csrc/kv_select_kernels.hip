@@ -285,12 +285,16 @@ __global__ __launch_bounds__(kThreads) void k_kv_select_pages(KvArgs a, RotaryAr
 
 }  // namespace
 
-hipError_t launch_kv_page_means(const KvArgs& a, uint16_t* means, hipStream_t s) {
+int64_t page_means_tasks(const KvArgs& a) {
   const int64_t page_tokens = (int64_t)a.slots * kKvBlock;
   // pages that the new tokens of one sequence can touch
   const int64_t pages = std::min<int64_t>((a.max_tokens + 2 * page_tokens - 2) / page_tokens, a.max_pages);
-  const int64_t tasks = pages * a.kv_heads * ((a.head_dim + 63) / 64);
-  if (tasks > INT32_MAX - 4) return hipErrorInvalidValue;
+  return pages * a.kv_heads * ((a.head_dim + 63) / 64);
+}
+
+hipError_t launch_kv_page_means(const KvArgs& a, uint16_t* means, hipStream_t s) {
+  const int64_t tasks = page_means_tasks(a);
+  if ((tasks + 3) / 4 > max_grid(kBlockThreads)) return hipErrorInvalidValue;
   if (tasks == 0) return hipSuccess;
   const dim3 grid((uint32_t)((tasks + 3) / 4), (uint32_t)a.num_seqs);
 #define CALL(D) k_kv_page_means<D><<<grid, kBlockThreads, 0, s>>>(a, means, (int)tasks)

@@ -517,19 +517,22 @@ Plan plan(const KvArgs& a, int q_heads, int count) {
   return p;
 }
 
+int64_t blocks_of(const KvArgs& a, const Plan& p) {
+  return p.wave ? ((int64_t)a.total_tokens + 3) / 4 * a.kv_heads
+                : (int64_t)a.total_tokens * a.kv_heads * p.tiles * p.splits;
+}
+
 template <int D>
 hipError_t launch_d(const KvArgs& a, const RotaryArgs& r, const AttnArgs& t, const int32_t* chosen,
                     int count, hipStream_t s) {
   const Plan p = plan(a, t.q_heads, count);
+  const int64_t blocks = blocks_of(a, p);
+  if (blocks > max_grid(kBlockThreads)) return hipErrorInvalidValue;
   if (p.wave) {
-    const int64_t blocks = ((int64_t)a.total_tokens + 3) / 4 * a.kv_heads;
-    if (blocks > UINT32_MAX / kBlockThreads) return hipErrorInvalidValue;
     auto* const kernel = p.group <= 4 ? k_kv_attn_pages_wave<D, 4> : k_kv_attn_pages_wave<D, 2>;
     kernel<<<(uint32_t)blocks, kBlockThreads, 0, s>>>(a, r, t, chosen, count, p.group);
     return hipGetLastError();
   }
-  const int64_t blocks = (int64_t)a.total_tokens * a.kv_heads * p.tiles * p.splits;
-  if (blocks > UINT32_MAX / kBlockThreads) return hipErrorInvalidValue;
   k_kv_attn_pages<D><<<(uint32_t)blocks, kBlockThreads, 0, s>>>(a, r, t, chosen, count, p.group, p.tiles,
                                                                 p.splits, p.chunk);
   const hipError_t e = hipGetLastError();
@@ -541,6 +544,10 @@ hipError_t launch_d(const KvArgs& a, const RotaryArgs& r, const AttnArgs& t, con
 }
 
 }  // namespace
+
+bool attn_pages_fits(const KvArgs& a, int q_heads, int count) {
+  return blocks_of(a, plan(a, q_heads, count)) <= max_grid(kBlockThreads);
+}
 
 size_t attn_pages_workspace_bytes(const KvArgs& a, int q_heads, int count) {
   const Plan p = plan(a, q_heads, count);

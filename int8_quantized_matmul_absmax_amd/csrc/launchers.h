@@ -154,14 +154,16 @@ struct BeamArgs {
 size_t beam_workspace_bytes(const BeamArgs& a);
 hipError_t launch_beam_select(const BeamArgs& a, hipStream_t s);
 
+// Threads of a launch along x stay below 2^32.
+constexpr int64_t max_grid(int threads) { return (((int64_t)1 << 32) - 1) / threads; }
+
 // Attention over the `count` pages that each token and key/value head lists.
 size_t attn_pages_workspace_bytes(const KvArgs& a, int q_heads, int count);
+bool attn_pages_fits(const KvArgs& a, int q_heads, int count);   // one launch
 hipError_t launch_kv_attention_pages(const KvArgs& a, const RotaryArgs& r, const AttnArgs& t,
                                      const int32_t* chosen, int count, hipStream_t s);
 // Mean keys of the pages that hold the batch's new tokens, and the choice of pages.
 constexpr int kMaxSelectPages = I8MM_MAX_SELECT_PAGES;
-// Threads of a launch along x stay below 2^32.
-constexpr int64_t max_grid(int threads) { return (((int64_t)1 << 32) - 1) / threads; }
 // Threads of a block of the choice, given its blocks and the candidates of one: 1024
 // where a compute unit has one block, which is with few blocks, and where keys fill its LDS
 // (means and choice, with 256 and 1024 threads). 8 blocks of 509 candidates 15.4 and
@@ -171,6 +173,7 @@ constexpr int64_t max_grid(int threads) { return (((int64_t)1 << 32) - 1) / thre
 constexpr int select_threads(int64_t blocks, int64_t candidates) {
   return candidates > 512 && (blocks <= 256 || candidates > 4096) && blocks <= max_grid(1024) ? 1024 : 256;
 }
+int64_t page_means_tasks(const KvArgs& a);   // waves for a sequence, four a block
 hipError_t launch_kv_page_means(const KvArgs& a, uint16_t* means, hipStream_t s);
 hipError_t launch_kv_select_pages(const KvArgs& a, const RotaryArgs& r, const uint16_t* q, int64_t q_ts,
                                   int64_t q_hs, int q_heads, const uint16_t* means, int count, int first,
