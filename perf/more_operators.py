@@ -724,7 +724,8 @@ def _exact_beam(case, s):
             if not int(s["live"][i, j]):
                 value[j] = -math.inf
                 value[j, s["eos"]] = s["scores"][i, j].double()
-        value = value.nan_to_num(nan=-math.inf).view(-1)
+        # (a row without words, all -infinity, has no softmax)
+        value = torch.where(torch.isnan(value), -math.inf, value).view(-1)
         row = []
         for _ in range(case["count"]):
             best = float(value.max())
