@@ -728,7 +728,7 @@ I8MM_API int int8_kv_cache_copy_pages(const i8mm_kv_cache* cache, uint16_t* k_me
  * elements are 4-byte aligned; an output that overlaps scores, live or another
  * output is refused (EINVAL).
  *
- * Exponentials are fp32 (a row's sum is within 2^-18 of itself); values are
+ * Exponentials are fp32 (a row's sum is within 2^-16 of itself); values are
  * compared in 64 bits and rounded to fp32 when they are written.
  * Errors: EINVAL, EALIGN, EWORKSPACE, ENODEVICE, ELAUNCH.
  */

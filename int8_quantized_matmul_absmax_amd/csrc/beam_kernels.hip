@@ -680,12 +680,17 @@ __global__ __launch_bounds__(kJoinThreads) void k_beam_join(BeamArgs a, int piec
 
 // Pieces: about four blocks a compute unit, and at least a step of each wave: 512 rows
 // of 131072 fp16 words 33 us, with eight blocks a compute unit 37 and sixteen 41 (256 of
-// 50257 fp32 words 20.1 us in all, with seven blocks 23.1). At
-// most kPieceMost words: a lane's 32-bit sum then takes eight parts of 32 terms
-// (16 of 16 for fp32), which keeps its error below 2^-18: in units of 2^-24, 10 and
-// 16 roundings of sums and joins, up to twice 16 of rescaling, the exponential's 2 and
-// its argument's, which for terms that matter is below the logarithm of their number
-// times log2(e), 24.
+// 50257 fp32 words 20.1 us in all, with seven blocks 23.1).
+//
+// At most kPieceMost words: a lane's 32-bit sum then takes eight parts of 32 terms
+// (16 of 16 for fp32), and a row's sum is within 2^-16 of itself. In units of 2^-24,
+// fp32 logits, 256 pieces: 20 additions of a lane, 45 where its maximum rises with each
+// part (a product and an exponential of 1 ulp: 3), 15 in the wave and the block, 18 in
+// the join, 2 of a term's own exponential, 2 of the logarithm, and the arguments'
+// roundings, which along a term's way to the row's maximum add up to 2.23 times its
+// distance t from it; the mean of t under the softmax is the entropy less the sum's
+// logarithm, for 2^24 words at most 13.1. Together 131 (with 1024 pieces of four parts,
+// too), and 90 for fp16, against 256.
 constexpr int64_t kPieceMost = 65536;
 struct Plan {
   int pieces, piece;
