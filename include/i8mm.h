@@ -624,7 +624,8 @@ I8MM_API size_t int8_kv_cache_attention_pages_workspace_bytes(const i8mm_kv_cach
  *   workspace   i8mm_kv_pages_workspace_bytes(num_rows, max_pages, num_pages) bytes,
  *               256-byte aligned (NULL when that is 0). What it holds on entry does
  *               not matter.
- * An output that overlaps an input or another output is refused (EINVAL).
+ * An output or a workspace that overlaps an input or another output is refused
+ * (EINVAL).
  *
  * num_seqs, num_rows up to 65535; max_pages * page_tokens up to 2^30;
  * num_rows * (max_pages + 1) and num_pages below 2^31; page_tokens as in the cache.
@@ -670,8 +671,8 @@ I8MM_API size_t i8mm_kv_pages_workspace_bytes(int64_t num_rows, int64_t max_page
  * both in ascending order, and the table names their new places.
  *
  *   page_table, seq_lens, sizes  as for i8mm_kv_pages_step.
- *   out_table   int32 [num_seqs, max_pages]; may be page_table (no other output
- *               may overlap an input or another output).
+ *   out_table   int32 [num_seqs, max_pages]; may be page_table (no other output,
+ *               nor the workspace, may overlap an input or another output).
  *   copies      int32 [num_pages / 2][3], as for i8mm_kv_pages_step, of whole
  *               pages. No page is both copied and copied to.
  *   counts      int32 [2]: copies; live.
@@ -725,8 +726,8 @@ I8MM_API int int8_kv_cache_copy_pages(const i8mm_kv_cache* cache, uint16_t* k_me
  *   workspace    i8mm_beam_select_workspace_bytes(...) bytes, 256-byte
  *            aligned. What it holds on entry does not matter.
  * Places beyond the candidates get -infinity, -1, -1 and 0. All arrays of 32-bit
- * elements are 4-byte aligned; an output that overlaps scores, live or another
- * output is refused (EINVAL).
+ * elements are 4-byte aligned; an output or a workspace that overlaps the
+ * logits (between their rows, too), scores, live or another output is refused (EINVAL).
  *
  * Exponentials are fp32 (a row's sum is within 2^-16 of itself); values are
  * compared in 64 bits and rounded to fp32 when they are written.

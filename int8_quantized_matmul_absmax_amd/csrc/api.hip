@@ -690,8 +690,8 @@ int int8_kv_cache_attention(const uint16_t* q, int64_t q_token_stride, int64_t q
 
 namespace {
 
-// Arrays of 32-bit elements, and whether any that is written shares memory with one that
-// is read or with another that is written.
+// Arrays in words of 32 bits, and whether any that is written (a workspace among them)
+// shares memory with one that is read or with another that is written.
 struct Words32 {
   const void* p;
   int64_t n;
@@ -706,7 +706,8 @@ int check_apart(const char* fn, std::initializer_list<Words32> written,
     bool shared = false;
     for (const Words32& r : read) shared = shared || overlap(*w, r);
     for (const Words32* o = w + 1; o != written.end(); ++o) shared = shared || overlap(*w, *o);
-    if (shared) return fail(I8MM_EINVAL, "%s: an output overlaps an input or another output", fn);
+    if (shared)
+      return fail(I8MM_EINVAL, "%s: an output or the workspace overlaps an input or another output", fn);
   }
   return I8MM_OK;
 }
@@ -787,11 +788,14 @@ int i8mm_beam_select(const void* logits, int logits_fp32, int64_t row_stride, co
   I8MM_TRY(check_ints(fn, "out_tokens", out_tokens, batch > 0));
   I8MM_TRY(check_ints(fn, "out_parents", out_parents, batch > 0));
   I8MM_TRY(check_ints(fn, "out_live", out_live, batch > 0));
-  I8MM_TRY(check_scratch(fn, workspace, workspace_bytes,
-                         batch == 0 ? 0 : i8mm::beam_workspace_bytes(a)));
+  const size_t need = batch == 0 ? 0 : i8mm::beam_workspace_bytes(a);
+  I8MM_TRY(check_scratch(fn, workspace, workspace_bytes, need));
+  // (from the first row's first word to the last row's last)
+  const int64_t span = rows > 0 ? (rows - 1) * row_stride + vocab : 0;
   I8MM_TRY(check_apart(fn, {{out_scores, batch * count}, {out_tokens, batch * count},
-                            {out_parents, batch * count}, {out_live, batch * count}},
-                       {{scores, rows}, {live, rows}}));
+                            {out_parents, batch * count}, {out_live, batch * count},
+                            {workspace, (int64_t)(need / 4)}},
+                       {{scores, rows}, {live, rows}, {logits, logits_fp32 ? span : (span + 1) / 2}}));
   if (batch == 0) return ok();
   I8MM_TRY(check_device());
   a.logits = logits;
@@ -874,10 +878,11 @@ int pages_step(const char* fn, const int32_t* page_table, const int32_t* seq_len
   I8MM_TRY(check_ints(fn, "full", full, batch));
   I8MM_TRY(check_ints(fn, "copies", copies, num_rows > 0));
   I8MM_TRY(check_ints(fn, "counts", counts, true));
-  I8MM_TRY(check_scratch(fn, workspace, workspace_bytes,
-                         i8mm::kv_pages_workspace_bytes(a, a.num_rows)));
+  const size_t need = i8mm::kv_pages_workspace_bytes(a, a.num_rows);
+  I8MM_TRY(check_scratch(fn, workspace, workspace_bytes, need));
   I8MM_TRY(check_apart(fn, {{out_table, num_rows * max_pages}, {out_lens, num_rows},
-                            {batch_lens, num_rows}, {full, 1}, {copies, 3 * num_rows}, {counts, 2}},
+                            {batch_lens, num_rows}, {full, 1}, {copies, 3 * num_rows}, {counts, 2},
+                            {workspace, (int64_t)(need / 4)}},
                        {{page_table, num_seqs * max_pages}, {seq_lens, num_seqs}, {parents, num_rows},
                         {keep, num_rows}, {new_tokens, num_rows}}));
   I8MM_TRY(check_device());
@@ -939,10 +944,11 @@ int i8mm_kv_pages_compact(const int32_t* page_table, const int32_t* seq_lens, in
   I8MM_TRY(check_ints(fn, "out_table", out_table, entries > 0));
   I8MM_TRY(check_ints(fn, "copies", copies, num_pages >= 2));
   I8MM_TRY(check_ints(fn, "counts", counts, true));
-  I8MM_TRY(check_scratch(fn, workspace, workspace_bytes,
-                         i8mm::kv_pages_workspace_bytes(a, a.num_seqs)));
+  const size_t need = i8mm::kv_pages_workspace_bytes(a, a.num_seqs);
+  I8MM_TRY(check_scratch(fn, workspace, workspace_bytes, need));
   // (a table is renamed entry by entry, in place too)
-  I8MM_TRY(check_apart(fn, {{out_table, entries}, {copies, num_pages / 2 * 3}, {counts, 2}},
+  I8MM_TRY(check_apart(fn, {{out_table, entries}, {copies, num_pages / 2 * 3}, {counts, 2},
+                            {workspace, (int64_t)(need / 4)}},
                        {{out_table == page_table ? nullptr : page_table, entries},
                         {seq_lens, num_seqs}}));
   I8MM_TRY(check_device());
