@@ -37,8 +37,5 @@ def __getattr__(name):
         return Int8Linear
     from . import ops as _ops
     if hasattr(_ops, name):
-        found = getattr(_ops, name)
-        if getattr(found, "__module__", None) == _ops.__name__:
-            globals()[name] = found   # (a call of its own is found at once from then on)
-        return found
+        return getattr(_ops, name)
     raise AttributeError(name)
