@@ -38,9 +38,10 @@ class BeamSearch:
         searches = page_table.shape[0]
         if beams < 1 or beams > ops.MAX_BEAM_COUNT:
             raise ValueError("beams must be 1 .. %d, got %s" % (ops.MAX_BEAM_COUNT, beams))
+        caches = list(caches)
         for c in caches:
             pool.check(c)
-        self.pool, self.caches, self.beams, self.eos = pool, list(caches), int(beams), eos
+        self.pool, self.caches, self.beams, self.eos = pool, caches, int(beams), eos
         self.max_len = max_len
         self.page_table, self.seq_lens = page_table, seq_lens
         self.scores = torch.zeros((searches, 1), dtype=torch.float32, device=page_table.device)
