@@ -480,7 +480,7 @@ struct Plan {
   bool wave;   // the kernel for many tokens
 };
 Plan plan(const KvArgs& a, int q_heads, int count) {
-  constexpr int64_t kMinChunk = 4 * kGroup, kMaxChunk = 2048, kMaxSplits = 1024;
+  constexpr int64_t kMinChunk = 4 * kGroup, kMaxSplits = 1024;
   const int64_t resident = (a.head_dim <= 128 ? 2 : 1) * 256;
   // Up to two chunks are not worth a join of up to 128 features: 32 rows of 512 tokens of
   // 128 features 8.8 us and 9.6 in two splits, 768 tokens 10.3 and 9.9 in three; of 256
@@ -506,9 +506,12 @@ Plan plan(const KvArgs& a, int q_heads, int count) {
   int64_t chunk = tokens;
   if (blocks < 2 * resident && tokens > kWhole) {
     // (no more splits than are resident at once: 96 blocks of 4096 tokens in six splits
-    // 29.5 us, in five 25.6; of 256 features 40 of 4096 in seven 32.0, in six 25.0)
+    // 29.5 us, in five 25.6; of 256 features 40 of 4096 in seven 32.0, in six 25.0. Nor for
+    // long chunks, however long: cut to 2048 tokens 512 blocks of 8192 take 195 us and
+    // whole 185, 1016 377 and 360, of 256 features 160 138 and 121; 320 blocks 125 and 138,
+    // which fill the card less well whole)
     const int64_t splits = std::max<int64_t>(resident / std::max<int64_t>(blocks, 1), 1);
-    chunk = std::min(std::max((tokens + splits - 1) / splits, kMinChunk), kMaxChunk);
+    chunk = std::max((tokens + splits - 1) / splits, kMinChunk);
   }
   chunk = std::max(chunk, tokens / kMaxSplits + 1);
   chunk = (chunk + kGroup - 1) / kGroup * kGroup;
