@@ -37,9 +37,6 @@ struct __attribute__((packed, aligned(2))) Loose16 {
 __device__ __forceinline__ uint32_t from_lane_below(uint32_t x) {
   return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x138, 0xf, 0xf, false);
 }
-__device__ __forceinline__ float lane_float(float x, int lane) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
-}
 
 // What a piece leaves: its base and its sum (the logits' exponentials add up to sum
 // times 2^base for fp16, e^base for fp32), then `count` values and as many indices, best first.
