@@ -30,10 +30,6 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
 
 
-def _stream(device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-
-
 def _raw_stream(device):
     # (the handle alone: a Stream object costs 2 us a call)
     return torch._C._cuda_getCurrentRawStream(device.index)
@@ -99,8 +95,7 @@ def int8_quantize_colwise_weight(W, Wq=None, sw=None):
     dev = _on_gpu(W=W, Wq=Wq, sw=sw)
     Wq = Wq if Wq is not None else torch.empty((N, K), dtype=torch.int8, device=dev)
     sw = sw if sw is not None else torch.empty((N,), dtype=torch.float32, device=dev)
-    _lib.check(lib.int8_quantize_colwise_weight(_ptr(W), N, K, _ptr(Wq), _ptr(sw),
-                                                _stream(dev)))
+    _run(dev, lib.int8_quantize_colwise_weight, _ptr(W), N, K, _ptr(Wq), _ptr(sw))
     return Wq, sw
 
 
@@ -120,8 +115,7 @@ def int8_quantize_rowwise(X, outlier_bitmap=None, Xq=None, sx=None):
     dev = _on_gpu(X=X, outlier_bitmap=outlier_bitmap, Xq=Xq, sx=sx)
     Xq = Xq if Xq is not None else torch.empty((M, K), dtype=torch.int8, device=dev)
     sx = sx if sx is not None else torch.empty((M,), dtype=torch.float32, device=dev)
-    _lib.check(lib.int8_quantize_rowwise(_ptr(X2), M, K, _ptr(outlier_bitmap), _ptr(Xq), _ptr(sx),
-                                         _stream(dev)))
+    _run(dev, lib.int8_quantize_rowwise, _ptr(X2), M, K, _ptr(outlier_bitmap), _ptr(Xq), _ptr(sx))
     return Xq, sx
 
 
@@ -142,8 +136,8 @@ def outlier_detect_gather(X, threshold=DEFAULT_THRESHOLD, gather=True):
     cols = torch.empty((max(K, 1),), dtype=torch.int32, device=dev)
     n = torch.empty((1,), dtype=torch.int32, device=dev)
     Xo = torch.empty((max(M * outlier_ld(K), 1),), dtype=torch.float16, device=dev) if gather else None
-    _lib.check(lib.outlier_detect_gather(_ptr(X2), M, K, float(threshold), _ptr(bitmap), _ptr(cols),
-                                         _ptr(n), _ptr(Xo), _stream(dev)))
+    _run(dev, lib.outlier_detect_gather, _ptr(X2), M, K, float(threshold), _ptr(bitmap), _ptr(cols),
+         _ptr(n), _ptr(Xo))
     return bitmap, cols, n, Xo
 
 
@@ -161,8 +155,8 @@ def outlier_detect_quantize(X, threshold=DEFAULT_THRESHOLD, workspace=None):
     dev = _on_gpu(X=X, workspace=workspace)
     if workspace is None:
         workspace = torch.empty((max(workspace_bytes(M, K), 1),), dtype=torch.uint8, device=dev)
-    _lib.check(lib.outlier_detect_quantize(_ptr(X2), M, K, float(threshold), _ptr(workspace),
-                                           workspace.numel(), _stream(dev)))
+    _run(dev, lib.outlier_detect_quantize, _ptr(X2), M, K, float(threshold), _ptr(workspace),
+         workspace.numel())
     return workspace
 
 
@@ -201,9 +195,8 @@ def int8_mm_dequant(Xq, Wq, sx, sw, Xo=None, cols=None, n=None, bias=None, want_
     if want_y:
         Y = out if out is not None else torch.empty((M, N), dtype=torch.float16, device=dev)
     C = torch.empty((M, N), dtype=torch.int32, device=dev) if want_int32 else None
-    _lib.check(lib.int8_mm_dequant(_ptr(Xq), _ptr(Wq), _ptr(sx), _ptr(sw), M, N, K, _ptr(Xo),
-                                   _ptr(cols), _ptr(n), _ptr(bias), _ptr(Y), _ptr(C),
-                                   _stream(dev)))
+    _run(dev, lib.int8_mm_dequant, _ptr(Xq), _ptr(Wq), _ptr(sx), _ptr(sw), M, N, K, _ptr(Xo),
+         _ptr(cols), _ptr(n), _ptr(bias), _ptr(Y), _ptr(C))
     if want_y and want_int32:
         return Y, C
     return Y if want_y else C
@@ -281,9 +274,8 @@ def linear_int8_mixed(X, Wq, sw, bias=None, threshold=DEFAULT_THRESHOLD, workspa
     if workspace is None:
         workspace = torch.empty((max(workspace_bytes(M, K, N), 1),), dtype=torch.uint8, device=dev)
     Y = out if out is not None else torch.empty((M, N), dtype=torch.float16, device=dev)
-    _lib.check(lib.linear_int8_mixed(_ptr(X2), M, K, _ptr(Wq), _ptr(sw), N, _ptr(bias),
-                                     float(threshold), _ptr(Y), _ptr(workspace),
-                                     workspace.numel(), _stream(dev)))
+    _run(dev, lib.linear_int8_mixed, _ptr(X2), M, K, _ptr(Wq), _ptr(sw), N, _ptr(bias),
+         float(threshold), _ptr(Y), _ptr(workspace), workspace.numel())
     return Y.reshape(*lead, N)
 
 
@@ -304,9 +296,9 @@ def linear_int8_mixed_fp16_weights(X, W, Wq, sw, quantize_weight=True, bias=None
     if workspace is None:
         workspace = torch.empty((max(workspace_bytes(M, K, N), 1),), dtype=torch.uint8, device=dev)
     Y = out if out is not None else torch.empty((M, N), dtype=torch.float16, device=dev)
-    _lib.check(lib.linear_int8_mixed_fp16_weights(
-        _ptr(X2), M, K, _ptr(W), N, _ptr(Wq), _ptr(sw), 1 if quantize_weight else 0, _ptr(bias),
-        float(threshold), _ptr(Y), _ptr(workspace), workspace.numel(), _stream(dev)))
+    _run(dev, lib.linear_int8_mixed_fp16_weights, _ptr(X2), M, K, _ptr(W), N, _ptr(Wq), _ptr(sw),
+         1 if quantize_weight else 0, _ptr(bias), float(threshold), _ptr(Y), _ptr(workspace),
+         workspace.numel())
     return Y.reshape(*lead, N)
 
 
@@ -318,7 +310,7 @@ def gelu_f16(X, out=None):
         _need(out, "out", torch.float16, min_numel=X.numel())
     dev = _on_gpu(X=X, out=out)
     Y = out if out is not None else torch.empty_like(X)
-    _lib.check(lib.i8mm_gelu_f16(_ptr(X), X.numel(), _ptr(Y), _stream(dev)))
+    _run(dev, lib.i8mm_gelu_f16, _ptr(X), X.numel(), _ptr(Y))
     return Y
 
 
@@ -387,8 +379,8 @@ def int8_kv_cache_append(k, v, cache, batch, rotary=None):
                                cache.device)
     vp, vts, vhs = _need_heads(v, "v", batch.total_tokens, cache.kv_heads, cache.head_dim,
                                cache.device)
-    _lib.check(lib.int8_kv_cache_append(kp, kts, khs, vp, vts, vhs, cache.ref, batch.ref, rot,
-                                        _raw_stream(cache.device)))
+    _run(cache.device, lib.int8_kv_cache_append, kp, kts, khs, vp, vts, vhs, cache.ref, batch.ref,
+         rot)
 
 
 def int8_kv_cache_attention_workspace_bytes(cache, batch, q_heads):
@@ -421,10 +413,9 @@ def int8_kv_cache_attention(q, cache, batch, rotary=None, scale=None, causal=Tru
         _on_gpu(q=q, out=out)
     held, wp, wn = _scratch(workspace, dev, lib.int8_kv_cache_attention_workspace_bytes, cache.ref,
                             batch.ref, heads)
-    _lib.check(lib.int8_kv_cache_attention(
-        qp, qts, qhs, heads, cache.ref, batch.ref, rot,
-        1.0 / math.sqrt(D) if scale is None else scale, 1 if causal else 0, window, slopes,
-        out.data_ptr(), wp, wn, _raw_stream(dev)))
+    _run(dev, lib.int8_kv_cache_attention, qp, qts, qhs, heads, cache.ref, batch.ref, rot,
+         1.0 / math.sqrt(D) if scale is None else scale, 1 if causal else 0, window, slopes,
+         out.data_ptr(), wp, wn)
     return out
 
 
@@ -435,8 +426,7 @@ def int8_kv_cache_read(cache, batch):
     _kv_args(cache, batch, None)
     k, v = torch.empty((2, batch.total_tokens, cache.kv_heads, cache.head_dim),
                        dtype=torch.float16, device=cache.device).unbind(0)
-    _lib.check(lib.int8_kv_cache_read(cache.ref, batch.ref, k.data_ptr(), v.data_ptr(),
-                                      _raw_stream(cache.device)))
+    _run(cache.device, lib.int8_kv_cache_read, cache.ref, batch.ref, k.data_ptr(), v.data_ptr())
     return k, v
 
 
