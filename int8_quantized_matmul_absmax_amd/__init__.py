@@ -19,6 +19,10 @@ def ensure_built():
 
 
 def __getattr__(name):
+    # (what ops has is looked up there each time, so that a replaced op is found)
+    found = getattr(globals().get("ops"), name, None)
+    if found is not None:
+        return found
     # ops and the module are imported on first use (they import torch)
     if name in ("ops", "linear", "synth", "kv_cache", "attention", "beam"):
         import importlib

@@ -140,11 +140,14 @@ class PageCopies:
     pages in use.
 
     Of a step also batch_lens int32 [rows], the lengths for a KVBatch of the new tokens,
-    and full int32 [1], the rows that had no room for all of theirs."""
+    and full int32 [1], the rows that had no room for all of theirs (of a compaction
+    None)."""
 
-    def __init__(self, pages, counts, pool, batch_lens=None, full=None):
-        self.pages, self.counts, self.pool = pages, counts, pool
-        self.batch_lens, self.full = batch_lens, full
+    def __init__(self, pages, counts, pool, step=None):
+        self.pages, self.counts, self.pool, self._step = pages, counts, pool, step
+
+    batch_lens = property(lambda self: self._step and self._step.batch_lens)
+    full = property(lambda self: self._step and self._step.full)
 
 
 class KVPages:
@@ -193,10 +196,9 @@ class KVPages:
         below max_len, the batches'), whose tokens would be stored over its last ones, in
         pages that it may share. copies.full says how many those are; what the table
         holds of them stays."""
-        table, lens, pages, counts, batch_lens, full = ops.kv_pages_step(
-            page_table, seq_lens, parents, self.num_pages, self.page_tokens, new_tokens, keep,
-            shared_workspace, max_len, True)
-        return table, lens, PageCopies(pages, counts, self, batch_lens, full)
+        step = ops._pages_step(page_table, seq_lens, parents, self.num_pages, self.page_tokens,
+                               new_tokens, keep, shared_workspace, max_len)
+        return step.table, step.lens, PageCopies(step.copies, step.counts, self, step)
 
     def compact(self, page_table, seq_lens):
         """The used pages to the front of the caches: the table with their new places

@@ -493,17 +493,30 @@ def int8_kv_cache_attention_pages(q, pages, cache, batch, rotary=None, scale=Non
     return out
 
 
-def kv_pages_step(page_table, seq_lens, parents, num_pages, page_tokens, new_tokens=1, keep=None,
-                  workspace=None, max_len=None, batch=False):
-    """The page table of the next step: row i keeps the first keep[i] tokens (None:
-    all) of row parents[i] (none for a parent outside the table) and has room for
-    new_tokens (an int, or int32 [rows]) after them. All int32 on the GPU.
+class _PagesStep:
+    """What a step of the page tables gives, in one tensor; views of it as they are
+    asked for (each costs as much as a call's checks)."""
 
-    Returns the table [rows, max_pages], the lengths [rows] (new tokens included),
-    the copies to make before the next append [rows, 3] and counts [2]: copies, and
-    pages that were wanting (their tokens are absent). With batch=True also the lengths
-    for a KVBatch of the new tokens [rows] (0 for a row that has none, or no room for all
-    of them, in the table or below max_len) and how many have no room [1]."""
+    def __init__(self, rows, width, device):
+        self.rows, self.width = rows, width
+        n = rows * width
+        self.at = (0, n, n + rows, n + 4 * rows, n + 4 * rows + 2, n + 4 * rows + 3)
+        self.out = torch.empty((n + 5 * rows + 3,), dtype=torch.int32, device=device)
+
+    def view(self, i, *shape):
+        return self.out.as_strided(shape, (shape[1], 1) if len(shape) == 2 else (1,), self.at[i])
+
+    table = property(lambda self: self.view(0, self.rows, self.width))
+    lens = property(lambda self: self.view(1, self.rows))
+    copies = property(lambda self: self.view(2, self.rows, 3))
+    counts = property(lambda self: self.view(3, 2))
+    full = property(lambda self: self.view(4, 1))
+    batch_lens = property(lambda self: self.view(5, self.rows))
+
+
+def _pages_step(page_table, seq_lens, parents, num_pages, page_tokens, new_tokens=1, keep=None,
+               workspace=None, max_len=None):
+    """kv_pages_step, its results as a _PagesStep."""
     lib = _lib.load_library()
     _need(page_table, "page_table", torch.int32, 2)
     seqs, width = page_table.shape
@@ -523,20 +536,33 @@ def kv_pages_step(page_table, seq_lens, parents, num_pages, page_tokens, new_tok
             raise ValueError("%s must hold %d numbers, got %d" % (name, rows, t.numel()))
     dev = _on_gpu(page_table=page_table, seq_lens=seq_lens, parents=parents, keep=keep,
                   new_tokens=each)
-    out = torch.empty((rows * (width + 5) + 3,), dtype=torch.int32, device=dev)
-    at = rows * width
-    table, lens = out.as_strided((rows, width), (width, 1)), out.as_strided((rows,), (1,), at)
-    copies = out.as_strided((rows, 3), (3, 1), at + rows)
-    counts = out.as_strided((2,), (1,), at + 4 * rows)
+    step = _PagesStep(rows, width, dev)
+    begin = step.out.data_ptr()
+    table, lens, copies, counts, full, batch_lens = [begin + 4 * i for i in step.at]
     held, wp, wn = _scratch(workspace, dev, lib.i8mm_kv_pages_workspace_bytes, rows, width, num_pages)
-    full = out.as_strided((1,), (1,), at + 4 * rows + 2)
-    batch_lens = out.as_strided((rows,), (1,), at + 4 * rows + 3)
     _run(dev, lib.i8mm_kv_pages_step_batch, page_table.data_ptr(), seq_lens.data_ptr(), seqs, width,
          parents.data_ptr(), None if keep is None else keep.data_ptr(),
          None if each is None else each.data_ptr(), new_all, rows, num_pages, page_tokens,
-         1 << 30 if max_len is None else int(max_len), table.data_ptr(), lens.data_ptr(),
-         batch_lens.data_ptr(), full.data_ptr(), copies.data_ptr(), counts.data_ptr(), wp, wn)
-    return (table, lens, copies, counts) + ((batch_lens, full) if batch else ())
+         1 << 30 if max_len is None else int(max_len), table, lens, batch_lens, full, copies, counts,
+         wp, wn)
+    return step
+
+
+def kv_pages_step(page_table, seq_lens, parents, num_pages, page_tokens, new_tokens=1, keep=None,
+                  workspace=None, max_len=None, batch=False):
+    """The page table of the next step: row i keeps the first keep[i] tokens (None:
+    all) of row parents[i] (none for a parent outside the table) and has room for
+    new_tokens (an int, or int32 [rows]) after them. All int32 on the GPU.
+
+    Returns the table [rows, max_pages], the lengths [rows] (new tokens included),
+    the copies to make before the next append [rows, 3] and counts [2]: copies, and
+    pages that were wanting (their tokens are absent). With batch=True also the lengths
+    for a KVBatch of the new tokens [rows] (0 for a row that has none, or no room for all
+    of them, in the table or below max_len) and how many have no room [1]."""
+    s = _pages_step(page_table, seq_lens, parents, num_pages, page_tokens, new_tokens, keep, workspace,
+                   max_len)
+    found = s.table, s.lens, s.copies, s.counts
+    return found + (s.batch_lens, s.full) if batch else found
 
 
 def kv_pages_compact(page_table, seq_lens, num_pages, page_tokens, workspace=None):
