@@ -243,7 +243,7 @@ struct Words {
 // with an insertion of about 100 instructions for each: 264 rows of 139286 fp16 words
 // with 24 places 36 us in place of 30, 80 of 50257 fp32 words with 10 12.2 and 10.6.)
 //
-// 512 rows of 131072 fp16 words: 30 us, 4.4 TB/s, of which the first and the last words
+// 512 rows of 131072 fp16 words: 31 us, 4.3 TB/s, of which the first and the last words
 // and the sorting take 6; 4 rows of 32000 words 6.7 us, a chain of waits.
 template <bool kHalf, bool kFew>
 __global__ __launch_bounds__(kBlockThreads) void k_beam_rows(BeamArgs a, int pieces, int piece) {
@@ -676,8 +676,8 @@ __global__ __launch_bounds__(kJoinThreads) void k_beam_join(BeamArgs a, int piec
 }
 
 // Pieces: about four blocks a compute unit, and at least a step of each wave: 512 rows
-// of 131072 fp16 words 33 us, with eight blocks a compute unit 37 and sixteen 41 (256 of
-// 50257 fp32 words 20.1 us in all, with seven blocks 23.1).
+// of 131072 fp16 words 31 us, with eight blocks a compute unit 35 and sixteen 41 (256 of
+// 50257 fp32 words 16.6 and 6.4 to join, with seven blocks 18.0 and 7.0).
 //
 // At most kPieceMost words: a lane's 32-bit sum then takes eight parts of 32 terms
 // (16 of 16 for fp32), and a row's sum is within 2^-16 of itself. In units of 2^-24,

@@ -255,11 +255,12 @@ __global__ __launch_bounds__(kBlockThreads, D <= 128 ? 2 : 1) void k_kv_attn_pag
 //
 // A wave's stages, keys of kCls groups and then their values, go through two buffers
 // of its part of LDS, each refilled as soon as it has been read (with 64 features
-// three and four take the room of a third block a compute unit: 180 us, so 165).
+// three and four take the room of a third block a compute unit: 176 and 179 us, so 154).
 //
 // 1367 tokens with lists of 32 pages of 48 tokens, 32 heads on 8 of 64 features (what
-// the lists name, 3.2 GB, comes from the L2s): 166 us, 19 TB/s, against 212 by the
-// kernel above; of 128 features 263 us, 24 TB/s, against 361: what the L2s give.
+// the lists name, 3.2 GB, comes from the L2s): traced 154 us (a pass among others 135, 24
+// TB/s), against 216 by the kernel above; of 128 features 284 us, 23 TB/s, against 387:
+// what the L2s give.
 template <int D, int kCls>
 struct WaveCfg {
   typedef Stage<D> S;
