@@ -20,9 +20,9 @@ def ensure_built():
 
 def __getattr__(name):
     # (what ops has is looked up there each time, so that a replaced op is found)
-    found = getattr(globals().get("ops"), name, None)
-    if found is not None:
-        return found
+    _ops = globals().get("ops")
+    if _ops is not None and hasattr(_ops, name):
+        return getattr(_ops, name)
     # ops and the module are imported on first use (they import torch)
     if name in ("ops", "linear", "synth", "kv_cache", "attention", "beam"):
         import importlib
