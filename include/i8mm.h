@@ -628,7 +628,8 @@ I8MM_API size_t int8_kv_cache_attention_pages_workspace_bytes(const i8mm_kv_cach
  * (EINVAL).
  *
  * num_seqs, num_rows up to 65535; max_pages * page_tokens up to 2^30;
- * num_rows * (max_pages + 1) and num_pages below 2^31; page_tokens as in the cache.
+ * num_seqs and num_rows, each times max_pages + 1, below 2^31; num_pages up to
+ * 2^31 - 8193; page_tokens as in the cache.
  * Errors: EINVAL, EALIGN, EWORKSPACE, ENODEVICE, ELAUNCH.
  */
 I8MM_API int i8mm_kv_pages_step(const int32_t* page_table, const int32_t* seq_lens,
